@@ -72,12 +72,25 @@ int current_device_info(DeviceInfo* out) {
   return FA_OK;
 }
 
+}  // namespace
+
+int device_status_word(int** status) {
+  DeviceInfo info;
+  const int st = current_device_info(&info);
+  if (st == FA_OK) *status = info.status;
+  return st;
+}
+
+namespace {
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + nb && y < x + na;
 }
+
+}  // namespace
 
 // Validates the element strides (sb, sh, sn) of [B, H, N, d] tensors and
 // orders the row, head and batch axes by increasing stride for the tensor
@@ -191,6 +204,8 @@ bool strided_overlap(const void* a, const void* b, int B, int H, int N, int d, c
 size_t span_bytes(int B, int H, int N, int d, const Strides& s, size_t elem) {
   return static_cast<size_t>((B - 1) * s.b + (H - 1) * s.h + (N - 1) * s.n + d) * elem;
 }
+
+namespace {
 
 // A bf16 [B, H, N, d] tensor with strides `st` as a tensor map: 3-D (d, N,
 // B*H) when st.merged, else 4-D with dimension 0 = d and dimensions 1..3 the
@@ -679,6 +694,7 @@ const char* fa_status_string(int status) {
     case FA_ERR_CUDA: return "FA_ERR_CUDA";
     case FA_ERR_DEVICE_TIMEOUT: return "FA_ERR_DEVICE_TIMEOUT";
     case FA_ERR_DEVICE_CHECK: return "FA_ERR_DEVICE_CHECK";
+    case FA_ERR_BAD_PAGE: return "FA_ERR_BAD_PAGE";
     default: return "FA_UNKNOWN_STATUS";
   }
 }

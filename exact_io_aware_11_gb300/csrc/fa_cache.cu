@@ -1,0 +1,364 @@
+// Writing K and V into the paged 8-bit cache and reading them back
+// (fa_cache_write, fa_cache_read).
+//
+// Mathematics: the rows of one (page, head) of K or V share a scale s, a power
+// of two: s = 2^e with e the smallest integer such that amax <= s * QMAX (448
+// for e4m3, 127 for int8). e comes from amax's exponent and one compare of its
+// mantissa, and x * 2^-e is exact, so a code depends on x and s alone and every
+// path forms the same one. A page that is partly filled keeps its rows when
+// the scale grows: their codes times 2^(e_old - e_new), rounded once more. In
+// e4m3 that is exact but for values that become subnormal; in int8 the errors of
+// repeated moves form a geometric series, at most one step in all.
+//
+// What bounds it: memory (2 bytes read and 1 written per element) for prompts,
+// latency for single tokens.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_cache_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+template <bool FP16>
+__device__ __forceinline__ float2 unpack2(uint32_t w) {
+  if constexpr (FP16) return __half22float2(*reinterpret_cast<__half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+template <bool FP16>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  if constexpr (FP16) {
+    __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<uint32_t*>(&v);
+  }
+  return pack_bf16(lo, hi);
+}
+
+// |x| where x is finite, else 0: an infinity or NaN does not set a scale.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a < INFINITY ? a : 0.f;
+}
+
+// The smallest power of two s >= 2^-126 with amax <= s * QMAX, exactly; 0 for
+// amax = 0. QMAX is 1.75 * 2^8 (e4m3) or 1.984375 * 2^6 (int8).
+template <bool INT8>
+__device__ __forceinline__ float scale_for(float amax) {
+  if (!(amax > 0.f)) return 0.f;
+  const uint32_t u = __float_as_uint(amax);
+  constexpr uint32_t kMant = INT8 ? 0x7e0000u : 0x600000u;  // mantissa of QMAX
+  constexpr int kExp = INT8 ? 6 : 8;
+  int e = static_cast<int>(u >> 23) - kExp + ((u & 0x7fffffu) > kMant ? 1 : 0);  // biased
+  e = max(e, 1);
+  return __uint_as_float(static_cast<uint32_t>(e) << 23);
+}
+__device__ __forceinline__ float inverse(float s) { return s > 0.f ? 1.f / s : 0.f; }
+
+// Two values to codes (ties to even, saturating), `lo` in the low byte.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode2(float lo, float hi) {
+  if constexpr (INT8) {
+    const int a = min(max(__float2int_rn(lo), -127), 127), b = min(max(__float2int_rn(hi), -127), 127);
+    return (static_cast<uint32_t>(a) & 0xffu) | ((static_cast<uint32_t>(b) & 0xffu) << 8);
+  } else {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+  }
+}
+// The two codes in the low 16 bits of w.
+template <bool INT8>
+__device__ __forceinline__ float2 decode2(uint32_t w) {
+  if constexpr (INT8) {
+    return make_float2(static_cast<float>(static_cast<int8_t>(w & 0xff)),
+                       static_cast<float>(static_cast<int8_t>((w >> 8) & 0xff)));
+  } else {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w & 0xffffu)));
+    return __half22float2(*reinterpret_cast<__half2*>(&h));
+  }
+}
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4(const float (&x)[4], float f) {
+  return encode2<INT8>(x[0] * f, x[1] * f) | (encode2<INT8>(x[2] * f, x[3] * f) << 16);
+}
+// Four codes times f, as codes again.
+template <bool INT8>
+__device__ __forceinline__ uint32_t move4(uint32_t w, float f) {
+  const float2 a = decode2<INT8>(w), b = decode2<INT8>(w >> 16);
+  const float x[4] = {a.x, a.y, b.x, b.y};
+  return encode4<INT8>(x, f);
+}
+
+// The tokens of sequence b that a call writes or reads: [first, end).
+struct Span {
+  long long first, end;
+};
+__device__ __forceinline__ Span span_of(const CacheRows& a, int b) {
+  const long long room = static_cast<long long>(a.c.table_width) << a.c.log2_page;
+  Span s;
+  s.first = a.start != nullptr ? max(0, __ldg(a.start + b)) : 0;
+  const int cnt = a.count != nullptr ? min(a.N, max(0, __ldg(a.count + b))) : a.N;
+  s.end = min(s.first + cnt, room);
+  return s;
+}
+// The page that entry i of sequence b's table row names, or -1 (reported).
+__device__ __forceinline__ int page_of(const CacheRows& a, int b, long long i) {
+  const int p = __ldg(a.c.table + b * a.c.table_stride + i);
+  if (p >= 0 && p < a.c.num_pages) return p;
+  report_bad_page(a.status);
+  return -1;
+}
+
+// Whole pages. A unit is one (sequence, page, head) of K or V; kT =
+// page * d / 32 threads hold its rows in registers, 32 elements each, so the
+// page is read once: the loads, the maximum over the unit, then the codes.
+// 16 bytes in and 8 bytes out per thread and row chunk, coalesced over the
+// unit's rows.
+template <bool FP16, bool INT8>
+__global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows a, int log2_t, int pages_per_seq,
+                                                                long long units) {
+  __shared__ float warp_max[16];
+  grid_dep_wait();
+  grid_dep_launch();
+  const int t = threadIdx.x & ((1 << log2_t) - 1);
+  const long long unit = ((static_cast<long long>(blockIdx.x) * blockDim.x) >> log2_t) + (threadIdx.x >> log2_t);
+  const int chunks = a.c.d >> 3, log2_chunks = a.c.d == 128 ? 4 : 3;
+  bool live = unit < units;
+  int kv = 0, h = 0, b = 0, page = -1;
+  Span sp{0, 0};
+  long long page0 = 0;
+  if (live) {
+    kv = static_cast<int>(unit & 1);
+    long long r = unit >> 1;
+    h = static_cast<int>(r % a.c.H);
+    r /= a.c.H;
+    const int rel = static_cast<int>(r % pages_per_seq);
+    b = static_cast<int>(r / pages_per_seq);
+    sp = span_of(a, b);
+    const long long pi = (sp.first >> a.c.log2_page) + rel;
+    page0 = pi << a.c.log2_page;
+    live = sp.first < sp.end && page0 < sp.end;
+    if (live) page = page_of(a, b, pi);
+    live = page >= 0;
+  }
+  uint4 x[4];
+  float amax = 0.f;
+  const uint16_t* src = a.x[kv] + b * a.st.b + h * a.st.h;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int idx = t + (k << log2_t), row = idx >> log2_chunks, ch = idx & (chunks - 1);
+    const long long tok = page0 + row;
+    x[k] = make_uint4(0, 0, 0, 0);
+    if (live && tok >= sp.first && tok < sp.end)
+      x[k] = __ldg(reinterpret_cast<const uint4*>(src + (tok - sp.first) * a.st.n + ch * 8));
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 f = unpack2<FP16>(w[i]);
+      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  if (log2_t > 5) {  // units of several warps
+    const int w = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) warp_max[w] = amax;
+    __syncthreads();
+    const int n = 1 << (log2_t - 5), w0 = w & ~(n - 1);
+    for (int i = 0; i < n; ++i) amax = fmaxf(amax, warp_max[w0 + i]);
+  }
+  float* const scale = a.c.scale[kv] + static_cast<long long>(page) * a.c.H + h;
+  const bool held = live && sp.first > page0;  // earlier tokens of this sequence lie in the page
+  const float s_old = held ? fmaxf(*scale, 0.f) : 0.f;
+  if (log2_t > 5)
+    __syncthreads();  // every thread of the unit has read the old scale
+  else
+    __syncwarp();
+  if (!live) return;
+  const float s = fmaxf(s_old, scale_for<INT8>(amax));
+  const float inv = inverse(s);
+  uint8_t* const dst = a.c.code[kv] + ((static_cast<long long>(page) * a.c.H + h) << a.c.log2_page) * a.c.d;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int idx = t + (k << log2_t), row = idx >> log2_chunks;
+    const long long tok = page0 + row;
+    uint2* const at = reinterpret_cast<uint2*>(dst + static_cast<long long>(idx) * 8);
+    if (tok >= sp.first && tok < sp.end) {
+      const float2 f0 = unpack2<FP16>(x[k].x), f1 = unpack2<FP16>(x[k].y);
+      const float2 f2 = unpack2<FP16>(x[k].z), f3 = unpack2<FP16>(x[k].w);
+      const float lo[4] = {f0.x, f0.y, f1.x, f1.y}, hi[4] = {f2.x, f2.y, f3.x, f3.y};
+      *at = make_uint2(encode4<INT8>(lo, inv), encode4<INT8>(hi, inv));
+    } else if (tok < sp.first && s > s_old) {
+      const uint2 w = *at;
+      *at = make_uint2(move4<INT8>(w.x, s_old * inv), move4<INT8>(w.y, s_old * inv));
+    }
+  }
+  if (t == 0) *scale = s;
+}
+
+// A few tokens (N <= kFew): one warp per (sequence, page, head) of K or V, a
+// row per lane group: lane l holds channels [4 l', 4 l' + 4) of a row, l' = l
+// modulo d / 4. The page's older rows are touched only when the scale grows.
+constexpr int kFew = 8;
+template <bool FP16, bool INT8>
+__global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a, int pages_per_seq, long long units) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  if (unit >= units) return;
+  const int lane = threadIdx.x & 31;
+  const int per_row = a.c.d >> 2, rows = 32 / per_row;  // lanes of a row, rows a warp takes at once: 1 or 2
+  const int sub = lane / per_row, ch = (lane - sub * per_row) * 4;
+  const int kv = static_cast<int>(unit & 1);
+  long long r = unit >> 1;
+  const int h = static_cast<int>(r % a.c.H);
+  r /= a.c.H;
+  const int rel = static_cast<int>(r % pages_per_seq), b = static_cast<int>(r / pages_per_seq);
+  const Span sp = span_of(a, b);
+  const long long pi = (sp.first >> a.c.log2_page) + rel, page0 = pi << a.c.log2_page;
+  if (sp.first >= sp.end || page0 >= sp.end) return;
+  const int page = page_of(a, b, pi);
+  if (page < 0) return;
+  const long long t0 = max(sp.first, page0), t1 = min(sp.end, page0 + (1LL << a.c.log2_page));
+  float* const scale = a.c.scale[kv] + static_cast<long long>(page) * a.c.H + h;
+  const bool held = sp.first > page0;
+  const float s_old = held ? fmaxf(*scale, 0.f) : 0.f;
+  const uint16_t* src = a.x[kv] + b * a.st.b + h * a.st.h + ch;
+  uint2 x[kFew];
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < kFew; ++k) {
+    const long long tok = t0 + k * rows + sub;
+    x[k] = make_uint2(0, 0);
+    if (tok < t1) x[k] = __ldg(reinterpret_cast<const uint2*>(src + (tok - sp.first) * a.st.n));
+  }
+#pragma unroll
+  for (int k = 0; k < kFew; ++k) {
+    const float2 f = unpack2<FP16>(x[k].x), g = unpack2<FP16>(x[k].y);
+    amax = fmaxf(fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y))), fmaxf(finite_abs(g.x), finite_abs(g.y)));
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  const float s = fmaxf(s_old, scale_for<INT8>(amax));
+  const float inv = inverse(s);
+  uint8_t* const dst = a.c.code[kv] + ((static_cast<long long>(page) * a.c.H + h) << a.c.log2_page) * a.c.d + ch;
+  if (s > s_old && held) {
+    const float f = s_old * inv;
+    const int n = static_cast<int>(sp.first - page0);
+#pragma unroll 4
+    for (int row = sub; row < n; row += rows) {
+      uint32_t* const at = reinterpret_cast<uint32_t*>(dst + row * a.c.d);
+      *at = move4<INT8>(*at, f);
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kFew; ++k) {
+    const long long tok = t0 + k * rows + sub;
+    if (tok < t1) {
+      const float2 f = unpack2<FP16>(x[k].x), g = unpack2<FP16>(x[k].y);
+      const float v[4] = {f.x, f.y, g.x, g.y};
+      *reinterpret_cast<uint32_t*>(dst + (tok - page0) * a.c.d) = encode4<INT8>(v, inv);
+    }
+  }
+  __syncwarp();  // the old scale has been read by every lane
+  if (lane == 0) *scale = s;
+}
+
+// Reading back: a thread takes 16 codes (one 16-byte load, two 16-byte
+// stores) of kRead rows a block's width apart, so that several loads are in
+// flight.
+constexpr int kRead = 4;
+template <bool FP16, bool INT8>
+__global__ void __launch_bounds__(256) cache_read_kernel(const CacheRows a, int tiles) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const int log2_chunks = a.c.d == 128 ? 3 : 2;
+  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+  const int h = bh % a.c.H, b = bh / a.c.H, kv = blockIdx.y;
+  const Span sp = span_of(a, b);
+  const int rows = 256 >> log2_chunks, ch = (threadIdx.x & ((1 << log2_chunks) - 1)) * 16;
+  const int n0 = tile * rows * kRead + (threadIdx.x >> log2_chunks);
+  uint16_t* const dst = a.x[kv] + b * a.st.b + h * a.st.h + ch;
+  uint4 w[kRead];
+  float s[kRead];
+#pragma unroll
+  for (int k = 0; k < kRead; ++k) {
+    const int n = n0 + k * rows;
+    const long long tok = sp.first + n;
+    w[k] = make_uint4(0, 0, 0, 0);
+    s[k] = 0.f;
+    if (n < a.N && tok < sp.end) {
+      const int page = page_of(a, b, tok >> a.c.log2_page);
+      if (page >= 0) {
+        const long long ph = static_cast<long long>(page) * a.c.H + h;
+        const long long row = (ph << a.c.log2_page) + (tok & ((1 << a.c.log2_page) - 1));
+        w[k] = *reinterpret_cast<const uint4*>(a.c.code[kv] + row * a.c.d + ch);
+        s[k] = a.c.scale[kv][ph];
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < kRead; ++k) {
+    const int n = n0 + k * rows;
+    if (n >= a.N) return;
+    const uint32_t in[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+    uint32_t out[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 lo = decode2<INT8>(in[i]), hi = decode2<INT8>(in[i] >> 16);
+      out[2 * i] = pack2<FP16>(lo.x * s[k], lo.y * s[k]);
+      out[2 * i + 1] = pack2<FP16>(hi.x * s[k], hi.y * s[k]);
+    }
+    uint4* const at = reinterpret_cast<uint4*>(dst + n * a.st.n);
+    at[0] = make_uint4(out[0], out[1], out[2], out[3]);
+    at[1] = make_uint4(out[4], out[5], out[6], out[7]);
+  }
+}
+
+template <bool FP16, bool INT8>
+cudaError_t write_variant(const CacheRows& a, cudaStream_t stream) {
+  // a run of N tokens touches at most this many pages, wherever it starts
+  const long long span_pages = ((static_cast<long long>(a.N) + a.c.page - 2) >> a.c.log2_page) + 1;
+  const int pages = static_cast<int>(span_pages < a.c.table_width ? span_pages : a.c.table_width);
+  const long long units = static_cast<long long>(a.B) * pages * a.c.H * 2;
+  if (a.N <= kFew) {
+    const long long blocks = (units + 3) / 4;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    return launch_pdl(cache_write_few_kernel<FP16, INT8>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream,
+                      a, pages, units);
+  }
+  const int log2_t = a.c.log2_page + (a.c.d == 128 ? 7 : 6) - 5;
+  const int threads = log2_t > 8 ? 512 : 256;
+  const long long per = threads >> log2_t, blocks = (units + per - 1) / per;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(cache_write_pages_kernel<FP16, INT8>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
+                    stream, a, log2_t, pages, units);
+}
+
+template <bool FP16, bool INT8>
+cudaError_t read_variant(const CacheRows& a, cudaStream_t stream) {
+  const int rows = (a.c.d == 128 ? 32 : 64) * kRead, tiles = (a.N + rows - 1) / rows;
+  const long long blocks = static_cast<long long>(a.B) * a.c.H * tiles;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+  return launch_pdl(cache_read_kernel<FP16, INT8>, dim3(static_cast<unsigned>(blocks), 2), dim3(256), 0, stream, a,
+                    tiles);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(const CacheRows& a, cudaStream_t stream) {
+  if (a.fp16) return a.c.int8 ? write_variant<true, true>(a, stream) : write_variant<true, false>(a, stream);
+  return a.c.int8 ? write_variant<false, true>(a, stream) : write_variant<false, false>(a, stream);
+}
+
+cudaError_t launch_cache_read(const CacheRows& a, cudaStream_t stream) {
+  if (a.fp16) return a.c.int8 ? read_variant<true, true>(a, stream) : read_variant<true, false>(a, stream);
+  return a.c.int8 ? read_variant<false, true>(a, stream) : read_variant<false, false>(a, stream);
+}
+
+}  // namespace fa

@@ -1,0 +1,175 @@
+// How the attention over the cache shares its work out, computed on the
+// device because the sequences' lengths live there.
+//
+// A unit is one (sequence, tile of query rows, cache head): row r of a tile is
+// query row r / G of head r % G of the cache head's group of G. A unit's steps
+// are the key tiles its rows see (at least one, so that units without keys
+// still write their rows). All units' steps lie end to end, ordered by
+// (sequence, row tile), then head; CTA c of C takes steps [T c / C, T (c + 1) / C),
+// an equal share whatever the lengths. A unit cut by a boundary leaves parts in
+// the workspace: slot 2 c for the part CTA c starts in the middle of, slot
+// 2 c + 1 for one it starts and does not finish. The CTA with a unit's last part
+// writes the unit's merge record.
+#pragma once
+
+#include "fa_cache_internal.h"
+
+namespace fa {
+
+struct AttnGrid {
+  int B, HK, N, G, D;
+  int rows;       // query rows of a tile
+  int row_tiles;  // tiles of N * G rows
+  int log2_keys;  // keys of a step
+  int cap;        // tokens a page table row has room for
+  int causal, split;
+  const int32_t* kv_len;
+  const int32_t* q_len;
+  // workspace (split only)
+  int4* record;   // [C]: entry, head, first CTA, last CTA of a cut unit; entry -1: none
+  float* m_part;  // [2 C][rows]
+  float* l_part;
+  float* o_part;  // [2 C][rows][D]
+};
+
+// One (sequence, row tile).
+struct AttnEntry {
+  int b, row0, kv, ql;  // first row of the tile; tokens and query rows of the sequence
+  int seen;             // tokens the tile's last row sees
+  int steps;
+};
+__device__ __forceinline__ AttnEntry attn_entry(const AttnGrid& g, int e) {
+  AttnEntry x;
+  x.b = e / g.row_tiles;
+  x.row0 = (e - x.b * g.row_tiles) * g.rows;
+  x.kv = min(g.cap, max(0, __ldg(g.kv_len + x.b)));
+  x.ql = g.q_len != nullptr ? min(g.N, max(0, __ldg(g.q_len + x.b))) : g.N;
+  const int rows = min(g.rows, x.ql * g.G - x.row0);
+  x.seen = 0;
+  if (rows > 0) x.seen = g.causal ? max(0, x.kv - x.ql + (x.row0 + rows - 1) / g.G + 1) : x.kv;
+  x.steps = max(1, (x.seen + (1 << g.log2_keys) - 1) >> g.log2_keys);
+  return x;
+}
+// Tokens that row r of the tile sees.
+__device__ __forceinline__ int attn_limit(const AttnGrid& g, const AttnEntry& x, int r) {
+  const int i = (x.row0 + r) / g.G;
+  if (i >= x.ql) return 0;
+  return g.causal ? max(0, x.kv - x.ql + i + 1) : x.kv;
+}
+
+// A CTA's place in the list: unit (e, h) at `step`, `pos` steps from the
+// list's start, until `end`.
+struct AttnCursor {
+  AttnEntry x;
+  int e, h, step;
+  long long pos, end;
+  __device__ __forceinline__ bool done(const AttnGrid& g) const {
+    // without a workspace a CTA finishes the units that start in its run
+    return pos >= end && (g.split || step == 0);
+  }
+  // To the next step; false when it starts another unit.
+  __device__ __forceinline__ bool next(const AttnGrid& g) {
+    ++pos;
+    if (++step < x.steps) return true;
+    next_unit(g);
+    return false;
+  }
+  __device__ __forceinline__ void next_unit(const AttnGrid& g) {
+    step = 0;
+    if (++h == g.HK) {
+      h = 0;
+      if (++e < g.B * g.row_tiles) x = attn_entry(g, e);
+    }
+  }
+};
+
+struct AttnShare {
+  long long total, first;  // steps in all; the first step of the entry `entry`
+  int entry, ctas;
+};
+
+// This CTA's cursor. Called by the whole CTA of kThreads threads; `sh` and
+// `part` (kThreads / 32 + 1 words) are shared memory.
+template <int kThreads>
+__device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* sh, long long* part) {
+  const int E = g.B * g.row_tiles, per = (E + kThreads - 1) / kThreads;
+  const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
+  long long mine = 0;
+  for (int e = e0; e < e1; ++e) mine += attn_entry(g, e).steps;
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+    if ((threadIdx.x & 31) >= o) incl += v;
+  }
+  if ((threadIdx.x & 31) == 31) part[threadIdx.x >> 5] = incl;
+  __syncthreads();
+  long long before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const long long v = part[w];
+    if (w < static_cast<int>(threadIdx.x >> 5)) before += v;
+    total += v;
+  }
+  before += incl - mine;
+  total *= g.HK;
+  const int C = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  const int c = blockIdx.x;
+  const long long s0 = c < C ? total * c / C : total;
+  if (threadIdx.x == 0) {
+    sh->total = total;
+    sh->ctas = C;
+    sh->entry = E;
+  }
+  __syncthreads();
+  long long p = before * g.HK;
+  if (s0 >= p && s0 < p + mine * g.HK) {
+    for (int e = e0; e < e1; ++e) {
+      const long long n = static_cast<long long>(attn_entry(g, e).steps) * g.HK;
+      if (s0 < p + n) {
+        sh->entry = e;
+        sh->first = p;
+        break;
+      }
+      p += n;
+    }
+  }
+  __syncthreads();
+  AttnCursor cur;
+  cur.e = sh->entry;
+  cur.h = 0;
+  cur.step = 0;
+  cur.pos = s0;
+  cur.end = c < C ? total * (c + 1) / C : total;
+  if (cur.e < E) {
+    cur.x = attn_entry(g, cur.e);
+    const long long rem = s0 - sh->first;
+    cur.h = static_cast<int>(rem / cur.x.steps);
+    cur.step = static_cast<int>(rem - static_cast<long long>(cur.h) * cur.x.steps);
+    if (!g.split && cur.step > 0) {  // the unit belongs to the CTA that it starts in
+      cur.pos += cur.x.steps - cur.step;
+      cur.next_unit(g);
+    }
+  } else {
+    cur.pos = cur.end = total;
+  }
+  return cur;
+}
+
+// The CTA whose run holds step s: the largest c with total * c / C <= s.
+__device__ __forceinline__ int attn_cta_of(long long s, long long total, int C) {
+  int c = static_cast<int>(min(static_cast<long long>(C - 1), s * C / total));
+  while (c + 1 < C && total * (c + 1) / C <= s) ++c;
+  while (c > 0 && total * c / C > s) --c;
+  return c;
+}
+
+// Keys of a step and rows of a tile of the kernel that a call of `rows` = N * G
+// query rows per (sequence, cache head) takes, and its CTAs.
+struct AttnPlan {
+  int rows, log2_keys, ctas;
+  long long units, cap_steps;
+};
+AttnPlan attn_plan(int B, int HK, long long rows, long long cap);
+
+}  // namespace fa

@@ -216,6 +216,16 @@ BwdWorkspace bwd_workspace_layout(int B, int H, int N, int d);
 // Streaming multiprocessors of the current device (cached per device).
 int sm_count();
 
+// Validation shared by the entry points (fa_api.cu).
+// FA_OK and the current device's status word, or why the device cannot be used.
+int device_status_word(int** status);
+// Strides of [B, H, N, d] tensors; false if they break the rules of fa.h.
+bool make_strides(int B, int H, int N, int d, long long sb, long long sh, long long sn, Strides* out);
+bool dense_strides(int B, int H, int N, int d, Strides* s);
+// Whether two 16-bit tensors with the same strides share an element.
+bool strided_overlap(const void* a, const void* b, int B, int H, int N, int d, const Strides& s);
+size_t span_bytes(int B, int H, int N, int d, const Strides& s, size_t elem);
+
 // Launches `kern` with programmatic dependent launch allowed: the grid may be
 // set up while the previous kernel on the stream is still running, and every
 // kernel of this library waits (griddepcontrol.wait) for its predecessor's

@@ -57,7 +57,8 @@ typedef enum {
   FA_ERR_UNSUPPORTED = 2,
   FA_ERR_CUDA = 3,
   FA_ERR_DEVICE_TIMEOUT = 4,
-  FA_ERR_DEVICE_CHECK = 5  /* checked builds only: a device-side bounds / alignment check failed */
+  FA_ERR_DEVICE_CHECK = 5, /* checked builds only: a device-side bounds / alignment check failed */
+  FA_ERR_BAD_PAGE = 6      /* fa_device_status: a page table entry was out of range and was skipped */
 } fa_status;
 
 struct CUstream_st; /* cudaStream_t == struct CUstream_st* */
@@ -308,11 +309,166 @@ int fa_attention_bwd(const void* q, const void* k, const void* v, const void* o,
                      int H, int N, int d, const fa_attention_options* opt, void* workspace,
                      size_t workspace_bytes, struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------
+ * Rotary positions, and a paged key/value cache held in 8 bits with the
+ * attention that reads it: what stands before attention in training, and
+ * around it in serving. These calls are not in the method's papers; they
+ * keep the conventions above (device pointers, caller-owned buffers,
+ * validation before any launch, asynchronous on `stream`) and add:
+ *   - dtype: the 16-bit type of the call's [B, H, N, d] tensors.
+ *   - Strides are element strides {batch, head, row} of one tensor, under the
+ *     rules of fa_attention_options; {0, 0, 0} means row-major.
+ *   - Sizes that live on the device (positions, lengths, page tables) are read
+ *     by the kernels when they run, so that a captured graph may be replayed
+ *     with other values. Lengths are clamped to what the page table and the
+ *     tensors hold. A page table entry that a call needs and that is not in
+ *     [0, num_pages) is skipped (nothing is read or written through it) and
+ *     fa_device_status reports FA_ERR_BAD_PAGE.
+ * ------------------------------------------------------------------------ */
+typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
+
+/* Options of fa_rotary_fwd / fa_rotary_bwd.
+ *   rotary_dim  : even, 2 .. d: the channels that are rotated, the first of
+ *                 each row; the others are copied.
+ *   interleaved : 1: pair i is channels (2i, 2i + 1); 0: (i, i + rotary_dim/2).
+ *   turns       : DEVICE uint64 [rotary_dim / 2]: turns (angle / 2 pi) that
+ *                 pair i makes per position, in units of 2^-64. The product
+ *                 with a position wraps to the exact fraction of a turn, so
+ *                 far positions lose nothing.
+ *   factor      : finite; multiplies cos and sin (1, or the attention factor
+ *                 of a scheme for long contexts).
+ *   positions   : DEVICE int32, element (b, n) at b*pos_stride_b + n*pos_stride_n
+ *                 (strides >= 0; 0 shares one row), or NULL: offset + n.
+ *   q_stride .. k_out_stride : {batch, head, row} of each tensor. */
+typedef struct fa_rotary_options {
+  int rotary_dim, interleaved, dtype;
+  float factor;
+  const uint64_t* turns;
+  const int32_t* positions;
+  int64_t pos_stride_b, pos_stride_n;
+  int32_t offset;
+  int64_t q_stride[3], q_out_stride[3], k_stride[3], k_out_stride[3];
+} fa_rotary_options;
+
+/* Rotary positions of queries and keys in one launch. With a, b the channels
+ * of pair i in the row at position p, and theta = 2 pi p turns[i] / 2^64:
+ *   a' = factor (a cos theta - b sin theta),  b' = factor (a sin theta + b cos theta).
+ *   q [B, Hq, N, d] -> q_out;  k [B, Hk, N, d] -> k_out, or both NULL with Hk = 0.
+ * d is 64 or 128. Angles, sines and products are in 32 bits, rounded once to
+ * dtype. A tensor may be rotated in place (same pointer and strides);
+ * any other overlap of an output is FA_ERR_INVALID_ARG. */
+int fa_rotary_fwd(const void* q, void* q_out, const void* k, void* k_out, int B, int Hq, int Hk,
+                  int N, int d, const fa_rotary_options* opt, struct CUstream_st* stream);
+
+/* Gradient of fa_rotary_fwd with respect to its inputs, from the gradients of
+ * its outputs with the same options: the rotation by -theta, times factor. */
+int fa_rotary_bwd(const void* dq_out, void* dq, const void* dk_out, void* dk, int B, int Hq,
+                  int Hk, int N, int d, const fa_rotary_options* opt, struct CUstream_st* stream);
+
+typedef enum { FA_CACHE_E4M3 = 0, FA_CACHE_INT8 = 1 } fa_cache_format;
+
+/* A pool of pages that hold K and V of one layer in 8 bits. Row j of page p,
+ * head h, channel c stands for the value code * scale:
+ *   k, v             : DEVICE 8-bit codes [num_pages, H, page_size, d]
+ *                      (e4m3, or int8), 16-byte aligned, contiguous;
+ *   k_scale, v_scale : DEVICE fp32 [num_pages, H], one scale for each page and
+ *                      head, finite and >= 0;
+ *   page_size        : 16, 32, 64 or 128 tokens;  d : 64 or 128.
+ * Token t of a sequence lies in row t % page_size of the page that its page
+ * table row names at t / page_size. */
+typedef struct fa_cache {
+  void* k;
+  void* v;
+  float* k_scale;
+  float* v_scale;
+  int num_pages, H, page_size, d, format;
+} fa_cache;
+
+/* Which tokens of which pages a call of fa_cache_write / fa_cache_read takes.
+ *   page_table : DEVICE int32, row b at b * table_stride, table_width entries;
+ *   start      : DEVICE int32 [B], the first token's place in the sequence,
+ *                or NULL for 0;
+ *   count      : DEVICE int32 [B], tokens of sequence b (clamped to [0, N] and
+ *                to the table's room), or NULL for N;
+ *   stride     : {batch, head, row} of the call's k and v [B, H, N, d]. */
+typedef struct fa_cache_range {
+  const int32_t* page_table;
+  int64_t table_stride;
+  int table_width;
+  const int32_t* start;
+  const int32_t* count;
+  int dtype;
+  int64_t stride[3];
+} fa_cache_range;
+
+/* Writes rows n < count[b] of k and v into the cache at tokens
+ * start[b] + n, quantised. For each page, head and tensor the scale becomes
+ * the smallest power of two s with |x| <= s * 448 (e4m3) or s * 127 (int8) for
+ * the finite values written to it, and no less than before where the page
+ * already holds earlier tokens of this sequence (its rows before start[b]);
+ * when it grows, those rows are moved to it. Codes are x / s to the nearest,
+ * ties to even. A power of two makes the division exact, and moving an e4m3 row
+ * only shifts its exponent (values that become subnormal are rounded
+ * again). Infinities are held as the largest code; NaN stays NaN in e4m3 and
+ * becomes 0 in int8. Rows behind the last token keep what they hold. Two
+ * sequences of one call must not write the same page. */
+int fa_cache_write(const fa_cache* cache, const void* k, const void* v, int B, int N,
+                   const fa_cache_range* range, struct CUstream_st* stream);
+
+/* Reads tokens start[b] + n, n < count[b], back as k and v (code * scale,
+ * rounded to dtype). Rows n >= count[b] are written as zeros. */
+int fa_cache_read(const fa_cache* cache, void* k, void* v, int B, int N,
+                  const fa_cache_range* range, struct CUstream_st* stream);
+
+/* Options of fa_cache_attention.
+ *   page_table, table_stride, table_width : as fa_cache_range;
+ *   kv_len : DEVICE int32 [B], tokens of sequence b in the cache (clamped to
+ *            [0, table_width * page_size]);
+ *   q_len  : DEVICE int32 [B], query rows of sequence b that count (clamped to
+ *            [0, N]), or NULL for N;
+ *   causal : 1: query row i sits at token kv_len[b] - q_len[b] + i and sees
+ *            the tokens up to it (the newest tokens' queries, their keys
+ *            already written); 0: every row sees all kv_len[b] tokens;
+ *   scale  : finite, > 0;  q_stride, o_stride : {batch, head, row}. */
+typedef struct fa_cache_attention_options {
+  const int32_t* page_table;
+  int64_t table_stride;
+  int table_width;
+  const int32_t* kv_len;
+  const int32_t* q_len;
+  int causal, dtype;
+  float scale;
+  int64_t q_stride[3], o_stride[3];
+} fa_cache_attention_options;
+
+/* Workspace with which fa_cache_attention spreads long sequences over every
+ * SM: each CTA takes an equal run of key tiles whatever the sequences' lengths,
+ * the parts of a (sequence, head) leave their O, maximum and sum in the
+ * workspace and a second kernel merges them. 0: not needed for these sizes, or
+ * the sizes are invalid. */
+size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, int N,
+                                          int table_width);
+
+/* Attention of q [B, Hq, N, d] over the cache: O = softmax(scale * q K^T) V in
+ * q's dtype and LSE (fp32 [B, Hq, N]); query head h reads cache head
+ * h / (Hq / H), Hq a multiple of H. N = 1 decodes, small N checks drafted
+ * tokens, large N runs a chunk of a prompt. The 8-bit codes are converted on
+ * chip (exactly) and the scales applied to the scores and the weights; pages
+ * with a V scale below 2^-100 count as zeros.
+ * Query rows that see no token, and rows i >= q_len[b], get O = 0, LSE = -inf.
+ *   workspace : DEVICE, 16-byte aligned, contents ignored, or NULL with
+ *               workspace_bytes = 0; with fewer bytes than
+ *               fa_cache_attention_workspace_bytes each (sequence, head) stays
+ *               on one CTA. Calls that share it must be ordered on the GPU. */
+int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache, int B, int Hq,
+                       int N, const fa_cache_attention_options* opt, void* workspace,
+                       size_t workspace_bytes, struct CUstream_st* stream);
+
 /* Device-side status of the current device: FA_OK, or FA_ERR_DEVICE_TIMEOUT
  * if a bounded wait inside a kernel gave up since the last call, or (in a
  * library built with FA_CHECKS=1) FA_ERR_DEVICE_CHECK if a TMA copy failed
- * its coordinate or alignment check and was skipped. Reading
- * clears it. Call only after synchronising the streams that ran the
+ * its coordinate or alignment check and was skipped, or FA_ERR_BAD_PAGE
+ * if a page table entry was out of range. Reading clears it. Call only after synchronising the streams that ran the
  * kernels. Returns FA_ERR_CUDA if the status word cannot be read. */
 int fa_device_status(void);
 
