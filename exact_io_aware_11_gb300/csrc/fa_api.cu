@@ -251,6 +251,24 @@ bool encode_rows(CUtensorMap* map, const void* base, int B, int H, int N, int d,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+}  // namespace
+
+// A pool of 8-bit codes as `rows` rows of d bytes; box = box_rows whole rows, swizzled
+// over the row's length (128 or 64 bytes).
+bool encode_code_rows(CUtensorMap* map, const void* base, long long rows, int d, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(d)};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(d), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[2] = {1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+namespace {
+
 // fp32 [B*H, rows, d] as a 3-D tensor map; box = 32 columns (128 bytes) x 128
 // rows x 1 head, 128-byte swizzle (the backward's dQ accumulator).
 bool encode_f32_rows(CUtensorMap* map, const void* base, int BH, int rows, int d) {

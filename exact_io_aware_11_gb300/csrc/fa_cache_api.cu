@@ -214,6 +214,8 @@ int check_attention_sizes(const fa_cache* cache, int B, int Hq, int N, int table
   if (B < 1 || B > 65535 || Hq < 1 || Hq > 65535 || N < 1 || table_width < 1 || Hq % cache->H != 0)
     return FA_ERR_INVALID_ARG;
   if (static_cast<long long>(table_width) * cache->page_size > INT_MAX - 256) return FA_ERR_INVALID_ARG;
+  // rows of the pool are coordinates of its tensor map
+  if (static_cast<long long>(cache->num_pages) * cache->H > INT_MAX / cache->page_size) return FA_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(N) * (Hq / cache->H);
   if (rows > INT_MAX - 256 || static_cast<long long>(B) * (rows / 8 + 1) > INT_MAX) return FA_ERR_INVALID_ARG;
   return FA_OK;
@@ -300,6 +302,10 @@ int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache
   a.kv_len = opt->kv_len;
   a.q_len = opt->q_len;
   a.wait_limit = kWaitLimitCycles;
+  const long long pool_rows = static_cast<long long>(cache->num_pages) * cache->H * cache->page_size;
+  if (!encode_code_rows(&a.tm[0], cache->k, pool_rows, cache->d, cache->page_size) ||
+      !encode_code_rows(&a.tm[1], cache->v, pool_rows, cache->d, cache->page_size))
+    return FA_ERR_CUDA;
   a.ws = static_cast<uint8_t*>(workspace);
   a.ws_bytes = workspace_bytes;
   return launch_cache_attention(a, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;

@@ -3,23 +3,25 @@
 //
 // Mathematics: with codes kc, vc and scales ks, vs of each page,
 //   x_j = scale log2e ks (q . kc_j),  y_j = x_j + log2 vs_j,  M = max_j y_j,
-//   w_j = 2^(y_j - M + 15),  O = sum_j w_j vc_j / sum_j w_j / vs_j,
-//   LSE = (M - 15 + log2 sum_j w_j / vs_j) ln 2.
+//   w_j = 2^(y_j - M + 11),  O = sum_j w_j vc_j / sum_j w_j / vs_j,
+//   LSE = (M - 11 + log2 sum_j w_j / vs_j) ln 2.
 // Taking V's scale into the exponent keeps it out of the products, and the
 // running maximum then sits on the weight that V is really given: the weights are
-// rounded to fp16 (11 bits, against bf16's 8) and 2^15 below the largest one
+// rounded to fp16 (11 bits, against bf16's 8) and 2^25 below the largest one
 // they still have all of them. The sum is formed from the unrounded weights. Codes of
 // either format are exact in fp16. A row of q is scaled by a power of two so that
 // its largest value lies in [2^14, 2^15): exact for every value within 2^-28 of it.
 //
-// What bounds it: reading the cache, d bytes per token, head and tensor. Each
-// warp streams its own key tiles (32 keys, K and V: 8 KB at d = 128) through a
-// ring of kStages cp.async stages of its own, with no barrier between warps
-// until a unit ends; 8 warps per SM keep 128 KB and more in flight, three times
-// what the latency asks for. Products run on the warp matrix instruction with
-// keys (K) and channels (V) on its 16 rows and the query rows on its 8 columns,
-// so that a group of 8 query rows costs one pass over the converted codes:
-// the tcgen05 form needs 128 rows and would convert through shared memory.
+// What bounds it: reading the cache, d bytes per token, head and tensor. A CTA
+// is one producer warp, which walks the page table and fills a ring of stages
+// (128 keys, K and V: 32 KB at d = 128) with TMA copies of whole pages, and four
+// consumer warps, each with 32 keys of every stage and a softmax of its own, which
+// meet only when a unit ends. The reference maximum moves only when a weight
+// would pass 2^4, so that most tiles need no reduction across lanes. Products run
+// on the warp matrix instruction with keys (K) and channels (V) on its 16 rows and
+// the query rows on its 8 columns, so that a group of 8 query rows costs one pass
+// over the converted codes: the tcgen05 form needs 128 rows and would convert
+// through shared memory.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -31,20 +33,26 @@ namespace fa {
 namespace {
 
 constexpr float kLn2 = 0.69314718055994530942f;
-constexpr int kWarps = 4, kThreads = kWarps * 32, kStages = 3;
+constexpr int kWarps = 4;                    // consumer warps; the producer follows them
+constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = 32;                    // keys of a warp's tile
-constexpr float kBias = 15.f;                // weights are at most 2^15
+constexpr int kKeys = kWarps * kTile;        // keys of a step
+constexpr float kSlack = 4.f;                // log2 units a weight may stand above the reference
+constexpr float kBias = 15.f - kSlack;       // weights are at most 2^15
 constexpr float kMinScale = 0x1p-100f;       // a page whose V scale is below it counts as zeros
 
-template <int D>
+template <int D, int NT>
 struct Layout {
-  static constexpr int kMat = kTile * D;               // K or V of a tile
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kMat = kKeys * D;               // K or V of a step
   static constexpr int kStage = 2 * kMat;
-  static constexpr int kRing = kWarps * kStages * kStage;
-  static constexpr int kScales = kWarps * kStages * 16;  // ks, vs of two 16-key groups
-  static constexpr int kMerge = kWarps * 8 * D * 4;
-  static constexpr int kSmem = kRing + kScales + kMerge;  // two CTAs per SM
-  static_assert(2 * (kSmem + 1024 + 512) <= 228 * 1024, "two CTAs per SM");
+  static constexpr int kRing = kStages * kStage;
+  static constexpr int kScales = kRing;                // [stages][8 groups of 16 keys] ks, vs
+  static constexpr int kMerge = kScales + kStages * 64;  // four rows of every warp, fp32
+  static constexpr int kQuery = kMerge + kWarps * 4 * D * 4;  // NT = 2: fragments of q, rows' factors
+  static constexpr int kBars = kQuery + (NT > 1 ? NT * (D / 16) * 256 + NT * 32 : 0);
+  static constexpr int kSmem = kBars + 2 * kStages * 8 + 1024;  // slack: 1024-byte alignment
+  static_assert(2 * (kSmem + 1024 + 1024) <= 228 * 1024, "two CTAs per SM");
 };
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
@@ -59,17 +67,6 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
   return fp16 ? pack_half(lo, hi) : pack_bf16(lo, hi);
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool real) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(real ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
@@ -118,8 +115,8 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   return y;
 }
 
-// Byte offset of 16-byte chunk c of row r in a tile: chunks are permuted
-// within 128-byte lines so that the reads of 8 lanes meet all banks.
+// Byte offset of 16-byte chunk c of row r in a tile, as the TMA copy's swizzle
+// leaves it: the reads of 8 lanes meet all banks (d = 64: of V, half of them).
 template <int D>
 __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
   if constexpr (D == 128) return r * 128 + ((c ^ (r & 7)) << 4);
@@ -153,11 +150,14 @@ __device__ __forceinline__ float load_query(const uint16_t* row, bool real, bool
   return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 }
 
-// A weight of zero does not mask a NaN. Where the rows of a unit see different
-// parts of a tile, V's NaN codes (e4m3 0x7f, 0xff) are taken out of it, and the
-// rows that see one of them get a NaN sum. Lane: keys key, + 1, + 8, + 9.
+// A weight of zero does not mask a NaN. Where not every row of a unit sees all
+// of a tile (its keys may be leftovers behind the sequence's end), V's NaN codes
+// (e4m3 0x7f, 0xff) are taken out of it, and the rows that see one of them get a
+// NaN sum; `gone`: no row sees any (a page that was not read).
+// Lane: keys key, + 1, + 8, + 9.
 template <int NT, int W>
-__device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], int key, const int (&lim)[NT][2], float (&l)[NT][2]) {
+__device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], bool gone, int key, const int (&lim)[NT][2],
+                                              float (&l)[NT][2]) {
   int first = 0x7fffffff;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -169,7 +169,7 @@ __device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], int key, cons
         first = min(first, key + (k & 1) + 8 * (k >> 1));
       }
     }
-  first = __reduce_min_sync(0xffffffffu, first);
+  first = gone ? 0x7fffffff : __reduce_min_sync(0xffffffffu, first);
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -177,111 +177,169 @@ __device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], int key, cons
       if (first < lim[n][k]) l[n][k] = __int_as_float(0x7fffffff);
 }
 
-// NT groups of 8 query rows per unit.
-template <int D, int NT, bool INT8>
-__global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttnLaunch a, const AttnGrid g) {
-  using L = Layout<D>;
-  constexpr int kM = D / 16;  // 16-channel tiles of O
-  constexpr int kRows = 8 * NT;
-  extern __shared__ __align__(1024) uint8_t smem[];
-  __shared__ AttnShare share;
-  __shared__ long long part[kWarps];
-  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-  grid_dep_wait();
-  grid_dep_launch();
-
-  AttnCursor cur = attn_share<kThreads>(g, &share, part);
-  if (g.split && threadIdx.x == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
-
-  const uint32_t ring = smem_u32(smem) + warp * kStages * L::kStage;
-  const uint32_t scales = smem_u32(smem) + L::kRing + warp * kStages * 16;
-  float* const merge = reinterpret_cast<float*>(smem + L::kRing + L::kScales);
-
-  // ---- the load side: this warp's tile of the load cursor's step
-  AttnCursor ld = cur;
+// The producer warp: every step of the CTA's run, a stage each. Lane i < 8 looks
+// after the step's i-th group of 16 keys: its page id is loaded two steps ahead,
+// the page's scales one step ahead, and the first lane of each page copies its
+// rows (the pages' K and V lie in rows of d bytes of one tensor map each).
+template <int D, int NT>
+__device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor ld, uint8_t* smem,
+                                        uint64_t* full, uint64_t* empty, const Watchdog& wd, int lane) {
+  using L = Layout<D, NT>;
+  constexpr int kStages = L::kStages;
   const CacheView& c = a.c;
-  int pid[2];
-  // page ids of the load cursor's tile (-1 where no key is needed or bad);
-  // a page holds one or both of the tile's 16-key groups
-  auto look_up = [&]() {
-#pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int key = (ld.step << g.log2_keys) + warp * kTile + u * 16;
-      pid[u] = -1;
-      if (!ld.done(g) && key < ld.x.seen) {
-        pid[u] = __ldg(c.table + ld.x.b * c.table_stride + (key >> c.log2_page));
-      }
-    }
+  const int per_page = min(c.page, kKeys) >> 4;  // groups of a page
+  const bool group = lane < kKeys / 16, leader = group && lane % per_page == 0;
+  // what is known of a coming step, per lane
+  struct Step {
+    bool live, want;  // within the run; the group holds keys that are seen
+    int pid, h, row;  // row: of the page, where the step's rows start
   };
-  auto issue = [&](int stage) {
-    if (!ld.done(g)) {
-      const int key0 = (ld.step << g.log2_keys) + warp * kTile;
-      const uint32_t dst = ring + stage * L::kStage;
-      const uint8_t* base[2][2];
-      int left[2];  // rows of each group that are read
-#pragma unroll
-      for (int u = 0; u < 2; ++u) {
-        const int key = key0 + u * 16;
-        const bool want = key < ld.x.seen, good = want && pid[u] >= 0 && pid[u] < c.num_pages;
-        if (want && !good && lane == 0) report_bad_page(a.status);
-        left[u] = good ? min(16, ld.x.seen - key) : 0;
-        const long long ph = good ? static_cast<long long>(pid[u]) * c.H + ld.h : 0;
-        const long long row = good ? (ph << c.log2_page) + (key & (c.page - 1)) : 0;
-        base[u][0] = c.code[0] + row * D;
-        base[u][1] = c.code[1] + row * D;
-        if (lane < 2) {  // lane: K's or V's scale
-          const uint32_t at = scales + stage * 16 + u * 8 + lane * 4;
-          if (good)
-            cp_async4(at, c.scale[lane] + ph);
-          else
-            asm volatile("st.shared.f32 [%0], %1;" ::"r"(at), "f"(-1.f) : "memory");
-        }
-      }
-      constexpr int kChunks = D / 16, kPer = 32 / kChunks;  // rows a warp copies at once
-      const int ch = lane % kChunks, r0 = lane / kChunks;
-#pragma unroll
-      for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-        for (int i = 0; i < kTile / kPer; ++i) {
-          const int r = r0 + i * kPer, u = (i * kPer) >> 4;
-          const int ru = r - u * 16;
-          cp_async16(dst + kv * L::kMat + tile_offset<D>(r, ch), base[u][kv] + ru * D + ch * 16, ru < left[u]);
-        }
+  auto look = [&]() {  // the cursor's step, then on
+    Step s{!ld.done(g), false, -1, 0, 0};
+    if (s.live) {
+      const int key = (ld.step << g.log2_keys) + lane * 16;
+      s.want = group && key < ld.x.seen;
+      s.h = ld.h;
+      s.row = key & (c.page - 1);
+      if (s.want) s.pid = __ldg(c.table + ld.x.b * c.table_stride + (key >> c.log2_page));
       ld.next(g);
     }
-    cp_async_commit();
-    look_up();
+    return s;
   };
-  look_up();
-#pragma unroll
-  for (int s = 0; s < kStages - 1; ++s) issue(s);
+  auto scales = [&](Step& s, float& ks, float& vs) {
+    const bool good = s.want && s.pid >= 0 && s.pid < c.num_pages;
+    if (s.want && !good) report_bad_page(a.status);
+    s.want = good;
+    ks = vs = -1.f;
+    if (good) {
+      const int ph = s.pid * c.H + s.h;
+      s.row += ph << c.log2_page;
+      ks = __ldg(c.scale[0] + ph);
+      vs = __ldg(c.scale[1] + ph);
+    }
+  };
+  float ks, vs;
+  Step now = look();
+  scales(now, ks, vs);
+  Step next = look();
+  int n = 0;  // steps issued
+  for (; now.live; ++n) {
+    const int st = n % kStages;
+    if (n >= kStages && !mbar_wait_warp(empty + st, ((n / kStages) - 1) & 1, wd)) break;
+    // The copies go out before their bytes are announced (the phase cannot end
+    // before lane 0 arrives) and before the scales, which may still be on their way.
+    if (leader && now.want) {
+      uint8_t* const dst = smem + st * L::kStage + lane * 16 * D;
+      tma_load_2d(dst, &a.tm[0], full + st, now.row);
+      tma_load_2d(dst + L::kMat, &a.tm[1], full + st, now.row);
+    }
+    const int copies = __popc(__ballot_sync(0xffffffffu, leader && now.want));
+    if (group)
+      *reinterpret_cast<float2*>(smem + L::kScales + st * 64 + lane * 8) = make_float2(ks, vs);
+    __syncwarp();
+    if (lane == 0) {
+      if (copies > 0)
+        mbar_expect_tx(full + st, copies * 2 * min(c.page, kKeys) * D);
+      else
+        mbar_arrive(full + st);
+    }
+    now = next;
+    scales(now, ks, vs);
+    next = look();
+  }
+  // let every copy in flight land before the CTA can exit
+  for (int i = max(0, n - kStages); i < n; ++i)
+    mbar_wait_drain(full + i % kStages, (i / kStages) & 1, a.wait_limit);
+}
+
+// NT groups of 8 query rows per unit.
+template <int D, int NT, bool INT8>
+__global__ void __launch_bounds__(kThreads, 2)
+    cache_attn_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
+  using L = Layout<D, NT>;
+  constexpr int kStages = L::kStages;
+  constexpr int kM = D / 16;  // 16-channel tiles of O
+  constexpr int kRows = 8 * NT;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ AttnShare share;
+  __shared__ long long part[kThreads / 32];
+  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+  __shared__ int abort_flag;
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
+  float* const merge = reinterpret_cast<float*>(smem + L::kMerge);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kBars);
+  uint64_t* const empty = full + kStages;
+  check_init(a.status);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(full + i, 1);
+      mbar_init(empty + i, kWarps);
+    }
+    abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&a.tm[0]);
+    tma_prefetch_desc(&a.tm[1]);
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  const Watchdog wd{a.wait_limit, a.status, &abort_flag};
+  AttnCursor cur = attn_share<kThreads>(g, &share, part);  // its barriers publish the above
+  if (warp == kWarps) {
+    produce<D, NT>(a, g, cur, smem, full, empty, wd, lane);
+    return;
+  }
+  if (g.split && threadIdx.x == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
+  bool alive = true;  // no wait has given up
   int stage = 0;
+  uint32_t phase = 0;
 
   while (!cur.done(g)) {
     // ---- a unit (or the CTA's part of one)
     const AttnEntry x = cur.x;
-    const int h = cur.h, step0 = cur.step;
+    const int h = cur.h, step0 = cur.step, steps = cur.run(g);
     const long long unit_first = cur.pos - cur.step;
-    uint32_t q[NT][D / 8];
+    // Queries: lane (gq, t) holds what the products take of row gq, channels
+    // [D/4 t, D/4 (t + 1)). Two groups of rows would take too many registers: each is
+    // then loaded by one warp and shared, in the order of the products.
+    uint32_t q[NT == 1 ? D / 8 : 1];
+    uint2* const qs = reinterpret_cast<uint2*>(smem + L::kQuery);
+    float* const rfs = reinterpret_cast<float*>(smem + L::kQuery + NT * (D / 16) * 256);
     float rf[NT][2];
     int lim[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    auto query = [&](int n, uint32_t (&w)[D / 8]) {
       const int r = x.row0 + n * 8 + gq, i = r / g.G;
-      const bool real = i < x.ql;
       const uint16_t* row = a.q + x.b * a.sq.b + static_cast<long long>(h * g.G + (r - i * g.G)) * a.sq.h + i * a.sq.n;
-      const float inv = load_query<D>(row, real, a.fp16, t, q[n]);
+      return load_query<D>(row, i < x.ql, a.fp16, t, w) * a.scale_log2;
+    };
+    if constexpr (NT == 1) {
+      const float f = query(0, q);
+      rf[0][0] = __shfl_sync(0xffffffffu, f, 2 * t * 4);
+      rf[0][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
+    } else {
+      if (warp < NT) {
+        uint32_t w[D / 8];
+        const float f = query(warp, w);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        rf[n][k] = __shfl_sync(0xffffffffu, inv, (2 * t + k) * 4) * a.scale_log2;
-        lim[n][k] = attn_limit(g, x, n * 8 + 2 * t + k);
+        for (int i = 0; i < D / 16; ++i) qs[(warp * (D / 16) + i) * 32 + lane] = make_uint2(w[2 * i], w[2 * i + 1]);
+        if (t == 0) rfs[warp * 8 + gq] = f;
+      }
+      named_bar_sync(1, kWarps * 32);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        rf[n][0] = rfs[n * 8 + 2 * t];
+        rf[n][1] = rfs[n * 8 + 2 * t + 1];
       }
     }
-    int low = lim[0][0];
+    int low = 0x7fffffff;  // keys below it are seen by every row
 #pragma unroll
-    for (int n = 0; n < NT; ++n) low = min(low, min(lim[n][0], lim[n][1]));
-    low = __reduce_min_sync(0xffffffffu, low);  // keys below it are seen by every row
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        lim[n][k] = attn_limit(g, x, n * 8 + 2 * t + k);
+        low = min(low, lim[n][k]);
+      }
+    low = __reduce_min_sync(0xffffffffu, low);
 
     float o[kM][NT][4];
     float m[NT][2], l[NT][2];
@@ -295,97 +353,113 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
       l[n][0] = l[n][1] = 0.f;
     }
 
-    int step = step0;
-    bool more = true;
-    while (more) {
-      cp_async_wait<kStages - 2>();
-      __syncwarp();
-      // the stage read in the last iteration is free: refill it
-      issue(stage == 0 ? kStages - 1 : stage - 1);
-      const int key0 = (step << g.log2_keys) + warp * kTile;
-      const uint32_t kt = ring + stage * L::kStage, vt = kt + L::kMat;
-      if (key0 < x.seen) {
-        const uint4 sc = lds128(scales + stage * 16);
+    int key0 = (step0 << g.log2_keys) + warp * kTile;
+    for (int step = 0; step < steps; ++step, key0 += kKeys) {
+      alive = alive && mbar_wait_warp(full + stage, phase, wd);
+      if (alive && key0 < x.seen) {
+        const uint32_t kt = smem_u32(smem) + stage * L::kStage, vt = kt + L::kMat;
+        const uint4 sc = lds128(smem_u32(smem) + L::kScales + stage * 64 + warp * 16);
         const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.z)};
         const float vs[2] = {fmaxf(__uint_as_float(sc.y), kMinScale), fmaxf(__uint_as_float(sc.w), kMinScale)};
         // S^T = K Q^T: keys gq, gq + 8 of each group, queries 2t, 2t + 1
         float s[2][NT][4];
 #pragma unroll
-        for (int u = 0; u < 2; ++u) {
+        for (int u = 0; u < 2; ++u)
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int k = 0; k < 4; ++k) s[u][n][k] = 0.f;
 #pragma unroll
-          for (int j = 0; j < D / 64; ++j) {
-            const int ch = (D / 64) * t + j;
-            const uint4 ka = lds128(kt + tile_offset<D>(u * 16 + gq, ch));
-            const uint4 kb = lds128(kt + tile_offset<D>(u * 16 + gq + 8, ch));
-            const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+        for (int j = 0; j < D / 64; ++j) {
+          uint32_t kw[2][2][4];  // group, half of its keys, word
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint4 v = lds128(kt + tile_offset<D>(warp * kTile + u * 16 + e * 8 + gq, (D / 64) * t + j));
+              kw[u][e][0] = v.x;
+              kw[u][e][1] = v.y;
+              kw[u][e][2] = v.z;
+              kw[u][e][3] = v.w;
+            }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint2 qf[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              qf[n] = NT == 1 ? make_uint2(q[NT == 1 ? (j * 4 + w) * 2 : 0], q[NT == 1 ? (j * 4 + w) * 2 + 1 : 0])
+                              : qs[(n * (D / 16) + j * 4 + w) * 32 + lane];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
               uint32_t a0, a1, a2, a3;
-              decode4<INT8>(wa[w], a0, a2);
-              decode4<INT8>(wb[w], a1, a3);
+              decode4<INT8>(kw[u][0][w], a0, a2);
+              decode4<INT8>(kw[u][1][w], a1, a3);
 #pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma16816(s[u][n], a0, a1, a2, a3, q[n][(j * 4 + w) * 2], q[n][(j * 4 + w) * 2 + 1]);
+              for (int n = 0; n < NT; ++n) mma16816(s[u][n], a0, a1, a2, a3, qf[n].x, qf[n].y);
             }
           }
         }
-        // y, the running maximum, the weights
+        // y, the reference maximum, the weights
         const float lv[2] = {__log2f(vs[0]), __log2f(vs[1])};
         const float iv[2] = {__fdividef(1.f, vs[0]), __fdividef(1.f, vs[1])};
-        const bool mixed = min(key0 + kTile, x.seen) > low;  // rows see different parts of the tile
         const bool edge = key0 + kTile > low || ks[0] < 0.f || ks[1] < 0.f;
-        bool moved = false;
-        float al[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) s[u][n][k] = fmaf(s[u][n][k], rf[n][k & 1] * ks[u], lv[u]);
+        if (edge) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (key0 + u * 16 + gq + 8 * (k >> 1) >= lim[n][k & 1] || ks[u] < 0.f) s[u][n][k] = -INFINITY;
+        }
+        float mx[NT][2];
+        bool above = false;  // a weight would pass 2^15
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int k = 0; k < 2; ++k) {
-            float mx = -INFINITY;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              const float f = rf[n][k] * ks[u];
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float y = fmaf(s[u][n][2 * e + k], f, lv[u]);
-                if (edge && (key0 + u * 16 + gq + 8 * e >= lim[n][k] || ks[u] < 0.f)) y = -INFINITY;
-                s[u][n][2 * e + k] = y;
-                mx = fmaxf(mx, y);
-              }
-            }
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = fmaxf(m[n][k], mx);
-            const float base = mn == -INFINITY ? 0.f : mn;
-            al[n][k] = ex2(m[n][k] - base);
-            moved |= mn > m[n][k];
-            m[n][k] = mn;
-            float sum = 0.f;
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-              float su = 0.f;
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float p = ex2(s[u][n][2 * e + k] - base + kBias);
-                s[u][n][2 * e + k] = p;
-                su += p;
-              }
-              sum = fmaf(su, iv[u], sum);
-            }
-            l[n][k] = fmaf(l[n][k], al[n][k], sum);
+            mx[n][k] = fmaxf(fmaxf(s[0][n][k], s[0][n][2 + k]), fmaxf(s[1][n][k], s[1][n][2 + k]));
+            above |= mx[n][k] > m[n][k] + kSlack;
           }
-        if (__any_sync(0xffffffffu, moved)) {
+        if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
-          for (int i = 0; i < kM; ++i)
+          for (int n = 0; n < NT; ++n) {
+            float al[2];
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int k = 0; k < 2; ++k) {
+              mx[n][k] = fmaxf(mx[n][k], __shfl_xor_sync(0xffffffffu, mx[n][k], 4));
+              mx[n][k] = fmaxf(mx[n][k], __shfl_xor_sync(0xffffffffu, mx[n][k], 8));
+              mx[n][k] = fmaxf(mx[n][k], __shfl_xor_sync(0xffffffffu, mx[n][k], 16));
+              const float mn = fmaxf(m[n][k], mx[n][k]);
+              al[k] = ex2(m[n][k] - (mn == -INFINITY ? 0.f : mn));
+              m[n][k] = mn;
+              l[n][k] *= al[k];
+            }
 #pragma unroll
-              for (int k = 0; k < 4; ++k) o[i][n][k] *= al[n][k & 1];
+            for (int i = 0; i < kM; ++i)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) o[i][n][k] *= al[k & 1];
+          }
         }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const float base = (m[n][k] == -INFINITY ? 0.f : m[n][k]) - kBias;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float p0 = ex2(s[u][n][k] - base), p1 = ex2(s[u][n][2 + k] - base);
+              s[u][n][k] = p0;
+              s[u][n][2 + k] = p1;
+              l[n][k] = fmaf(p0 + p1, iv[u], l[n][k]);
+            }
+          }
         // O^T += V^T P^T: channels (D/8) gq + 2i, + 1 on the rows of tile i
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -399,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
           uint32_t v[4][D / 32];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r = u * 16 + 2 * t + (k & 1) + 8 * (k >> 1);
+            const int r = warp * kTile + u * 16 + 2 * t + (k & 1) + 8 * (k >> 1);
             if constexpr (D == 128) {
               const uint4 w = lds128(vt + tile_offset<D>(r, gq));
               v[k][0] = w.x;
@@ -412,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
               v[k][1] = w.y;
             }
           }
-          if (!INT8 && mixed) poison_unseen(v, key0 + u * 16 + 2 * t, lim, l);
+          if (!INT8 && edge) poison_unseen(v, ks[u] < 0.f, key0 + u * 16 + 2 * t, lim, l);
 #pragma unroll
           for (int i = 0; i < kM; ++i) {
             const uint32_t sel = (i & 1) ? 0x7362 : 0x5140;
@@ -424,11 +498,14 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
           }
         }
       }
-      stage = stage == kStages - 1 ? 0 : stage + 1;
-      ++step;
-      const bool same = cur.next(g);
-      more = same && !cur.done(g);
+      __syncwarp();  // every lane has read the stage
+      if (lane == 0) mbar_arrive(empty + stage);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
     }
+    cur.skip(g, steps);
 
     // ---- join the warps' keys
 #pragma unroll
@@ -442,30 +519,30 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
           sm_l[warp][n * 8 + 2 * t + k] = l[n][k];
         }
       }
-    __syncthreads();
-    const bool whole = step0 == 0 && step == x.steps;
+    named_bar_sync(1, kWarps * 32);
+    const bool last = step0 + steps == x.steps, whole = step0 == 0 && last;
     const int slot = 2 * blockIdx.x + (step0 == 0 ? 1 : 0);
-    if (g.split && !whole && step == x.steps && threadIdx.x == 0)
+    if (g.split && !whole && last && threadIdx.x == 0)
       g.record[blockIdx.x] =
           make_int4(x.b * g.row_tiles + x.row0 / g.rows, h, attn_cta_of(unit_first, share.total, share.ctas), 0);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
+    for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const int r = n * 8 + 2 * t + k;
-        float M = sm_m[0][r];
+      for (int k = 0; k < 2; ++k) {  // rows n * 8 + 2 t + k
+        {
+          const int r = n * 8 + 2 * t + k;
+          float M = sm_m[0][r];
 #pragma unroll
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
-        const float f = ex2(m[n][k] - (M == -INFINITY ? 0.f : M));
-        float* const at = merge + (warp * 8 + 2 * t + k) * D + gq * (D / 8);
+          for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
+          const float f = ex2(m[n][k] - (M == -INFINITY ? 0.f : M));
+          float* const at = merge + (warp * 4 + t) * D + gq * (D / 8);
 #pragma unroll
-        for (int i = 0; i < kM; ++i)
-          *reinterpret_cast<float2*>(at + 2 * i) = make_float2(o[i][n][k] * f, o[i][n][2 + k] * f);
-      }
-      __syncthreads();
-      {
-        constexpr int kPer = 8 * D / kThreads;  // channels of a row per thread
-        const int r8 = threadIdx.x / 16, d0 = (threadIdx.x & 15) * kPer, r = n * 8 + r8;
+          for (int i = 0; i < kM; ++i)
+            *reinterpret_cast<float2*>(at + 2 * i) = make_float2(o[i][n][k] * f, o[i][n][2 + k] * f);
+        }
+        named_bar_sync(1, kWarps * 32);
+        constexpr int kPer = D / 32;  // channels of a row per lane
+        const int d0 = lane * kPer, r = n * 8 + 2 * warp + k;
         float M = sm_m[0][r];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
@@ -476,16 +553,15 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
         for (int w = 0; w < kWarps; ++w) {
           sum = fmaf(sm_l[w][r], ex2(sm_m[w][r] - (M == -INFINITY ? 0.f : M)), sum);
 #pragma unroll
-          for (int d = 0; d < kPer; ++d) acc[d] += merge[(w * 8 + r8) * D + d0 + d];
+          for (int d = 0; d < kPer; ++d) acc[d] += merge[(w * 4 + warp) * D + d0 + d];
         }
         const int row = x.row0 + r, i = row / g.G;
         if (!whole) {
           const long long pr = static_cast<long long>(slot) * g.rows + r;
 #pragma unroll
-          for (int d = 0; d < kPer; d += 4)
-            *reinterpret_cast<float4*>(g.o_part + pr * D + d0 + d) =
-                make_float4(acc[d], acc[d + 1], acc[d + 2], acc[d + 3]);
-          if (d0 == 0) {
+          for (int d = 0; d < kPer; d += 2)
+            *reinterpret_cast<float2*>(g.o_part + pr * D + d0 + d) = make_float2(acc[d], acc[d + 1]);
+          if (lane == 0) {
             g.m_part[pr] = M;
             g.l_part[pr] = sum;
           }
@@ -494,103 +570,132 @@ __global__ void __launch_bounds__(kThreads, 2) cache_attn_kernel(const CacheAttn
           const float inv = none ? 0.f : 1.f / sum;
           const int head = h * g.G + (row - i * g.G);
           uint16_t* const dst = a.o + x.b * a.so.b + head * a.so.h + i * a.so.n + d0;
-          uint32_t w[kPer / 2];
 #pragma unroll
-          for (int d = 0; d < kPer / 2; ++d)
-            w[d] = none ? 0u : pack16(acc[2 * d] * inv, acc[2 * d + 1] * inv, a.fp16);
-          if constexpr (kPer == 8)
-            *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
-          else
-            *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-          if (d0 == 0)
+          for (int d = 0; d < kPer; d += 2)
+            *reinterpret_cast<uint32_t*>(dst + d) = none ? 0u : pack16(acc[d] * inv, acc[d + 1] * inv, a.fp16);
+          if (lane == 0)
             a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + i] =
                 none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2;
         }
+        named_bar_sync(1, kWarps * 32);
       }
-      __syncthreads();
-    }
   }
-  cp_async_wait<0>();
 }
 
 // Merges the units that were cut. Block (c, y) looks at CTA c's record (the
-// unit whose last part c ran); each warp takes rows of it: with m_q, l_q, O_q
-// of part q and M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q.
-// Lane: four consecutive channels (two at d = 64) of every part, 16-byte loads.
+// unit whose last part c ran) and takes rows 2 y and 2 y + 1 of it, four warps
+// each, which take every fourth part and then join theirs: with m_q, l_q, O_q of
+// part q and M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q. A lane holds
+// D / 32 consecutive channels and loads eight parts at a time, statistics and all,
+// so that a row of 76 parts takes three round trips (one warp to a row, four parts
+// at a time and the maximum in a pass of its own: 36 us; 8 us so).
 template <int D>
-__global__ void __launch_bounds__(256) cache_attn_merge_kernel(const CacheAttnLaunch a, const AttnGrid g) {
+__global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
+  constexpr int kV = D / 32, kBatch = 8;
+  __shared__ float sm_m[8], sm_l[8], sm_o[8][D];
   grid_dep_wait();
   grid_dep_launch();
   const int4 rec = g.record[blockIdx.x];
   if (rec.x < 0) return;
-  const AttnEntry x = attn_entry(g, rec.x);
-  const int c0 = rec.z, c1 = blockIdx.x, lane = threadIdx.x & 31;
-  constexpr int kV = D / 32;
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < g.rows; r += gridDim.y * 8) {
-    const int row = x.row0 + r, i = row / g.G;
-    if (i >= g.N) continue;
-    float M = -INFINITY;
-    for (int q = c0 + lane; q <= c1; q += 32) {
-      const int slot = 2 * q + (q == c0 ? 1 : 0);
-      M = fmaxf(M, g.m_part[static_cast<long long>(slot) * g.rows + r]);
-    }
+  const int c0 = rec.z, c1 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.y * 2 + (warp >> 2);
+  float acc[kV], sum = 0.f, M = -INFINITY;
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    const float base = M == -INFINITY ? 0.f : M;
-    float acc[kV], sum = 0.f;
+  for (int d = 0; d < kV; ++d) acc[d] = 0.f;
+  for (int q0 = c0 + (warp & 3); q0 <= c1; q0 += 4 * kBatch) {
+    float mq[kBatch], lq[kBatch], v[kBatch][kV];
 #pragma unroll
-    for (int d = 0; d < kV; ++d) acc[d] = 0.f;
-#pragma unroll 4
-    for (int q = c0; q <= c1; ++q) {
-      const long long pr = static_cast<long long>(2 * q + (q == c0 ? 1 : 0)) * g.rows + r;
-      const float f = ex2(g.m_part[pr] - base);
-      sum = fmaf(g.l_part[pr], f, sum);
-      float v[kV];
-      if constexpr (kV == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(g.o_part + pr * D + lane * 4);
-        v[0] = w.x;
-        v[1] = w.y;
-        v[2] = w.z;
-        v[3] = w.w;
-      } else {
-        const float2 w = *reinterpret_cast<const float2*>(g.o_part + pr * D + lane * 2);
-        v[0] = w.x;
-        v[1] = w.y;
+    for (int k = 0; k < kBatch; ++k) {
+      const int q = q0 + 4 * k;
+      mq[k] = -INFINITY;
+      lq[k] = 0.f;
+#pragma unroll
+      for (int d = 0; d < kV; ++d) v[k][d] = 0.f;
+      if (q <= c1) {
+        const long long pr = static_cast<long long>(2 * q + (q == c0 ? 1 : 0)) * g.rows + r;
+        mq[k] = g.m_part[pr];
+        lq[k] = g.l_part[pr];
+        if constexpr (kV == 4) {
+          const float4 w = *reinterpret_cast<const float4*>(g.o_part + pr * D + lane * 4);
+          v[k][0] = w.x;
+          v[k][1] = w.y;
+          v[k][2] = w.z;
+          v[k][3] = w.w;
+        } else {
+          const float2 w = *reinterpret_cast<const float2*>(g.o_part + pr * D + lane * 2);
+          v[k][0] = w.x;
+          v[k][1] = w.y;
+        }
       }
-#pragma unroll
-      for (int d = 0; d < kV; ++d) acc[d] = fmaf(v[d], f, acc[d]);
     }
-    const bool none = sum == 0.f;
-    const float inv = none ? 0.f : 1.f / sum;
-    const int head = rec.y * g.G + (row - i * g.G);
-    uint16_t* const dst = a.o + x.b * a.so.b + head * a.so.h + i * a.so.n + lane * kV;
-    uint32_t w[kV / 2];
+    float Mn = M;
 #pragma unroll
-    for (int d = 0; d < kV / 2; ++d) w[d] = none ? 0u : pack16(acc[2 * d] * inv, acc[2 * d + 1] * inv, a.fp16);
-    if constexpr (kV == 4)
-      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-    else
-      *reinterpret_cast<uint32_t*>(dst) = w[0];
-    if (lane == 0)
-      a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + i] =
-          none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2;
+    for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, mq[k]);
+    const float base = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - base);
+    M = Mn;
+    sum *= e;
+#pragma unroll
+    for (int d = 0; d < kV; ++d) acc[d] *= e;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const float f = ex2(mq[k] - base);
+      sum = fmaf(lq[k], f, sum);
+#pragma unroll
+      for (int d = 0; d < kV; ++d) acc[d] = fmaf(v[k][d], f, acc[d]);
+    }
   }
+#pragma unroll
+  for (int d = 0; d < kV; ++d) sm_o[warp][lane * kV + d] = acc[d];
+  if (lane == 0) {
+    sm_m[warp] = M;
+    sm_l[warp] = sum;
+  }
+  __syncthreads();
+  const int b = rec.x / g.row_tiles, row = (rec.x - b * g.row_tiles) * g.rows + r, i = row / g.G;
+  if ((warp & 3) != 0 || i >= g.N) return;
+  float all = M;
+#pragma unroll
+  for (int w = 1; w < 4; ++w) all = fmaxf(all, sm_m[warp + w]);
+  const float base = all == -INFINITY ? 0.f : all;
+  sum = 0.f;
+#pragma unroll
+  for (int d = 0; d < kV; ++d) acc[d] = 0.f;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = ex2(sm_m[warp + w] - base);
+    sum = fmaf(sm_l[warp + w], f, sum);
+#pragma unroll
+    for (int d = 0; d < kV; ++d) acc[d] = fmaf(sm_o[warp + w][lane * kV + d], f, acc[d]);
+  }
+  const bool none = sum == 0.f;
+  const float inv = none ? 0.f : 1.f / sum;
+  const int head = rec.y * g.G + (row - i * g.G);
+  uint16_t* const dst = a.o + b * a.so.b + head * a.so.h + i * a.so.n + lane * kV;
+  uint32_t w[kV / 2];
+#pragma unroll
+  for (int d = 0; d < kV / 2; ++d) w[d] = none ? 0u : pack16(acc[2 * d] * inv, acc[2 * d + 1] * inv, a.fp16);
+  if constexpr (kV == 4)
+    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+  else
+    *reinterpret_cast<uint32_t*>(dst) = w[0];
+  if (lane == 0)
+    a.lse[(static_cast<long long>(b) * a.Hq + head) * g.N + i] = none ? -INFINITY : (all - kBias + log2f(sum)) * kLn2;
 }
 
 template <int D, int NT, bool INT8>
 cudaError_t launch_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
   auto kern = cache_attn_kernel<D, NT, INT8>;
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(kern), Layout<D>::kSmem);
+  const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(kern), Layout<D, NT>::kSmem);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3(ctas), dim3(kThreads), Layout<D>::kSmem, stream, a, g);
+  return launch_pdl(kern, dim3(ctas), dim3(kThreads), Layout<D, NT>::kSmem, stream, a, g);
 }
 
 template <int D, bool INT8>
 cudaError_t launch_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
   cudaError_t e = g.rows == 8 ? launch_rows<D, 1, INT8>(a, g, ctas, stream) : launch_rows<D, 2, INT8>(a, g, ctas, stream);
   if (e != cudaSuccess || !g.split) return e;
-  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, (g.rows + 7) / 8), dim3(256), 0, stream, a, g);
+  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, g.rows / 2), dim3(256), 0, stream, a, g);
 }
 
 struct AttnWorkspace {

@@ -54,6 +54,7 @@ cudaError_t launch_cache_write(const CacheRows& a, cudaStream_t stream);
 cudaError_t launch_cache_read(const CacheRows& a, cudaStream_t stream);
 
 struct CacheAttnLaunch {
+  CUtensorMap tm[2];  // K's and V's codes as rows of d bytes, boxes of a page
   CacheView c;
   const uint16_t* q;
   uint16_t* o;
@@ -71,6 +72,8 @@ struct CacheAttnLaunch {
 };
 cudaError_t launch_cache_attention(const CacheAttnLaunch& a, cudaStream_t stream);
 size_t cache_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width);
+
+bool encode_code_rows(CUtensorMap* map, const void* base, long long rows, int d, int box_rows);
 
 // Records a page table entry out of range (fa_device_status).
 static __device__ __noinline__ void report_bad_page(int* status) {

@@ -26,7 +26,7 @@ struct AttnGrid {
   const int32_t* kv_len;
   const int32_t* q_len;
   // workspace (split only)
-  int4* record;   // [C]: entry, head, first CTA, last CTA of a cut unit; entry -1: none
+  int4* record;   // [C]: entry, head, first CTA of a cut unit that c ends; entry -1: none
   float* m_part;  // [2 C][rows]
   float* l_part;
   float* o_part;  // [2 C][rows][D]
@@ -67,12 +67,19 @@ struct AttnCursor {
     // without a workspace a CTA finishes the units that start in its run
     return pos >= end && (g.split || step == 0);
   }
-  // To the next step; false when it starts another unit.
-  __device__ __forceinline__ bool next(const AttnGrid& g) {
+  __device__ __forceinline__ void next(const AttnGrid& g) {
     ++pos;
-    if (++step < x.steps) return true;
-    next_unit(g);
-    return false;
+    if (++step == x.steps) next_unit(g);
+  }
+  // Steps of this unit that are the CTA's.
+  __device__ __forceinline__ int run(const AttnGrid& g) const {
+    const int left = x.steps - step;
+    return g.split && end - pos < left ? static_cast<int>(end - pos) : left;
+  }
+  __device__ __forceinline__ void skip(const AttnGrid& g, int n) {
+    pos += n;
+    step += n;
+    if (step == x.steps) next_unit(g);
   }
   __device__ __forceinline__ void next_unit(const AttnGrid& g) {
     step = 0;

@@ -451,7 +451,7 @@ size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, 
 
 /* Attention of q [B, Hq, N, d] over the cache: O = softmax(scale * q K^T) V in
  * q's dtype and LSE (fp32 [B, Hq, N]); query head h reads cache head
- * h / (Hq / H), Hq a multiple of H. N = 1 decodes, small N checks drafted
+ * h / (Hq / H), Hq a multiple of H; num_pages * H * page_size < 2^31. N = 1 decodes, small N checks drafted
  * tokens, large N runs a chunk of a prompt. The 8-bit codes are converted on
  * chip (exactly) and the scales applied to the scores and the weights; pages
  * with a V scale below 2^-100 count as zeros.
