@@ -26,20 +26,16 @@
 #include <cuda_fp16.h>
 
 #include "fa_cache_internal.h"
+#include "fa_cache_math.cuh"
 #include "fa_cache_sched.cuh"
-#include "fa_ptx.cuh"
 
 namespace fa {
 namespace {
 
-constexpr float kLn2 = 0.69314718055994530942f;
 constexpr int kWarps = 4;                    // consumer warps; the producer follows them
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = 32;                    // keys of a warp's tile
 constexpr int kKeys = kWarps * kTile;        // keys of a step
-constexpr float kSlack = 4.f;                // log2 units a weight may stand above the reference
-constexpr float kBias = 15.f - kSlack;       // weights are at most 2^15
-constexpr float kMinScale = 0x1p-100f;       // a page whose V scale is below it counts as zeros
 
 template <int D, int NT>
 struct Layout {
@@ -54,51 +50,6 @@ struct Layout {
   static constexpr int kSmem = kBars + 2 * kStages * 8 + 1024;  // slack: 1024-byte alignment
   static_assert(2 * (kSmem + 1024 + 1024) <= 228 * 1024, "two CTAs per SM");
 };
-
-__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
-  if (fp16) return __half22float2(*reinterpret_cast<__half2*>(&w));
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
-  __half2 v = __floats2half2_rn(lo, hi);
-  return *reinterpret_cast<uint32_t*>(&v);
-}
-__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
-  return fp16 ? pack_half(lo, hi) : pack_bf16(lo, hi);
-}
-
-__device__ __forceinline__ uint4 lds128(uint32_t a) {
-  uint4 v;
-  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
-  return v;
-}
-__device__ __forceinline__ uint2 lds64(uint32_t a) {
-  uint2 v;
-  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
-  return v;
-}
-
-// The codes in bytes 0, 1 (lo) and 2, 3 (hi) of a word, as fp16 pairs. For
-// int8 the byte plus 128 becomes the mantissa of 1024 + b and 1152 comes off.
-template <bool INT8>
-__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  if constexpr (INT8) {
-    w ^= 0x80808080u;
-    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
-    const uint32_t k = 0x64806480u;
-    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&k));
-    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&k));
-    lo = *reinterpret_cast<const uint32_t*>(&x);
-    hi = *reinterpret_cast<const uint32_t*>(&y);
-  } else {
-    asm("{\n\t.reg .b16 a, b;\n\t"
-        "mov.b32 {a, b}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(w));
-  }
-}
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                          uint32_t b0, uint32_t b1) {
@@ -575,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             *reinterpret_cast<uint32_t*>(dst + d) = none ? 0u : pack16(acc[d] * inv, acc[d + 1] * inv, a.fp16);
           if (lane == 0)
             a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + i] =
-                none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2;
+                none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
         }
         named_bar_sync(1, kWarps * 32);
       }
@@ -599,6 +550,7 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
   if (rec.x < 0) return;
   const int c0 = rec.z, c1 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int r = blockIdx.y * 2 + (warp >> 2);
+  const int b = rec.x / g.row_tiles, row = (rec.x - b * g.row_tiles) * g.rows + r, i = row / g.G;
   float acc[kV], sum = 0.f, M = -INFINITY;
 #pragma unroll
   for (int d = 0; d < kV; ++d) acc[d] = 0.f;
@@ -611,7 +563,7 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
       lq[k] = 0.f;
 #pragma unroll
       for (int d = 0; d < kV; ++d) v[k][d] = 0.f;
-      if (q <= c1) {
+      if (q <= c1 && i < g.N) {
         const long long pr = static_cast<long long>(2 * q + (q == c0 ? 1 : 0)) * g.rows + r;
         mq[k] = g.m_part[pr];
         lq[k] = g.l_part[pr];
@@ -651,7 +603,6 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
     sm_l[warp] = sum;
   }
   __syncthreads();
-  const int b = rec.x / g.row_tiles, row = (rec.x - b * g.row_tiles) * g.rows + r, i = row / g.G;
   if ((warp & 3) != 0 || i >= g.N) return;
   float all = M;
 #pragma unroll
@@ -679,7 +630,7 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
   else
     *reinterpret_cast<uint32_t*>(dst) = w[0];
   if (lane == 0)
-    a.lse[(static_cast<long long>(b) * a.Hq + head) * g.N + i] = none ? -INFINITY : (all - kBias + log2f(sum)) * kLn2;
+    a.lse[(static_cast<long long>(b) * a.Hq + head) * g.N + i] = none ? -INFINITY : (all - kBias + log2f(sum)) * kLn2Cache;
 }
 
 template <int D, int NT, bool INT8>
@@ -693,9 +644,12 @@ cudaError_t launch_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, c
 
 template <int D, bool INT8>
 cudaError_t launch_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  cudaError_t e = g.rows == 8 ? launch_rows<D, 1, INT8>(a, g, ctas, stream) : launch_rows<D, 2, INT8>(a, g, ctas, stream);
+  cudaError_t e = g.rows > 16  ? launch_cache_attention_tiles(a, g, ctas, stream)
+                  : g.rows > 8 ? launch_rows<D, 2, INT8>(a, g, ctas, stream)
+                               : launch_rows<D, 1, INT8>(a, g, ctas, stream);
   if (e != cudaSuccess || !g.split) return e;
-  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, g.rows / 2), dim3(256), 0, stream, a, g);
+  const long long live = min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G);
+  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, static_cast<unsigned>((live + 1) / 2)), dim3(256), 0, stream, a, g);
 }
 
 struct AttnWorkspace {
@@ -715,12 +669,12 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
   AttnPlan p{};
-  p.rows = rows <= 8 ? 8 : 16;
+  p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
   p.log2_keys = 7;
   p.units = static_cast<long long>(B) * HK * ((rows + p.rows - 1) / p.rows);
   p.cap_steps = (cap + 127) >> 7;
   if (p.cap_steps < 1) p.cap_steps = 1;
-  const long long most = 2LL * sm_count();
+  const long long most = (p.rows > 16 ? 1LL : 2LL) * sm_count();  // CTAs that an SM holds
   p.ctas = static_cast<int>(p.units >= most || p.units * p.cap_steps >= most ? most : p.units * p.cap_steps);
   return p;
 }

@@ -1,0 +1,62 @@
+// What the kernels of the attention over the cache share: the conversions of
+// 16-bit types and of the 8-bit codes, and the weights' reference.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "fa_ptx.cuh"
+
+namespace fa {
+
+constexpr float kLn2Cache = 0.69314718055994530942f;
+constexpr float kSlack = 4.f;                // log2 units a weight may stand above the reference
+constexpr float kBias = 15.f - kSlack;       // weights are at most 2^15
+constexpr float kMinScale = 0x1p-100f;       // a page whose V scale is below it counts as zeros
+
+__device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
+  if (fp16) return __half22float2(*reinterpret_cast<__half2*>(&w));
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
+  return fp16 ? pack_half(lo, hi) : pack_bf16(lo, hi);
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(a));
+  return v;
+}
+
+// The codes in bytes 0, 1 (lo) and 2, 3 (hi) of a word, as fp16 pairs. For
+// int8 the byte plus 128 becomes the mantissa of 1024 + b and 1152 comes off.
+template <bool INT8>
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if constexpr (INT8) {
+    w ^= 0x80808080u;
+    const uint32_t a = __byte_perm(w, 0x64646464u, 0x4140), b = __byte_perm(w, 0x64646464u, 0x4342);
+    const uint32_t k = 0x64806480u;
+    const __half2 x = __hsub2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&k));
+    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&k));
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  } else {
+    asm("{\n\t.reg .b16 a, b;\n\t"
+        "mov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  }
+}
+
+}  // namespace fa

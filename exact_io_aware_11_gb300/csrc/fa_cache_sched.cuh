@@ -179,4 +179,7 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap);
 
+// Tiles of 128 (g.rows) or 2 x 128 query rows on tcgen05 (fa_cache_tile.cu).
+cudaError_t launch_cache_attention_tiles(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream);
+
 }  // namespace fa
