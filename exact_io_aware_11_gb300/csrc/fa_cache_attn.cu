@@ -283,12 +283,16 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     }
     int low = 0x7fffffff;  // keys below it are seen by every row
+    bool real[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
-        lim[n][k] = attn_limit(g, x, n * 8 + 2 * t + k);
-        low = min(low, lim[n][k]);
+        const int r = n * 8 + 2 * t + k;
+        lim[n][k] = attn_limit(g, x, r);
+        // columns that stand for no query (their q is zero) do not make a tile an edge
+        real[n][k] = (x.row0 + r) / g.G < x.ql;
+        if (real[n][k]) low = min(low, lim[n][k]);
       }
     low = __reduce_min_sync(0xffffffffu, low);
 
@@ -465,6 +469,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       for (int k = 0; k < 2; ++k) {
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) l[n][k] += __shfl_xor_sync(0xffffffffu, l[n][k], w);
+        if (!real[n][k]) {
+          l[n][k] = 0.f;
+          m[n][k] = -INFINITY;
+        }
         if (gq == 0) {
           sm_m[warp][n * 8 + 2 * t + k] = m[n][k];
           sm_l[warp][n * 8 + 2 * t + k] = l[n][k];
@@ -533,13 +541,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
 }
 
-// Merges the units that were cut. Block (c, y) looks at CTA c's record (the
-// unit whose last part c ran) and takes rows 2 y and 2 y + 1 of it, four warps
-// each, which take every fourth part and then join theirs: with m_q, l_q, O_q of
-// part q and M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q. A lane holds
-// D / 32 consecutive channels and loads eight parts at a time, statistics and all,
-// so that a row of 76 parts takes three round trips (one warp to a row, four parts
-// at a time and the maximum in a pass of its own: 36 us; 8 us so).
+// Merges the units that were cut. Blocks (c, y) look at CTA c's record (the unit
+// whose last part c ran) and share its rows out: with m_q, l_q, O_q of part q and
+// M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q. A lane holds D / 32
+// consecutive channels and loads eight parts at a time, statistics and all. A unit
+// of few parts (many query rows) gives each of the block's 8 warps a row; one of
+// more parts gives a row four warps, which take every fourth part and then join
+// theirs (a row of 76 parts with one warp, four at a time: 36 us; 8 us so).
 template <int D>
 __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
   constexpr int kV = D / 32, kBatch = 8;
@@ -549,88 +557,96 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
   const int4 rec = g.record[blockIdx.x];
   if (rec.x < 0) return;
   const int c0 = rec.z, c1 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.y * 2 + (warp >> 2);
-  const int b = rec.x / g.row_tiles, row = (rec.x - b * g.row_tiles) * g.rows + r, i = row / g.G;
-  float acc[kV], sum = 0.f, M = -INFINITY;
+  const int W = c1 - c0 < 4 ? 1 : 4, sub = warp & (W - 1);  // warps of a row
+  const int b = rec.x / g.row_tiles, row0 = (rec.x - b * g.row_tiles) * g.rows;
+  const int live = static_cast<int>(min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G - row0));
+  for (int r0 = blockIdx.y * (8 / W); r0 < live; r0 += gridDim.y * (8 / W)) {  // uniform over the block
+    const int r = r0 + warp / W;
+    float acc[kV], sum = 0.f, M = -INFINITY;
 #pragma unroll
-  for (int d = 0; d < kV; ++d) acc[d] = 0.f;
-  for (int q0 = c0 + (warp & 3); q0 <= c1; q0 += 4 * kBatch) {
-    float mq[kBatch], lq[kBatch], v[kBatch][kV];
+    for (int d = 0; d < kV; ++d) acc[d] = 0.f;
+    for (int q0 = c0 + sub; q0 <= c1 && r < live; q0 += W * kBatch) {
+      float mq[kBatch], lq[kBatch], v[kBatch][kV];
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int q = q0 + 4 * k;
-      mq[k] = -INFINITY;
-      lq[k] = 0.f;
+      for (int k = 0; k < kBatch; ++k) {
+        const int q = q0 + W * k;
+        mq[k] = -INFINITY;
+        lq[k] = 0.f;
 #pragma unroll
-      for (int d = 0; d < kV; ++d) v[k][d] = 0.f;
-      if (q <= c1 && i < g.N) {
-        const long long pr = static_cast<long long>(2 * q + (q == c0 ? 1 : 0)) * g.rows + r;
-        mq[k] = g.m_part[pr];
-        lq[k] = g.l_part[pr];
-        if constexpr (kV == 4) {
-          const float4 w = *reinterpret_cast<const float4*>(g.o_part + pr * D + lane * 4);
-          v[k][0] = w.x;
-          v[k][1] = w.y;
-          v[k][2] = w.z;
-          v[k][3] = w.w;
-        } else {
-          const float2 w = *reinterpret_cast<const float2*>(g.o_part + pr * D + lane * 2);
-          v[k][0] = w.x;
-          v[k][1] = w.y;
+        for (int d = 0; d < kV; ++d) v[k][d] = 0.f;
+        if (q <= c1) {
+          const long long pr = static_cast<long long>(2 * q + (q == c0 ? 1 : 0)) * g.rows + r;
+          mq[k] = g.m_part[pr];
+          lq[k] = g.l_part[pr];
+          if constexpr (kV == 4) {
+            const float4 w = *reinterpret_cast<const float4*>(g.o_part + pr * D + lane * 4);
+            v[k][0] = w.x;
+            v[k][1] = w.y;
+            v[k][2] = w.z;
+            v[k][3] = w.w;
+          } else {
+            const float2 w = *reinterpret_cast<const float2*>(g.o_part + pr * D + lane * 2);
+            v[k][0] = w.x;
+            v[k][1] = w.y;
+          }
         }
       }
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, mq[k]);
+      const float base = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - base);
+      M = Mn;
+      sum *= e;
+#pragma unroll
+      for (int d = 0; d < kV; ++d) acc[d] *= e;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = ex2(mq[k] - base);
+        sum = fmaf(lq[k], f, sum);
+#pragma unroll
+        for (int d = 0; d < kV; ++d) acc[d] = fmaf(v[k][d], f, acc[d]);
+      }
     }
-    float Mn = M;
+    if (W > 1) {
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, mq[k]);
-    const float base = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - base);
-    M = Mn;
-    sum *= e;
+      for (int d = 0; d < kV; ++d) sm_o[warp][lane * kV + d] = acc[d];
+      if (lane == 0) {
+        sm_m[warp] = M;
+        sm_l[warp] = sum;
+      }
+      __syncthreads();
+      if (sub == 0) {
 #pragma unroll
-    for (int d = 0; d < kV; ++d) acc[d] *= e;
+        for (int w = 1; w < 4; ++w) M = fmaxf(M, sm_m[warp + w]);
+        const float base = M == -INFINITY ? 0.f : M;
+        sum = 0.f;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const float f = ex2(mq[k] - base);
-      sum = fmaf(lq[k], f, sum);
+        for (int d = 0; d < kV; ++d) acc[d] = 0.f;
 #pragma unroll
-      for (int d = 0; d < kV; ++d) acc[d] = fmaf(v[k][d], f, acc[d]);
+        for (int w = 0; w < 4; ++w) {
+          const float f = ex2(sm_m[warp + w] - base);
+          sum = fmaf(sm_l[warp + w], f, sum);
+#pragma unroll
+          for (int d = 0; d < kV; ++d) acc[d] = fmaf(sm_o[warp + w][lane * kV + d], f, acc[d]);
+        }
+      }
+      __syncthreads();
     }
+    if (sub != 0 || r >= live) continue;
+    const int row = row0 + r, i = row / g.G, head = rec.y * g.G + (row - i * g.G);
+    const bool none = sum == 0.f;
+    const float inv = none ? 0.f : 1.f / sum;
+    uint16_t* const dst = a.o + b * a.so.b + head * a.so.h + i * a.so.n + lane * kV;
+    uint32_t w[kV / 2];
+#pragma unroll
+    for (int d = 0; d < kV / 2; ++d) w[d] = none ? 0u : pack16(acc[2 * d] * inv, acc[2 * d + 1] * inv, a.fp16);
+    if constexpr (kV == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+    else
+      *reinterpret_cast<uint32_t*>(dst) = w[0];
+    if (lane == 0)
+      a.lse[(static_cast<long long>(b) * a.Hq + head) * g.N + i] = none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
   }
-#pragma unroll
-  for (int d = 0; d < kV; ++d) sm_o[warp][lane * kV + d] = acc[d];
-  if (lane == 0) {
-    sm_m[warp] = M;
-    sm_l[warp] = sum;
-  }
-  __syncthreads();
-  if ((warp & 3) != 0 || i >= g.N) return;
-  float all = M;
-#pragma unroll
-  for (int w = 1; w < 4; ++w) all = fmaxf(all, sm_m[warp + w]);
-  const float base = all == -INFINITY ? 0.f : all;
-  sum = 0.f;
-#pragma unroll
-  for (int d = 0; d < kV; ++d) acc[d] = 0.f;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    const float f = ex2(sm_m[warp + w] - base);
-    sum = fmaf(sm_l[warp + w], f, sum);
-#pragma unroll
-    for (int d = 0; d < kV; ++d) acc[d] = fmaf(sm_o[warp + w][lane * kV + d], f, acc[d]);
-  }
-  const bool none = sum == 0.f;
-  const float inv = none ? 0.f : 1.f / sum;
-  const int head = rec.y * g.G + (row - i * g.G);
-  uint16_t* const dst = a.o + b * a.so.b + head * a.so.h + i * a.so.n + lane * kV;
-  uint32_t w[kV / 2];
-#pragma unroll
-  for (int d = 0; d < kV / 2; ++d) w[d] = none ? 0u : pack16(acc[2 * d] * inv, acc[2 * d + 1] * inv, a.fp16);
-  if constexpr (kV == 4)
-    *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-  else
-    *reinterpret_cast<uint32_t*>(dst) = w[0];
-  if (lane == 0)
-    a.lse[(static_cast<long long>(b) * a.Hq + head) * g.N + i] = none ? -INFINITY : (all - kBias + log2f(sum)) * kLn2Cache;
 }
 
 template <int D, int NT, bool INT8>
@@ -644,12 +660,15 @@ cudaError_t launch_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, c
 
 template <int D, bool INT8>
 cudaError_t launch_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  cudaError_t e = g.rows > 16  ? launch_cache_attention_tiles(a, g, ctas, stream)
+  cudaError_t e = g.rows > 16  ? (INT8 ? launch_cache_attention_tiles_int8(a, g, ctas, stream)
+                                       : launch_cache_attention_tiles_e4m3(a, g, ctas, stream))
                   : g.rows > 8 ? launch_rows<D, 2, INT8>(a, g, ctas, stream)
                                : launch_rows<D, 1, INT8>(a, g, ctas, stream);
   if (e != cudaSuccess || !g.split) return e;
   const long long live = min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G);
-  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, static_cast<unsigned>((live + 1) / 2)), dim3(256), 0, stream, a, g);
+  // blocks of a unit: two rows each, and no more than 16 (most CTAs have no record)
+  const unsigned y = static_cast<unsigned>(live < 32 ? (live + 1) / 2 : 16);
+  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, y), dim3(256), 0, stream, a, g);
 }
 
 struct AttnWorkspace {

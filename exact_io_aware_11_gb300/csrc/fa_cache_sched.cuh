@@ -179,7 +179,11 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap);
 
-// Tiles of 128 (g.rows) or 2 x 128 query rows on tcgen05 (fa_cache_tile.cu).
-cudaError_t launch_cache_attention_tiles(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream);
+// Tiles of 128 (g.rows) or 2 x 128 query rows on tcgen05 (fa_cache_tile.cuh), one
+// translation unit for each format.
+cudaError_t launch_cache_attention_tiles_e4m3(const CacheAttnLaunch& a, const AttnGrid& g, int ctas,
+                                              cudaStream_t stream);
+cudaError_t launch_cache_attention_tiles_int8(const CacheAttnLaunch& a, const AttnGrid& g, int ctas,
+                                              cudaStream_t stream);
 
 }  // namespace fa

@@ -1,0 +1,726 @@
+// Attention over the paged 8-bit cache, many query rows per cache head (drafted
+// tokens of large groups, chunks of a prompt): tiles of 128 query rows on
+// tcgen05.
+//
+// Mathematics, units, shares and parts: as in fa_cache_attn.cu. A unit has NQ tiles of
+// 128 query rows (NQ = 2 above 128 rows), whose S = Q K^T and O += P V run as 128 x
+// 128 x d products with fp16 operands and fp32 accumulators in TMEM. A task is one
+// tile's step; task k uses S buffer k mod 2, and the issue order
+//   S(0) S(1) | PV(0) S(2) PV(1) S(3) ...
+// lets one task's softmax run under the other's products: the two tiles of a
+// unit at NQ = 2, a tile's consecutive steps at NQ = 1.
+//
+// Warps: 4 NQ softmax warps (a thread owns a query row, the TMEM lane of its
+// warp's quarter), 4 / NQ converter warps (codes to fp16 tiles in the swizzled form
+// the products read), the MMA issuer, the TMA producer. The codes are converted
+// unscaled: K's scale multiplies the scores and V's joins the exponent, both
+// constant over 16 columns, so that the converters do nothing but convert.
+//
+// What bounds it: with 256 rows a step is 2048 cycles of products and as many of
+// exponentials, with 96 KB of shared-memory traffic for the conversion beside the 192 KB
+// that the products read; with few rows, the conversion and the cache itself.
+#pragma once
+
+#include "fa_cache_internal.h"
+#include "fa_cache_math.cuh"
+#include "fa_cache_sched.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kKeys = 128;
+constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 fp16 columns, 128-byte swizzle
+constexpr int kScaleSlots = 8;          // steps whose scales are kept
+
+template <int D, int NQ>
+struct TileLayout {
+  // NQ = 2: 12 warps, so that a softmax thread can hold a step's 128 scores (168 registers)
+  static constexpr int kConvWarps = NQ == 2 ? 2 : 4;
+  static constexpr int kConv = 4 * NQ, kMma = kConv + kConvWarps, kLoad = kMma + 1;  // warps
+  static constexpr int kThreads = (kLoad + 1) * 32;
+  static constexpr int kTile = (D / 64) * kChunkBytes;  // one fp16 tile
+  static constexpr int kRaw = kKeys * D;                // K or V codes of a step
+  static constexpr int kStg = D == 128 ? (NQ == 2 ? 2 : 4) : 8;  // raw tiles in flight
+  static constexpr int oQ = 0, oK = NQ * kTile, oV = oK + 2 * kTile, oRaw = oV + 2 * kTile;
+  static constexpr int oScales = oRaw + kStg * kRaw;    // [slots][8 groups] ks, log2 vs, 1 / vs, vs counts
+  static constexpr int oNan = oScales + kScaleSlots * 128;  // [8] first NaN key of V per unit
+  static constexpr int oBars = oNan + 32;
+  static constexpr int kBars = 2 * kStg + 17;
+  static constexpr int kSmem = oBars + kBars * 8 + 16 + 1024;
+  static_assert(kSmem + 512 <= 227 * 1024, "shared memory of one CTA");
+  static constexpr uint32_t cO = 256;                   // TMEM column of O
+};
+
+// f32 += f16 x f16
+constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
+  return idesc_bf16(M, N, false, b_mn_major) & ~((1u << 7) | (1u << 10));
+}
+
+struct TileBars {
+  uint64_t *raw_full, *raw_empty, *kfull, *kempty, *vfull, *vempty, *qfull, *sfull, *pfull, *odone, *fin;
+};
+
+// Producer: the raw tiles K(n), V(n) of every step, as pages. Lane i < 8 looks
+// after the step's i-th group of 16 keys (page id two steps ahead, scales one).
+// It also writes the record of a cut unit that the CTA ends, well before that end.
+template <int D, int NQ>
+__device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor ld,
+                                             const AttnShare& share, uint8_t* smem, const TileBars& b,
+                                             const Watchdog& wd, int lane) {
+  using L = TileLayout<D, NQ>;
+  const CacheView& c = a.c;
+  const int rows = min(c.page, kKeys), per_page = rows >> 4;
+  const bool group = lane < kKeys / 16, leader = group && lane % per_page == 0;
+  struct Step {
+    bool live, want;
+    int pid, h, row;
+  };
+  bool first = true;
+  auto look = [&]() {
+    Step s{!ld.done(g), false, -1, 0, 0};
+    if (s.live) {
+      if (first && ld.step > 0 && g.split && ld.run(g) == ld.x.steps - ld.step && lane == 0)
+        g.record[blockIdx.x] = make_int4(ld.e, ld.h, attn_cta_of(ld.pos - ld.step, share.total, share.ctas), 0);
+      first = false;
+      const int key = (ld.step << g.log2_keys) + lane * 16;
+      s.want = group && key < ld.x.seen;
+      s.h = ld.h;
+      s.row = key & (c.page - 1);
+      if (s.want) s.pid = __ldg(c.table + ld.x.b * c.table_stride + (key >> c.log2_page));
+      ld.next(g);
+    }
+    return s;
+  };
+  auto scales = [&](Step& s, float& ks, float& vs) {
+    const bool good = s.want && s.pid >= 0 && s.pid < c.num_pages;
+    if (s.want && !good) report_bad_page(a.status);
+    s.want = good;
+    ks = -1.f;
+    vs = 1.f;
+    if (good) {
+      const int ph = s.pid * c.H + s.h;
+      s.row += ph << c.log2_page;
+      ks = __ldg(c.scale[0] + ph);
+      vs = __ldg(c.scale[1] + ph);
+    }
+  };
+  float ks, vs;
+  Step now = look();
+  scales(now, ks, vs);
+  Step next = look();
+  int tile = 0;  // raw tiles issued
+  bool ok = true;
+  for (int n = 0; now.live && ok; ++n) {
+    const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, leader && now.want)) * rows * D;
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const int st = tile % L::kStg;
+      if (tile >= L::kStg && !mbar_wait_warp(b.raw_empty + st, ((tile / L::kStg) - 1) & 1, wd)) {
+        ok = false;
+        break;
+      }
+      if (leader && now.want)
+        tma_load_2d(smem + L::oRaw + st * L::kRaw + lane * 16 * D, &a.tm[kv], b.raw_full + st, now.row);
+      if (kv == 0 && group) {
+        const float v = fmaxf(vs, kMinScale);
+        *reinterpret_cast<float4*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16) =
+            make_float4(ks, __log2f(v), 1.f / v, vs > kMinScale ? 1.f : 0.f);
+      }
+      __syncwarp();
+      if (lane == 0) {
+        if (bytes > 0)
+          mbar_expect_tx(b.raw_full + st, bytes);
+        else
+          mbar_arrive(b.raw_full + st);
+      }
+      ++tile;
+    }
+    now = next;
+    scales(now, ks, vs);
+    next = look();
+  }
+  for (int i = max(0, tile - L::kStg); i < tile; ++i)  // copies in flight land before the CTA exits
+    mbar_wait_drain(b.raw_full + i % L::kStg, (i / L::kStg) & 1, a.wait_limit);
+}
+
+// Converters: each warp takes its 32 (64) rows of every raw tile, 16 codes a lane at a
+// time. At d = 128 the 8 lanes of a shared-memory phase take four chunks of rows r
+// and r ^ 5: the rows differ in bit 2 (so their raw chunks, at c ^ (r & 7), fall
+// apart) and in bit 0 (so do the results, at 2 c ^ (r & 7)), and every bank is met
+// once in both directions.
+// Where a row of queries may not see a key of V (x.seen and the first row's limit
+// bound those keys), its NaN codes are taken out, and the first such key is kept
+// for the unit: the rows that see it become NaN.
+template <int D, int NQ, bool INT8>
+__device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor cv, uint8_t* smem,
+                                             const TileBars& b, const Watchdog& wd, int cw, int lane) {
+  using L = TileLayout<D, NQ>;
+  // the row of the lane's i-th piece, and its chunk
+  constexpr int kRows = kKeys / L::kConvWarps, kPieces = kRows * D / 512;
+  const int ch = D == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
+  auto row_of = [&](int i) {
+    if constexpr (D == 128) {
+      const int p = (lane >> 4) + 2 * (i & 1);
+      return cw * kRows + (i >> 1) * 8 + ((lane & 4) ? p ^ 5 : p);
+    }
+    return cw * kRows + i * 8 + (lane >> 2);
+  };
+  int* const nan_key = reinterpret_cast<int*>(smem + L::oNan);
+  int n = 0;  // steps converted
+  for (int unit = 0; !cv.done(g); ++unit) {
+  // slot of the unit three on; the one five back, which used it, has ended (a unit
+  // has a step at least, and K(n) waits for the scores of step n - 2)
+  if (cw == 0 && lane == 0) nan_key[(unit + 3) & 7] = 0x7fffffff;
+  const int seen = cv.x.seen, low = attn_limit(g, cv.x, 0), steps = cv.run(g);
+  int key0 = cv.step << g.log2_keys;
+  for (const int end = n + steps; n < end; ++n, key0 += kKeys) {
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+      const int tile = 2 * n + kv, st = tile % L::kStg, slot = n & 1;
+      if (!mbar_wait_warp(b.raw_full + st, (tile / L::kStg) & 1, wd)) return;
+      if (n >= 2 && !mbar_wait_warp((kv ? b.vempty : b.kempty) + slot, ((n >> 1) - 1) & 1, wd)) return;
+      const uint32_t src = smem_u32(smem) + L::oRaw + st * L::kRaw;
+      const uint32_t dst = smem_u32(smem) + (kv ? L::oV : L::oK) + slot * L::kTile;
+      bool check = false;
+      if (!INT8 && kv == 1) {
+        const float ks = lane < 8 ? *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16) : 0.f;
+        check = key0 + kKeys > low || __any_sync(0xffffffffu, ks < 0.f);
+      }
+      auto from = [&](int r) {
+        return lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
+      };
+      auto put = [&](const uint4& v, int r) {
+        uint32_t w[8];
+        decode4<INT8>(v.x, w[0], w[1]);
+        decode4<INT8>(v.y, w[2], w[3]);
+        decode4<INT8>(v.z, w[4], w[5]);
+        decode4<INT8>(v.w, w[6], w[7]);
+        const uint32_t row = dst + (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128;
+        const int unit16 = (ch & 3) * 2 ^ (r & 7);
+        st_shared_v4(row + (unit16 << 4), w[0], w[1], w[2], w[3]);
+        st_shared_v4(row + ((unit16 ^ 1) << 4), w[4], w[5], w[6], w[7]);
+      };
+      if (!check) {
+#pragma unroll 1
+        for (int i0 = 0; i0 < kPieces; i0 += D / 16) {
+          uint4 v[D / 16];
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) v[i] = from(row_of(i0 + i));
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) put(v[i], row_of(i0 + i));
+        }
+      } else {
+#pragma unroll 1
+        for (int i = 0; i < kPieces; ++i) {
+          const int r = row_of(i), key = key0 + r;
+          const uint4 v = from(r);
+          const float ks = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16);
+          uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
+          if (key >= low || ks < 0.f) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+              w[k] &= ~nan;
+              any |= nan;
+            }
+            if (any != 0u && key < seen && !(ks < 0.f)) atomicMin(nan_key + (unit & 7), key);
+          }
+          put(make_uint4(w[0], w[1], w[2], w[3]), r);
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive((kv ? b.vfull : b.kfull) + slot);
+        mbar_arrive(b.raw_empty + st);
+      }
+    }
+  }
+  cv.skip(g, steps);
+  }
+}
+
+// Loads a warp's 32 rows of queries (lane r knows row r's offset, -1: zeros) as whole
+// rows, D / 8 lanes to a row, and writes them as fp16 into the swizzled tile at `dst`.
+// bf16 rows are scaled by a power of two that puts their largest value into [2^14, 2^15)
+// (fp16 rows already are what the products take); row `lane`'s inverse factor comes back.
+template <int D, bool FP16>
+__device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at, uint32_t dst, int lane) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;  // lanes of a row, rows at once, loads in flight
+  const int c = lane % kLanes, sub = lane / kLanes;
+  float inv = 1.f;
+#pragma unroll 1
+  for (int r0 = 0; r0 < 32; r0 += kAtOnce * kBatch) {
+    uint4 w[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const long long at = __shfl_sync(0xffffffffu, q_at, r0 + i * kAtOnce + sub);
+      w[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(q + at) + c) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int r = r0 + i * kAtOnce + sub;
+      uint32_t h[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      if constexpr (!FP16) {
+        // the largest magnitude as an integer: bf16 patterns order like their values
+        uint32_t mx = __vmaxu2(__vmaxu2(h[0] & 0x7fff7fffu, h[1] & 0x7fff7fffu), __vmaxu2(h[2] & 0x7fff7fffu, h[3] & 0x7fff7fffu));
+        mx = max(mx & 0xffffu, mx >> 16);
+#pragma unroll
+        for (int o = 1; o < kLanes; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+        const int e = max(15, static_cast<int>(mx >> 7));
+        const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          h[k] = pack_half(__uint_as_float(h[k] << 16) * f, __uint_as_float(h[k] & 0xffff0000u) * f);
+        // row r's factor to lane r: it lies with the lanes of one sub of one i
+        const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) {
+          const float v = __shfl_sync(0xffffffffu, back, k * kLanes);
+          if (lane == r0 + i * kAtOnce + k) inv = v;
+        }
+      }
+      st_shared_v4(dst + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
+    }
+  }
+  return inv;
+}
+
+// Writes 32 rows x 128 bytes, a lane's row as 8 pieces of 16 bytes, to the rows' own
+// places: through `box` (4 KB of shared memory, pieces permuted within a row), so that
+// 8 lanes write a row's 128 bytes together. at: of row `lane`, nullptr: not written.
+__device__ __forceinline__ void store_rows(uint32_t box, const uint4 (&w)[8], uint8_t* at, int lane) {
+  __syncwarp();  // the box's last pieces have been read
+#pragma unroll
+  for (int i = 0; i < 8; ++i) st_shared_v4(box + lane * 128 + ((i ^ (lane & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+  __syncwarp();
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const int r = k * 4 + (lane >> 3);
+    const uint4 v = lds128(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+    uint8_t* const p = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), r));
+    if (p != nullptr) *reinterpret_cast<uint4*>(p + (lane & 7) * 16) = v;
+  }
+}
+
+// The largest of N scores from column c0 of a chunk.
+template <int N>
+__device__ __forceinline__ float largest_of(const uint32_t (&v)[32], int c0) {
+  float m[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = __uint_as_float(v[c0 + i]);
+#pragma unroll
+  for (int q = 4; q + 8 <= N; q += 8)
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      m[i] = max3(m[i], __uint_as_float(v[c0 + q + i]), __uint_as_float(v[c0 + q + 4 + i]));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) m[i] = fmaxf(m[i], __uint_as_float(v[c0 + N - 4 + i]));
+  return max3(max3(m[0], m[1], m[2]), m[3], m[3]);
+}
+
+// Weights 2^(v mul + add) of N scores, packed to fp16 pairs from p[p0]; their sum
+// comes back, unrounded. Pairs of columns share the packed fp32 instructions.
+template <int N>
+__device__ __forceinline__ float weigh(const uint32_t (&v)[32], int c0, float mul, float add, uint32_t (&p)[16], int p0) {
+  const uint64_t mul2 = f2_pack(mul, mul), add2 = f2_pack(add, add);
+  uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+  for (int q = 0; q < N / 2; ++q) {
+    float x0, x1;
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c0 + 2 * q]), __uint_as_float(v[c0 + 2 * q + 1])), mul2, add2), x0, x1);
+    const float w0 = ex2(x0), w1 = ex2(x1);
+    p[p0 + q] = pack_half(w0, w1);
+    sum[q & 1] = f2_add(sum[q & 1], f2_pack(w0, w1));
+  }
+  float s0, s1;
+  f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+  return s0 + s1;
+}
+
+// P16: pages of 16 tokens, whose scales change every 16 columns (32 and more
+// otherwise).
+template <int D, int NQ, bool INT8, bool P16>
+__global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
+    cache_attn_tile_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
+  using L = TileLayout<D, NQ>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ AttnShare share;
+  __shared__ long long part[L::kThreads / 32];
+  uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  TileBars b;
+  {
+    uint64_t* p = reinterpret_cast<uint64_t*>(smem + L::oBars);
+    b.raw_full = p;
+    b.raw_empty = p + L::kStg;
+    p += 2 * L::kStg;
+    b.kfull = p;
+    b.kempty = p + 2;
+    b.vfull = p + 4;
+    b.vempty = p + 6;
+    b.qfull = p + 8;
+    b.sfull = p + 10;
+    b.pfull = p + 12;
+    b.odone = p + 14;
+    b.fin = p + 16;
+  }
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::oBars + L::kBars * 8);
+  int* const abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
+  check_init(a.status);
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < L::kStg; ++i) {
+      mbar_init(b.raw_full + i, 1);
+      mbar_init(b.raw_empty + i, L::kConvWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b.kfull + i, L::kConvWarps);
+      mbar_init(b.kempty + i, 1);
+      mbar_init(b.vfull + i, L::kConvWarps);
+      mbar_init(b.vempty + i, 1);
+      mbar_init(b.qfull + i, 4);
+      mbar_init(b.sfull + i, 1);
+      mbar_init(b.pfull + i, 4);
+      mbar_init(b.odone + i, 1);
+    }
+    mbar_init(b.fin, 1);
+    *abort_flag = 0;
+    for (int i = 0; i < 8; ++i) reinterpret_cast<int*>(smem + L::oNan)[i] = 0x7fffffff;
+    fence_mbar_init();
+    tma_prefetch_desc(&a.tm[0]);
+    tma_prefetch_desc(&a.tm[1]);
+  }
+  if (warp == L::kMma) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  grid_dep_wait();
+  grid_dep_launch();
+  AttnCursor cur = attn_share<L::kThreads>(g, &share, part);  // its barriers publish the above
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const Watchdog wd{a.wait_limit, a.status, abort_flag};
+  if (warp == L::kLoad) {
+    if (g.split && lane == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    tile_produce<D, NQ>(a, g, cur, share, smem, b, wd, lane);
+  } else if (warp == L::kMma) {
+    // ------------------------------------------------------------ MMA issuer (whole warp)
+    constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
+    const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::oQ), 16, 1024);
+    const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::oK), 16, 1024);
+    const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::oV), kChunkBytes, 1024);  // MN-major
+    int task0 = 0, step0 = 0;  // of the unit, over the CTA's run
+    bool ok = true;
+    for (int unit = 0; ok && !cur.done(g); ++unit) {
+      const int steps = cur.run(g), tasks = steps * NQ;
+      for (int t = 0; ok && t < NQ; ++t) ok = mbar_wait_spin_w(b.qfull + t, unit & 1, wd);
+      if (!ok) break;
+      auto issue_s = [&](int i) -> bool {
+        const int t = NQ == 2 ? i & 1 : 0, n = step0 + (NQ == 2 ? i >> 1 : i), buf = (task0 + i) & 1;
+        if (!mbar_wait_spin_w(b.kfull + (n & 1), (n >> 1) & 1, wd)) return false;
+        tc_fence_after();  // the softmax has read the buffer's last scores (pfull was awaited)
+        const uint64_t qd = desc_adv(q_desc, t * L::kTile), kd = desc_adv(k_desc, (n & 1) * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t off = (kk >> 2) * kChunkBytes + (kk & 3) * 32;
+          mma_ss_w(tmem + buf * 128, desc_adv(qd, off), desc_adv(kd, off), kIdS, kk > 0 ? 1u : 0u);
+        }
+        mma_commit_w(b.sfull + buf);
+        if (t == NQ - 1) mma_commit_w(b.kempty + (n & 1));
+        return true;
+      };
+      auto issue_pv = [&](int i) -> bool {
+        const int t = NQ == 2 ? i & 1 : 0, n = step0 + (NQ == 2 ? i >> 1 : i), buf = (task0 + i) & 1;
+        if (!mbar_wait_spin_w(b.pfull + buf, ((task0 + i) >> 1) & 1, wd)) return false;
+        if (!mbar_wait_spin_w(b.vfull + (n & 1), (n >> 1) & 1, wd)) return false;
+        tc_fence_after();
+        const uint64_t vd = desc_adv(v_desc, (n & 1) * L::kTile);
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          mma_ts_w(tmem + L::cO + t * D, tmem + buf * 128 + kk * 8, desc_adv(vd, kk * 2048), kIdO,
+                   (kk > 0 || i >= NQ) ? 1u : 0u);
+        mma_commit_w(b.odone + buf);
+        if (t == NQ - 1) mma_commit_w(b.vempty + (n & 1));
+        return true;
+      };
+      ok = issue_s(0);
+      if (ok && tasks > 1) ok = issue_s(1);
+      for (int i = 0; ok && i < tasks; ++i) {
+        ok = issue_pv(i);
+        if (ok && i + 2 < tasks) ok = issue_s(i + 2);
+      }
+      task0 += tasks;
+      step0 += steps;
+      cur.skip(g, steps);
+    }
+    mma_commit_w(b.fin);
+    mbar_wait_drain(b.fin, 0, a.wait_limit);
+    __syncwarp();
+  } else if (warp >= L::kConv && warp < L::kMma) {
+    tile_convert<D, NQ, INT8>(a, g, cur, smem, b, wd, warp - L::kConv, lane);
+  } else if (warp < L::kConv) {
+    // ------------------------------------------------------------ softmax
+    const int t = NQ == 2 ? warp >> 2 : 0;
+    const int rl = (warp & 3) * 32 + lane;  // row of the tile, TMEM lane
+    const int r = t * 128 + rl;
+    const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+    int task0 = 0, step0 = 0;
+    bool ok = true;
+    for (int unit = 0; ok && !cur.done(g); ++unit) {
+      const AttnEntry x = cur.x;
+      const int h = cur.h, first = cur.step, steps = cur.run(g);
+      const int row = x.row0 + r, qi = row / g.G, lim = attn_limit(g, x, r);
+      const int head = h * g.G + (row - qi * g.G);
+      // The warp's 32 rows of queries to fp16, scaled by a power of two each, into the swizzled
+      // tile (the last unit's scores are done: its last P V was awaited).
+      const long long q_at = qi < x.ql ? x.b * a.sq.b + static_cast<long long>(head) * a.sq.h + qi * a.sq.n : -1;
+      const uint32_t q_dst = smem_u32(smem) + L::oQ + t * L::kTile + (warp & 3) * 32 * 128;
+      const float rf = a.scale_log2 * (a.fp16 ? tile_queries<D, true>(a.q, q_at, q_dst, lane) : tile_queries<D, false>(a.q, q_at, q_dst, lane));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(b.qfull + t);
+      const bool live = __any_sync(0xffffffffu, lim > 0);  // rows of this warp see keys
+      // rows that stand for no query (their q is zero) do not make a step an edge
+      const int low = __reduce_min_sync(0xffffffffu, qi < x.ql ? lim : 0x7fffffff);
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < steps; ++j) {
+        const int i = j * NQ + t, k = task0 + i, buf = k & 1;
+        if (!mbar_wait_warp<true>(b.sfull + buf, (k >> 1) & 1, wd)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (live) {
+          const int key0 = (first + j) << g.log2_keys;
+          const uint32_t s_tm = lane_base + buf * 128;
+          // constants of the step's groups of 16 columns, read where they are used
+          const uint32_t sc_at = smem_u32(smem) + L::oScales + ((step0 + j) % kScaleSlots) * 128;
+          auto sc = [&](int i) {
+            const uint4 w = lds128(sc_at + i * 16);
+            return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
+          };
+          const float4 mine = sc(lane & 7);
+          // every row sees every key, and every page was read and counts
+          const bool plain = key0 + kKeys <= low && !__any_sync(0xffffffffu, mine.x < 0.f || mine.w == 0.f);
+          const int room = lim - key0;  // columns below it are seen
+          constexpr int kG = P16 ? 16 : 32;  // columns that share their scales
+          float tmax = -INFINITY;            // the largest y of the row
+          // One round trip to TMEM takes about 300 cycles while products run, whatever it
+          // brings, so a plain step's scores are read kHold chunks of 32 columns at a time: all
+          // at once, and held, where registers allow it, else the second half, the first (whose
+          // weights are formed next, and go over its columns) and the second again.
+          constexpr int kHold = NQ == 2 ? 4 : 2;
+          uint32_t v[kHold][32];
+          auto read = [&](int c0) {
+#pragma unroll
+            for (int c = 0; c < kHold; ++c) tmem_ld32(s_tm + (c0 + c) * 32, v[c]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < kHold; ++c) reg_fence(v[c]);
+          };
+          if (plain) {
+#pragma unroll
+            for (int c0 = 4 - kHold; c0 >= 0; c0 -= kHold) {
+              read(c0);
+#pragma unroll
+              for (int c = 0; c < kHold; ++c)
+#pragma unroll
+                for (int u = 0; u < 32 / kG; ++u) {
+                  const float4 f = sc((c0 + c) * 2 + u);
+                  tmax = fmaxf(tmax, fmaf(largest_of<kG>(v[c], u * kG), rf * f.x, f.y));
+                }
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32];
+              tmem_ld32(s_tm + c * 32, v);
+              tmem_wait_ld();
+              reg_fence(v);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float4 f = sc(c * 2 + u);
+                const int lim16 = f.x < 0.f ? 0 : room - (c * 32 + u * 16);
+#pragma unroll
+                for (int q = 0; q < 16; ++q) v[u * 16 + q] = q < lim16 ? v[u * 16 + q] : 0xff800000u;
+                const float y = fmaf(largest_of<16>(v, u * 16), rf * f.x, f.y);
+                tmax = fmaxf(tmax, lim16 > 0 ? y : -INFINITY);
+              }
+            }
+          }
+          const bool grow = tmax > m + kSlack;
+          const float m_new = grow ? tmax : m;
+          const float base = (m_new == -INFINITY ? 0.f : m_new) - kBias;
+          const bool moved = __any_sync(0xffffffffu, grow);
+          const float alpha = grow ? ex2(m - (m_new == -INFINITY ? 0.f : m_new)) : 1.f;
+          m = m_new;
+          l *= alpha;
+          // the weights, over the first half of the scores' columns as those are read
+          if (plain) {
+#pragma unroll
+            for (int c0 = 0; c0 < 4; c0 += kHold) {
+              if (c0 > 0) read(c0);
+#pragma unroll
+              for (int c = 0; c < kHold; ++c) {
+                uint32_t p[16];
+#pragma unroll
+                for (int u = 0; u < 32 / kG; ++u) {
+                  const float4 f = sc((c0 + c) * 2 + u);
+                  l = fmaf(weigh<kG>(v[c], u * kG, rf * f.x, f.y - base, p, u * kG / 2), f.z, l);
+                }
+                tmem_st16(s_tm + (c0 + c) * 16, p);
+              }
+            }
+          } else {
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              uint32_t v[32], p[16];
+              tmem_ld32(s_tm + c * 32, v);
+              tmem_wait_ld();
+              reg_fence(v);
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const float4 f = sc(c * 2 + u);
+                const int lim16 = f.x < 0.f ? 0 : room - (c * 32 + u * 16);
+                const float mul16 = rf * f.x, add = f.y - base;
+                float s = 0.f;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                  float x0 = fmaf(__uint_as_float(v[u * 16 + 2 * q]), mul16, add);
+                  float x1 = fmaf(__uint_as_float(v[u * 16 + 2 * q + 1]), mul16, add);
+                  x0 = 2 * q < lim16 ? x0 : -INFINITY;
+                  x1 = 2 * q + 1 < lim16 ? x1 : -INFINITY;
+                  const float p0 = ex2(x0), p1 = ex2(x1);
+                  s += p0 + p1;
+                  p[u * 8 + q] = f.w == 0.f ? 0u : pack_half(p0, p1);  // a page of zeros
+                }
+                l = fmaf(s, f.z, l);
+              }
+              tmem_st16(s_tm + c * 16, p);
+            }
+          }
+          if (moved && j > 0) {  // the tile's last P V is done before O is rescaled
+            const int kp = k - NQ;
+            if (!mbar_wait_warp<true>(b.odone + (kp & 1), (kp >> 1) & 1, wd)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t o[32];
+              tmem_ld32(lane_base + L::cO + t * D + c * 32, o);
+              tmem_wait_ld();
+              reg_fence(o);
+#pragma unroll
+              for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
+              tmem_st32(lane_base + L::cO + t * D + c * 32, o);
+            }
+          }
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.pfull + buf);
+      }
+      if (!ok) break;
+      // ---------------------------------------------------------- epilogue
+      {
+        const int k = task0 + (steps - 1) * NQ + t;
+        if (!mbar_wait_warp<true>(b.odone + (k & 1), (k >> 1) & 1, wd)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+      }
+      if (!INT8 && *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4) < lim) l = __int_as_float(0x7fffffff);
+      if (qi >= x.ql) {
+        l = 0.f;
+        m = -INFINITY;
+      }
+      const bool last = first + steps == x.steps, whole = first == 0 && last;
+      // rows leave through this warp's part of the tile of queries, which is done with
+      const uint32_t box = smem_u32(smem) + L::oQ + t * L::kTile + (warp & 3) * 4096;
+      const bool none = l == 0.f, row_ok = qi < g.N;
+      if (whole) {
+        const float inv = none ? 0.f : 1.f / l;
+        uint16_t* const dst = a.o + x.b * a.so.b + static_cast<long long>(head) * a.so.h + qi * a.so.n;
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint4 w[8];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            uint32_t o[32];
+            tmem_ld32(lane_base + L::cO + t * D + c * 64 + e * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              uint32_t h[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                h[q] = none ? 0u : pack16(__uint_as_float(o[8 * v + 2 * q]) * inv, __uint_as_float(o[8 * v + 2 * q + 1]) * inv, a.fp16);
+              w[e * 4 + v] = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+          }
+          store_rows(box, w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
+        }
+        if (row_ok)
+          a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
+      } else {
+        const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+        const long long pr = static_cast<long long>(slot) * g.rows + r;
+        if (row_ok) {
+          g.m_part[pr] = m;
+          g.l_part[pr] = l;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tmem_ld32(lane_base + L::cO + t * D + c * 32, o);
+          tmem_wait_ld();
+          reg_fence(o);
+          uint4 w[8];  // rows that see nothing leave zeros: their accumulators hold whatever P was
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            w[v] = none ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          store_rows(box, w, row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 32) : nullptr, lane);
+        }
+      }
+      tc_fence_before();  // O is read before the next unit's P V
+      task0 += steps * NQ;
+      step0 += steps;
+      cur.skip(g, steps);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == L::kMma) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int D, int NQ, bool INT8, bool P16>
+cudaError_t launch_tile_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+  using L = TileLayout<D, NQ>;
+  auto kern = cache_attn_tile_kernel<D, NQ, INT8, P16>;
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(kern), L::kSmem);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(kern, dim3(ctas), dim3(L::kThreads), L::kSmem, stream, a, g);
+}
+
+template <int D, bool INT8>
+cudaError_t launch_tile_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+  if (a.c.page == 16)
+    return g.rows == 256 ? launch_tile_variant<D, 2, INT8, true>(a, g, ctas, stream)
+                         : launch_tile_variant<D, 1, INT8, true>(a, g, ctas, stream);
+  return g.rows == 256 ? launch_tile_variant<D, 2, INT8, false>(a, g, ctas, stream)
+                       : launch_tile_variant<D, 1, INT8, false>(a, g, ctas, stream);
+}
+
+}  // namespace
+}  // namespace fa

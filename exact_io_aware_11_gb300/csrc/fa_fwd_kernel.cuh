@@ -115,13 +115,6 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
   return p + ((1024u - (a & 1023u)) & 1023u);
 }
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float m;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
-  return m;
-}
-
-
 // One work unit: Q tiles 2p and 2p+1 (qtB = -1 if absent) of one (batch,
 // head), restricted to the K/V steps [sb, se) of the unit. Without a block
 // mask or key padding, step j is K/V tile j, so a unit of a split item covers
