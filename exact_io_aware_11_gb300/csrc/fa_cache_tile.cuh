@@ -42,14 +42,33 @@ struct TileLayout {
   static constexpr int kRaw = kKeys * D;                // K or V codes of a step
   static constexpr int kStg = D == 128 ? (NQ == 2 ? 2 : 4) : 8;  // raw tiles in flight
   static constexpr int oQ = 0, oK = NQ * kTile, oV = oK + 2 * kTile, oRaw = oV + 2 * kTile;
-  static constexpr int oScales = oRaw + kStg * kRaw;    // [slots][8 groups] ks, log2 vs, 1 / vs, vs counts
+  static constexpr int oScales = oRaw + kStg * kRaw;    // [slots][8 groups] ks, log2 vs, 1 / vs, 1 (0: V of zeros, -1: not read)
   static constexpr int oNan = oScales + kScaleSlots * 128;  // [8] first NaN key of V per unit
-  static constexpr int oBars = oNan + 32;
-  static constexpr int kBars = 2 * kStg + 17;
+  // Slots for the descriptions of units (TileUnit). Units have a step at least. The producer
+  // describes a unit two steps before it issues K(n), for which K(n - kStg / 2) is
+  // converted, so the scores of the step two before that are formed, so the weights of
+  // the step NQ = 1: two, NQ = 2: one before that are done; that step's unit may still be read.
+  static constexpr int kUnits = kStg <= 2 ? 8 : 16;
+  static_assert(2 + kStg / 2 + 2 + (NQ == 1 ? 2 : 1) < kUnits, "a unit's description outlives its use");
+  static constexpr int oUnits = oNan + 32;
+  static constexpr int oBars = oUnits + kUnits * 32;
+  static constexpr int kBars = 2 * kStg + 17 + kUnits;
   static constexpr int kSmem = oBars + kBars * 8 + 16 + 1024;
-  static_assert(kSmem + 512 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(kSmem + 128 <= 227 * 1024, "shared memory of one CTA");
   static constexpr uint32_t cO = 256;                   // TMEM column of O
 };
+
+// A unit (or the CTA's part of one), as the producer writes it down for the other warps,
+// which then carry little more than counters through their loops. steps 0: no more.
+struct __align__(16) TileUnit {
+  int b, row0, h, first;  // sequence, first row, cache head, first step
+  int steps, kv, ql, seen_last;  // seen: tokens the last row sees; top bit: the unit ends here
+};
+__device__ __forceinline__ int unit_limit(const AttnGrid& g, const TileUnit& x, int r) {
+  const int i = (x.row0 + r) / g.G;
+  if (i >= x.ql) return 0;
+  return g.causal ? max(0, x.kv - x.ql + i + 1) : x.kv;
+}
 
 // f32 += f16 x f16
 constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
@@ -57,12 +76,13 @@ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
 }
 
 struct TileBars {
-  uint64_t *raw_full, *raw_empty, *kfull, *kempty, *vfull, *vempty, *qfull, *sfull, *pfull, *odone, *fin;
+  uint64_t *raw_full, *raw_empty, *kfull, *kempty, *vfull, *vempty, *qfull, *sfull, *pfull, *odone, *fin, *ufull;
 };
 
 // Producer: the raw tiles K(n), V(n) of every step, as pages. Lane i < 8 looks
 // after the step's i-th group of 16 keys (page id two steps ahead, scales one).
-// It also writes the record of a cut unit that the CTA ends, well before that end.
+// It also describes the units to the other warps (TileLayout::kUnits), and
+// writes the record of a cut unit that the CTA ends, well before that end.
 template <int D, int NQ>
 __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor ld,
                                              const AttnShare& share, uint8_t* smem, const TileBars& b,
@@ -75,13 +95,27 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     bool live, want;
     int pid, h, row;
   };
+  int units = 0;
   bool first = true;
+  auto describe = [&](const TileUnit& u) {
+    if (lane == 0) {
+      *reinterpret_cast<TileUnit*>(smem + L::oUnits + units % L::kUnits * 32) = u;
+      mbar_arrive(b.ufull + units % L::kUnits);
+    }
+    ++units;
+  };
   auto look = [&]() {
     Step s{!ld.done(g), false, -1, 0, 0};
     if (s.live) {
-      if (first && ld.step > 0 && g.split && ld.run(g) == ld.x.steps - ld.step && lane == 0)
-        g.record[blockIdx.x] = make_int4(ld.e, ld.h, attn_cta_of(ld.pos - ld.step, share.total, share.ctas), 0);
-      first = false;
+      if (first || ld.step == 0) {
+        const int steps = ld.run(g);
+        const bool ends = ld.step + steps == ld.x.steps;
+        describe(TileUnit{ld.x.b, ld.x.row0, ld.h, ld.step, steps, ld.x.kv, ld.x.ql,
+                          static_cast<int>(static_cast<unsigned>(ld.x.seen) | (ends ? 0x80000000u : 0u))});
+        if (ld.step > 0 && ends && g.split && lane == 0)
+          g.record[blockIdx.x] = make_int4(ld.e, ld.h, attn_cta_of(ld.pos - ld.step, share.total, share.ctas), 0);
+        first = false;
+      }
       const int key = (ld.step << g.log2_keys) + lane * 16;
       s.want = group && key < ld.x.seen;
       s.h = ld.h;
@@ -95,8 +129,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     const bool good = s.want && s.pid >= 0 && s.pid < c.num_pages;
     if (s.want && !good) report_bad_page(a.status);
     s.want = good;
-    ks = -1.f;
-    vs = 1.f;
+    ks = vs = 1.f;
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
@@ -124,7 +157,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       if (kv == 0 && group) {
         const float v = fmaxf(vs, kMinScale);
         *reinterpret_cast<float4*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16) =
-            make_float4(ks, __log2f(v), 1.f / v, vs > kMinScale ? 1.f : 0.f);
+            make_float4(ks, __log2f(v), 1.f / v, !now.want ? -1.f : vs > kMinScale ? 1.f : 0.f);
       }
       __syncwarp();
       if (lane == 0) {
@@ -139,6 +172,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     scales(now, ks, vs);
     next = look();
   }
+  describe(TileUnit{0, 0, 0, 0, 0, 0, 0, 0});
   for (int i = max(0, tile - L::kStg); i < tile; ++i)  // copies in flight land before the CTA exits
     mbar_wait_drain(b.raw_full + i % L::kStg, (i / L::kStg) & 1, a.wait_limit);
 }
@@ -152,7 +186,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
 // bound those keys), its NaN codes are taken out, and the first such key is kept
 // for the unit: the rows that see it become NaN.
 template <int D, int NQ, bool INT8>
-__device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor cv, uint8_t* smem,
+__device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, uint8_t* smem,
                                              const TileBars& b, const Watchdog& wd, int cw, int lane) {
   using L = TileLayout<D, NQ>;
   // the row of the lane's i-th piece, and its chunk
@@ -167,13 +201,16 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
   };
   int* const nan_key = reinterpret_cast<int*>(smem + L::oNan);
   int n = 0;  // steps converted
-  for (int unit = 0; !cv.done(g); ++unit) {
+  for (int unit = 0;; ++unit) {
+  if (!mbar_wait_warp(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) return;
+  const TileUnit x = *reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32);
+  if (x.steps == 0) return;
   // slot of the unit three on; the one five back, which used it, has ended (a unit
   // has a step at least, and K(n) waits for the scores of step n - 2)
   if (cw == 0 && lane == 0) nan_key[(unit + 3) & 7] = 0x7fffffff;
-  const int seen = cv.x.seen, low = attn_limit(g, cv.x, 0), steps = cv.run(g);
-  int key0 = cv.step << g.log2_keys;
-  for (const int end = n + steps; n < end; ++n, key0 += kKeys) {
+  const int seen = x.seen_last & 0x7fffffff, low = unit_limit(g, x, 0);
+  int key0 = x.first << g.log2_keys;
+  for (const int end = n + x.steps; n < end; ++n, key0 += kKeys) {
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
       const int tile = 2 * n + kv, st = tile % L::kStg, slot = n & 1;
@@ -183,8 +220,8 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
       const uint32_t dst = smem_u32(smem) + (kv ? L::oV : L::oK) + slot * L::kTile;
       bool check = false;
       if (!INT8 && kv == 1) {
-        const float ks = lane < 8 ? *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16) : 0.f;
-        check = key0 + kKeys > low || __any_sync(0xffffffffu, ks < 0.f);
+        const float read = lane < 8 ? *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16 + 12) : 0.f;
+        check = key0 + kKeys > low || __any_sync(0xffffffffu, read < 0.f);
       }
       auto from = [&](int r) {
         return lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
@@ -214,16 +251,16 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
         for (int i = 0; i < kPieces; ++i) {
           const int r = row_of(i), key = key0 + r;
           const uint4 v = from(r);
-          const float ks = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16);
+          const float read = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
           uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
-          if (key >= low || ks < 0.f) {
+          if (key >= low || read < 0.f) {
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
               w[k] &= ~nan;
               any |= nan;
             }
-            if (any != 0u && key < seen && !(ks < 0.f)) atomicMin(nan_key + (unit & 7), key);
+            if (any != 0u && key < seen && !(read < 0.f)) atomicMin(nan_key + (unit & 7), key);
           }
           put(make_uint4(w[0], w[1], w[2], w[3]), r);
         }
@@ -236,14 +273,13 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
       }
     }
   }
-  cv.skip(g, steps);
   }
 }
 
-// Loads a warp's 32 rows of queries (lane r knows row r's offset, -1: zeros) as whole
-// rows, D / 8 lanes to a row, and writes them as fp16 into the swizzled tile at `dst`.
-// bf16 rows are scaled by a power of two that puts their largest value into [2^14, 2^15)
-// (fp16 rows already are what the products take); row `lane`'s inverse factor comes back.
+// Loads a warp's 32 rows of queries (lane r knows row r's offset, -1: zeros) as whole rows,
+// D / 8 lanes to a row, and writes them as fp16 into the swizzled tile at `dst`. bf16 rows are
+// scaled by a power of two that puts their largest value into [2^14, 2^15) (fp16 rows already
+// are what the products take); row `lane`'s inverse factor comes back.
 template <int D, bool FP16>
 __device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at, uint32_t dst, int lane) {
   constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;  // lanes of a row, rows at once, loads in flight
@@ -257,28 +293,32 @@ __device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at,
       const long long at = __shfl_sync(0xffffffffu, q_at, r0 + i * kAtOnce + sub);
       w[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(q + at) + c) : make_uint4(0, 0, 0, 0);
     }
+    uint32_t mx[kBatch];  // the largest magnitude as an integer: bf16 patterns order like their values
+    if constexpr (!FP16) {
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const uint32_t a = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                    __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+        mx[i] = max(a & 0xffffu, a >> 16);
+      }
+#pragma unroll
+      for (int o = 1; o < kLanes; o <<= 1)
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) mx[i] = max(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
+    }
 #pragma unroll
     for (int i = 0; i < kBatch; ++i) {
       const int r = r0 + i * kAtOnce + sub;
       uint32_t h[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
       if constexpr (!FP16) {
-        // the largest magnitude as an integer: bf16 patterns order like their values
-        uint32_t mx = __vmaxu2(__vmaxu2(h[0] & 0x7fff7fffu, h[1] & 0x7fff7fffu), __vmaxu2(h[2] & 0x7fff7fffu, h[3] & 0x7fff7fffu));
-        mx = max(mx & 0xffffu, mx >> 16);
-#pragma unroll
-        for (int o = 1; o < kLanes; o <<= 1) mx = max(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const int e = max(15, static_cast<int>(mx >> 7));
+        const int e = max(15, static_cast<int>(mx[i] >> 7));
         const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
           h[k] = pack_half(__uint_as_float(h[k] << 16) * f, __uint_as_float(h[k] & 0xffff0000u) * f);
-        // row r's factor to lane r: it lies with the lanes of one sub of one i
         const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) {
-          const float v = __shfl_sync(0xffffffffu, back, k * kLanes);
-          if (lane == r0 + i * kAtOnce + k) inv = v;
-        }
+        const float v = __shfl_sync(0xffffffffu, back, (lane & (kAtOnce - 1)) * kLanes);  // row r0 + i kAtOnce + that
+        if (lane / kAtOnce == r0 / kAtOnce + i) inv = v;
       }
       st_shared_v4(dst + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
     }
@@ -286,20 +326,22 @@ __device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at,
   return inv;
 }
 
-// Writes 32 rows x 128 bytes, a lane's row as 8 pieces of 16 bytes, to the rows' own
-// places: through `box` (4 KB of shared memory, pieces permuted within a row), so that
-// 8 lanes write a row's 128 bytes together. at: of row `lane`, nullptr: not written.
-__device__ __forceinline__ void store_rows(uint32_t box, const uint4 (&w)[8], uint8_t* at, int lane) {
+// Writes 32 rows x 16 N bytes, a lane's row as N = 4 or 8 pieces, to the rows' own places:
+// through `box` (4 KB of shared memory, pieces permuted within a row), so that N lanes write
+// a row's bytes together. at: of row `lane`, nullptr: not written.
+template <int N>
+__device__ __forceinline__ void store_rows(uint32_t box, const uint4 (&w)[N], uint8_t* at, int lane) {
   __syncwarp();  // the box's last pieces have been read
 #pragma unroll
-  for (int i = 0; i < 8; ++i) st_shared_v4(box + lane * 128 + ((i ^ (lane & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+  for (int i = 0; i < N; ++i)
+    st_shared_v4(box + lane * (16 * N) + ((i ^ (lane & (N - 1))) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
   __syncwarp();
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int r = k * 4 + (lane >> 3);
-    const uint4 v = lds128(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+  for (int k = 0; k < N; ++k) {
+    const int r = k * (32 / N) + lane / N;
+    const uint4 v = lds128(box + r * (16 * N) + (((lane & (N - 1)) ^ (r & (N - 1))) << 4));
     uint8_t* const p = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), r));
-    if (p != nullptr) *reinterpret_cast<uint4*>(p + (lane & 7) * 16) = v;
+    if (p != nullptr) *reinterpret_cast<uint4*>(p + (lane & (N - 1)) * 16) = v;
   }
 }
 
@@ -319,22 +361,21 @@ __device__ __forceinline__ float largest_of(const uint32_t (&v)[32], int c0) {
   return max3(max3(m[0], m[1], m[2]), m[3], m[3]);
 }
 
-// Weights 2^(v mul + add) of N scores, packed to fp16 pairs from p[p0]; their sum
-// comes back, unrounded. Pairs of columns share the packed fp32 instructions.
-template <int N>
-__device__ __forceinline__ float weigh(const uint32_t (&v)[32], int c0, float mul, float add, uint32_t (&p)[16], int p0) {
+// Weights 2^(v mul + add) of 16 scores, packed to fp16 pairs; their sum comes back,
+// unrounded. Pairs of columns share the packed fp32 instructions.
+__device__ __forceinline__ float weigh16(const uint32_t (&v)[32], int c0, float mul, float add, uint32_t (&p)[8]) {
   const uint64_t mul2 = f2_pack(mul, mul), add2 = f2_pack(add, add);
-  uint64_t sum[2] = {0ull, 0ull};
+  uint64_t sum = 0ull;
 #pragma unroll
-  for (int q = 0; q < N / 2; ++q) {
+  for (int q = 0; q < 8; ++q) {
     float x0, x1;
     f2_unpack(f2_fma(f2_pack(__uint_as_float(v[c0 + 2 * q]), __uint_as_float(v[c0 + 2 * q + 1])), mul2, add2), x0, x1);
     const float w0 = ex2(x0), w1 = ex2(x1);
-    p[p0 + q] = pack_half(w0, w1);
-    sum[q & 1] = f2_add(sum[q & 1], f2_pack(w0, w1));
+    p[q] = pack_half(w0, w1);
+    sum = f2_add(sum, f2_pack(w0, w1));
   }
   float s0, s1;
-  f2_unpack(f2_add(sum[0], sum[1]), s0, s1);
+  f2_unpack(sum, s0, s1);
   return s0 + s1;
 }
 
@@ -364,6 +405,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     b.pfull = p + 12;
     b.odone = p + 14;
     b.fin = p + 16;
+    b.ufull = p + 17;
   }
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::oBars + L::kBars * 8);
   int* const abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -384,6 +426,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
       mbar_init(b.odone + i, 1);
     }
     mbar_init(b.fin, 1);
+    for (int i = 0; i < L::kUnits; ++i) mbar_init(b.ufull + i, 1);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) reinterpret_cast<int*>(smem + L::oNan)[i] = 0x7fffffff;
     fence_mbar_init();
@@ -412,8 +455,10 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::oV), kChunkBytes, 1024);  // MN-major
     int task0 = 0, step0 = 0;  // of the unit, over the CTA's run
     bool ok = true;
-    for (int unit = 0; ok && !cur.done(g); ++unit) {
-      const int steps = cur.run(g), tasks = steps * NQ;
+    for (int unit = 0; ok; ++unit) {
+      if (!mbar_wait_spin_w(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) break;
+      const int steps = reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32)->steps, tasks = steps * NQ;
+      if (steps == 0) break;
       for (int t = 0; ok && t < NQ; ++t) ok = mbar_wait_spin_w(b.qfull + t, unit & 1, wd);
       if (!ok) break;
       auto issue_s = [&](int i) -> bool {
@@ -452,156 +497,105 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
       }
       task0 += tasks;
       step0 += steps;
-      cur.skip(g, steps);
     }
     mma_commit_w(b.fin);
     mbar_wait_drain(b.fin, 0, a.wait_limit);
     __syncwarp();
   } else if (warp >= L::kConv && warp < L::kMma) {
-    tile_convert<D, NQ, INT8>(a, g, cur, smem, b, wd, warp - L::kConv, lane);
+    tile_convert<D, NQ, INT8>(a, g, smem, b, wd, warp - L::kConv, lane);
   } else if (warp < L::kConv) {
     // ------------------------------------------------------------ softmax
     const int t = NQ == 2 ? warp >> 2 : 0;
     const int rl = (warp & 3) * 32 + lane;  // row of the tile, TMEM lane
-    const int r = t * 128 + rl;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-    int task0 = 0, step0 = 0;
-    bool ok = true;
-    for (int unit = 0; ok && !cur.done(g); ++unit) {
-      const AttnEntry x = cur.x;
-      const int h = cur.h, first = cur.step, steps = cur.run(g);
-      const int row = x.row0 + r, qi = row / g.G, lim = attn_limit(g, x, r);
-      const int head = h * g.G + (row - qi * g.G);
-      // The warp's 32 rows of queries to fp16, scaled by a power of two each, into the swizzled
-      // tile (the last unit's scores are done: its last P V was awaited).
-      const long long q_at = qi < x.ql ? x.b * a.sq.b + static_cast<long long>(head) * a.sq.h + qi * a.sq.n : -1;
-      const uint32_t q_dst = smem_u32(smem) + L::oQ + t * L::kTile + (warp & 3) * 32 * 128;
-      const float rf = a.scale_log2 * (a.fp16 ? tile_queries<D, true>(a.q, q_at, q_dst, lane) : tile_queries<D, false>(a.q, q_at, q_dst, lane));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(b.qfull + t);
-      const bool live = __any_sync(0xffffffffu, lim > 0);  // rows of this warp see keys
-      // rows that stand for no query (their q is zero) do not make a step an edge
-      const int low = __reduce_min_sync(0xffffffffu, qi < x.ql ? lim : 0x7fffffff);
+    // this warp's rows of the tile of queries: also its box for whole rows on their way out
+    const uint32_t q_at = smem_u32(smem) + L::oQ + t * L::kTile + (warp & 3) * 4096;
+    int task = t, step_n = 0;  // of this tile; steps so far (for the slots of the scales)
+    for (int unit = 0;; ++unit) {
+      if (!mbar_wait_warp<true>(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) break;
+      const TileUnit* const ux = reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32);
+      const int steps = ux->steps;
+      if (steps == 0) break;
+      int lim, low;
+      float rf;
+      bool live;
+      {
+        const TileUnit x = *ux;
+        const int row = x.row0 + t * 128 + rl, qi = row / g.G;
+        lim = unit_limit(g, x, t * 128 + rl);
+        // The warp's 32 rows of queries to fp16, scaled by a power of two each, into the
+        // swizzled tile (the last unit's scores are done: its last P V was awaited).
+        const long long at = qi < x.ql ? x.b * a.sq.b + static_cast<long long>(x.h * g.G + (row - qi * g.G)) * a.sq.h + qi * a.sq.n : -1;
+        rf = a.scale_log2 * (a.fp16 ? tile_queries<D, true>(a.q, at, q_at, lane) : tile_queries<D, false>(a.q, at, q_at, lane));
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.qfull + t);
+        live = __any_sync(0xffffffffu, lim > 0);  // rows of this warp see keys
+        // rows that stand for no query (their q is zero) do not make a step an edge
+        low = __reduce_min_sync(0xffffffffu, qi < x.ql ? lim : 0x7fffffff) - (x.first << g.log2_keys);
+        lim -= x.first << g.log2_keys;  // both from here on relative to the step's first key
+      }
       float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < steps; ++j) {
-        const int i = j * NQ + t, k = task0 + i, buf = k & 1;
-        if (!mbar_wait_warp<true>(b.sfull + buf, (k >> 1) & 1, wd)) {
+      bool ok = true;
+      for (int j = 0; j < steps; ++j, task += NQ, ++step_n, lim -= kKeys, low -= kKeys) {
+        const uint32_t s_tm = lane_base + (task & 1) * 128;
+        if (!mbar_wait_warp<true>(b.sfull + (task & 1), (task >> 1) & 1, wd)) {
           ok = false;
           break;
         }
         tc_fence_after();
         if (live) {
-          const int key0 = (first + j) << g.log2_keys;
-          const uint32_t s_tm = lane_base + buf * 128;
-          // constants of the step's groups of 16 columns, read where they are used
-          const uint32_t sc_at = smem_u32(smem) + L::oScales + ((step0 + j) % kScaleSlots) * 128;
-          auto sc = [&](int i) {
-            const uint4 w = lds128(sc_at + i * 16);
-            return make_float4(__uint_as_float(w.x), __uint_as_float(w.y), __uint_as_float(w.z), __uint_as_float(w.w));
-          };
-          const float4 mine = sc(lane & 7);
-          // every row sees every key, and every page was read and counts
-          const bool plain = key0 + kKeys <= low && !__any_sync(0xffffffffu, mine.x < 0.f || mine.w == 0.f);
-          const int room = lim - key0;  // columns below it are seen
+          // constants of the step's groups of 16 columns (plain loads, free to move ahead of
+          // the stores to TMEM below)
+          const float4* const scp = reinterpret_cast<const float4*>(smem + L::oScales + (step_n % kScaleSlots) * 128);
+          auto sc = [&](int i) { return scp[i]; };
+          // The whole row at once, held: a round trip to TMEM takes about 300 cycles while
+          // products run, whatever it brings.
+          uint32_t v[4][32];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, v[c]);
+          // whether every row sees every key, and every page was read and counts
+          const bool plain = kKeys <= low && !__any_sync(0xffffffffu, sc(lane & 7).w != 1.f);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) reg_fence(v[c]);
+          if (!plain) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              const int lim16 = sc(u).w < 0.f ? 0 : lim - u * 16;
+#pragma unroll
+              for (int q = 0; q < 16; ++q)
+                v[u >> 1][(u & 1) * 16 + q] = q < lim16 ? v[u >> 1][(u & 1) * 16 + q] : 0xff800000u;
+            }
+          }
+          // the largest y of the row; the factor stays above zero, so that masked scores stay at -inf
           constexpr int kG = P16 ? 16 : 32;  // columns that share their scales
-          float tmax = -INFINITY;            // the largest y of the row
-          // One round trip to TMEM takes about 300 cycles while products run, whatever it
-          // brings, so a plain step's scores are read kHold chunks of 32 columns at a time: all
-          // at once, and held, where registers allow it, else the second half, the first (whose
-          // weights are formed next, and go over its columns) and the second again.
-          constexpr int kHold = NQ == 2 ? 4 : 2;
-          uint32_t v[kHold][32];
-          auto read = [&](int c0) {
+          float tmax = -INFINITY;
 #pragma unroll
-            for (int c = 0; c < kHold; ++c) tmem_ld32(s_tm + (c0 + c) * 32, v[c]);
-            tmem_wait_ld();
-#pragma unroll
-            for (int c = 0; c < kHold; ++c) reg_fence(v[c]);
-          };
-          if (plain) {
-#pragma unroll
-            for (int c0 = 4 - kHold; c0 >= 0; c0 -= kHold) {
-              read(c0);
-#pragma unroll
-              for (int c = 0; c < kHold; ++c)
-#pragma unroll
-                for (int u = 0; u < 32 / kG; ++u) {
-                  const float4 f = sc((c0 + c) * 2 + u);
-                  tmax = fmaxf(tmax, fmaf(largest_of<kG>(v[c], u * kG), rf * f.x, f.y));
-                }
-            }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32];
-              tmem_ld32(s_tm + c * 32, v);
-              tmem_wait_ld();
-              reg_fence(v);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float4 f = sc(c * 2 + u);
-                const int lim16 = f.x < 0.f ? 0 : room - (c * 32 + u * 16);
-#pragma unroll
-                for (int q = 0; q < 16; ++q) v[u * 16 + q] = q < lim16 ? v[u * 16 + q] : 0xff800000u;
-                const float y = fmaf(largest_of<16>(v, u * 16), rf * f.x, f.y);
-                tmax = fmaxf(tmax, lim16 > 0 ? y : -INFINITY);
-              }
-            }
+          for (int u = 0; u < kKeys / kG; ++u) {
+            const float4 f = sc(u * (kG / 16));
+            tmax = fmaxf(tmax, fmaf(largest_of<kG>(v[u * kG / 32], (u * kG) & 31), fmaxf(rf * f.x, 1e-37f), f.y));
           }
           const bool grow = tmax > m + kSlack;
-          const float m_new = grow ? tmax : m;
-          const float base = (m_new == -INFINITY ? 0.f : m_new) - kBias;
           const bool moved = __any_sync(0xffffffffu, grow);
-          const float alpha = grow ? ex2(m - (m_new == -INFINITY ? 0.f : m_new)) : 1.f;
-          m = m_new;
+          const float alpha = grow ? ex2(m - tmax) : 1.f;
+          if (grow) m = tmax;
           l *= alpha;
-          // the weights, over the first half of the scores' columns as those are read
-          if (plain) {
+          const float base = (m == -INFINITY ? 0.f : m) - kBias;
+          // the weights, over the first half of the score columns
 #pragma unroll
-            for (int c0 = 0; c0 < 4; c0 += kHold) {
-              if (c0 > 0) read(c0);
+          for (int u = 0; u < 8; ++u) {
+            const float4 f = sc(P16 ? u : u & 6);
+            uint32_t p[8];
+            l = fmaf(weigh16(v[u >> 1], (u & 1) * 16, fmaxf(rf * f.x, 1e-37f), f.y - base, p), f.z, l);
+            if (!plain && f.w == 0.f) {  // a page of zeros
 #pragma unroll
-              for (int c = 0; c < kHold; ++c) {
-                uint32_t p[16];
-#pragma unroll
-                for (int u = 0; u < 32 / kG; ++u) {
-                  const float4 f = sc((c0 + c) * 2 + u);
-                  l = fmaf(weigh<kG>(v[c], u * kG, rf * f.x, f.y - base, p, u * kG / 2), f.z, l);
-                }
-                tmem_st16(s_tm + (c0 + c) * 16, p);
-              }
+              for (int q = 0; q < 8; ++q) p[q] = 0u;
             }
-          } else {
-#pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
-              uint32_t v[32], p[16];
-              tmem_ld32(s_tm + c * 32, v);
-              tmem_wait_ld();
-              reg_fence(v);
-#pragma unroll
-              for (int u = 0; u < 2; ++u) {
-                const float4 f = sc(c * 2 + u);
-                const int lim16 = f.x < 0.f ? 0 : room - (c * 32 + u * 16);
-                const float mul16 = rf * f.x, add = f.y - base;
-                float s = 0.f;
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                  float x0 = fmaf(__uint_as_float(v[u * 16 + 2 * q]), mul16, add);
-                  float x1 = fmaf(__uint_as_float(v[u * 16 + 2 * q + 1]), mul16, add);
-                  x0 = 2 * q < lim16 ? x0 : -INFINITY;
-                  x1 = 2 * q + 1 < lim16 ? x1 : -INFINITY;
-                  const float p0 = ex2(x0), p1 = ex2(x1);
-                  s += p0 + p1;
-                  p[u * 8 + q] = f.w == 0.f ? 0u : pack_half(p0, p1);  // a page of zeros
-                }
-                l = fmaf(s, f.z, l);
-              }
-              tmem_st16(s_tm + c * 16, p);
-            }
+            tmem_st8(s_tm + u * 8, p);
           }
           if (moved && j > 0) {  // the tile's last P V is done before O is rescaled
-            const int kp = k - NQ;
+            const int kp = task - NQ;
             if (!mbar_wait_warp<true>(b.odone + (kp & 1), (kp >> 1) & 1, wd)) {
               ok = false;
               break;
@@ -609,41 +603,38 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
             tc_fence_after();
 #pragma unroll 1
             for (int c = 0; c < D / 32; ++c) {
+              const uint32_t at = lane_base + L::cO + t * D + c * 32;
               uint32_t o[32];
-              tmem_ld32(lane_base + L::cO + t * D + c * 32, o);
+              tmem_ld32(at, o);
               tmem_wait_ld();
               reg_fence(o);
 #pragma unroll
               for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__uint_as_float(o[q]) * alpha);
-              tmem_st32(lane_base + L::cO + t * D + c * 32, o);
+              tmem_st32(at, o);
             }
           }
           tmem_wait_st();
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(b.pfull + buf);
+        if (lane == 0) mbar_arrive(b.pfull + (task & 1));
       }
       if (!ok) break;
       // ---------------------------------------------------------- epilogue
-      {
-        const int k = task0 + (steps - 1) * NQ + t;
-        if (!mbar_wait_warp<true>(b.odone + (k & 1), (k >> 1) & 1, wd)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-      }
-      if (!INT8 && *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4) < lim) l = __int_as_float(0x7fffffff);
+      if (!mbar_wait_warp<true>(b.odone + ((task - NQ) & 1), ((task - NQ) >> 1) & 1, wd)) break;
+      tc_fence_after();
+      const TileUnit x = *ux;
+      const int r = t * 128 + rl, row = x.row0 + r, qi = row / g.G, head = x.h * g.G + (row - qi * g.G);
+      if (!INT8 && *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4) < unit_limit(g, x, r))
+        l = __int_as_float(0x7fffffff);
       if (qi >= x.ql) {
         l = 0.f;
         m = -INFINITY;
       }
-      const bool last = first + steps == x.steps, whole = first == 0 && last;
       // rows leave through this warp's part of the tile of queries, which is done with
-      const uint32_t box = smem_u32(smem) + L::oQ + t * L::kTile + (warp & 3) * 4096;
       const bool none = l == 0.f, row_ok = qi < g.N;
-      if (whole) {
+      const uint32_t o_tm = lane_base + L::cO + t * D;
+      if (x.first == 0 && x.seen_last < 0) {  // the whole unit
         const float inv = none ? 0.f : 1.f / l;
         uint16_t* const dst = a.o + x.b * a.so.b + static_cast<long long>(head) * a.so.h + qi * a.so.n;
 #pragma unroll 1
@@ -652,25 +643,24 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t o[32];
-            tmem_ld32(lane_base + L::cO + t * D + c * 64 + e * 32, o);
+            tmem_ld32(o_tm + c * 64 + e * 32, o);
             tmem_wait_ld();
             reg_fence(o);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
-              uint32_t h[4];
+              uint32_t hw[4];
 #pragma unroll
               for (int q = 0; q < 4; ++q)
-                h[q] = none ? 0u : pack16(__uint_as_float(o[8 * v + 2 * q]) * inv, __uint_as_float(o[8 * v + 2 * q + 1]) * inv, a.fp16);
-              w[e * 4 + v] = make_uint4(h[0], h[1], h[2], h[3]);
+                hw[q] = none ? 0u : pack16(__uint_as_float(o[8 * v + 2 * q]) * inv, __uint_as_float(o[8 * v + 2 * q + 1]) * inv, a.fp16);
+              w[e * 4 + v] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
             }
           }
-          store_rows(box, w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
+          store_rows(q_at, w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
         }
         if (row_ok)
           a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
       } else {
-        const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
-        const long long pr = static_cast<long long>(slot) * g.rows + r;
+        const long long pr = static_cast<long long>(2 * blockIdx.x + (x.first == 0 ? 1 : 0)) * g.rows + r;
         if (row_ok) {
           g.m_part[pr] = m;
           g.l_part[pr] = l;
@@ -678,20 +668,18 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          tmem_ld32(lane_base + L::cO + t * D + c * 32, o);
+          tmem_ld32(o_tm + c * 32, o);
           tmem_wait_ld();
           reg_fence(o);
           uint4 w[8];  // rows that see nothing leave zeros: their accumulators hold whatever P was
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             w[v] = none ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-          store_rows(box, w, row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 32) : nullptr, lane);
+          store_rows(q_at, w, row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 32) : nullptr, lane);
         }
       }
+      __syncwarp();      // the box has been read
       tc_fence_before();  // O is read before the next unit's P V
-      task0 += steps * NQ;
-      step0 += steps;
-      cur.skip(g, steps);
     }
   }
 
