@@ -41,6 +41,34 @@ __device__ __forceinline__ float finite_abs(float x) {
   return a < INFINITY ? a : 0.f;
 }
 
+// The magnitudes of two packed 16-bit values, and their maxima, NaN on top.
+__device__ __forceinline__ uint32_t magnitudes(uint32_t w) { return w & 0x7fff7fffu; }
+template <bool FP16>
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  uint32_t m;
+  if constexpr (FP16)
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  else
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(a), "r"(b));
+  return m;
+}
+template <bool FP16>
+__device__ __forceinline__ void values8(const uint4& x, float (&v)[2][4]) {
+  const float2 f0 = unpack2<FP16>(x.x), f1 = unpack2<FP16>(x.y), f2 = unpack2<FP16>(x.z), f3 = unpack2<FP16>(x.w);
+  v[0][0] = f0.x;
+  v[0][1] = f0.y;
+  v[0][2] = f1.x;
+  v[0][3] = f1.y;
+  v[1][0] = f2.x;
+  v[1][1] = f2.y;
+  v[1][2] = f3.x;
+  v[1][3] = f3.y;
+}
+template <bool FP16>
+__device__ __forceinline__ bool has_nonfinite(uint32_t mag) {
+  return mag >= (FP16 ? 0x7c00u : 0x7f80u);
+}
+
 // The smallest power of two s >= 2^-126 with amax <= s * QMAX, exactly; 0 for
 // amax = 0. QMAX is 1.75 * 2^8 (e4m3) or 1.984375 * 2^6 (int8).
 template <bool INT8>
@@ -53,7 +81,7 @@ __device__ __forceinline__ float scale_for(float amax) {
   e = max(e, 1);
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
-__device__ __forceinline__ float inverse(float s) { return s > 0.f ? 1.f / s : 0.f; }
+__device__ __forceinline__ float inverse(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
 
 // Two values to codes (ties to even, saturating), `lo` in the low byte.
 template <bool INT8>
@@ -78,6 +106,18 @@ __device__ __forceinline__ float2 decode2(uint32_t w) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(w & 0xffffu)));
     return __half22float2(*reinterpret_cast<__half2*>(&h));
   }
+}
+// Four finite values times f to codes, |x f| <= QMAX. int8: adding 1.5 * 2^23 leaves the
+// nearest integer (ties to even) in the low bits, in one fma with the product.
+template <bool INT8>
+__device__ __forceinline__ uint32_t encode4_finite(const float (&x)[4], float f) {
+  if constexpr (INT8) {
+    const float k = 12582912.f;
+    const uint32_t a = __float_as_uint(fmaf(x[0], f, k)), b = __float_as_uint(fmaf(x[1], f, k));
+    const uint32_t c = __float_as_uint(fmaf(x[2], f, k)), d = __float_as_uint(fmaf(x[3], f, k));
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
+  }
+  return encode2<INT8>(x[0] * f, x[1] * f) | (encode2<INT8>(x[2] * f, x[3] * f) << 16);
 }
 template <bool INT8>
 __device__ __forceinline__ uint32_t encode4(const float (&x)[4], float f) {
@@ -111,94 +151,146 @@ __device__ __forceinline__ int page_of(const CacheRows& a, int b, long long i) {
   return -1;
 }
 
-// Whole pages. A unit is one (sequence, page, head) of K or V; kT =
-// page * d / 32 threads hold its rows in registers, 32 elements each, so the
-// page is read once: the loads, the maximum over the unit, then the codes.
-// 16 bytes in and 8 bytes out per thread and row chunk, coalesced over the
-// unit's rows.
+// Unit number to (sequence, page, head).
+struct UnitAt {
+  int h, rel, b;
+  __device__ __forceinline__ UnitAt(unsigned unit, int H, int pages_per_seq) {
+    const unsigned q = unit / static_cast<unsigned>(H);
+    h = static_cast<int>(unit - q * static_cast<unsigned>(H));
+    b = static_cast<int>(q / static_cast<unsigned>(pages_per_seq));
+    rel = static_cast<int>(q - static_cast<unsigned>(b) * static_cast<unsigned>(pages_per_seq));
+  }
+};
+
+// Whole pages. A unit is one (sequence, page, head), K and V together; its page * d / 32
+// threads hold its rows in registers, 32 elements of each, so the page is read once:
+// the loads, the maxima over the unit, then the codes. 16 bytes in and 8 bytes out per
+// thread and piece, coalesced over the unit's rows. Beside the memory the instructions
+// around few elements bind it, so K and V share a thread's place, places within the page
+// are 32-bit, and a thread's four pieces lie a constant stride apart.
 template <bool FP16, bool INT8>
 __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows a, int log2_t, int pages_per_seq,
-                                                                long long units) {
-  __shared__ float warp_max[16];
+                                                                unsigned units) {
+  __shared__ uint32_t warp_max[2][16];
   grid_dep_wait();
   grid_dep_launch();
   const int t = threadIdx.x & ((1 << log2_t) - 1);
-  const long long unit = ((static_cast<long long>(blockIdx.x) * blockDim.x) >> log2_t) + (threadIdx.x >> log2_t);
-  const int chunks = a.c.d >> 3, log2_chunks = a.c.d == 128 ? 4 : 3;
-  bool live = unit < units;
-  int kv = 0, h = 0, b = 0, page = -1;
-  Span sp{0, 0};
-  long long page0 = 0;
-  if (live) {
-    kv = static_cast<int>(unit & 1);
-    long long r = unit >> 1;
-    h = static_cast<int>(r % a.c.H);
-    r /= a.c.H;
-    const int rel = static_cast<int>(r % pages_per_seq);
-    b = static_cast<int>(r / pages_per_seq);
-    sp = span_of(a, b);
-    const long long pi = (sp.first >> a.c.log2_page) + rel;
-    page0 = pi << a.c.log2_page;
-    live = sp.first < sp.end && page0 < sp.end;
-    if (live) page = page_of(a, b, pi);
-    live = page >= 0;
+  const unsigned unit = blockIdx.x * (blockDim.x >> log2_t) + (threadIdx.x >> log2_t);
+  const int log2_chunks = a.c.d == 128 ? 4 : 3;
+  int h = 0, b = 0, page = -1;
+  int lo = 0, hi = 0;    // rows of the page that are written
+  long long before = 0;  // the page's first row counted from the call's first token
+  if (unit < units) {
+    const UnitAt u(unit, a.c.H, pages_per_seq);
+    h = u.h;
+    b = u.b;
+    const Span sp = span_of(a, b);
+    const long long pi = (sp.first >> a.c.log2_page) + u.rel, page0 = pi << a.c.log2_page;
+    before = page0 - sp.first;
+    lo = static_cast<int>(max(0LL, -before));
+    hi = static_cast<int>(min(static_cast<long long>(a.c.page), sp.end - page0));
+    if (lo < hi) page = page_of(a, b, pi);  // needed after the loads below, which do not wait for it
   }
-  uint4 x[4];
-  float amax = 0.f;
-  const uint16_t* src = a.x[kv] + b * a.st.b + h * a.st.h;
+  const int row0 = t >> log2_chunks, row_step = 1 << (log2_t - log2_chunks);
+  const long long at0 = b * a.st.b + h * a.st.h + (before + row0) * a.st.n + (t & ((1 << log2_chunks) - 1)) * 8;
+  const long long src_step = row_step * a.st.n;
+  uint4 x[2][4];
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int idx = t + (k << log2_t), row = idx >> log2_chunks, ch = idx & (chunks - 1);
-    const long long tok = page0 + row;
-    x[k] = make_uint4(0, 0, 0, 0);
-    if (live && tok >= sp.first && tok < sp.end)
-      x[k] = __ldg(reinterpret_cast<const uint4*>(src + (tok - sp.first) * a.st.n + ch * 8));
-  }
+  for (int kv = 0; kv < 2; ++kv) {
+    const uint16_t* const src = a.x[kv] + at0;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const uint32_t w[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = unpack2<FP16>(w[i]);
-      amax = fmaxf(amax, fmaxf(finite_abs(f.x), finite_abs(f.y)));
+    for (int k = 0; k < 4; ++k) {
+      const int row = row0 + k * row_step;
+      x[kv][k] = row >= lo && row < hi ? __ldg(reinterpret_cast<const uint4*>(src + k * src_step)) : make_uint4(0, 0, 0, 0);
     }
   }
+  const long long ph = static_cast<long long>(page) * a.c.H + h;
+  const bool held = page >= 0 && lo > 0;  // earlier tokens of this sequence lie in the page
+  float s_old[2], amax[2];
+  uint32_t big[2];  // maxima of magnitudes, as patterns; NaN and infinities on top
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+  for (int kv = 0; kv < 2; ++kv) {
+    // by every thread, before the barriers below; written after them
+    s_old[kv] = held ? fmaxf(a.c.scale[kv][ph], 0.f) : 0.f;
+    uint32_t m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      m[k] = max2<FP16>(max2<FP16>(magnitudes(x[kv][k].x), magnitudes(x[kv][k].y)),
+                        max2<FP16>(magnitudes(x[kv][k].z), magnitudes(x[kv][k].w)));
+    const uint32_t v = max2<FP16>(max2<FP16>(m[0], m[1]), max2<FP16>(m[2], m[3]));
+    big[kv] = __reduce_max_sync(0xffffffffu, max(v & 0xffffu, v >> 16));
+  }
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, unit_warps = 1 << max(0, log2_t - 5);
+  const int peer = (w & ~(unit_warps - 1)) + (lane & (unit_warps - 1));  // a warp of this unit, by lane
   if (log2_t > 5) {  // units of several warps
-    const int w = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) warp_max[w] = amax;
+    if (lane < 2) warp_max[lane][w] = lane == 0 ? big[0] : big[1];
     __syncthreads();
-    const int n = 1 << (log2_t - 5), w0 = w & ~(n - 1);
-    for (int i = 0; i < n; ++i) amax = fmaxf(amax, warp_max[w0 + i]);
-  }
-  float* const scale = a.c.scale[kv] + static_cast<long long>(page) * a.c.H + h;
-  const bool held = live && sp.first > page0;  // earlier tokens of this sequence lie in the page
-  const float s_old = held ? fmaxf(*scale, 0.f) : 0.f;
-  if (log2_t > 5)
-    __syncthreads();  // every thread of the unit has read the old scale
-  else
-    __syncwarp();
-  if (!live) return;
-  const float s = fmaxf(s_old, scale_for<INT8>(amax));
-  const float inv = inverse(s);
-  uint8_t* const dst = a.c.code[kv] + ((static_cast<long long>(page) * a.c.H + h) << a.c.log2_page) * a.c.d;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const int idx = t + (k << log2_t), row = idx >> log2_chunks;
-    const long long tok = page0 + row;
-    uint2* const at = reinterpret_cast<uint2*>(dst + static_cast<long long>(idx) * 8);
-    if (tok >= sp.first && tok < sp.end) {
-      const float2 f0 = unpack2<FP16>(x[k].x), f1 = unpack2<FP16>(x[k].y);
-      const float2 f2 = unpack2<FP16>(x[k].z), f3 = unpack2<FP16>(x[k].w);
-      const float lo[4] = {f0.x, f0.y, f1.x, f1.y}, hi[4] = {f2.x, f2.y, f3.x, f3.y};
-      *at = make_uint2(encode4<INT8>(lo, inv), encode4<INT8>(hi, inv));
-    } else if (tok < sp.first && s > s_old) {
-      const uint2 w = *at;
-      *at = make_uint2(move4<INT8>(w.x, s_old * inv), move4<INT8>(w.y, s_old * inv));
+    for (int kv = 0; kv < 2; ++kv) big[kv] = __reduce_max_sync(0xffffffffu, warp_max[kv][peer]);
+  }
+  const bool finite = !has_nonfinite<FP16>(max(big[0], big[1]));
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) amax[kv] = unpack2<FP16>(big[kv]).x;
+  // Infinities and NaN are rare: only then second maxima, over the finite values (a
+  // block's units of several warps share barriers, so all of them take them).
+  if (log2_t > 5 ? __syncthreads_or(!finite) : !finite) {
+    for (int kv = 0; kv < 2; ++kv) {
+      float f = 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint4 q = kv ? x[1][k] : x[0][k];
+        const uint32_t v[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float2 e = unpack2<FP16>(v[i]);
+          f = fmaxf(f, fmaxf(finite_abs(e.x), finite_abs(e.y)));
+        }
+      }
+      uint32_t bits = __reduce_max_sync(0xffffffffu, __float_as_uint(f));
+      if (log2_t > 5) {
+        __syncthreads();
+        if (lane == 0) warp_max[0][w] = bits;
+        __syncthreads();
+        bits = __reduce_max_sync(0xffffffffu, warp_max[0][peer]);
+      }
+      if (kv)
+        amax[1] = __uint_as_float(bits);
+      else
+        amax[0] = __uint_as_float(bits);
     }
   }
-  if (t == 0) *scale = s;
+  if (page < 0) return;
+  if (log2_t == 5) __syncwarp();
+#pragma unroll
+  for (int kv = 0; kv < 2; ++kv) {
+    const float s = fmaxf(s_old[kv], scale_for<INT8>(amax[kv]));
+    const float inv = inverse(s);
+    uint8_t* const dst = a.c.code[kv] + (ph << a.c.log2_page) * a.c.d + t * 8;
+    if (finite && lo == 0 && hi == a.c.page) {  // a whole page of finite values
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        float v[2][4];
+        values8<FP16>(x[kv][k], v);
+        *reinterpret_cast<uint2*>(dst + (k * 8 << log2_t)) =
+            make_uint2(encode4_finite<INT8>(v[0], inv), encode4_finite<INT8>(v[1], inv));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int row = row0 + k * row_step;
+        uint2* const at = reinterpret_cast<uint2*>(dst + (k * 8 << log2_t));
+        if (row >= lo && row < hi) {
+          float v[2][4];
+          values8<FP16>(x[kv][k], v);
+          *at = make_uint2(encode4<INT8>(v[0], inv), encode4<INT8>(v[1], inv));
+        } else if (row < lo && s > s_old[kv]) {
+          const uint2 c = *at;
+          *at = make_uint2(move4<INT8>(c.x, s_old[kv] * inv), move4<INT8>(c.y, s_old[kv] * inv));
+        }
+      }
+    }
+    if (t == 0) a.c.scale[kv][ph] = s;
+  }
 }
 
 // A few tokens (N <= kFew): one warp per (sequence, page, head) of K or V, a
@@ -206,21 +298,18 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
 // modulo d / 4. The page's older rows are touched only when the scale grows.
 constexpr int kFew = 8;
 template <bool FP16, bool INT8>
-__global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a, int pages_per_seq, long long units) {
+__global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a, int pages_per_seq, unsigned units) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long unit = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
+  const unsigned unit = blockIdx.x * 4 + (threadIdx.x >> 5);
   if (unit >= units) return;
   const int lane = threadIdx.x & 31;
   const int per_row = a.c.d >> 2, rows = 32 / per_row;  // lanes of a row, rows a warp takes at once: 1 or 2
   const int sub = lane / per_row, ch = (lane - sub * per_row) * 4;
-  const int kv = static_cast<int>(unit & 1);
-  long long r = unit >> 1;
-  const int h = static_cast<int>(r % a.c.H);
-  r /= a.c.H;
-  const int rel = static_cast<int>(r % pages_per_seq), b = static_cast<int>(r / pages_per_seq);
+  const UnitAt u(unit >> 1, a.c.H, pages_per_seq);
+  const int kv = static_cast<int>(unit & 1u), h = u.h, b = u.b;
   const Span sp = span_of(a, b);
-  const long long pi = (sp.first >> a.c.log2_page) + rel, page0 = pi << a.c.log2_page;
+  const long long pi = (sp.first >> a.c.log2_page) + u.rel, page0 = pi << a.c.log2_page;
   if (sp.first >= sp.end || page0 >= sp.end) return;
   const int page = page_of(a, b, pi);
   if (page < 0) return;
@@ -272,14 +361,15 @@ __global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a,
 // Reading back: a thread takes 16 codes (one 16-byte load, two 16-byte
 // stores) of kRead rows a block's width apart, so that several loads are in
 // flight.
-constexpr int kRead = 4;
+constexpr int kRead = 2;
 template <bool FP16, bool INT8>
 __global__ void __launch_bounds__(256) cache_read_kernel(const CacheRows a, int tiles) {
   grid_dep_wait();
   grid_dep_launch();
   const int log2_chunks = a.c.d == 128 ? 3 : 2;
-  const int tile = blockIdx.x % tiles, bh = blockIdx.x / tiles;
-  const int h = bh % a.c.H, b = bh / a.c.H, kv = blockIdx.y;
+  const unsigned bh = blockIdx.x / static_cast<unsigned>(tiles);
+  const int tile = static_cast<int>(blockIdx.x - bh * static_cast<unsigned>(tiles));
+  const int b = static_cast<int>(bh / static_cast<unsigned>(a.c.H)), h = static_cast<int>(bh) - b * a.c.H, kv = blockIdx.y;
   const Span sp = span_of(a, b);
   const int rows = 256 >> log2_chunks, ch = (threadIdx.x & ((1 << log2_chunks) - 1)) * 16;
   const int n0 = tile * rows * kRead + (threadIdx.x >> log2_chunks);
@@ -325,19 +415,17 @@ cudaError_t write_variant(const CacheRows& a, cudaStream_t stream) {
   // a run of N tokens touches at most this many pages, wherever it starts
   const long long span_pages = ((static_cast<long long>(a.N) + a.c.page - 2) >> a.c.log2_page) + 1;
   const int pages = static_cast<int>(span_pages < a.c.table_width ? span_pages : a.c.table_width);
-  const long long units = static_cast<long long>(a.B) * pages * a.c.H * 2;
+  const long long units = static_cast<long long>(a.B) * pages * a.c.H;
+  if (units > 0x3fffffffLL) return cudaErrorInvalidValue;
+  const unsigned n = static_cast<unsigned>(units);
   if (a.N <= kFew) {
-    const long long blocks = (units + 3) / 4;
-    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    return launch_pdl(cache_write_few_kernel<FP16, INT8>, dim3(static_cast<unsigned>(blocks)), dim3(128), 0, stream,
-                      a, pages, units);
+    return launch_pdl(cache_write_few_kernel<FP16, INT8>, dim3((2 * n + 3) / 4), dim3(128), 0, stream, a, pages, 2 * n);
   }
   const int log2_t = a.c.log2_page + (a.c.d == 128 ? 7 : 6) - 5;
   const int threads = log2_t > 8 ? 512 : 256;
-  const long long per = threads >> log2_t, blocks = (units + per - 1) / per;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  return launch_pdl(cache_write_pages_kernel<FP16, INT8>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
-                    stream, a, log2_t, pages, units);
+  const unsigned per = static_cast<unsigned>(threads >> log2_t);
+  return launch_pdl(cache_write_pages_kernel<FP16, INT8>, dim3((n + per - 1) / per), dim3(threads), 0, stream, a,
+                    log2_t, pages, n);
 }
 
 template <bool FP16, bool INT8>

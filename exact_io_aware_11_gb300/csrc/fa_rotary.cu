@@ -75,92 +75,101 @@ __device__ __forceinline__ RowAt row_at(const RotaryLaunch& a, int b, int h, int
   return RowAt{t.x + b * t.sx.b + hh * t.sx.h + n * t.sx.n, t.y + b * t.sy.b + hh * t.sy.h + n * t.sy.n};
 }
 
-// One thread: 8 pairs (half layout: two 16-byte chunks r/2 apart) or 4 pairs
-// (interleaved: one chunk) of `hpt` heads of one row, or one chunk of channels
-// behind the rotated ones, which are copied.
-template <bool FP16, bool INTERLEAVED>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryLaunch a, int jobs, int hpt, int hgroups,
-                                                     long long total) {
+// A thread's row and heads from its index: job fastest, then row, head group, batch.
+// I: 32 bits where the indices fit (a 64-bit division costs as much as two pairs' sines).
+template <typename I>
+struct Item {
+  int job, n, b, h0, h1;
+  __device__ __forceinline__ Item(const RotaryLaunch& a, I idx, int jobs, int hpt, int hgroups) {
+    I rest = idx / static_cast<I>(jobs);
+    job = static_cast<int>(idx - rest * static_cast<I>(jobs));
+    const I bg = rest / static_cast<I>(a.N);
+    n = static_cast<int>(rest - bg * static_cast<I>(a.N));
+    b = static_cast<int>(bg / static_cast<I>(hgroups));
+    h0 = static_cast<int>(bg - static_cast<I>(b) * static_cast<I>(hgroups)) * hpt;
+    h1 = min(h0 + hpt, a.Hq + a.Hk);
+  }
+};
+
+constexpr int kBatch = 4;
+// One thread: 32 bytes of `hpt` heads of one row. Half layout: 8 pairs, two chunks r/2
+// apart, or two chunks of the channels behind the rotated ones; interleaved: 8 pairs, two
+// adjacent chunks. Channels that are not rotated go the same way and keep their bits, so
+// that the lanes of a warp stay together.
+template <bool FP16, bool INTERLEAVED, typename I>
+__global__ void __launch_bounds__(256) rotary_kernel(const RotaryLaunch a, int jobs, int hpt, int hgroups, I total) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const I idx = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
   if (idx >= total) return;
-  const int job = static_cast<int>(idx % jobs);
-  const long long rest = idx / jobs;
-  const int n = static_cast<int>(rest % a.N);
-  const long long bg = rest / a.N;
-  const int hg = static_cast<int>(bg % hgroups), b = static_cast<int>(bg / hgroups);
-  const int h0 = hg * hpt, h1 = min(h0 + hpt, a.Hq + a.Hk);
-  const int rot_jobs = INTERLEAVED ? (a.r + 7) / 8 : a.r / 16;
-  if (job >= rot_jobs) {  // copied channels
-    const int c = INTERLEAVED ? job * 8 : a.r + (job - rot_jobs) * 8;
-    for (int h = h0; h < h1; ++h) {
-      const RowAt p = row_at(a, b, h, n);
-      if (p.x != p.y) *reinterpret_cast<uint4*>(p.y + c) = *reinterpret_cast<const uint4*>(p.x + c);
-    }
-    return;
-  }
-  const int pos = position(a, b, n);
-  if constexpr (INTERLEAVED) {
-    float c[4], s[4];
+  const Item<I> it(a, idx, jobs, hpt, hgroups);
+  const int rot_jobs = INTERLEAVED ? (a.r + 15) / 16 : a.r / 16;
+  const bool rot = it.job < rot_jobs;
+  const int ca = INTERLEAVED ? it.job * 16 : rot ? it.job * 8 : a.r + (it.job - rot_jobs) * 8;
+  const int cb = INTERLEAVED ? ca + 8 : rot ? a.r / 2 + it.job * 8 : ca + (a.d - a.r) / 2;
+  const int pairs = rot ? min(8, a.r / 2 - it.job * 8) : 0;  // fewer: interleaved, the last rotated chunks
+  float c[8], s[8];
+  if (rot) {
+    const int pos = position(a, it.b, it.n);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       c[i] = 1.f;
       s[i] = 0.f;
-      if (job * 8 + 2 * i < a.r) turn_of(__ldg(a.turns + job * 4 + i), pos, a.fcos, a.fsin, c[i], s[i]);
+      if (i < pairs) turn_of(__ldg(a.turns + it.job * 8 + i), pos, a.fcos, a.fsin, c[i], s[i]);
     }
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-      const RowAt p = row_at(a, b, h, n);
-      uint4 v = *reinterpret_cast<const uint4*>(p.x + job * 8);
-      uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  }
+  // kBatch heads' loads in flight: written out, because the compiler may not move a load
+  // ahead of another head's store (the call may be in place)
+  for (int h0 = it.h0; h0 < it.h1; h0 += kBatch) {
+    uint4 v[kBatch][2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (job * 8 + 2 * i < a.r) {
-          const float2 x = unpack2<FP16>(w[i]);
-          w[i] = pack2<FP16>(x.x * c[i] - x.y * s[i], x.x * s[i] + x.y * c[i]);
+    for (int k = 0; k < kBatch; ++k) {
+      if (h0 + k < it.h1) {
+        const uint16_t* const x = row_at(a, it.b, h0 + k, it.n).x;
+        v[k][0] = *reinterpret_cast<const uint4*>(x + ca);
+        v[k][1] = *reinterpret_cast<const uint4*>(x + cb);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (h0 + k >= it.h1) break;
+      uint32_t wa[4] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w};
+      uint32_t wb[4] = {v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
+      if (rot) {
+        if constexpr (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack2<FP16>(wa[i]), y = unpack2<FP16>(wb[i]);
+            if (i < pairs) wa[i] = pack2<FP16>(x.x * c[i] - x.y * s[i], x.x * s[i] + x.y * c[i]);
+            if (4 + i < pairs) wb[i] = pack2<FP16>(y.x * c[4 + i] - y.y * s[4 + i], y.x * s[4 + i] + y.y * c[4 + i]);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 x = unpack2<FP16>(wa[i]), y = unpack2<FP16>(wb[i]);
+            wa[i] = pack2<FP16>(x.x * c[2 * i] - y.x * s[2 * i], x.y * c[2 * i + 1] - y.y * s[2 * i + 1]);
+            wb[i] = pack2<FP16>(x.x * s[2 * i] + y.x * c[2 * i], x.y * s[2 * i + 1] + y.y * c[2 * i + 1]);
+          }
         }
       }
-      *reinterpret_cast<uint4*>(p.y + job * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-    }
-  } else {
-    float c[8], s[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) turn_of(__ldg(a.turns + job * 8 + i), pos, a.fcos, a.fsin, c[i], s[i]);
-    const int hi = a.r / 2;
-#pragma unroll 4
-    for (int h = h0; h < h1; ++h) {
-      const RowAt p = row_at(a, b, h, n);
-      const uint4 va = *reinterpret_cast<const uint4*>(p.x + job * 8);
-      const uint4 vb = *reinterpret_cast<const uint4*>(p.x + hi + job * 8);
-      uint32_t wa[4] = {va.x, va.y, va.z, va.w}, wb[4] = {vb.x, vb.y, vb.z, vb.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const float2 xa = unpack2<FP16>(wa[i]), xb = unpack2<FP16>(wb[i]);
-        wa[i] = pack2<FP16>(xa.x * c[2 * i] - xb.x * s[2 * i], xa.y * c[2 * i + 1] - xb.y * s[2 * i + 1]);
-        wb[i] = pack2<FP16>(xa.x * s[2 * i] + xb.x * c[2 * i], xa.y * s[2 * i + 1] + xb.y * c[2 * i + 1]);
-      }
-      *reinterpret_cast<uint4*>(p.y + job * 8) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
-      *reinterpret_cast<uint4*>(p.y + hi + job * 8) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
+      uint16_t* const y = row_at(a, it.b, h0 + k, it.n).y;
+      *reinterpret_cast<uint4*>(y + ca) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
+      *reinterpret_cast<uint4*>(y + cb) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
     }
   }
 }
 
 // Half layout whose second channels do not start on a chunk (r / 2 not a
 // multiple of 8): a thread takes one pair, or one copied channel, at a time.
-template <bool FP16>
+template <bool FP16, typename I>
 __global__ void __launch_bounds__(256) rotary_pairs_kernel(const RotaryLaunch a, int jobs, int hpt, int hgroups,
-                                                           long long total) {
+                                                           I total) {
   grid_dep_wait();
   grid_dep_launch();
-  const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const I idx = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
   if (idx >= total) return;
-  const int job = static_cast<int>(idx % jobs);
-  const long long rest = idx / jobs;
-  const int n = static_cast<int>(rest % a.N);
-  const long long bg = rest / a.N;
-  const int hg = static_cast<int>(bg % hgroups), b = static_cast<int>(bg / hgroups);
-  const int h0 = hg * hpt, h1 = min(h0 + hpt, a.Hq + a.Hk);
+  const Item<I> it(a, idx, jobs, hpt, hgroups);
+  const int job = it.job, n = it.n, b = it.b, h0 = it.h0, h1 = it.h1;
   const int half = a.r / 2;
   if (job >= half) {
     const int ch = a.r + (job - half);
@@ -181,13 +190,24 @@ __global__ void __launch_bounds__(256) rotary_pairs_kernel(const RotaryLaunch a,
   }
 }
 
-// Heads a thread takes: as many as leave the GPU 4096 threads per SM twice
-// over, at most 8 (more brings nothing: the sines are then a tenth of the work).
+// Heads a thread takes: as many as leave every SM 1024 threads, at most 8 (the sines are
+// then a fifth of a thread's instructions).
 int heads_per_thread(long long threads_at_one, int heads) {
-  const long long enough = static_cast<long long>(sm_count()) * 4096;
+  const long long enough = static_cast<long long>(sm_count()) * 1024;
   int hpt = 1;
   while (hpt < 8 && hpt < heads && threads_at_one / (hpt * 2) >= enough) hpt *= 2;
   return hpt;
+}
+
+template <bool FP16, typename I>
+cudaError_t launch_typed(const RotaryLaunch& a, bool chunks, unsigned blocks, int jobs, int hpt, int hgroups,
+                         long long total, cudaStream_t stream) {
+  const dim3 grid(blocks), block(256);
+  const I n = static_cast<I>(total);
+  if (!chunks) return launch_pdl(rotary_pairs_kernel<FP16, I>, grid, block, 0, stream, a, jobs, hpt, hgroups, n);
+  if (a.interleaved)
+    return launch_pdl(rotary_kernel<FP16, true, I>, grid, block, 0, stream, a, jobs, hpt, hgroups, n);
+  return launch_pdl(rotary_kernel<FP16, false, I>, grid, block, 0, stream, a, jobs, hpt, hgroups, n);
 }
 
 }  // namespace
@@ -195,21 +215,18 @@ int heads_per_thread(long long threads_at_one, int heads) {
 cudaError_t launch_rotary(const RotaryLaunch& a, cudaStream_t stream) {
   const int heads = a.Hq + a.Hk;
   const bool chunks = a.interleaved || a.r % 16 == 0;
-  const int jobs = a.interleaved ? a.d / 8 : chunks ? a.r / 16 + (a.d - a.r) / 8 : a.r / 2 + (a.d - a.r);
+  const int jobs = chunks ? a.d / 16 : a.r / 2 + (a.d - a.r);
   const long long rows = static_cast<long long>(a.B) * a.N;
   const int hpt = heads_per_thread(rows * jobs * heads, heads);
   const int hgroups = (heads + hpt - 1) / hpt;
   const long long total = rows * jobs * hgroups, blocks = (total + 255) / 256;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-  const dim3 grid(static_cast<unsigned>(blocks)), block(256);
-  if (!chunks)
-    return a.fp16 ? launch_pdl(rotary_pairs_kernel<true>, grid, block, 0, stream, a, jobs, hpt, hgroups, total)
-                  : launch_pdl(rotary_pairs_kernel<false>, grid, block, 0, stream, a, jobs, hpt, hgroups, total);
-  if (a.interleaved)
-    return a.fp16 ? launch_pdl(rotary_kernel<true, true>, grid, block, 0, stream, a, jobs, hpt, hgroups, total)
-                  : launch_pdl(rotary_kernel<false, true>, grid, block, 0, stream, a, jobs, hpt, hgroups, total);
-  return a.fp16 ? launch_pdl(rotary_kernel<true, false>, grid, block, 0, stream, a, jobs, hpt, hgroups, total)
-                : launch_pdl(rotary_kernel<false, false>, grid, block, 0, stream, a, jobs, hpt, hgroups, total);
+  const unsigned nb = static_cast<unsigned>(blocks);
+  if (total + 255 <= 0xffffffffLL)
+    return a.fp16 ? launch_typed<true, unsigned>(a, chunks, nb, jobs, hpt, hgroups, total, stream)
+                  : launch_typed<false, unsigned>(a, chunks, nb, jobs, hpt, hgroups, total, stream);
+  return a.fp16 ? launch_typed<true, unsigned long long>(a, chunks, nb, jobs, hpt, hgroups, total, stream)
+                : launch_typed<false, unsigned long long>(a, chunks, nb, jobs, hpt, hgroups, total, stream);
 }
 
 }  // namespace fa
