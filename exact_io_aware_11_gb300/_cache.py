@@ -8,7 +8,6 @@ stream it runs on.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import math
 
@@ -59,40 +58,41 @@ SIGNATURES["fa_cache_attention_workspace_bytes"] = (_SZ, [ctypes.POINTER(CacheSt
 SIGNATURES["fa_cache_attention"] = (_I, [_P, _P, _P, ctypes.POINTER(CacheStruct), _I, _I, _I,
                                          ctypes.POINTER(CacheAttentionOptions), _P, _SZ, _P])
 
-_SAME = contextlib.nullcontext()
+# These calls are made once per layer and token: the checks below read each attribute once,
+# and the stream comes from the binding that torch.cuda.current_stream wraps (0.1 us against 2).
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
-def _on(device, stream):
-    """Context that makes `device` current and, if one is given, `stream`."""
+def _on(call, device, stream, *args):
+    """call(*args) with `device` current and, if one is given, `stream`."""
     if stream is not None:
-        return torch.cuda.stream(stream)
-    return _SAME if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+        if stream.device != device:
+            raise ValueError("the stream belongs to another device than the tensors")
+        with torch.cuda.stream(stream):
+            return call(*args)
+    if device.index == torch.cuda.current_device():
+        return call(*args)
+    with torch.cuda.device(device):
+        return call(*args)
 
 
-def _check_stream(device, stream):
-    if stream is not None and stream.device != device:
-        raise ValueError("the stream belongs to another device than the tensors")
-
-
-def _check_rows(t, what, device=None, dtype=None):
-    """A CUDA bf16 or fp16 [B, H, N, d] view with a contiguous d axis."""
+def _rows(t, what, device=None, dtype=None):
+    """Checks a CUDA bf16 or fp16 [B, H, N, d] view with a contiguous d axis; its shape and
+    element strides (b, h, n), 0 on axes that are never stepped."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{what} must be a CUDA tensor")
-    if t.dtype not in _DTYPES or t.dim() != 4 or t.stride(3) != 1:
+    n, s, dt = t.shape, t.stride(), t.dtype
+    if dt not in _DTYPES or len(n) != 4 or s[3] != 1:
         raise ValueError(f"{what} must be a bf16 or fp16 [B, H, N, d] view with a contiguous last axis")
     if device is not None and t.device != device:
         raise ValueError(f"{what} is on another device")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and dt != dtype:
         raise ValueError(f"{what} has another dtype than the call's other tensors")
-
-
-def _row_strides(t):
-    """Element strides (b, h, n), 0 on axes that are never stepped."""
-    s, n = t.stride(), t.shape
-    out = (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
-    if out == (0, 0, 0) and n[0] * n[1] * n[2] > 1:
+    sb, sh, sn = s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0
+    if not (sb or sh or sn) and n[0] * n[1] * n[2] > 1:
         raise ValueError("rows must not overlap")  # three zeros would mean row-major
-    return out
+    return n, (sb, sh, sn)
 
 
 def _check_int(t, what, device, dim):
@@ -116,9 +116,16 @@ def _check_table(t, device, B):
     return t.data_ptr(), t.stride(0) if B > 1 else 0, t.shape[1]
 
 
-def _like(t):
-    """An empty tensor of t's shape that keeps [B, N, H, d] storage where t has it."""
-    return torch.empty_like(t)
+def _out(t, like, shape, what, device):
+    """The output `t`, or a new tensor like `like` (which keeps [B, N, H, d] storage), and its strides."""
+    if t is None:
+        t = torch.empty_like(like)
+        s = t.stride()
+        return t, (s[0] if shape[0] > 1 else 0, s[1] if shape[1] > 1 else 0, s[2] if shape[2] > 1 else 0)
+    n, s = _rows(t, what, device, like.dtype)
+    if n != shape:
+        raise ValueError(f"{what} has another shape than its input")
+    return t, s
 
 
 def _done(rc, where):
@@ -190,50 +197,47 @@ def rotary_frequencies(rotary_dim: int, base: float = 10000.0, scaling: str | No
     return Rotary(w, attention, interleaved, device)
 
 
-def _rotary(name, q, rotary, k, positions, offset, out, k_out, stream):
-    _check_rows(q, "q")
-    dev = q.device
-    B, Hq, N, d = q.shape
+def _rotary(name, q, rotary, k, positions, offset, out, k_out):
+    n, qs = _rows(q, "q")
+    dev, dt = q.device, q.dtype
+    B, Hq, N, d = n
     if not isinstance(rotary, Rotary) or rotary.turns.device != dev:
         raise ValueError("rotary must be a Rotary on the tensors' device")
     if k is not None:
-        _check_rows(k, "k", dev, q.dtype)
-        if k.shape[0] != B or k.shape[2:] != q.shape[2:]:
+        nk, ks = _rows(k, "k", dev, dt)
+        if nk[0] != B or nk[2] != N or nk[3] != d:
             raise ValueError("k must be [B, heads, N, d] with q's B, N and d")
     elif k_out is not None:
         raise ValueError("k_out without k")
-    ps = (None, 0, 0)
+    pp, pb, pn = None, 0, 0
     if positions is not None:
         if offset:
             raise ValueError("give positions or an offset, not both")
-        if not isinstance(positions, torch.Tensor) or positions.dim() not in (1, 2):
+        if not isinstance(positions, torch.Tensor) or positions.dtype != torch.int32 or positions.device != dev:
+            raise ValueError("positions must be an int32 tensor on the tensors' device")
+        np_ = positions.shape
+        if len(np_) not in (1, 2) or np_[-1] != N or (len(np_) == 2 and np_[0] != B):
             raise ValueError("positions must be int32 [N] or [B, N]")
-        _check_int(positions, "positions", dev, positions.dim())
-        if positions.shape[-1] != N or (positions.dim() == 2 and positions.shape[0] != B):
-            raise ValueError("positions must be int32 [N] or [B, N]")
-        ps = (positions.data_ptr(), positions.stride(0) if positions.dim() == 2 else 0, positions.stride(-1))
-    if not -2 ** 31 <= int(offset) < 2 ** 31:
+        sp = positions.stride()
+        pp, pb, pn = positions.data_ptr(), sp[0] if len(np_) == 2 else 0, sp[-1]
+    if not -2 ** 31 <= offset < 2 ** 31:
         raise ValueError("offset must fit in 32 bits")
-    _check_stream(dev, stream)
-    with _on(dev, stream):
-        y = _like(q) if out is None else out
-        z = None if k is None else _like(k) if k_out is None else k_out
-        if out is not None:
-            _check_rows(out, "out", dev, q.dtype)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        if k_out is not None:
-            _check_rows(k_out, "k_out", dev, q.dtype)
-            if k_out.shape != k.shape:
-                raise ValueError("k_out must have k's shape")
-        none = (0, 0, 0)
-        opt = RotaryOptions(rotary.rotary_dim, int(rotary.interleaved), _DTYPES[q.dtype], rotary.factor,
-                            rotary.turns.data_ptr(), *ps, int(offset), *_row_strides(q), *_row_strides(y),
-                            *(none if k is None else _row_strides(k)), *(none if k is None else _row_strides(z)))
-        _done(getattr(lib(), name)(q.data_ptr(), y.data_ptr(), None if k is None else k.data_ptr(),
-                                   None if k is None else z.data_ptr(), B, Hq, 0 if k is None else k.shape[1], N, d, opt,
-                                   torch.cuda.current_stream(dev).cuda_stream), name)
+    y, ys = _out(out, q, n, "out", dev)
+    z, kp, zp, Hk = None, None, None, 0
+    zs = none = (0, 0, 0)
+    if k is not None:
+        z, zs = _out(k_out, k, nk, "k_out", dev)
+        kp, zp, Hk = k.data_ptr(), z.data_ptr(), nk[1]
+    opt = RotaryOptions(rotary.rotary_dim, rotary.interleaved, _DTYPES[dt], rotary.factor, rotary.turns.data_ptr(), pp, pb, pn,
+                        offset, *qs, *ys, *(none if k is None else ks), *zs)
+    _done(getattr(lib(), name)(q.data_ptr(), y.data_ptr(), kp, zp, B, Hq, Hk, N, d, opt, _raw_stream(dev.index)), name)
     return y if k is None else (y, z)
+
+
+def _device_of(t, what):
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{what} must be a CUDA tensor")
+    return t.device
 
 
 def rotary_forward(q, rotary: Rotary, k=None, positions=None, offset: int = 0, out=None, k_out=None, stream=None):
@@ -241,13 +245,13 @@ def rotary_forward(q, rotary: Rotary, k=None, positions=None, offset: int = 0, o
     its position (fa_rotary_fwd); with k [B, Hk, N, d], (q, k) in one launch.
     positions: int32 [N] or [B, N] on the device, or None for offset + n.
     out=q (k_out=k) rotates in place."""
-    return _rotary("fa_rotary_fwd", q, rotary, k, positions, offset, out, k_out, stream)
+    return _on(_rotary, _device_of(q, "q"), stream, "fa_rotary_fwd", q, rotary, k, positions, int(offset), out, k_out)
 
 
 def rotary_backward(dq, rotary: Rotary, dk=None, positions=None, offset: int = 0, out=None, k_out=None, stream=None):
     """Gradients with respect to rotary_forward's inputs from those of its outputs
     (fa_rotary_bwd), with the same rotary and positions: dq, or (dq, dk)."""
-    return _rotary("fa_rotary_bwd", dq, rotary, dk, positions, offset, out, k_out, stream)
+    return _on(_rotary, _device_of(dq, "dq"), stream, "fa_rotary_bwd", dq, rotary, dk, positions, int(offset), out, k_out)
 
 
 # ------------------------------------------------------------------ the cache
@@ -271,6 +275,7 @@ class KVCache:
         if page not in (16, 32, 64, 128) or d not in (64, 128):
             raise ValueError("page_size must be 16, 32, 64 or 128 and d 64 or 128")
         self._tensors = (k, v, k_scale, v_scale)
+        self.device, self.heads, self.page_size, self.head_dim = k.device, H, page, d
         self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, H, page, d,
                                    _FORMATS[k.dtype])
 
@@ -284,28 +289,26 @@ class KVCache:
     v = property(lambda self: self._tensors[1])
     k_scale = property(lambda self: self._tensors[2])
     v_scale = property(lambda self: self._tensors[3])
-    page_size = property(lambda self: self._struct.page_size)
-    heads = property(lambda self: self._struct.H)
-    head_dim = property(lambda self: self._struct.d)
 
 
 def _check_cache(cache):
     if not isinstance(cache, KVCache):
         raise ValueError("cache must be a KVCache")
-    return cache.k.device
+    return cache.device
 
 
-def _cache_rows(name, cache, k, v, page_table, start, count, stream):
-    dev = cache.k.device
-    B, H, N, d = k.shape
-    if v.shape != k.shape or H != cache.heads or d != cache.head_dim:
+def _cache_rows(name, cache, k, v, page_table, start, count):
+    dev = cache.device
+    n, ks = _rows(k, "k", dev)
+    nv, vs = _rows(v, "v", dev, k.dtype)
+    B, H, N, d = n
+    if nv != n or H != cache.heads or d != cache.head_dim:
         raise ValueError("k and v must be [B, H, N, d] with the cache's H and d")
-    if _row_strides(k) != _row_strides(v):
+    if ks != vs:
         raise ValueError("k and v must share strides")
     rng = CacheRange(*_check_table(page_table, dev, B), _check_lengths(start, "start", dev, B),
-                     _check_lengths(count, "count", dev, B), _DTYPES[k.dtype], *_row_strides(k))
-    _done(getattr(lib(), name)(cache._struct, k.data_ptr(), v.data_ptr(), B, N, rng,
-                               torch.cuda.current_stream(dev).cuda_stream), name)
+                     _check_lengths(count, "count", dev, B), _DTYPES[k.dtype], *ks)
+    _done(getattr(lib(), name)(cache._struct, k.data_ptr(), v.data_ptr(), B, N, rng, _raw_stream(dev.index)), name)
 
 
 def cache_write(cache: KVCache, k, v, page_table, start, count=None, stream=None) -> None:
@@ -314,44 +317,38 @@ def cache_write(cache: KVCache, k, v, page_table, start, count=None, stream=None
     count=None all N rows. Where a page is shared by the old and the new tokens of a
     sequence, its older rows move to the page's new scale if that grew. Two
     sequences of one call must not write the same page."""
-    dev = _check_cache(cache)
-    _check_rows(k, "k", dev)
-    _check_rows(v, "v", dev, k.dtype)
-    _check_stream(dev, stream)
-    with _on(dev, stream):
-        _cache_rows("fa_cache_write", cache, k, v, page_table, start, count, stream)
+    _on(_cache_rows, _check_cache(cache), stream, "fa_cache_write", cache, k, v, page_table, start, count)
 
 
 def cache_read(cache: KVCache, page_table, count, N: int, start=None, dtype=torch.bfloat16, k_out=None, v_out=None,
                stream=None):
     """k, v [B, H, N, d] of tokens start[b] + n, n < count[b], of the cache, in dtype
     (fa_cache_read); rows n >= count[b] are zeros."""
-    dev = _check_cache(cache)
+    return _on(_cache_read, _check_cache(cache), stream, cache, page_table, count, int(N), start, dtype, k_out, v_out)
+
+
+def _cache_read(cache, page_table, count, N, start, dtype, k_out, v_out):
+    dev = cache.device
     _check_int(page_table, "page_table", dev, 2)
-    if int(N) < 1:
+    if N < 1:
         raise ValueError("N must be at least 1")
     if (k_out is None) != (v_out is None):
         raise ValueError("give both k_out and v_out, or neither")
     if dtype not in _DTYPES:
         raise ValueError("dtype must be bf16 or fp16")
-    _check_stream(dev, stream)
-    with _on(dev, stream):
-        shape = (page_table.shape[0], cache.heads, int(N), cache.head_dim)
-        k, v = (torch.empty(shape, dtype=dtype, device=dev) if t is None else t for t in (k_out, v_out))
-        for t in (k, v):
-            _check_rows(t, "k_out, v_out", dev, dtype)
-            if tuple(t.shape) != shape:
-                raise ValueError("k_out and v_out must be [B, H, N, d]")
-        _cache_rows("fa_cache_read", cache, k, v, page_table, start, count, stream)
-    return k, v
+    shape = (page_table.shape[0], cache.heads, N, cache.head_dim)
+    if k_out is None:
+        k_out, v_out = torch.empty(shape, dtype=dtype, device=dev), torch.empty(shape, dtype=dtype, device=dev)
+    elif k_out.dtype != dtype or tuple(k_out.shape) != shape:
+        raise ValueError("k_out and v_out must be [B, H, N, d] of the call's dtype")
+    _cache_rows("fa_cache_read", cache, k_out, v_out, page_table, start, count)
+    return k_out, v_out
 
 
 def cache_attention_workspace_bytes(cache: KVCache, B: int, heads: int, N: int, pages: int) -> int:
     """Workspace bytes with which cache_attention spreads sequences over every SM, for q
     [B, heads, N, d] and a page table of `pages` columns (0: none needed)."""
-    dev = _check_cache(cache)
-    with _on(dev, None):
-        return int(lib().fa_cache_attention_workspace_bytes(cache._struct, B, heads, N, pages))
+    return _on(lib().fa_cache_attention_workspace_bytes, _check_cache(cache), None, cache._struct, B, heads, N, pages)
 
 
 def cache_attention(q, cache: KVCache, page_table, kv_len, q_len=None, causal: bool = True, scale: float | None = None,
@@ -362,38 +359,35 @@ def cache_attention(q, cache: KVCache, page_table, kv_len, q_len=None, causal: b
     that see no token, and rows i >= q_len[b], get O = 0 and LSE = -inf. `workspace`:
     uint8 of cache_attention_workspace_bytes(...) bytes, kept by the caller, allocated
     here if None; split=False does without."""
-    dev = _check_cache(cache)
-    _check_rows(q, "q", dev)
-    B, H, N, d = q.shape
+    return _on(_cache_attention, _check_cache(cache), stream, q, cache, page_table, kv_len, q_len, causal, scale, out, lse,
+               workspace, split)
+
+
+def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, lse, workspace, split):
+    dev = cache.device
+    n, qs = _rows(q, "q", dev)
+    B, H, N, d = n
     if d != cache.head_dim or H % cache.heads:
         raise ValueError("q must have the cache's d and a multiple of its heads")
-    _check_stream(dev, stream)
     if kv_len is None:
         raise ValueError("kv_len is needed")
     table, table_stride, pages = _check_table(page_table, dev, B)
-    with _on(dev, stream):
-        o = _like(q) if out is None else out
-        if out is not None:
-            _check_rows(out, "out", dev, q.dtype)
-            if out.shape != q.shape:
-                raise ValueError("out must have q's shape")
-        if lse is None:
-            l = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-        else:
-            l = lse
-            if l.dtype != torch.float32 or l.device != dev or tuple(l.shape) != (B, H, N) or not l.is_contiguous():
-                raise ValueError("lse must be contiguous float32 [B, H, N]")
-        ws = workspace
-        if ws is None and split:
-            need = lib().fa_cache_attention_workspace_bytes(cache._struct, B, H, N, pages)
-            ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-        elif ws is not None and (not ws.is_cuda or ws.device != dev or not ws.is_contiguous()):
+    kl, ql = _check_lengths(kv_len, "kv_len", dev, B), _check_lengths(q_len, "q_len", dev, B)
+    o, os = _out(out, q, n, "out", dev)
+    if lse is None:
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+    elif lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, H, N] on the tensors' device")
+    L = lib()
+    if workspace is not None:
+        if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
-        n = ws.numel() * ws.element_size() if ws is not None else 0
-        opt = CacheAttentionOptions(table, table_stride, pages, _check_lengths(kv_len, "kv_len", dev, B),
-                                    _check_lengths(q_len, "q_len", dev, B), int(bool(causal)), _DTYPES[q.dtype],
-                                    d ** -0.5 if scale is None else float(scale), *_row_strides(q), *_row_strides(o))
-        _done(lib().fa_cache_attention(q.data_ptr(), o.data_ptr(), l.data_ptr(), cache._struct, B, H, N, opt,
-                                       ws.data_ptr() if n else None, n, torch.cuda.current_stream(dev).cuda_stream),
-              "fa_cache_attention")
-    return o, l
+        need = workspace.numel() * workspace.element_size()
+    else:
+        need = L.fa_cache_attention_workspace_bytes(cache._struct, B, H, N, pages) if split else 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    opt = CacheAttentionOptions(table, table_stride, pages, kl, ql, 1 if causal else 0, _DTYPES[q.dtype],
+                                d ** -0.5 if scale is None else scale, *qs, *os)
+    _done(L.fa_cache_attention(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache._struct, B, H, N, opt,
+                               workspace.data_ptr() if need else None, need, _raw_stream(dev.index)), "fa_cache_attention")
+    return o, lse
