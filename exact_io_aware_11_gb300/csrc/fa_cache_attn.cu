@@ -698,9 +698,23 @@ AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
   return p;
 }
 
+// Whether units are cut, from the sizes that the host knows (capacities, not lengths).
+// Cutting shares the steps out evenly but adds the merge and, with many rows, units that
+// begin within a CTA's run: worth about 6.5 steps (single tokens, steps of 0.7 us: 12 units
+// of 4 steps 10.4 us cut, 8.4 whole; of 8 steps 10.4 and 11.5; 64 units of 8 steps 15.1 and
+// 14.5; 192 of 8 steps 14.6 and 12.5, of 16 steps 18.5 both; 32 tiles of 8 steps 28.8 and 22.7,
+// of 16 steps 30.9 and 33.2). Beyond 16 steps unequal lengths may cost more than that, so
+// those are always cut.
+static bool attn_cut(const AttnPlan& p) {
+  if (p.cap_steps <= 4) return false;
+  if (p.cap_steps > 16) return true;
+  const long long rounds = (p.units + p.ctas - 1) / p.ctas;
+  return static_cast<double>(rounds * p.cap_steps) - static_cast<double>(p.units * p.cap_steps) / p.ctas > 6.5;
+}
+
 size_t cache_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width) {
   const AttnPlan p = attn_plan(B, HK, static_cast<long long>(N) * G, static_cast<long long>(table_width) * page);
-  return p.cap_steps > 1 ? attn_workspace(p.ctas, p.rows, d).total : 0;
+  return attn_cut(p) ? attn_workspace(p.ctas, p.rows, d).total : 0;
 }
 
 cudaError_t launch_cache_attention(const CacheAttnLaunch& a, cudaStream_t stream) {
@@ -720,7 +734,7 @@ cudaError_t launch_cache_attention(const CacheAttnLaunch& a, cudaStream_t stream
   g.kv_len = a.kv_len;
   g.q_len = a.q_len;
   const AttnWorkspace w = attn_workspace(p.ctas, p.rows, a.c.d);
-  g.split = p.cap_steps > 1 && a.ws != nullptr && a.ws_bytes >= w.total;
+  g.split = attn_cut(p) && a.ws != nullptr && a.ws_bytes >= w.total;
   if (g.split) {
     g.record = reinterpret_cast<int4*>(a.ws);
     g.m_part = reinterpret_cast<float*>(a.ws + w.m_off);

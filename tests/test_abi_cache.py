@@ -126,7 +126,8 @@ def test_attention_workspace(L):
         c = _cache.CacheStruct(None, None, None, None, 4, H, page, d, 0)
         return L.fa_cache_attention_workspace_bytes(c, B, Hq, N, width)
     assert need() > 0
-    assert need(width=8) == 0                   # 128 tokens: one step, nothing to split
+    assert need(width=8) == 0 and need(width=32) == 0   # 512 tokens: too little to cut
+    assert need(B=200, width=64) == 0           # 400 units of 1024 tokens fill the GPU whole
     assert need(Hq=7) == 0 and need(page=24) == 0 and need(width=0) == 0 and need(B=0) == 0
     # at most what a fixed number of CTAs leave behind, however long the sequences
     assert need(width=1 << 20) == need(width=1 << 22)

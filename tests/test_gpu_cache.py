@@ -322,7 +322,7 @@ def test_broadcast_table_wide_rows_and_strides(fa):
 
 
 def test_other_stream_and_graphs_that_share_a_workspace(fa):
-    lens = [700, 300]
+    lens = [2700, 300]
     m = filled(fa, 2, 2, 64, 128, "e4m3", lens, seed=8)
     q = queries(2, 8, 1, 128, "bf16", 14)
     t, n = m.table.cuda(), torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -339,7 +339,8 @@ def test_other_stream_and_graphs_that_share_a_workspace(fa):
         with torch.cuda.graph(g):
             outs.append(fa.cache_attention(q, m.cache, t, n, workspace=ws))
         graphs.append(g)
-    for new in ([700, 300], [64, 1], [129, 0], [650, 299]):
+    assert ws.numel() > 0
+    for new in ([2700, 300], [64, 1], [129, 0], [2650, 299]):
         n.copy_(torch.tensor(new, dtype=torch.int32))
         for g in graphs:
             g.replay()
@@ -348,6 +349,173 @@ def test_other_stream_and_graphs_that_share_a_workspace(fa):
     ws.fill_(255)
     graphs[0].replay()
     check_attention(fa, m, q, new, o=outs[0][0], lse=outs[0][1])
+
+
+def gpu_reference(q, cache, table, lens, qlens, causal, scale):
+    """The definition in fp64 torch products for whole batches: O, LSE and the two magnitudes of the bounds."""
+    B, H, N, d = q.shape
+    HK, page = cache.heads, cache.page_size
+    at = table.long()
+    raw = lambda t: t.view(torch.uint8)[at].view(t.dtype)  # noqa: E731
+    k, v = ((raw(c).double() * s[at].double()[..., None, None]).transpose(1, 2).flatten(2, 3)
+            for c, s in ((cache.k, cache.k_scale), (cache.v, cache.v_scale)))
+    L = k.shape[2]
+    j, i = torch.arange(L, device=q.device), torch.arange(N, device=q.device)[:, None]
+    lens, qlens = (torch.tensor(t, device=q.device)[:, None, None] for t in (lens, qlens))
+    see = ((i < qlens) & (j <= lens - qlens + i if causal else j < lens) & (j < lens))[:, None, None]
+    behind = ~(j < lens[:, 0])[:, None, :, None]
+    k, v = k.masked_fill(behind, 0), v.masked_fill(behind, 0)
+    qd = q.double().reshape(B, HK, H // HK * N, d)
+    x = (qd @ k.transpose(2, 3) * scale).view(B, HK, H // HK, N, L).masked_fill(~see, -torch.inf)
+    big = (qd.abs() @ k.abs().transpose(2, 3) * scale).view(B, HK, H // HK, N, L).masked_fill(~see, 0).amax(-1)
+    m = x.amax(-1, keepdim=True).nan_to_num(neginf=0.0)
+    p = torch.exp(x - m)
+    l = p.sum(-1, keepdim=True)
+    p = (p / l.clamp(min=1e-300)).view(B, HK, H // HK * N, L)
+    lse = (m + torch.log(l)).view(B, H, N)
+    return (p @ v).view(B, H, N, d), lse, (p @ v.abs()).view(B, H, N, d), big.view(B, H, N)
+
+
+def random_cache(fa, P, HK, page, d, fmt, seed):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    codes = []
+    for _ in "kv":
+        x = torch.randn((P, HK, page, d), generator=g, device="cuda") * 40
+        codes.append((x.round() if fmt == "int8" else x).clamp(-127, 127).to(CODE[fmt]))
+    return fa.KVCache(*codes, *(torch.exp2(torch.randint(-8, -4, (P, HK), generator=g, device="cuda").float()) for _ in "kv"))
+
+
+def check_batch(fa, q, cache, table, lens, qlens, causal=True, **kw):
+    i32 = lambda t: torch.tensor(t, dtype=torch.int32, device="cuda")  # noqa: E731
+    scale = q.shape[3] ** -0.5
+    o, lse = fa.cache_attention(q, cache, table, i32(lens), q_len=i32(qlens), causal=causal, **kw)
+    wo, wl, mag, big = gpu_reference(q, cache, table, lens, qlens, causal, scale)
+    torch.cuda.synchronize()
+    assert fa.device_status() == fa.FA_OK
+    eps = torch.finfo(q.dtype).eps
+    assert torch.equal(torch.isneginf(lse), torch.isneginf(wl))
+    tol = eps / 2 * wo.abs() + mag * (2.0 ** -11 + 2 * (2.0 ** -17 * big + 2.0 ** -20))[..., None] + 2.0 ** -25
+    err = (o.double() - wo).abs()
+    assert (err <= tol).all(), f"O off by {(err / tol).max().item():.2f} bounds at {(err > tol).nonzero()[0].tolist()}"
+    fin = ~torch.isneginf(wl)
+    tl = 2.0 ** -17 * big + 2.0 ** -19 + 2.0 ** -22 * wl.abs()
+    assert ((lse.double() - wl).abs()[fin] <= tl[fin]).all()
+    return o, lse
+
+
+@pytest.mark.parametrize("fmt,dt", [("e4m3", "bf16"), ("int8", "fp16")])
+@pytest.mark.parametrize("d,page,H,HK,N,B,longest", [
+    (64, 16, 40, 20, 9, 170, 120),      # thousands of units of one step: their descriptions wrap
+    (128, 64, 40, 20, 9, 170, 128), (128, 16, 32, 16, 1, 300, 100), (64, 32, 18, 2, 16, 8, 3000),
+    (128, 128, 3, 1, 341, 3, 2500), (64, 64, 2, 1, 1000, 2, 4000), (128, 16, 8, 2, 260, 2, 1500), (64, 16, 5, 1, 700, 1, 900),
+])
+def test_many_units_and_long_chunks(fa, d, page, H, HK, N, B, longest, fmt, dt):
+    g = torch.Generator().manual_seed(B + N)
+    W = -(-longest // page)
+    P = min(4000, B * W + 1)
+    cache = random_cache(fa, P, HK, page, d, fmt, seed=N)
+    table = torch.randint(0, P, (B, W), generator=g, dtype=torch.int32).cuda()   # sequences may share pages
+    lens = torch.randint(0, longest + 1, (B,), generator=g).tolist()
+    lens[-1] = longest
+    qlens = torch.randint(0, N + 1, (B,), generator=g).tolist()
+    qlens[-1] = N
+    q = queries(B, H, N, d, dt, 16)
+    for causal in (True, False):
+        a = check_batch(fa, q, cache, table, lens, qlens, causal)
+    b = check_batch(fa, q, cache, table, lens, qlens, False, split=False)
+    assert torch.isneginf(a[1]).equal(torch.isneginf(b[1]))
+
+
+@pytest.mark.parametrize("G,N", [(1, 3), (2, 12), (1, 40), (4, 60), (1, 400)])
+def test_nan_behind_a_row_has_no_effect_on_it(fa, G, N):
+    """NaN in K and V at token t reaches the rows that see t, all of each of them, and no other row, in every
+    kernel; rows of other heads and sequences stay as they are."""
+    L = max(N, 1) + 90
+    m = filled(fa, 2, 2, 16, 64, "e4m3", [L, L], seed=20)
+    q = queries(2, 2 * G, N, 64, "bf16", 17)
+    i32 = torch.tensor([L, L], dtype=torch.int32, device="cuda")
+    want, wl = fa.cache_attention(q, m.cache, m.table.cuda(), i32)
+    at = [L - N + N // 2, L - 1]
+    for n, t in zip("vk", at):
+        m.codes[n][int(m.table[1, t // 16]), 1, t % 16, 3] = 0xff
+        getattr(m.cache, n).view(torch.uint8).copy_(torch.from_numpy(m.codes[n]))
+    o, lse = fa.cache_attention(q, m.cache, m.table.cuda(), i32)
+    hit = torch.zeros_like(lse, dtype=torch.bool)
+    hit[1, G:, N // 2:] = True
+    assert torch.isnan(o[1, G:, N // 2:]).any(-1).all()
+    assert not torch.isnan(o[~hit]).any() and not torch.isnan(lse[~hit]).any()
+    assert torch.equal(o[~hit], want[~hit]) and torch.equal(lse[~hit], wl[~hit])
+
+
+def test_offsets_beyond_32_bits(fa):
+    """A pool whose codes pass 2^32 bytes: the last pages are written, read back and attended over."""
+    HK, page, d = 8, 128, 128
+    P = 2 ** 32 // (HK * page * d) + 40
+    cache = fa.KVCache.empty(P, HK, d, page, torch.float8_e4m3fn)
+    table = torch.tensor([[P - 1, 3, P - 7], [P - 30, P - 2, 1]], dtype=torch.int32, device="cuda")
+    k, v = rows(2, HK, 300, d, "bf16", 30, "bnhd"), rows(2, HK, 300, d, "bf16", 31, "bnhd")
+    n = torch.tensor([300, 257], dtype=torch.int32, device="cuda")
+    fa.cache_write(cache, k, v, table, None, n)
+    got, _ = fa.cache_read(cache, table, n, 300)
+    step = k.double().abs().amax((2, 3), keepdim=True) / 448 * 2 * 32 / 2     # half a step of the largest binade
+    live = (torch.arange(300, device="cuda") < n[:, None])[:, None, :, None]
+    assert ((got.double() - k.double()).abs() * live <= step).all() and not (got * ~live).any()
+    for N, G in ((1, 2), (20, 2)):
+        check_batch(fa, queries(2, HK * G, N, d, "bf16", 32), cache, table, [300, 257], [N, N])
+
+
+def test_two_calls_at_once(fa):
+    """Two streams, each with its own outputs and workspace."""
+    cache = random_cache(fa, 600, 4, 64, 128, "e4m3", seed=3)
+    table = torch.randperm(600, generator=torch.Generator().manual_seed(4)).to(torch.int32)[:520].reshape(4, 130).cuda()
+    lens = [8000, 17, 5000, 129]
+    q = [queries(4, 8, N, 128, "bf16", 40 + N) for N in (1, 30)]
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    want = [fa.cache_attention(x, cache, table, n) for x in q]
+    streams = [torch.cuda.Stream() for _ in q]
+    torch.cuda.synchronize()
+    got = [[fa.cache_attention(x, cache, table, n, stream=s) for _ in range(4)] for x, s in zip(q, streams)]
+    torch.cuda.synchronize()
+    for w, runs in zip(want, got):
+        for r in runs:
+            assert torch.equal(w[0], r[0]) and torch.equal(w[1], r[1])
+
+
+def test_captured_decoding_step(fa):
+    """Rotary, write and attention of one token in one graph, replayed as the sequences grow."""
+    B, HK, G, d, page, W = 3, 2, 4, 64, 16, 6
+    m = Model(fa, B * W, HK, page, d, "e4m3", B, W, seed=21)
+    rot = fa.rotary_frequencies(d)
+    q, k, v = (queries(B, h, 1, d, "bf16", 60 + h) for h in (HK * G, HK, HK))
+    qr, kr = torch.empty_like(q), torch.empty_like(k)
+    table, start, n = m.table.cuda(), torch.tensor([0, 15, 31], dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    o, lse = torch.empty_like(q), torch.empty((B, HK * G, 1), device="cuda")
+
+    def step():
+        fa.rotary_forward(q, rot, k=k, positions=start[:, None], out=qr, k_out=kr)
+        fa.cache_write(m.cache, kr, v, table, start)
+        torch.add(start, 1, out=n)
+        fa.cache_attention(qr, m.cache, table, n, out=o, lse=lse)
+
+    for t in "kv":  # sequences that start at 15 and 31 hold leftovers before: make them plain values
+        m.codes[t][:] = oc.encode(np.random.default_rng(5).standard_normal(m.codes[t].shape) * 50, "e4m3")
+        getattr(m.cache, t).view(torch.uint8).copy_(torch.from_numpy(m.codes[t]))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    at = start.tolist()
+    for i in range(5):
+        for t, x in enumerate((q, k, v)):
+            x.copy_(queries(B, x.shape[1], 1, d, "bf16", 70 + 3 * i + t))
+        graph.replay()
+        torch.cuda.synchronize()
+        for name, x in (("k", kr), ("v", v)):
+            oc.write(m.codes[name], m.scale[name], f64(x), m.table.numpy(), at, [1] * B, page, "e4m3")
+        m.same()
+        at = [a + 1 for a in at]
+        check_attention(fa, m, qr, at, o=o, lse=lse)
+        start.add_(1)
 
 
 def test_refusals(fa):
