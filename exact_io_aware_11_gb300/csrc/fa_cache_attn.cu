@@ -483,7 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int slot = 2 * blockIdx.x + (step0 == 0 ? 1 : 0);
     if (g.split && !whole && last && threadIdx.x == 0)
       g.record[blockIdx.x] =
-          make_int4(x.b * g.row_tiles + x.row0 / g.rows, h, attn_cta_of(unit_first, share.total, share.ctas), 0);
+          make_int4(x.b * g.row_tiles + x.row0 / g.rows, h, attn_cta_of(unit_first, share), 0);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -545,9 +545,9 @@ __global__ void __launch_bounds__(kThreads, 2)
 // whose last part c ran) and share its rows out: with m_q, l_q, O_q of part q and
 // M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q. A lane holds D / 32
 // consecutive channels and loads eight parts at a time, statistics and all. A unit
-// of few parts (many query rows) gives each of the block's 8 warps a row; one of
-// more parts gives a row four warps, which take every fourth part and then join
-// theirs (a row of 76 parts with one warp, four at a time: 36 us; 8 us so).
+// of few parts gives each of the block's 8 warps a row; one of more parts gives a row
+// four or eight warps, which take every fourth or eighth part and then join theirs (a
+// row of 76 parts with one warp, four at a time: 36 us by itself, with four warps 8 us).
 template <int D>
 __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
   constexpr int kV = D / 32, kBatch = 8;
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
   const int4 rec = g.record[blockIdx.x];
   if (rec.x < 0) return;
   const int c0 = rec.z, c1 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int W = c1 - c0 < 4 ? 1 : 4, sub = warp & (W - 1);  // warps of a row
+  const int W = c1 - c0 < 4 ? 1 : c1 - c0 < 32 ? 4 : 8, sub = warp & (W - 1);  // warps of a row
   const int b = rec.x / g.row_tiles, row0 = (rec.x - b * g.row_tiles) * g.rows;
   const int live = static_cast<int>(min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G - row0));
   for (int r0 = blockIdx.y * (8 / W); r0 < live; r0 += gridDim.y * (8 / W)) {  // uniform over the block
@@ -616,14 +616,12 @@ __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_cons
       }
       __syncthreads();
       if (sub == 0) {
-#pragma unroll
-        for (int w = 1; w < 4; ++w) M = fmaxf(M, sm_m[warp + w]);
+        for (int w = 1; w < W; ++w) M = fmaxf(M, sm_m[warp + w]);
         const float base = M == -INFINITY ? 0.f : M;
         sum = 0.f;
 #pragma unroll
         for (int d = 0; d < kV; ++d) acc[d] = 0.f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
+        for (int w = 0; w < W; ++w) {
           const float f = ex2(sm_m[warp + w] - base);
           sum = fmaf(sm_l[warp + w], f, sum);
 #pragma unroll
@@ -666,8 +664,8 @@ cudaError_t launch_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas
                                : launch_rows<D, 1, INT8>(a, g, ctas, stream);
   if (e != cudaSuccess || !g.split) return e;
   const long long live = min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G);
-  // blocks of a unit: two rows each, and no more than 16 (most CTAs have no record)
-  const unsigned y = static_cast<unsigned>(live < 32 ? (live + 1) / 2 : 16);
+  // blocks of a unit: a row each, and no more than 16 (most CTAs have no record)
+  const unsigned y = static_cast<unsigned>(live < 16 ? live : 16);
   return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, y), dim3(256), 0, stream, a, g);
 }
 

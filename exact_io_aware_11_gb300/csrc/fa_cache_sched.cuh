@@ -5,8 +5,8 @@
 // query row r / G of head r % G of the cache head's group of G. A unit's steps
 // are the key tiles its rows see (at least one, so that units without keys
 // still write their rows). All units' steps lie end to end, ordered by
-// (sequence, row tile), then head; CTA c of C takes steps [T c / C, T (c + 1) / C),
-// an equal share whatever the lengths. A unit cut by a boundary leaves parts in
+// (sequence, row tile), then head; CTA c of C takes T / C of the T steps, and one more if
+// c < T mod C, an equal share whatever the lengths. A unit cut by a boundary leaves parts in
 // the workspace: slot 2 c for the part CTA c starts in the middle of, slot
 // 2 c + 1 for one it starts and does not finish. The CTA with a unit's last part
 // writes the unit's merge record.
@@ -90,19 +90,35 @@ struct AttnCursor {
   }
 };
 
+// The steps' division: CTA c starts at c * each + min(c, extra).
 struct AttnShare {
-  long long total, first;  // steps in all; the first step of the entry `entry`
-  int entry, ctas;
+  long long first;  // the first step of `entry`
+  long long each;
+  int extra, ctas, entry;
+  AttnEntry x;      // of `entry`
 };
 
+// n / d for n that mostly fits 32 bits (a 64-bit division takes some 400 cycles).
+__device__ __forceinline__ long long attn_div(long long n, long long d) {
+  if (((n | d) >> 32) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
+  return n / d;
+}
+__device__ __forceinline__ long long attn_start(const AttnShare& s, int c) {
+  return c * s.each + min(c, s.extra);
+}
+
 // This CTA's cursor. Called by the whole CTA of kThreads threads; `sh` and
-// `part` (kThreads / 32 + 1 words) are shared memory.
+// `part` (kThreads / 32 words) are shared memory.
 template <int kThreads>
 __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* sh, long long* part) {
   const int E = g.B * g.row_tiles, per = (E + kThreads - 1) / kThreads;
   const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
+  AttnEntry own{};  // the thread's only entry, where it has just one
   long long mine = 0;
-  for (int e = e0; e < e1; ++e) mine += attn_entry(g, e).steps;
+  for (int e = e0; e < e1; ++e) {
+    own = attn_entry(g, e);
+    mine += own.steps;
+  }
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -110,6 +126,7 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
     if ((threadIdx.x & 31) >= o) incl += v;
   }
   if ((threadIdx.x & 31) == 31) part[threadIdx.x >> 5] = incl;
+  if (threadIdx.x == 0) sh->entry = E;
   __syncthreads();
   long long before = 0, total = 0;
 #pragma unroll
@@ -120,26 +137,30 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   }
   before += incl - mine;
   total *= g.HK;
-  const int C = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  AttnShare d{};
+  d.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
+  d.each = attn_div(total, d.ctas);
+  d.extra = static_cast<int>(total - d.each * d.ctas);
   const int c = blockIdx.x;
-  const long long s0 = c < C ? total * c / C : total;
-  if (threadIdx.x == 0) {
-    sh->total = total;
-    sh->ctas = C;
-    sh->entry = E;
-  }
-  __syncthreads();
+  const long long s0 = c < d.ctas ? attn_start(d, c) : total;
   long long p = before * g.HK;
   if (s0 >= p && s0 < p + mine * g.HK) {
     for (int e = e0; e < e1; ++e) {
-      const long long n = static_cast<long long>(attn_entry(g, e).steps) * g.HK;
+      const AttnEntry x = per == 1 ? own : attn_entry(g, e);
+      const long long n = static_cast<long long>(x.steps) * g.HK;
       if (s0 < p + n) {
         sh->entry = e;
         sh->first = p;
+        sh->x = x;
         break;
       }
       p += n;
     }
+  }
+  if (threadIdx.x == 0) {
+    sh->each = d.each;
+    sh->extra = d.extra;
+    sh->ctas = d.ctas;
   }
   __syncthreads();
   AttnCursor cur;
@@ -147,11 +168,11 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   cur.h = 0;
   cur.step = 0;
   cur.pos = s0;
-  cur.end = c < C ? total * (c + 1) / C : total;
+  cur.end = c < d.ctas ? attn_start(d, c + 1) : total;
   if (cur.e < E) {
-    cur.x = attn_entry(g, cur.e);
+    cur.x = sh->x;
     const long long rem = s0 - sh->first;
-    cur.h = static_cast<int>(rem / cur.x.steps);
+    cur.h = static_cast<int>(attn_div(rem, cur.x.steps));
     cur.step = static_cast<int>(rem - static_cast<long long>(cur.h) * cur.x.steps);
     if (!g.split && cur.step > 0) {  // the unit belongs to the CTA that it starts in
       cur.pos += cur.x.steps - cur.step;
@@ -163,12 +184,10 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   return cur;
 }
 
-// The CTA whose run holds step s: the largest c with total * c / C <= s.
-__device__ __forceinline__ int attn_cta_of(long long s, long long total, int C) {
-  int c = static_cast<int>(min(static_cast<long long>(C - 1), s * C / total));
-  while (c + 1 < C && total * (c + 1) / C <= s) ++c;
-  while (c > 0 && total * c / C > s) --c;
-  return c;
+// The CTA whose run holds step s.
+__device__ __forceinline__ int attn_cta_of(long long s, const AttnShare& d) {
+  const long long longer = d.extra * (d.each + 1);  // steps of the CTAs that have one more
+  return static_cast<int>(s < longer ? attn_div(s, d.each + 1) : d.extra + attn_div(s - longer, d.each));
 }
 
 // Keys of a step and rows of a tile of the kernel that a call of `rows` = N * G

@@ -54,7 +54,7 @@ struct TileLayout {
   static constexpr int oBars = oUnits + kUnits * 32;
   static constexpr int kBars = 2 * kStg + 17 + kUnits;
   static constexpr int kSmem = oBars + kBars * 8 + 16 + 1024;
-  static_assert(kSmem + 128 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(kSmem + sizeof(AttnShare) + 16 <= 227 * 1024, "shared memory of one CTA");
   static constexpr uint32_t cO = 256;                   // TMEM column of O
 };
 
@@ -113,7 +113,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
         describe(TileUnit{ld.x.b, ld.x.row0, ld.h, ld.step, steps, ld.x.kv, ld.x.ql,
                           static_cast<int>(static_cast<unsigned>(ld.x.seen) | (ends ? 0x80000000u : 0u))});
         if (ld.step > 0 && ends && g.split && lane == 0)
-          g.record[blockIdx.x] = make_int4(ld.e, ld.h, attn_cta_of(ld.pos - ld.step, share.total, share.ctas), 0);
+          g.record[blockIdx.x] = make_int4(ld.e, ld.h, attn_cta_of(ld.pos - ld.step, share), 0);
         first = false;
       }
       const int key = (ld.step << g.log2_keys) + lane * 16;
@@ -387,7 +387,6 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   using L = TileLayout<D, NQ>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShare share;
-  __shared__ long long part[L::kThreads / 32];
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   TileBars b;
@@ -440,7 +439,8 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   tc_fence_before();
   grid_dep_wait();
   grid_dep_launch();
-  AttnCursor cur = attn_share<L::kThreads>(g, &share, part);  // its barriers publish the above
+  // its barriers publish the above; the slots of the scales are not in use yet
+  AttnCursor cur = attn_share<L::kThreads>(g, &share, reinterpret_cast<long long*>(smem + L::oScales));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{a.wait_limit, a.status, abort_flag};
