@@ -544,13 +544,13 @@ __global__ void __launch_bounds__(kThreads, 2)
 // Merges the units that were cut. Blocks (c, y) look at CTA c's record (the unit
 // whose last part c ran) and share its rows out: with m_q, l_q, O_q of part q and
 // M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q. A lane holds D / 32
-// consecutive channels and loads eight parts at a time, statistics and all. A unit
+// consecutive channels and loads four parts at a time, statistics and all. A unit
 // of few parts gives each of the block's 8 warps a row; one of more parts gives a row
 // four or eight warps, which take every fourth or eighth part and then join theirs (a
 // row of 76 parts with one warp, four at a time: 36 us by itself, with four warps 8 us).
 template <int D>
 __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
-  constexpr int kV = D / 32, kBatch = 8;
+  constexpr int kV = D / 32, kBatch = 4;
   __shared__ float sm_m[8], sm_l[8], sm_o[8][D];
   grid_dep_wait();
   grid_dep_launch();
@@ -664,8 +664,8 @@ cudaError_t launch_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas
                                : launch_rows<D, 1, INT8>(a, g, ctas, stream);
   if (e != cudaSuccess || !g.split) return e;
   const long long live = min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G);
-  // blocks of a unit: a row each, and no more than 16 (most CTAs have no record)
-  const unsigned y = static_cast<unsigned>(live < 16 ? live : 16);
+  // blocks of a unit: a row each, and no more than 32 (most CTAs have no record)
+  const unsigned y = static_cast<unsigned>(live < 32 ? live : 32);
   return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, y), dim3(256), 0, stream, a, g);
 }
 
@@ -686,7 +686,7 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
   AttnPlan p{};
-  p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 128 ? 128 : 256;
+  p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
   p.log2_keys = 7;
   p.units = static_cast<long long>(B) * HK * ((rows + p.rows - 1) / p.rows);
   p.cap_steps = (cap + 127) >> 7;

@@ -198,7 +198,7 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap);
 
-// Tiles of 128 (g.rows) or 2 x 128 query rows on tcgen05 (fa_cache_tile.cuh), one
+// Tiles of 64, 128 (g.rows) or 2 x 128 query rows on tcgen05 (fa_cache_tile.cuh), one
 // translation unit for each format.
 cudaError_t launch_cache_attention_tiles_e4m3(const CacheAttnLaunch& a, const AttnGrid& g, int ctas,
                                               cudaStream_t stream);

@@ -52,7 +52,7 @@ struct TileLayout {
   static_assert(2 + kStg / 2 + 2 + (NQ == 1 ? 2 : 1) < kUnits, "a unit's description outlives its use");
   static constexpr int oUnits = oNan + 32;
   static constexpr int oBars = oUnits + kUnits * 32;
-  static constexpr int kBars = 2 * kStg + 17 + kUnits;
+  static constexpr int kBars = 2 * kStg + 17 + kUnits + 5;
   static constexpr int kSmem = oBars + kBars * 8 + 16 + 1024;
   static_assert(kSmem + sizeof(AttnShare) + 16 <= 227 * 1024, "shared memory of one CTA");
   static constexpr uint32_t cO = 256;                   // TMEM column of O
@@ -76,7 +76,7 @@ constexpr uint32_t idesc_f16(int M, int N, bool b_mn_major) {
 }
 
 struct TileBars {
-  uint64_t *raw_full, *raw_empty, *kfull, *kempty, *vfull, *vempty, *qfull, *sfull, *pfull, *odone, *fin, *ufull;
+  uint64_t *raw_full, *raw_empty, *kfull, *kempty, *vfull, *vempty, *qfull, *sfull, *pfull, *odone, *fin, *ufull, *rep_out, *rep_in, *rep_done;
 };
 
 // Producer: the raw tiles K(n), V(n) of every step, as pages. Lane i < 8 looks
@@ -380,8 +380,10 @@ __device__ __forceinline__ float weigh16(const uint32_t (&v)[32], int c0, float 
 }
 
 // P16: pages of 16 tokens, whose scales change every 16 columns (32 and more
-// otherwise).
-template <int D, int NQ, bool INT8, bool P16>
+// otherwise). REP = 2 (units of up to 64 rows): the rows stand in the tile twice, and each
+// copy's warps take half of a step's keys, with weights of zero for the others; a unit ends
+// with the copies joined. All four softmax warps then work, each on half the columns.
+template <int D, int NQ, int REP, bool INT8, bool P16>
 __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     cache_attn_tile_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
   using L = TileLayout<D, NQ>;
@@ -405,6 +407,9 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     b.odone = p + 14;
     b.fin = p + 16;
     b.ufull = p + 17;
+    b.rep_out = p + 17 + L::kUnits;  // [2] pairs of warps
+    b.rep_in = b.rep_out + 2;        // [2]
+    b.rep_done = b.rep_out + 4;
   }
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(smem + L::oBars + L::kBars * 8);
   int* const abort_flag = reinterpret_cast<int*>(tmem_slot + 1);
@@ -425,6 +430,11 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
       mbar_init(b.odone + i, 1);
     }
     mbar_init(b.fin, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(b.rep_out + i, 1);
+      mbar_init(b.rep_in + i, 1);
+    }
+    mbar_init(b.rep_done, 2);
     for (int i = 0; i < L::kUnits; ++i) mbar_init(b.ufull + i, 1);
     *abort_flag = 0;
     for (int i = 0; i < 8; ++i) reinterpret_cast<int*>(smem + L::oNan)[i] = 0x7fffffff;
@@ -505,8 +515,12 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     tile_convert<D, NQ, INT8>(a, g, smem, b, wd, warp - L::kConv, lane);
   } else if (warp < L::kConv) {
     // ------------------------------------------------------------ softmax
+    static_assert(REP == 1 || NQ == 1, "copies of rows stand in one tile");
+    constexpr int kCols = kKeys / REP, kChunks = kCols / 32;  // this warp's columns
     const int t = NQ == 2 ? warp >> 2 : 0;
-    const int rl = (warp & 3) * 32 + lane;  // row of the tile, TMEM lane
+    const int rep = REP == 2 ? (warp >> 1) & 1 : 0, pair = warp & 1;
+    const int rl = (REP == 2 ? pair : warp & 3) * 32 + lane;  // row of the unit's tile
+    const int col0 = rep * kCols;
     const uint32_t lane_base = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
     // this warp's rows of the tile of queries: also its box for whole rows on their way out
     const uint32_t q_at = smem_u32(smem) + L::oQ + t * L::kTile + (warp & 3) * 4096;
@@ -521,6 +535,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
       bool live;
       {
         const TileUnit x = *ux;
+        if (REP == 2 && unit > 0 && !mbar_wait_warp<true>(b.rep_done, (unit - 1) & 1, wd)) break;
         const int row = x.row0 + t * 128 + rl, qi = row / g.G;
         lim = unit_limit(g, x, t * 128 + rl);
         // The warp's 32 rows of queries to fp16, scaled by a power of two each, into the
@@ -532,8 +547,8 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         if (lane == 0) mbar_arrive(b.qfull + t);
         live = __any_sync(0xffffffffu, lim > 0);  // rows of this warp see keys
         // rows that stand for no query (their q is zero) do not make a step an edge
-        low = __reduce_min_sync(0xffffffffu, qi < x.ql ? lim : 0x7fffffff) - (x.first << g.log2_keys);
-        lim -= x.first << g.log2_keys;  // both from here on relative to the step's first key
+        low = __reduce_min_sync(0xffffffffu, qi < x.ql ? lim : 0x7fffffff) - (x.first << g.log2_keys) - col0;
+        lim -= (x.first << g.log2_keys) + col0;  // both from here on relative to the step's first key of these columns
       }
       float m = -INFINITY, l = 0.f;
       bool ok = true;
@@ -547,21 +562,21 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         if (live) {
           // constants of the step's groups of 16 columns (plain loads, free to move ahead of
           // the stores to TMEM below)
-          const float4* const scp = reinterpret_cast<const float4*>(smem + L::oScales + (step_n % kScaleSlots) * 128);
+          const float4* const scp = reinterpret_cast<const float4*>(smem + L::oScales + (step_n % kScaleSlots) * 128) + col0 / 16;
           auto sc = [&](int i) { return scp[i]; };
           // The whole row at once, held: a round trip to TMEM takes about 300 cycles while
           // products run, whatever it brings.
-          uint32_t v[4][32];
+          uint32_t v[kChunks][32];
 #pragma unroll
-          for (int c = 0; c < 4; ++c) tmem_ld32(s_tm + c * 32, v[c]);
+          for (int c = 0; c < kChunks; ++c) tmem_ld32(s_tm + col0 + c * 32, v[c]);
           // whether every row sees every key, and every page was read and counts
-          const bool plain = kKeys <= low && !__any_sync(0xffffffffu, sc(lane & 7).w != 1.f);
+          const bool plain = kCols <= low && !__any_sync(0xffffffffu, sc(lane & (kCols / 16 - 1)).w != 1.f);
           tmem_wait_ld();
 #pragma unroll
-          for (int c = 0; c < 4; ++c) reg_fence(v[c]);
+          for (int c = 0; c < kChunks; ++c) reg_fence(v[c]);
           if (!plain) {
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < kCols / 16; ++u) {
               const int lim16 = sc(u).w < 0.f ? 0 : lim - u * 16;
 #pragma unroll
               for (int q = 0; q < 16; ++q)
@@ -572,7 +587,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
           constexpr int kG = P16 ? 16 : 32;  // columns that share their scales
           float tmax = -INFINITY;
 #pragma unroll
-          for (int u = 0; u < kKeys / kG; ++u) {
+          for (int u = 0; u < kCols / kG; ++u) {
             const float4 f = sc(u * (kG / 16));
             tmax = fmaxf(tmax, fmaf(largest_of<kG>(v[u * kG / 32], (u * kG) & 31), fmaxf(rf * f.x, 1e-37f), f.y));
           }
@@ -584,15 +599,25 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
           const float base = (m == -INFINITY ? 0.f : m) - kBias;
           // the weights, over the first half of the score columns
 #pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            const float4 f = sc(P16 ? u : u & 6);
-            uint32_t p[8];
-            l = fmaf(weigh16(v[u >> 1], (u & 1) * 16, fmaxf(rf * f.x, 1e-37f), f.y - base, p), f.z, l);
-            if (!plain && f.w == 0.f) {  // a page of zeros
+          for (int c = 0; c < kChunks; ++c) {
+            uint32_t p[2][8];
+            float part[2];
 #pragma unroll
-              for (int q = 0; q < 8; ++q) p[q] = 0u;
+            for (int u = 0; u < 2; ++u) {
+              const float4 f = sc(c * 2 + (P16 ? u : 0));
+              part[u] = f.z * weigh16(v[c], u * 16, fmaxf(rf * f.x, 1e-37f), f.y - base, p[u]);
+              if (!plain && f.w == 0.f) {  // a page of zeros
+#pragma unroll
+                for (int q = 0; q < 8; ++q) p[u][q] = 0u;
+              }
             }
-            tmem_st8(s_tm + u * 8, p);
+            l += part[0] + part[1];
+            tmem_st8x2(s_tm + col0 / 2 + c * 16, p);
+          }
+          if constexpr (REP == 2) {  // the other copy's keys
+            const uint32_t none[2][8] = {};
+#pragma unroll
+            for (int c = 0; c < kChunks; ++c) tmem_st8x2(s_tm + (kCols - col0) / 2 + c * 16, none);
           }
           if (moved && j > 0) {  // the tile's last P V is done before O is rescaled
             const int kp = task - NQ;
@@ -623,6 +648,59 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
       // ---------------------------------------------------------- epilogue
       if (!mbar_wait_warp<true>(b.odone + ((task - NQ) & 1), ((task - NQ) >> 1) & 1, wd)) break;
       tc_fence_after();
+      const uint32_t o_tm = lane_base + L::cO + t * D;
+      // rows leave through boxes of 4 KB in the tile of queries, which is done with: this warp's
+      // own part of it; REP = 2: the places where the other copy left them
+      const uint32_t box = REP == 2 ? smem_u32(smem) + L::oQ + pair * (L::kTile / 2) : q_at;
+      float f0 = 1.f, f1 = 0.f;  // REP = 2: what both copies' O are multiplied by
+      if constexpr (REP == 2) {
+        if (rep == 1) {
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(box + lane * 8), "f"(m), "f"(l) : "memory");
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b.rep_out + pair);
+          if (!mbar_wait_warp<true>(b.rep_in + pair, unit & 1, wd)) break;
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(o_tm + c * 32, o);
+            tmem_wait_ld();
+            reg_fence(o);
+#pragma unroll
+            for (int v = 0; v < 8; ++v)
+              st_shared_v4(box + c * 4096 + lane * 128 + ((v ^ (lane & 7)) << 4), o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+          }
+          __syncwarp();
+          if (lane == 0) mbar_arrive(b.rep_out + pair);
+          tc_fence_before();
+          continue;
+        }
+        if (!mbar_wait_warp<true>(b.rep_out + pair, 0, wd)) break;
+        const uint2 other = lds64(box + lane * 8);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(b.rep_in + pair);
+        const float M = fmaxf(m, __uint_as_float(other.x)), base = M == -INFINITY ? 0.f : M;
+        f0 = ex2(m - base);
+        f1 = ex2(__uint_as_float(other.x) - base);
+        l = l * f0 + __uint_as_float(other.y) * f1;
+        m = M;
+        if (!mbar_wait_warp<true>(b.rep_out + pair, 1, wd)) break;
+      }
+      // 32 channels of the row's O, from column 32 c
+      auto read_o = [&](int c, uint32_t (&o)[32]) {
+        tmem_ld32(o_tm + c * 32, o);
+        tmem_wait_ld();
+        reg_fence(o);
+        if constexpr (REP == 2) {
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const uint4 w = lds128(box + c * 4096 + lane * 128 + ((v ^ (lane & 7)) << 4));
+            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              o[4 * v + q] = __float_as_uint(__uint_as_float(o[4 * v + q]) * f0 + __uint_as_float(ww[q]) * f1);
+          }
+        }
+      };
       const TileUnit x = *ux;
       const int r = t * 128 + rl, row = x.row0 + r, qi = row / g.G, head = x.h * g.G + (row - qi * g.G);
       if (!INT8 && *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4) < unit_limit(g, x, r))
@@ -631,9 +709,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         l = 0.f;
         m = -INFINITY;
       }
-      // rows leave through this warp's part of the tile of queries, which is done with
       const bool none = l == 0.f, row_ok = qi < g.N;
-      const uint32_t o_tm = lane_base + L::cO + t * D;
       if (x.first == 0 && x.seen_last < 0) {  // the whole unit
         const float inv = none ? 0.f : 1.f / l;
         uint16_t* const dst = a.o + x.b * a.so.b + static_cast<long long>(head) * a.so.h + qi * a.so.n;
@@ -643,9 +719,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             uint32_t o[32];
-            tmem_ld32(o_tm + c * 64 + e * 32, o);
-            tmem_wait_ld();
-            reg_fence(o);
+            read_o(c * 2 + e, o);
 #pragma unroll
             for (int v = 0; v < 4; ++v) {
               uint32_t hw[4];
@@ -655,7 +729,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
               w[e * 4 + v] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
             }
           }
-          store_rows(q_at, w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
+          store_rows(box + (REP == 2 ? c * 8192 : 0), w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
         }
         if (row_ok)
           a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
@@ -668,18 +742,17 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
-          tmem_ld32(o_tm + c * 32, o);
-          tmem_wait_ld();
-          reg_fence(o);
+          read_o(c, o);
           uint4 w[8];  // rows that see nothing leave zeros: their accumulators hold whatever P was
 #pragma unroll
           for (int v = 0; v < 8; ++v)
             w[v] = none ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-          store_rows(q_at, w, row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 32) : nullptr, lane);
+          store_rows(box + (REP == 2 ? c * 4096 : 0), w, row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 32) : nullptr, lane);
         }
       }
-      __syncwarp();      // the box has been read
+      __syncwarp();       // the boxes have been read
       tc_fence_before();  // O is read before the next unit's P V
+      if (REP == 2 && lane == 0) mbar_arrive(b.rep_done);
     }
   }
 
@@ -691,23 +764,27 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   }
 }
 
-template <int D, int NQ, bool INT8, bool P16>
+template <int D, int NQ, int REP, bool INT8, bool P16>
 cudaError_t launch_tile_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
   using L = TileLayout<D, NQ>;
-  auto kern = cache_attn_tile_kernel<D, NQ, INT8, P16>;
+  auto kern = cache_attn_tile_kernel<D, NQ, REP, INT8, P16>;
   static std::atomic<unsigned long long> smem_set{0};
   const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(kern), L::kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(ctas), dim3(L::kThreads), L::kSmem, stream, a, g);
 }
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool P16>
 cudaError_t launch_tile_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  if (a.c.page == 16)
-    return g.rows == 256 ? launch_tile_variant<D, 2, INT8, true>(a, g, ctas, stream)
-                         : launch_tile_variant<D, 1, INT8, true>(a, g, ctas, stream);
-  return g.rows == 256 ? launch_tile_variant<D, 2, INT8, false>(a, g, ctas, stream)
-                       : launch_tile_variant<D, 1, INT8, false>(a, g, ctas, stream);
+  if (g.rows == 64) return launch_tile_variant<D, 1, 2, INT8, P16>(a, g, ctas, stream);
+  return g.rows == 128 ? launch_tile_variant<D, 1, 1, INT8, P16>(a, g, ctas, stream)
+                       : launch_tile_variant<D, 2, 1, INT8, P16>(a, g, ctas, stream);
+}
+
+template <int D, bool INT8>
+cudaError_t launch_tiles(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+  return a.c.page == 16 ? launch_tile_rows<D, INT8, true>(a, g, ctas, stream)
+                        : launch_tile_rows<D, INT8, false>(a, g, ctas, stream);
 }
 
 }  // namespace

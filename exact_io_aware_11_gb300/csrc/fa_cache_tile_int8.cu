@@ -5,7 +5,7 @@
 namespace fa {
 
 cudaError_t launch_cache_attention_tiles_int8(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  return a.c.d == 128 ? launch_tile_rows<128, true>(a, g, ctas, stream) : launch_tile_rows<64, true>(a, g, ctas, stream);
+  return a.c.d == 128 ? launch_tiles<128, true>(a, g, ctas, stream) : launch_tiles<64, true>(a, g, ctas, stream);
 }
 
 }  // namespace fa
