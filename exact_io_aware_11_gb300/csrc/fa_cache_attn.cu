@@ -129,9 +129,9 @@ __device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], bool gone, in
 }
 
 // The producer warp: every step of the CTA's run, a stage each. Lane i < 8 looks
-// after the step's i-th group of 16 keys: its page id is loaded two steps ahead,
-// the page's scales one step ahead, and the first lane of each page copies its
-// rows (the pages' K and V lie in rows of d bytes of one tensor map each).
+// after the step's i-th group of 16 keys: its page id is loaded three steps ahead,
+// the page's scales two steps ahead (one step is less than their way from memory),
+// and the first lane of each page copies its rows (the pages' K and V lie in rows of d bytes of one tensor map each).
 template <int D, int NT>
 __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor ld, uint8_t* smem,
                                         uint64_t* full, uint64_t* empty, const Watchdog& wd, int lane) {
@@ -144,9 +144,10 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
   struct Step {
     bool live, want;  // within the run; the group holds keys that are seen
     int pid, h, row;  // row: of the page, where the step's rows start
+    float ks, vs;
   };
   auto look = [&]() {  // the cursor's step, then on
-    Step s{!ld.done(g), false, -1, 0, 0};
+    Step s{!ld.done(g), false, -1, 0, 0, -1.f, -1.f};
     if (s.live) {
       const int key = (ld.step << g.log2_keys) + lane * 16;
       s.want = group && key < ld.x.seen;
@@ -157,22 +158,21 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
     }
     return s;
   };
-  auto scales = [&](Step& s, float& ks, float& vs) {
+  auto scales = [&](Step& s) {
     const bool good = s.want && s.pid >= 0 && s.pid < c.num_pages;
     if (s.want && !good) report_bad_page(a.status);
     s.want = good;
-    ks = vs = -1.f;
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
-      ks = __ldg(c.scale[0] + ph);
-      vs = __ldg(c.scale[1] + ph);
+      s.ks = __ldg(c.scale[0] + ph);
+      s.vs = __ldg(c.scale[1] + ph);
     }
   };
-  float ks, vs;
-  Step now = look();
-  scales(now, ks, vs);
-  Step next = look();
+  Step now = look(), next = look();
+  scales(now);
+  scales(next);
+  Step third = look();
   int n = 0;  // steps issued
   for (; now.live; ++n) {
     const int st = n % kStages;
@@ -186,7 +186,7 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
     }
     const int copies = __popc(__ballot_sync(0xffffffffu, leader && now.want));
     if (group)
-      *reinterpret_cast<float2*>(smem + L::kScales + st * 64 + lane * 8) = make_float2(ks, vs);
+      *reinterpret_cast<float2*>(smem + L::kScales + st * 64 + lane * 8) = make_float2(now.ks, now.vs);
     __syncwarp();
     if (lane == 0) {
       if (copies > 0)
@@ -195,8 +195,9 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
         mbar_arrive(full + st);
     }
     now = next;
-    scales(now, ks, vs);
-    next = look();
+    next = third;
+    scales(next);
+    third = look();
   }
   // let every copy in flight land before the CTA can exit
   for (int i = max(0, n - kStages); i < n; ++i)

@@ -37,7 +37,8 @@ struct TileLayout {
   // NQ = 2: 12 warps, so that a softmax thread can hold a step's 128 scores (168 registers)
   static constexpr int kConvWarps = NQ == 2 ? 2 : 4;
   static constexpr int kConv = 4 * NQ, kMma = kConv + kConvWarps, kLoad = kMma + 1;  // warps
-  static constexpr int kThreads = (kLoad + 1) * 32;
+  static constexpr int kLoaders = NQ == 1 ? 2 : 1;  // NQ = 1: a warp each for K and V
+  static constexpr int kThreads = (kLoad + kLoaders) * 32;
   static constexpr int kTile = (D / 64) * kChunkBytes;  // one fp16 tile
   static constexpr int kRaw = kKeys * D;                // K or V codes of a step
   static constexpr int kStg = D == 128 ? (NQ == 2 ? 2 : 4) : 8;  // raw tiles in flight
@@ -45,11 +46,11 @@ struct TileLayout {
   static constexpr int oScales = oRaw + kStg * kRaw;    // [slots][8 groups] ks, log2 vs, 1 / vs, 1 (0: V of zeros, -1: not read)
   static constexpr int oNan = oScales + kScaleSlots * 128;  // [8] first NaN key of V per unit
   // Slots for the descriptions of units (TileUnit). Units have a step at least. The producer
-  // describes a unit two steps before it issues K(n), for which K(n - kStg / 2) is
+  // describes a unit three steps before it issues K(n), for which K(n - kStg / 2) is
   // converted, so the scores of the step two before that are formed, so the weights of
   // the step NQ = 1: two, NQ = 2: one before that are done; that step's unit may still be read.
   static constexpr int kUnits = kStg <= 2 ? 8 : 16;
-  static_assert(2 + kStg / 2 + 2 + (NQ == 1 ? 2 : 1) < kUnits, "a unit's description outlives its use");
+  static_assert(3 + kStg / 2 + 2 + (NQ == 1 ? 2 : 1) < kUnits, "a unit's description outlives its use");
   static constexpr int oUnits = oNan + 32;
   static constexpr int oBars = oUnits + kUnits * 32;
   static constexpr int kBars = 2 * kStg + 17 + kUnits + 5;
@@ -80,13 +81,15 @@ struct TileBars {
 };
 
 // Producer: the raw tiles K(n), V(n) of every step, as pages. Lane i < 8 looks
-// after the step's i-th group of 16 keys (page id two steps ahead, scales one).
-// It also describes the units to the other warps (TileLayout::kUnits), and
+// after the step's i-th group of 16 keys (page id three steps ahead, scales two: one step is
+// less than their way from memory).
+// With NQ = 1 K and V have a warp each: a step of 16-token pages is 16 copies, which take one
+// warp some 75 cycles each to issue. K's also describes the units to the other warps (TileLayout::kUnits), and
 // writes the record of a cut unit that the CTA ends, well before that end.
 template <int D, int NQ>
 __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor ld,
                                              const AttnShare& share, uint8_t* smem, const TileBars& b,
-                                             const Watchdog& wd, int lane) {
+                                             const Watchdog& wd, int loader, int lane) {
   using L = TileLayout<D, NQ>;
   const CacheView& c = a.c;
   const int rows = min(c.page, kKeys), per_page = rows >> 4;
@@ -94,6 +97,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
   struct Step {
     bool live, want;
     int pid, h, row;
+    float ks, vs;
   };
   int units = 0;
   bool first = true;
@@ -105,9 +109,9 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     ++units;
   };
   auto look = [&]() {
-    Step s{!ld.done(g), false, -1, 0, 0};
+    Step s{!ld.done(g), false, -1, 0, 0, 1.f, 1.f};
     if (s.live) {
-      if (first || ld.step == 0) {
+      if (loader == 0 && (first || ld.step == 0)) {
         const int steps = ld.run(g);
         const bool ends = ld.step + steps == ld.x.steps;
         describe(TileUnit{ld.x.b, ld.x.row0, ld.h, ld.step, steps, ld.x.kv, ld.x.ql,
@@ -125,28 +129,29 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     }
     return s;
   };
-  auto scales = [&](Step& s, float& ks, float& vs) {
+  auto scales = [&](Step& s) {
     const bool good = s.want && s.pid >= 0 && s.pid < c.num_pages;
     if (s.want && !good) report_bad_page(a.status);
     s.want = good;
-    ks = vs = 1.f;
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
-      ks = __ldg(c.scale[0] + ph);
-      vs = __ldg(c.scale[1] + ph);
+      s.ks = __ldg(c.scale[0] + ph);
+      s.vs = __ldg(c.scale[1] + ph);
     }
   };
-  float ks, vs;
-  Step now = look();
-  scales(now, ks, vs);
-  Step next = look();
-  int tile = 0;  // raw tiles issued
+  Step now = look(), next = look();
+  scales(now);
+  scales(next);
+  Step third = look();
+  int tile = 0, issued = 0;  // raw tiles: K(n) is 2 n, V(n) 2 n + 1
   bool ok = true;
   for (int n = 0; now.live && ok; ++n) {
     const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, leader && now.want)) * rows * D;
 #pragma unroll
     for (int kv = 0; kv < 2; ++kv) {
+      if (L::kLoaders == 2 && kv != loader) continue;
+      tile = 2 * n + kv;
       const int st = tile % L::kStg;
       if (tile >= L::kStg && !mbar_wait_warp(b.raw_empty + st, ((tile / L::kStg) - 1) & 1, wd)) {
         ok = false;
@@ -155,9 +160,9 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       if (leader && now.want)
         tma_load_2d(smem + L::oRaw + st * L::kRaw + lane * 16 * D, &a.tm[kv], b.raw_full + st, now.row);
       if (kv == 0 && group) {
-        const float v = fmaxf(vs, kMinScale);
+        const float v = fmaxf(now.vs, kMinScale);
         *reinterpret_cast<float4*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16) =
-            make_float4(ks, __log2f(v), 1.f / v, !now.want ? -1.f : vs > kMinScale ? 1.f : 0.f);
+            make_float4(now.ks, __log2f(v), 1.f / v, !now.want ? -1.f : now.vs > kMinScale ? 1.f : 0.f);
       }
       __syncwarp();
       if (lane == 0) {
@@ -166,15 +171,16 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
         else
           mbar_arrive(b.raw_full + st);
       }
-      ++tile;
+      issued = tile + 1;
     }
     now = next;
-    scales(now, ks, vs);
-    next = look();
+    next = third;
+    scales(next);
+    third = look();
   }
-  describe(TileUnit{0, 0, 0, 0, 0, 0, 0, 0});
-  for (int i = max(0, tile - L::kStg); i < tile; ++i)  // copies in flight land before the CTA exits
-    mbar_wait_drain(b.raw_full + i % L::kStg, (i / L::kStg) & 1, a.wait_limit);
+  if (loader == 0) describe(TileUnit{0, 0, 0, 0, 0, 0, 0, 0});
+  for (int i = max(0, issued - L::kStg); i < issued; ++i)  // copies in flight land before the CTA exits
+    if (L::kLoaders == 1 || (i & 1) == loader) mbar_wait_drain(b.raw_full + i % L::kStg, (i / L::kStg) & 1, a.wait_limit);
 }
 
 // Converters: each warp takes its 32 (64) rows of every raw tile, 16 codes a lane at a
@@ -454,9 +460,9 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{a.wait_limit, a.status, abort_flag};
-  if (warp == L::kLoad) {
-    if (g.split && lane == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    tile_produce<D, NQ>(a, g, cur, share, smem, b, wd, lane);
+  if (warp >= L::kLoad) {
+    if (g.split && warp == L::kLoad && lane == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    tile_produce<D, NQ>(a, g, cur, share, smem, b, wd, warp - L::kLoad, lane);
   } else if (warp == L::kMma) {
     // ------------------------------------------------------------ MMA issuer (whole warp)
     constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
