@@ -315,8 +315,8 @@ def cache_write(cache: KVCache, k, v, page_table, start, count=None, stream=None
     """Quantises rows n < count[b] of k, v [B, H, N, d] into the cache at tokens
     start[b] + n (fa_cache_write). start, count: int32 [B]; start=None means 0,
     count=None all N rows. Where a page is shared by the old and the new tokens of a
-    sequence, its older rows move to the page's new scale if that grew. Two
-    sequences of one call must not write the same page."""
+    sequence, its older rows move to the page's new scale if that grew. The entries of
+    page_table that a call writes through must name different pages."""
     _on(_cache_rows, _check_cache(cache), stream, "fa_cache_write", cache, k, v, page_table, start, count)
 
 

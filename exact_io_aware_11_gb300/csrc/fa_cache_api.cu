@@ -65,8 +65,9 @@ int rotary(const void* q, void* q_out, const void* k, void* k_out, int B, int Hq
   if (opt->turns == nullptr || !aligned(opt->turns, 8)) return FA_ERR_INVALID_ARG;
   if (!aligned(opt->positions, 4) || opt->pos_stride_b < 0 || opt->pos_stride_n < 0) return FA_ERR_INVALID_ARG;
   const size_t turns_bytes = static_cast<size_t>(opt->rotary_dim) / 2 * 8;
-  const long long lim = 1LL << 40;
+  const long long lim = 1LL << 31;  // their products with B and N fit 64 bits
   if (opt->pos_stride_b > lim || opt->pos_stride_n > lim) return FA_ERR_INVALID_ARG;
+  if (opt->positions == nullptr && opt->offset > INT_MAX - (N - 1)) return FA_ERR_INVALID_ARG;
   const size_t pos_bytes = static_cast<size_t>((B - 1) * opt->pos_stride_b + (N - 1) * opt->pos_stride_n + 1) * 4;
   Tensor in[2], out[2];
   const int tensors = Hk > 0 ? 2 : 1;
@@ -132,7 +133,7 @@ int check_cache(const fa_cache* c, const int32_t* table, int64_t table_stride, i
       !aligned(table, 4))
     return FA_ERR_INVALID_ARG;
   if (width < 1 || table_stride < 0 || table_stride > (1LL << 40) ||
-      static_cast<long long>(width) * c->page_size > INT_MAX - 256)
+      static_cast<long long>(width) * c->page_size > INT_MAX - 1024)
     return FA_ERR_INVALID_ARG;
   v->code[0] = static_cast<uint8_t*>(c->k);
   v->code[1] = static_cast<uint8_t*>(c->v);
@@ -213,11 +214,11 @@ int check_attention_sizes(const fa_cache* cache, int B, int Hq, int N, int table
   if (st != FA_OK) return st;
   if (B < 1 || B > 65535 || Hq < 1 || Hq > 65535 || N < 1 || table_width < 1 || Hq % cache->H != 0)
     return FA_ERR_INVALID_ARG;
-  if (static_cast<long long>(table_width) * cache->page_size > INT_MAX - 256) return FA_ERR_INVALID_ARG;
+  if (static_cast<long long>(table_width) * cache->page_size > INT_MAX - 1024) return FA_ERR_INVALID_ARG;
   // rows of the pool are coordinates of its tensor map
   if (static_cast<long long>(cache->num_pages) * cache->H > INT_MAX / cache->page_size) return FA_ERR_INVALID_ARG;
   const long long rows = static_cast<long long>(N) * (Hq / cache->H);
-  if (rows > INT_MAX - 256 || static_cast<long long>(B) * (rows / 8 + 1) > INT_MAX) return FA_ERR_INVALID_ARG;
+  if (rows > INT_MAX - 1024 || static_cast<long long>(B) * (rows / 8 + 1) > INT_MAX - 1024) return FA_ERR_INVALID_ARG;
   return FA_OK;
 }
 
@@ -264,7 +265,8 @@ int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache
   if ((st = check_attention_sizes(cache, B, Hq, N, opt->table_width)) != FA_OK) return st;
   if (opt->dtype != FA_BF16 && opt->dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
   if (opt->causal != 0 && opt->causal != 1) return FA_ERR_INVALID_ARG;
-  if (!std::isfinite(opt->scale) || !(opt->scale > 0.f)) return FA_ERR_INVALID_ARG;
+  const float scale_log2 = opt->scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2) || !(opt->scale > 0.f)) return FA_ERR_INVALID_ARG;
   if (opt->kv_len == nullptr || !aligned(opt->kv_len, 4) || !aligned(opt->q_len, 4)) return FA_ERR_INVALID_ARG;
   if (lse == nullptr || !aligned(lse, 16)) return FA_ERR_INVALID_ARG;
   if ((workspace == nullptr && workspace_bytes != 0) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
@@ -298,7 +300,7 @@ int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache
   a.G = Hq / cache->H;
   a.fp16 = opt->dtype == FA_FP16;
   a.causal = opt->causal;
-  a.scale_log2 = opt->scale * 1.4426950408889634f;
+  a.scale_log2 = scale_log2;
   a.kv_len = opt->kv_len;
   a.q_len = opt->q_len;
   a.wait_limit = kWaitLimitCycles;

@@ -338,7 +338,8 @@ typedef enum { FA_BF16 = 0, FA_FP16 = 1 } fa_dtype;
  *   factor      : finite; multiplies cos and sin (1, or the attention factor
  *                 of a scheme for long contexts).
  *   positions   : DEVICE int32, element (b, n) at b*pos_stride_b + n*pos_stride_n
- *                 (strides >= 0; 0 shares one row), or NULL: offset + n.
+ *                 (strides 0 .. 2^31; 0 shares one row), or NULL: offset + n, which
+ *                 must fit 32 bits.
  *   q_stride .. k_out_stride : {batch, head, row} of each tensor. */
 typedef struct fa_rotary_options {
   int rotary_dim, interleaved, dtype;
@@ -410,8 +411,8 @@ typedef struct fa_cache_range {
  * ties to even. A power of two makes the division exact, and moving an e4m3 row
  * only shifts its exponent (values that become subnormal are rounded
  * again). Infinities are held as the largest code; NaN stays NaN in e4m3 and
- * becomes 0 in int8. Rows behind the last token keep what they hold. Two
- * sequences of one call must not write the same page. */
+ * becomes 0 in int8. Rows behind the last token keep what they hold. The page
+ * table entries that a call writes through must name different pages. */
 int fa_cache_write(const fa_cache* cache, const void* k, const void* v, int B, int N,
                    const fa_cache_range* range, struct CUstream_st* stream);
 
@@ -429,7 +430,7 @@ int fa_cache_read(const fa_cache* cache, void* k, void* v, int B, int N,
  *   causal : 1: query row i sits at token kv_len[b] - q_len[b] + i and sees
  *            the tokens up to it (the newest tokens' queries, their keys
  *            already written); 0: every row sees all kv_len[b] tokens;
- *   scale  : finite, > 0;  q_stride, o_stride : {batch, head, row}. */
+ *   scale  : > 0, scale * log2(e) finite;  q_stride, o_stride : {batch, head, row}. */
 typedef struct fa_cache_attention_options {
   const int32_t* page_table;
   int64_t table_stride;

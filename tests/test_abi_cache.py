@@ -50,6 +50,8 @@ def rotary(L, name="fa_rotary_fwd", **kw):
     (dict(B=0), 1), (dict(N=0), 1), (dict(Hq=0), 1), (dict(Hk=-1), 1), (dict(B=65536), 1), (dict(d=96), 2), (dict(dtype=2), 2),
     (dict(r=0), 1), (dict(r=66), 1), (dict(r=63), 1), (dict(inter=2), 1), (dict(factor=float("inf")), 1), (dict(pb=-1), 1),
     (dict(sq=(2048, 512, 60)), 1), (dict(sq=(2048, 64, 64)), 1),
+    (dict(pos=None, off=2 ** 31 - 8), OK), (dict(pos=None, off=2 ** 31 - 7), 1),  # the last row's position, N = 8
+    (dict(pb=2 ** 31 + 1), 1), (dict(pn=2 ** 31 + 1), 1), (dict(off=2 ** 31 - 1), OK),
 ])
 @pytest.mark.parametrize("name", ["fa_rotary_fwd", "fa_rotary_bwd"])
 def test_rotary(L, name, kw, expect):
@@ -111,7 +113,7 @@ def attention(L, **kw):
     (dict(), OK), (dict(ql=None, causal=0), OK), (dict(ws=None, wsn=0), OK), (dict(wsn=0), OK), (dict(Hq=2), OK),
     (dict(cache=False), 1), (dict(opt=False), 1), (dict(q=None), 1), (dict(o=None), 1), (dict(lse=None), 1), (dict(kvl=None), 1),
     (dict(tab=None), 1), (dict(Hq=7), 1), (dict(Hq=0), 1), (dict(B=0), 1), (dict(N=0), 1), (dict(N=1 << 30), 1), (dict(tw=0), 1),
-    (dict(tw=1 << 27), 1), (dict(causal=2), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(dtype=3), 2),
+    (dict(tw=1 << 27), 1), (dict(causal=2), 1), (dict(scale=0.0), 1), (dict(scale=float("nan")), 1), (dict(scale=3e38), 1), (dict(dtype=3), 2),
     (dict(page=8), 2), (dict(cd=32), 2), (dict(fmt=-1), 2), (dict(ws=None), 1), (dict(ws=A + 10 * SPAN + 8), 1),
     (dict(o=A + 7 * SPAN), 1), (dict(lse=A + 8 * SPAN), 1), (dict(o=A), 1), (dict(lse=A + 4 * SPAN), 1), (dict(ws=A + 7 * SPAN), 1),
     (dict(ws=A + 9 * SPAN), 1), (dict(ws=A + SPAN), 1), (dict(o=A + 5 * SPAN), 1), (dict(lse=A + 6 * SPAN), 1),
