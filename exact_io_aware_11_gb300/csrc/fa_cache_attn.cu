@@ -316,7 +316,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const uint32_t kt = smem_u32(smem) + stage * L::kStage, vt = kt + L::kMat;
         const uint4 sc = lds128(smem_u32(smem) + L::kScales + stage * 64 + warp * 16);
         const float ks[2] = {__uint_as_float(sc.x), __uint_as_float(sc.z)};
-        const float vs[2] = {fmaxf(__uint_as_float(sc.y), kMinScale), fmaxf(__uint_as_float(sc.w), kMinScale)};
+        const bool zero[2] = {!(__uint_as_float(sc.y) > kMinScale), !(__uint_as_float(sc.w) > kMinScale)};
+        const float vs[2] = {zero[0] ? kZeroScale : __uint_as_float(sc.y), zero[1] ? kZeroScale : __uint_as_float(sc.w)};
         // S^T = K Q^T: keys gq, gq + 8 of each group, queries 2t, 2t + 1
         float s[2][NT][4];
 #pragma unroll
@@ -420,11 +421,10 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
           uint32_t p0[NT], p1[NT];
-          const bool zero = !(vs[u] > kMinScale);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            p0[n] = transpose8x8(zero ? 0u : pack_half(s[u][n][0], s[u][n][1]));
-            p1[n] = transpose8x8(zero ? 0u : pack_half(s[u][n][2], s[u][n][3]));
+            p0[n] = transpose8x8(zero[u] ? 0u : pack_half(s[u][n][0], s[u][n][1]));
+            p1[n] = transpose8x8(zero[u] ? 0u : pack_half(s[u][n][2], s[u][n][3]));
           }
           uint32_t v[4][D / 32];
 #pragma unroll

@@ -12,7 +12,11 @@ namespace fa {
 constexpr float kLn2Cache = 0.69314718055994530942f;
 constexpr float kSlack = 4.f;                // log2 units a weight may stand above the reference
 constexpr float kBias = 15.f - kSlack;       // weights are at most 2^15
-constexpr float kMinScale = 0x1p-100f;       // a page whose V scale is below it counts as zeros
+constexpr float kMinScale = 0x1p-100f;       // a page whose V scale is not above it counts as zeros
+// V scale that stands in for a page of zeros, whose weights count in the sum alone. A weight whose
+// exponent lies 2^-137 below the reference is lost to the sum as well, so the stand-in is
+// near the scales that occur: pages of zeros keep 2^-47 of the sum beside scales up to 2^30.
+constexpr float kZeroScale = 0x1p-60f;
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {
   if (fp16) return __half22float2(*reinterpret_cast<__half2*>(&w));

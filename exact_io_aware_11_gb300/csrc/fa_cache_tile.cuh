@@ -160,9 +160,10 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       if (leader && now.want)
         tma_load_2d(smem + L::oRaw + st * L::kRaw + lane * 16 * D, &a.tm[kv], b.raw_full + st, now.row);
       if (kv == 0 && group) {
-        const float v = fmaxf(now.vs, kMinScale);
+        const bool counts = now.vs > kMinScale;
+        const float v = counts ? now.vs : kZeroScale;
         *reinterpret_cast<float4*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16) =
-            make_float4(now.ks, __log2f(v), 1.f / v, !now.want ? -1.f : now.vs > kMinScale ? 1.f : 0.f);
+            make_float4(now.ks, __log2f(v), 1.f / v, !now.want ? -1.f : counts ? 1.f : 0.f);
       }
       __syncwarp();
       if (lane == 0) {

@@ -264,6 +264,19 @@ def test_scales_far_apart(fa):
         check_attention(fa, m, queries(1, 2, 1, 64, "bf16", 9), lens, scale=1.0)
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("d,G,N", [(128, 1, 1), (64, 6, 2), (128, 8, 4), (64, 2, 60), (128, 4, 50)])
+def test_pages_of_zeros_beside_large_values(fa, d, G, N, fmt):
+    """Tokens whose V is zero take their share of the weights whatever the other pages' scale."""
+    page, W = 32, 9
+    cache = random_cache(fa, W, 2, page, d, fmt, seed=31)
+    cache.v_scale[:] = 2.0 ** 30
+    cache.v_scale[::2] = 0.0
+    cache.v_scale[1] = 2.0 ** -30
+    table = torch.arange(W, dtype=torch.int32, device="cuda")[None]
+    check_batch(fa, queries(1, 2 * G, N, d, "bf16", 32), cache, table, [W * page - 3], [N])
+
+
 @pytest.mark.parametrize("mul", [2.0 ** -60, 2.0 ** 90])
 def test_queries_far_from_one(fa, mul):
     """bf16 queries beyond fp16's range: the row's power of two takes them in."""
