@@ -30,6 +30,14 @@ __device__ __forceinline__ uint32_t pack16(float lo, float hi, bool fp16) {
   return fp16 ? pack_half(lo, hi) : pack_bf16(lo, hi);
 }
 
+// 16 bytes to shared memory, `bytes` of them (0 or 16) from p and zeros behind; and the wait
+// for all of the thread's copies.
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* p, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(__cvta_generic_to_global(p)), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a));

@@ -5,9 +5,10 @@
 // query row r / G of head r % G of the cache head's group of G. A unit's steps
 // are the key tiles its rows see (at least one, so that units without keys
 // still write their rows). All units' steps lie end to end, ordered by
-// (sequence, row tile), then head; CTA c of C takes T / C of the T steps, and one more if
-// c < T mod C, an equal share whatever the lengths. A unit cut by a boundary leaves parts in
-// the workspace: slot 2 c for the part CTA c starts in the middle of, slot
+// (sequence, row tile), then head, and before each unit's first a gap of `lead` steps: about
+// what it costs a CTA to begin one more unit (AttnPlan). CTA c of C takes T / C of the T
+// places, and one more if c < T mod C, an equal share whatever the lengths. A unit cut by a
+// boundary leaves parts in the workspace: slot 2 c for the part CTA c starts in the middle of, slot
 // 2 c + 1 for one it starts and does not finish. The CTA with a unit's last part
 // writes the unit's merge record.
 #pragma once
@@ -23,13 +24,14 @@ struct AttnGrid {
   int log2_keys;  // keys of a step
   int cap;        // tokens a page table row has room for
   int causal, split;
+  int lead;       // places without a step before each unit
   const int32_t* kv_len;
   const int32_t* q_len;
   // workspace (split only)
   int4* record;   // [C]: entry, head, first CTA of a cut unit that c ends; entry -1: none
   float* m_part;  // [2 C][rows]
   float* l_part;
-  float* o_part;  // [2 C][rows][D]
+  float* o_part;  // [2 C][rows][D]; tiles: [2 C][rows / 32][D / 4][32 rows][4]
 };
 
 // One (sequence, row tile).
@@ -57,8 +59,8 @@ __device__ __forceinline__ int attn_limit(const AttnGrid& g, const AttnEntry& x,
   return g.causal ? max(0, x.kv - x.ql + i + 1) : x.kv;
 }
 
-// A CTA's place in the list: unit (e, h) at `step`, `pos` steps from the
-// list's start, until `end`.
+// A CTA's place in the list: unit (e, h) at `step`, which is `pos` places from the
+// list's start; the CTA's run lasts until `end`.
 struct AttnCursor {
   AttnEntry x;
   int e, h, step;
@@ -83,6 +85,7 @@ struct AttnCursor {
   }
   __device__ __forceinline__ void next_unit(const AttnGrid& g) {
     step = 0;
+    pos += g.lead;
     if (++h == g.HK) {
       h = 0;
       if (++e < g.B * g.row_tiles) x = attn_entry(g, e);
@@ -90,9 +93,9 @@ struct AttnCursor {
   }
 };
 
-// The steps' division: CTA c starts at c * each + min(c, extra).
+// The places' division: CTA c starts at c * each + min(c, extra).
 struct AttnShare {
-  long long first;  // the first step of `entry`
+  long long first;  // the first place of `entry`
   long long each;
   int extra, ctas, entry;
   AttnEntry x;      // of `entry`
@@ -117,7 +120,7 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   long long mine = 0;
   for (int e = e0; e < e1; ++e) {
     own = attn_entry(g, e);
-    mine += own.steps;
+    mine += own.steps + g.lead;
   }
   long long incl = mine;
 #pragma unroll
@@ -147,7 +150,7 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   if (s0 >= p && s0 < p + mine * g.HK) {
     for (int e = e0; e < e1; ++e) {
       const AttnEntry x = per == 1 ? own : attn_entry(g, e);
-      const long long n = static_cast<long long>(x.steps) * g.HK;
+      const long long n = static_cast<long long>(x.steps + g.lead) * g.HK;
       if (s0 < p + n) {
         sh->entry = e;
         sh->first = p;
@@ -172,8 +175,11 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   if (cur.e < E) {
     cur.x = sh->x;
     const long long rem = s0 - sh->first;
-    cur.h = static_cast<int>(attn_div(rem, cur.x.steps));
-    cur.step = static_cast<int>(rem - static_cast<long long>(cur.h) * cur.x.steps);
+    const int places = cur.x.steps + g.lead;
+    cur.h = static_cast<int>(attn_div(rem, places));
+    const int at = static_cast<int>(rem - static_cast<long long>(cur.h) * places) - g.lead;
+    cur.step = max(0, at);
+    cur.pos += cur.step - at;
     if (!g.split && cur.step > 0) {  // the unit belongs to the CTA that it starts in
       cur.pos += cur.x.steps - cur.step;
       cur.next_unit(g);
@@ -184,7 +190,7 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   return cur;
 }
 
-// The CTA whose run holds step s.
+// The CTA whose run holds place s.
 __device__ __forceinline__ int attn_cta_of(long long s, const AttnShare& d) {
   const long long longer = d.extra * (d.each + 1);  // steps of the CTAs that have one more
   return static_cast<int>(s < longer ? attn_div(s, d.each + 1) : d.extra + attn_div(s - longer, d.each));
@@ -193,7 +199,7 @@ __device__ __forceinline__ int attn_cta_of(long long s, const AttnShare& d) {
 // Keys of a step and rows of a tile of the kernel that a call of `rows` = N * G
 // query rows per (sequence, cache head) takes, and its CTAs.
 struct AttnPlan {
-  int rows, log2_keys, ctas;
+  int rows, log2_keys, ctas, lead;
   long long units, cap_steps;
 };
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap);

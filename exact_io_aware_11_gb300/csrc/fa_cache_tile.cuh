@@ -176,7 +176,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     }
     now = next;
     next = third;
-    scales(next);
+    scales(next);  // before the next load of a page id: waiting for one waits for all of its kind
     third = look();
   }
   if (loader == 0) describe(TileUnit{0, 0, 0, 0, 0, 0, 0, 0});
@@ -209,146 +209,130 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
   int* const nan_key = reinterpret_cast<int*>(smem + L::oNan);
   int n = 0;  // steps converted
   for (int unit = 0;; ++unit) {
-  if (!mbar_wait_warp(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) return;
-  const TileUnit x = *reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32);
-  if (x.steps == 0) return;
-  // slot of the unit three on; the one five back, which used it, has ended (a unit
-  // has a step at least, and K(n) waits for the scores of step n - 2)
-  if (cw == 0 && lane == 0) nan_key[(unit + 3) & 7] = 0x7fffffff;
-  const int seen = x.seen_last & 0x7fffffff, low = unit_limit(g, x, 0);
-  int key0 = x.first << g.log2_keys;
-  for (const int end = n + x.steps; n < end; ++n, key0 += kKeys) {
+    if (!mbar_wait_warp(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) return;
+    const TileUnit x = *reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32);
+    if (x.steps == 0) return;
+    // slot of the unit three on; the one five back, which used it, has ended (a unit
+    // has a step at least, and K(n) waits for the scores of step n - 2)
+    if (cw == 0 && lane == 0) nan_key[(unit + 3) & 7] = 0x7fffffff;
+    const int seen = x.seen_last & 0x7fffffff, low = unit_limit(g, x, 0);
+    int key0 = x.first << g.log2_keys;
+    for (const int end = n + x.steps; n < end; ++n, key0 += kKeys) {
 #pragma unroll
-    for (int kv = 0; kv < 2; ++kv) {
-      const int tile = 2 * n + kv, st = tile % L::kStg, slot = n & 1;
-      if (!mbar_wait_warp(b.raw_full + st, (tile / L::kStg) & 1, wd)) return;
-      if (n >= 2 && !mbar_wait_warp((kv ? b.vempty : b.kempty) + slot, ((n >> 1) - 1) & 1, wd)) return;
-      const uint32_t src = smem_u32(smem) + L::oRaw + st * L::kRaw;
-      const uint32_t dst = smem_u32(smem) + (kv ? L::oV : L::oK) + slot * L::kTile;
-      bool check = false;
-      if (!INT8 && kv == 1) {
-        const float read = lane < 8 ? *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16 + 12) : 0.f;
-        check = key0 + kKeys > low || __any_sync(0xffffffffu, read < 0.f);
-      }
-      auto from = [&](int r) {
-        return lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
-      };
-      auto put = [&](const uint4& v, int r) {
-        uint32_t w[8];
-        decode4<INT8>(v.x, w[0], w[1]);
-        decode4<INT8>(v.y, w[2], w[3]);
-        decode4<INT8>(v.z, w[4], w[5]);
-        decode4<INT8>(v.w, w[6], w[7]);
-        const uint32_t row = dst + (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128;
-        const int unit16 = (ch & 3) * 2 ^ (r & 7);
-        st_shared_v4(row + (unit16 << 4), w[0], w[1], w[2], w[3]);
-        st_shared_v4(row + ((unit16 ^ 1) << 4), w[4], w[5], w[6], w[7]);
-      };
-      if (!check) {
-#pragma unroll 1
-        for (int i0 = 0; i0 < kPieces; i0 += D / 16) {
-          uint4 v[D / 16];
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) v[i] = from(row_of(i0 + i));
-#pragma unroll
-          for (int i = 0; i < D / 16; ++i) put(v[i], row_of(i0 + i));
+      for (int kv = 0; kv < 2; ++kv) {
+        const int tile = 2 * n + kv, st = tile % L::kStg, slot = n & 1;
+        if (!mbar_wait_warp(b.raw_full + st, (tile / L::kStg) & 1, wd)) return;
+        if (n >= 2 && !mbar_wait_warp((kv ? b.vempty : b.kempty) + slot, ((n >> 1) - 1) & 1, wd)) return;
+        const uint32_t src = smem_u32(smem) + L::oRaw + st * L::kRaw;
+        const uint32_t dst = smem_u32(smem) + (kv ? L::oV : L::oK) + slot * L::kTile;
+        bool check = false;
+        if (!INT8 && kv == 1) {
+          const float read = lane < 8 ? *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16 + 12) : 0.f;
+          check = key0 + kKeys > low || __any_sync(0xffffffffu, read < 0.f);
         }
-      } else {
+        auto from = [&](int r) {
+          return lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
+        };
+        auto put = [&](const uint4& v, int r) {
+          uint32_t w[8];
+          decode4<INT8>(v.x, w[0], w[1]);
+          decode4<INT8>(v.y, w[2], w[3]);
+          decode4<INT8>(v.z, w[4], w[5]);
+          decode4<INT8>(v.w, w[6], w[7]);
+          const uint32_t row = dst + (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128;
+          const int unit16 = (ch & 3) * 2 ^ (r & 7);
+          st_shared_v4(row + (unit16 << 4), w[0], w[1], w[2], w[3]);
+          st_shared_v4(row + ((unit16 ^ 1) << 4), w[4], w[5], w[6], w[7]);
+        };
+        if (!check) {
 #pragma unroll 1
-        for (int i = 0; i < kPieces; ++i) {
-          const int r = row_of(i), key = key0 + r;
-          const uint4 v = from(r);
-          const float read = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
-          uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
-          if (key >= low || read < 0.f) {
+          for (int i0 = 0; i0 < kPieces; i0 += D / 16) {
+            uint4 v[D / 16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-              w[k] &= ~nan;
-              any |= nan;
-            }
-            if (any != 0u && key < seen && !(read < 0.f)) atomicMin(nan_key + (unit & 7), key);
+            for (int i = 0; i < D / 16; ++i) v[i] = from(row_of(i0 + i));
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) put(v[i], row_of(i0 + i));
           }
-          put(make_uint4(w[0], w[1], w[2], w[3]), r);
+        } else {
+#pragma unroll 1
+          for (int i = 0; i < kPieces; ++i) {
+            const int r = row_of(i), key = key0 + r;
+            const uint4 v = from(r);
+            const float read = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
+            uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
+            if (key >= low || read < 0.f) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                w[k] &= ~nan;
+                any |= nan;
+              }
+              if (any != 0u && key < seen && !(read < 0.f)) atomicMin(nan_key + (unit & 7), key);
+            }
+            put(make_uint4(w[0], w[1], w[2], w[3]), r);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive((kv ? b.vfull : b.kfull) + slot);
+          mbar_arrive(b.raw_empty + st);
         }
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) {
-        mbar_arrive((kv ? b.vfull : b.kfull) + slot);
-        mbar_arrive(b.raw_empty + st);
-      }
     }
-  }
   }
 }
 
-// Loads a warp's 32 rows of queries (lane r knows row r's offset, -1: zeros) as whole rows,
-// D / 8 lanes to a row, and writes them as fp16 into the swizzled tile at `dst`. bf16 rows are
-// scaled by a power of two that puts their largest value into [2^14, 2^15) (fp16 rows already
-// are what the products take); row `lane`'s inverse factor comes back.
-template <int D, bool FP16>
-__device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at, uint32_t dst, int lane) {
-  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes, kBatch = 8;  // lanes of a row, rows at once, loads in flight
+// Copies a warp's 32 rows of queries (lane r knows row r's offset, -1: zeros) into the
+// swizzled tile at `dst`, D / 8 lanes to a row. fp16 rows already are what the products take;
+// bf16 rows become fp16 there, scaled by a power of two that puts their largest value into
+// [2^14, 2^15): a lane takes its own row, and its inverse factor comes back. Short loops: this
+// runs once a unit, and code met for the first time costs more than its instructions (unrolled,
+// with the rows in registers, 4.5 us for a CTA's first unit and 2.6 us for its next).
+template <int D>
+__device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at, bool fp16, uint32_t dst, int lane) {
+  constexpr int kLanes = D / 8, kAtOnce = 32 / kLanes;  // lanes of a row, rows at once
   const int c = lane % kLanes, sub = lane / kLanes;
-  float inv = 1.f;
-#pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += kAtOnce * kBatch) {
-    uint4 w[kBatch];
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const long long at = __shfl_sync(0xffffffffu, q_at, r0 + i * kAtOnce + sub);
-      w[i] = at >= 0 ? __ldg(reinterpret_cast<const uint4*>(q + at) + c) : make_uint4(0, 0, 0, 0);
-    }
-    uint32_t mx[kBatch];  // the largest magnitude as an integer: bf16 patterns order like their values
-    if constexpr (!FP16) {
-#pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const uint32_t a = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
-                                    __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
-        mx[i] = max(a & 0xffffu, a >> 16);
-      }
-#pragma unroll
-      for (int o = 1; o < kLanes; o <<= 1)
-#pragma unroll
-        for (int i = 0; i < kBatch; ++i) mx[i] = max(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], o));
-    }
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int r = r0 + i * kAtOnce + sub;
-      uint32_t h[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-      if constexpr (!FP16) {
-        const int e = max(15, static_cast<int>(mx[i] >> 7));
-        const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          h[k] = pack_half(__uint_as_float(h[k] << 16) * f, __uint_as_float(h[k] & 0xffff0000u) * f);
-        const float back = __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
-        const float v = __shfl_sync(0xffffffffu, back, (lane & (kAtOnce - 1)) * kLanes);  // row r0 + i kAtOnce + that
-        if (lane / kAtOnce == r0 / kAtOnce + i) inv = v;
-      }
-      st_shared_v4(dst + (c >> 3) * kChunkBytes + r * 128 + (((c & 7) ^ (r & 7)) << 4), h[0], h[1], h[2], h[3]);
-    }
+  auto place = [&](int r, int chunk) { return dst + (chunk >> 3) * kChunkBytes + r * 128 + (((chunk & 7) ^ (r & 7)) << 4); };
+#pragma unroll 2
+  for (int r = sub; r < 32; r += kAtOnce) {
+    const long long at = __shfl_sync(0xffffffffu, q_at, r);
+    cp_async_16(place(r, c), q + (at >= 0 ? at + c * 8 : 0), at >= 0 ? 16u : 0u);
   }
-  return inv;
+  cp_async_wait();
+  __syncwarp();
+  if (fp16) return 1.f;
+  uint32_t mx = 0u;  // the largest magnitude as an integer: bf16 patterns order like their values
+#pragma unroll 4
+  for (int i = 0; i < kLanes; ++i) {
+    const uint4 w = lds128(place(lane, i));
+    mx = __vmaxu2(mx, __vmaxu2(__vmaxu2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu), __vmaxu2(w.z & 0x7fff7fffu, w.w & 0x7fff7fffu)));
+  }
+  const int e = max(15, static_cast<int>(max(mx & 0xffffu, mx >> 16) >> 7));
+  const float f = __uint_as_float(static_cast<uint32_t>(268 - e) << 23);
+  auto half2_of = [&](uint32_t w) { return pack_half(__uint_as_float(w << 16) * f, __uint_as_float(w & 0xffff0000u) * f); };
+#pragma unroll 4
+  for (int i = 0; i < kLanes; ++i) {
+    const uint4 w = lds128(place(lane, i));
+    st_shared_v4(place(lane, i), half2_of(w.x), half2_of(w.y), half2_of(w.z), half2_of(w.w));
+  }
+  return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 }
 
-// Writes 32 rows x 16 N bytes, a lane's row as N = 4 or 8 pieces, to the rows' own places:
-// through `box` (4 KB of shared memory, pieces permuted within a row), so that N lanes write
-// a row's bytes together. at: of row `lane`, nullptr: not written.
-template <int N>
-__device__ __forceinline__ void store_rows(uint32_t box, const uint4 (&w)[N], uint8_t* at, int lane) {
+// Writes 32 rows x 128 bytes, a lane's row as 8 pieces, to the rows' own places: through `box`
+// (4 KB of shared memory, pieces permuted within a row), so that 8 lanes write a row's bytes
+// together. at: of row `lane`, nullptr: not written.
+__device__ __forceinline__ void store_rows(uint32_t box, const uint4 (&w)[8], uint8_t* at, int lane) {
   __syncwarp();  // the box's last pieces have been read
 #pragma unroll
-  for (int i = 0; i < N; ++i)
-    st_shared_v4(box + lane * (16 * N) + ((i ^ (lane & (N - 1))) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
+  for (int i = 0; i < 8; ++i) st_shared_v4(box + lane * 128 + ((i ^ (lane & 7)) << 4), w[i].x, w[i].y, w[i].z, w[i].w);
   __syncwarp();
 #pragma unroll
-  for (int k = 0; k < N; ++k) {
-    const int r = k * (32 / N) + lane / N;
-    const uint4 v = lds128(box + r * (16 * N) + (((lane & (N - 1)) ^ (r & (N - 1))) << 4));
+  for (int k = 0; k < 8; ++k) {
+    const int r = k * 4 + lane / 8;
+    const uint4 v = lds128(box + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
     uint8_t* const p = reinterpret_cast<uint8_t*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(at), r));
-    if (p != nullptr) *reinterpret_cast<uint4*>(p + (lane & (N - 1)) * 16) = v;
+    if (p != nullptr) *reinterpret_cast<uint4*>(p + (lane & 7) * 16) = v;
   }
 }
 
@@ -548,7 +532,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         // The warp's 32 rows of queries to fp16, scaled by a power of two each, into the
         // swizzled tile (the last unit's scores are done: its last P V was awaited).
         const long long at = qi < x.ql ? x.b * a.sq.b + static_cast<long long>(x.h * g.G + (row - qi * g.G)) * a.sq.h + qi * a.sq.n : -1;
-        rf = a.scale_log2 * (a.fp16 ? tile_queries<D, true>(a.q, at, q_at, lane) : tile_queries<D, false>(a.q, at, q_at, lane));
+        rf = a.scale_log2 * tile_queries<D>(a.q, at, a.fp16, q_at, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b.qfull + t);
@@ -667,14 +651,18 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
           if (lane == 0) mbar_arrive(b.rep_out + pair);
           if (!mbar_wait_warp<true>(b.rep_in + pair, unit & 1, wd)) break;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(o_tm + c * 32, o);
-            tmem_wait_ld();
-            reg_fence(o);
+          for (int c = 0; c < D / 64; ++c) {
+            uint32_t o[2][32];
 #pragma unroll
-            for (int v = 0; v < 8; ++v)
-              st_shared_v4(box + c * 4096 + lane * 128 + ((v ^ (lane & 7)) << 4), o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
+            for (int e = 0; e < 2; ++e) tmem_ld32(o_tm + (c * 2 + e) * 32, o[e]);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              reg_fence(o[e]);
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                st_shared_v4(box + (c * 2 + e) * 4096 + v * 512 + lane * 16, o[e][4 * v], o[e][4 * v + 1], o[e][4 * v + 2], o[e][4 * v + 3]);
+            }
           }
           __syncwarp();
           if (lane == 0) mbar_arrive(b.rep_out + pair);
@@ -692,19 +680,23 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         m = M;
         if (!mbar_wait_warp<true>(b.rep_out + pair, 1, wd)) break;
       }
-      // 32 channels of the row's O, from column 32 c
-      auto read_o = [&](int c, uint32_t (&o)[32]) {
-        tmem_ld32(o_tm + c * 32, o);
+      // 64 channels of the row's O, from column 64 c
+      auto read_o = [&](int c, uint32_t (&o)[2][32]) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) tmem_ld32(o_tm + (c * 2 + e) * 32, o[e]);
         tmem_wait_ld();
-        reg_fence(o);
-        if constexpr (REP == 2) {
 #pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const uint4 w = lds128(box + c * 4096 + lane * 128 + ((v ^ (lane & 7)) << 4));
-            const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+        for (int e = 0; e < 2; ++e) {
+          reg_fence(o[e]);
+          if constexpr (REP == 2) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-              o[4 * v + q] = __float_as_uint(__uint_as_float(o[4 * v + q]) * f0 + __uint_as_float(ww[q]) * f1);
+            for (int v = 0; v < 8; ++v) {
+              const uint4 w = lds128(box + (c * 2 + e) * 4096 + v * 512 + lane * 16);
+              const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                o[e][4 * v + q] = __float_as_uint(__uint_as_float(o[e][4 * v + q]) * f0 + __uint_as_float(ww[q]) * f1);
+            }
           }
         }
       };
@@ -722,39 +714,42 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         uint16_t* const dst = a.o + x.b * a.so.b + static_cast<long long>(head) * a.so.h + qi * a.so.n;
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[2][32];
+          read_o(c, o);
           uint4 w[8];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t o[32];
-            read_o(c * 2 + e, o);
+          for (int v = 0; v < 8; ++v) {
+            uint32_t hw[4];
 #pragma unroll
-            for (int v = 0; v < 4; ++v) {
-              uint32_t hw[4];
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                hw[q] = none ? 0u : pack16(__uint_as_float(o[8 * v + 2 * q]) * inv, __uint_as_float(o[8 * v + 2 * q + 1]) * inv, a.fp16);
-              w[e * 4 + v] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
+            for (int q = 0; q < 4; ++q) {
+              const int k = (v & 3) * 8 + 2 * q;
+              hw[q] = none ? 0u : pack16(__uint_as_float(o[v >> 2][k]) * inv, __uint_as_float(o[v >> 2][k + 1]) * inv, a.fp16);
             }
+            w[v] = make_uint4(hw[0], hw[1], hw[2], hw[3]);
           }
           store_rows(box + (REP == 2 ? c * 8192 : 0), w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
         }
         if (row_ok)
           a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
       } else {
+        // a part, in the order of the registers: 512 bytes a warp and store
         const long long pr = static_cast<long long>(2 * blockIdx.x + (x.first == 0 ? 1 : 0)) * g.rows + r;
         if (row_ok) {
           g.m_part[pr] = m;
           g.l_part[pr] = l;
         }
+        uint4* const dst = reinterpret_cast<uint4*>(g.o_part) + (pr >> 5) * (D / 4 * 32) + lane;
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t o[32];
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t o[2][32];
           read_o(c, o);
-          uint4 w[8];  // rows that see nothing leave zeros: their accumulators hold whatever P was
+          if (row_ok) {  // rows that see nothing leave zeros: their accumulators hold whatever P was
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            w[v] = none ? make_uint4(0, 0, 0, 0) : make_uint4(o[4 * v], o[4 * v + 1], o[4 * v + 2], o[4 * v + 3]);
-          store_rows(box + (REP == 2 ? c * 4096 : 0), w, row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 32) : nullptr, lane);
+            for (int v = 0; v < 16; ++v) {
+              const uint32_t* const w = o[v >> 3] + (v & 7) * 4;
+              dst[(c * 16 + v) * 32] = none ? make_uint4(0, 0, 0, 0) : make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
         }
       }
       __syncwarp();       // the boxes have been read
