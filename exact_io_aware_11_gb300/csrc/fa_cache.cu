@@ -422,7 +422,7 @@ cudaError_t write_variant(const CacheRows& a, cudaStream_t stream) {
     return launch_pdl(cache_write_few_kernel<FP16, INT8>, dim3((2 * n + 3) / 4), dim3(128), 0, stream, a, pages, 2 * n);
   }
   const int log2_t = a.c.log2_page + (a.c.d == 128 ? 7 : 6) - 5;
-  const int threads = log2_t > 8 ? 512 : 256;
+  const int threads = log2_t > 8 ? 512 : log2_t > 7 ? 256 : 128;
   const unsigned per = static_cast<unsigned>(threads >> log2_t);
   return launch_pdl(cache_write_pages_kernel<FP16, INT8>, dim3((n + per - 1) / per), dim3(threads), 0, stream, a,
                     log2_t, pages, n);

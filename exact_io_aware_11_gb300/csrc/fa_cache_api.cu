@@ -100,6 +100,7 @@ int rotary(const void* q, void* q_out, const void* k, void* k_out, int B, int Hq
   a.r = opt->rotary_dim;
   a.interleaved = opt->interleaved;
   a.fp16 = opt->dtype == FA_FP16;
+  a.inner = Hq > 1 && N > 1 && in[0].st.h < in[0].st.n;
   a.fcos = opt->factor;
   a.fsin = back ? -opt->factor : opt->factor;
   a.turns = reinterpret_cast<const unsigned long long*>(opt->turns);

@@ -545,23 +545,23 @@ __global__ void __launch_bounds__(kThreads, 2)
 // Merges the units that were cut. Blocks (c, y) look at CTA c's record (the unit
 // whose last part c ran) and share its rows out: with m_q, l_q, O_q of part q and
 // M = max_q m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q. A lane holds D / 32
-// consecutive channels and loads four parts at a time, statistics and all. A unit
+// consecutive channels and loads five parts at a time, statistics and all. A unit
 // of few parts gives each of the block's 8 warps a row; one of more parts gives a row
-// four or eight warps, which take every fourth or eighth part and then join theirs (a
+// four or all of them, which take every fourth or eighth part and then join theirs (a
 // row of 76 parts with one warp, four at a time: 36 us by itself, with four warps 8 us).
 template <int D>
 __global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
-  constexpr int kV = D / 32, kBatch = 4;
-  __shared__ float sm_m[8], sm_l[8], sm_o[8][D];
+  constexpr int kV = D / 32, kBatch = 5, kRowWarps = 8;
+  __shared__ float sm_m[kRowWarps], sm_l[kRowWarps], sm_o[kRowWarps][D];
   grid_dep_wait();
   grid_dep_launch();
   const int4 rec = g.record[blockIdx.x];
   if (rec.x < 0) return;
   const int c0 = rec.z, c1 = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int W = c1 - c0 < 4 ? 1 : c1 - c0 < 32 ? 4 : 8, sub = warp & (W - 1);  // warps of a row
+  const int W = c1 - c0 < kBatch ? 1 : c1 - c0 < 4 * kBatch ? 4 : kRowWarps, sub = warp & (W - 1);  // warps of a row
   const int b = rec.x / g.row_tiles, row0 = (rec.x - b * g.row_tiles) * g.rows;
   const int live = static_cast<int>(min(static_cast<long long>(g.rows), static_cast<long long>(g.N) * g.G - row0));
-  for (int r0 = blockIdx.y * (8 / W); r0 < live; r0 += gridDim.y * (8 / W)) {  // uniform over the block
+  for (int r0 = blockIdx.y * (kRowWarps / W); r0 < live; r0 += gridDim.y * (kRowWarps / W)) {  // uniform over the block
     const int r = r0 + warp / W;
     float acc[kV], sum = 0.f, M = -INFINITY;
 #pragma unroll
@@ -739,9 +739,8 @@ cudaError_t launch_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas
   if (g.rows > 16)
     return launch_pdl(cache_attn_merge_tiles_kernel<D>, dim3(ctas, static_cast<unsigned>((live + 31) / 32)), dim3(D * 2), 0,
                       stream, a, g);
-  // blocks of a unit: a row each, and no more than 32 (most CTAs have no record)
-  const unsigned y = static_cast<unsigned>(live < 32 ? live : 32);
-  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, y), dim3(256), 0, stream, a, g);
+  // blocks of a unit: a row each (most CTAs have no record)
+  return launch_pdl(cache_attn_merge_kernel<D>, dim3(ctas, static_cast<unsigned>(live)), dim3(256), 0, stream, a, g);
 }
 
 struct AttnWorkspace {

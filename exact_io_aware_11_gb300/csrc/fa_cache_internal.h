@@ -21,7 +21,7 @@ struct RotaryTensor {
 struct RotaryLaunch {
   RotaryTensor t[2];  // queries, keys
   int B, Hq, Hk, N, d, r;
-  int interleaved, fp16;
+  int interleaved, fp16, inner;  // inner: a row's heads lie closer together than a head's rows
   float fcos, fsin;  // factor, and factor with the direction's sign
   const unsigned long long* turns;
   const int32_t* pos;

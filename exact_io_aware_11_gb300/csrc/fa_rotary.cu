@@ -75,39 +75,62 @@ __device__ __forceinline__ RowAt row_at(const RotaryLaunch& a, int b, int h, int
   return RowAt{t.x + b * t.sx.b + hh * t.sx.h + n * t.sx.n, t.y + b * t.sy.b + hh * t.sy.h + n * t.sy.n};
 }
 
-// A thread's row and heads from its index: job fastest, then row, head group, batch.
+// A thread's row and heads from its index. Of the G = hgroups threads of a row, thread g takes
+// heads g, g + G, g + 2G ... The job runs fastest, then what lies closer in memory: the row
+// or, where the heads of a row lie together (a.inner), the thread of the row; batches last.
 // I: 32 bits where the indices fit (a 64-bit division costs as much as two pairs' sines).
 template <typename I>
 struct Item {
-  int job, n, b, h0, h1;
-  __device__ __forceinline__ Item(const RotaryLaunch& a, I idx, int jobs, int hpt, int hgroups) {
-    I rest = idx / static_cast<I>(jobs);
+  int job, n, b, h0, heads;
+  __device__ __forceinline__ Item(const RotaryLaunch& a, I idx, int jobs, int hgroups) {
+    const I first = static_cast<I>(a.inner ? hgroups : a.N), second = static_cast<I>(a.inner ? a.N : hgroups);
+    const I rest = idx / static_cast<I>(jobs);
     job = static_cast<int>(idx - rest * static_cast<I>(jobs));
-    const I bg = rest / static_cast<I>(a.N);
-    n = static_cast<int>(rest - bg * static_cast<I>(a.N));
-    b = static_cast<int>(bg / static_cast<I>(hgroups));
-    h0 = static_cast<int>(bg - static_cast<I>(b) * static_cast<I>(hgroups)) * hpt;
-    h1 = min(h0 + hpt, a.Hq + a.Hk);
+    const I up = rest / first;
+    const int lo = static_cast<int>(rest - up * first);
+    b = static_cast<int>(up / second);
+    const int hi = static_cast<int>(up - static_cast<I>(b) * second);
+    n = a.inner ? hi : lo;
+    h0 = a.inner ? lo : hi;
+    heads = a.Hq + a.Hk;
   }
 };
 
-constexpr int kBatch = 4;
-// One thread: 32 bytes of `hpt` heads of one row. Half layout: 8 pairs, two chunks r/2
+// Heads' loads in flight, threads of a block, and heads of a thread at most. GPU time of
+// 8 x 24 x 1024 x 64 and of 1 x 32 x 16384 x 128, one direction: (2, 128, 4) 11.5, 43.2 us (4390,
+// 6210 GB/s); 8 heads 11.5, 44.8; blocks of 256 12.0, 45.5; batches of 4 and 8 heads 12.7, 51.5;
+// batches of 8 (120 registers) 11.8, 43.1.
+constexpr int kBatch = 2, kThreads = 128, kMaxHeads = 4;
+// One thread: 32 bytes of some heads of one row. Half layout: 8 pairs, two chunks r/2
 // apart, or two chunks of the channels behind the rotated ones; interleaved: 8 pairs, two
 // adjacent chunks. Channels that are not rotated go the same way and keep their bits, so
 // that the lanes of a warp stay together.
 template <bool FP16, bool INTERLEAVED, typename I>
-__global__ void __launch_bounds__(256) rotary_kernel(const RotaryLaunch a, int jobs, int hpt, int hgroups, I total) {
+__global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const RotaryLaunch a, int jobs, int hgroups, I total) {
   grid_dep_wait();
   grid_dep_launch();
-  const I idx = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
+  const I idx = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x;
   if (idx >= total) return;
-  const Item<I> it(a, idx, jobs, hpt, hgroups);
+  const Item<I> it(a, idx, jobs, hgroups);
   const int rot_jobs = INTERLEAVED ? (a.r + 15) / 16 : a.r / 16;
   const bool rot = it.job < rot_jobs;
   const int ca = INTERLEAVED ? it.job * 16 : rot ? it.job * 8 : a.r + (it.job - rot_jobs) * 8;
   const int cb = INTERLEAVED ? ca + 8 : rot ? a.r / 2 + it.job * 8 : ca + (a.d - a.r) / 2;
   const int pairs = rot ? min(8, a.r / 2 - it.job * 8) : 0;  // fewer: interleaved, the last rotated chunks
+  // A batch of heads' loads in flight: written out, because the compiler may not move a load
+  // ahead of another head's store (the call may be in place). The first one's cross the sines.
+  uint4 v[kBatch][2];
+  auto load = [&](int h0) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (h0 + k * hgroups < it.heads) {
+        const uint16_t* const x = row_at(a, it.b, h0 + k * hgroups, it.n).x;
+        v[k][0] = *reinterpret_cast<const uint4*>(x + ca);
+        v[k][1] = *reinterpret_cast<const uint4*>(x + cb);
+      }
+    }
+  };
+  load(it.h0);
   float c[8], s[8];
   if (rot) {
     const int pos = position(a, it.b, it.n);
@@ -118,21 +141,11 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryLaunch a, int j
       if (i < pairs) turn_of(__ldg(a.turns + it.job * 8 + i), pos, a.fcos, a.fsin, c[i], s[i]);
     }
   }
-  // kBatch heads' loads in flight: written out, because the compiler may not move a load
-  // ahead of another head's store (the call may be in place)
-  for (int h0 = it.h0; h0 < it.h1; h0 += kBatch) {
-    uint4 v[kBatch][2];
+  for (int h0 = it.h0; h0 < it.heads; h0 += kBatch * hgroups) {
+    if (h0 > it.h0) load(h0);
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (h0 + k < it.h1) {
-        const uint16_t* const x = row_at(a, it.b, h0 + k, it.n).x;
-        v[k][0] = *reinterpret_cast<const uint4*>(x + ca);
-        v[k][1] = *reinterpret_cast<const uint4*>(x + cb);
-      }
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (h0 + k >= it.h1) break;
+      if (h0 + k * hgroups >= it.heads) break;
       uint32_t wa[4] = {v[k][0].x, v[k][0].y, v[k][0].z, v[k][0].w};
       uint32_t wb[4] = {v[k][1].x, v[k][1].y, v[k][1].z, v[k][1].w};
       if (rot) {
@@ -152,7 +165,7 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryLaunch a, int j
           }
         }
       }
-      uint16_t* const y = row_at(a, it.b, h0 + k, it.n).y;
+      uint16_t* const y = row_at(a, it.b, h0 + k * hgroups, it.n).y;
       *reinterpret_cast<uint4*>(y + ca) = make_uint4(wa[0], wa[1], wa[2], wa[3]);
       *reinterpret_cast<uint4*>(y + cb) = make_uint4(wb[0], wb[1], wb[2], wb[3]);
     }
@@ -162,18 +175,17 @@ __global__ void __launch_bounds__(256) rotary_kernel(const RotaryLaunch a, int j
 // Half layout whose second channels do not start on a chunk (r / 2 not a
 // multiple of 8): a thread takes one pair, or one copied channel, at a time.
 template <bool FP16, typename I>
-__global__ void __launch_bounds__(256) rotary_pairs_kernel(const RotaryLaunch a, int jobs, int hpt, int hgroups,
-                                                           I total) {
+__global__ void __launch_bounds__(kThreads) rotary_pairs_kernel(const RotaryLaunch a, int jobs, int hgroups, I total) {
   grid_dep_wait();
   grid_dep_launch();
-  const I idx = static_cast<I>(blockIdx.x) * 256 + threadIdx.x;
+  const I idx = static_cast<I>(blockIdx.x) * kThreads + threadIdx.x;
   if (idx >= total) return;
-  const Item<I> it(a, idx, jobs, hpt, hgroups);
-  const int job = it.job, n = it.n, b = it.b, h0 = it.h0, h1 = it.h1;
+  const Item<I> it(a, idx, jobs, hgroups);
+  const int job = it.job, n = it.n, b = it.b;
   const int half = a.r / 2;
   if (job >= half) {
     const int ch = a.r + (job - half);
-    for (int h = h0; h < h1; ++h) {
+    for (int h = it.h0; h < it.heads; h += hgroups) {
       const RowAt p = row_at(a, b, h, n);
       if (p.x != p.y) p.y[ch] = p.x[ch];
     }
@@ -182,7 +194,7 @@ __global__ void __launch_bounds__(256) rotary_pairs_kernel(const RotaryLaunch a,
   float c, s;
   turn_of(__ldg(a.turns + job), position(a, b, n), a.fcos, a.fsin, c, s);
 #pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
+  for (int h = it.h0; h < it.heads; h += hgroups) {
     const RowAt p = row_at(a, b, h, n);
     const float xa = unpack1<FP16>(p.x[job]), xb = unpack1<FP16>(p.x[half + job]);
     p.y[job] = pack1<FP16>(xa * c - xb * s);
@@ -190,24 +202,24 @@ __global__ void __launch_bounds__(256) rotary_pairs_kernel(const RotaryLaunch a,
   }
 }
 
-// Heads a thread takes: as many as leave every SM 1024 threads, at most 8 (the sines are
-// then a fifth of a thread's instructions).
+// Heads a thread takes: as many as leave every SM 1024 threads, at most kMaxHeads (the
+// sines are then a third of a thread's instructions).
 int heads_per_thread(long long threads_at_one, int heads) {
   const long long enough = static_cast<long long>(sm_count()) * 1024;
   int hpt = 1;
-  while (hpt < 8 && hpt < heads && threads_at_one / (hpt * 2) >= enough) hpt *= 2;
+  while (hpt < kMaxHeads && hpt < heads && threads_at_one / (hpt * 2) >= enough) hpt *= 2;
   return hpt;
 }
 
 template <bool FP16, typename I>
-cudaError_t launch_typed(const RotaryLaunch& a, bool chunks, unsigned blocks, int jobs, int hpt, int hgroups,
+cudaError_t launch_typed(const RotaryLaunch& a, bool chunks, unsigned blocks, int jobs, int hgroups,
                          long long total, cudaStream_t stream) {
-  const dim3 grid(blocks), block(256);
+  const dim3 grid(blocks), block(kThreads);
   const I n = static_cast<I>(total);
-  if (!chunks) return launch_pdl(rotary_pairs_kernel<FP16, I>, grid, block, 0, stream, a, jobs, hpt, hgroups, n);
+  if (!chunks) return launch_pdl(rotary_pairs_kernel<FP16, I>, grid, block, 0, stream, a, jobs, hgroups, n);
   if (a.interleaved)
-    return launch_pdl(rotary_kernel<FP16, true, I>, grid, block, 0, stream, a, jobs, hpt, hgroups, n);
-  return launch_pdl(rotary_kernel<FP16, false, I>, grid, block, 0, stream, a, jobs, hpt, hgroups, n);
+    return launch_pdl(rotary_kernel<FP16, true, I>, grid, block, 0, stream, a, jobs, hgroups, n);
+  return launch_pdl(rotary_kernel<FP16, false, I>, grid, block, 0, stream, a, jobs, hgroups, n);
 }
 
 }  // namespace
@@ -219,14 +231,14 @@ cudaError_t launch_rotary(const RotaryLaunch& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.B) * a.N;
   const int hpt = heads_per_thread(rows * jobs * heads, heads);
   const int hgroups = (heads + hpt - 1) / hpt;
-  const long long total = rows * jobs * hgroups, blocks = (total + 255) / 256;
+  const long long total = rows * jobs * hgroups, blocks = (total + kThreads - 1) / kThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
   const unsigned nb = static_cast<unsigned>(blocks);
-  if (total + 255 <= 0xffffffffLL)
-    return a.fp16 ? launch_typed<true, unsigned>(a, chunks, nb, jobs, hpt, hgroups, total, stream)
-                  : launch_typed<false, unsigned>(a, chunks, nb, jobs, hpt, hgroups, total, stream);
-  return a.fp16 ? launch_typed<true, unsigned long long>(a, chunks, nb, jobs, hpt, hgroups, total, stream)
-                : launch_typed<false, unsigned long long>(a, chunks, nb, jobs, hpt, hgroups, total, stream);
+  if (total + kThreads <= 0xffffffffLL)
+    return a.fp16 ? launch_typed<true, unsigned>(a, chunks, nb, jobs, hgroups, total, stream)
+                  : launch_typed<false, unsigned>(a, chunks, nb, jobs, hgroups, total, stream);
+  return a.fp16 ? launch_typed<true, unsigned long long>(a, chunks, nb, jobs, hgroups, total, stream)
+                : launch_typed<false, unsigned long long>(a, chunks, nb, jobs, hgroups, total, stream);
 }
 
 }  // namespace fa
