@@ -191,7 +191,8 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
 // once in both directions.
 // Where a row of queries may not see a key of V (x.seen and the first row's limit
 // bound those keys), its NaN codes are taken out, and the first such key is kept
-// for the unit: the rows that see it become NaN.
+// for the unit: the rows that see it become NaN. Pages of zeros, and groups of keys that were
+// not read, become zeros.
 template <int D, int NQ, bool INT8>
 __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, uint8_t* smem,
                                              const TileBars& b, const Watchdog& wd, int cw, int lane) {
@@ -226,9 +227,9 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
         const uint32_t src = smem_u32(smem) + L::oRaw + st * L::kRaw;
         const uint32_t dst = smem_u32(smem) + (kv ? L::oV : L::oK) + slot * L::kTile;
         bool check = false;
-        if (!INT8 && kv == 1) {
-          const float read = lane < 8 ? *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + lane * 16 + 12) : 0.f;
-          check = key0 + kKeys > low || __any_sync(0xffffffffu, read < 0.f);
+        if (kv == 1) {
+          const float counts = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (lane & 7) * 16 + 12);
+          check = (!INT8 && key0 + kKeys > low) || __any_sync(0xffffffffu, counts != 1.f);
         }
         auto from = [&](int r) {
           return lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
@@ -258,16 +259,18 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
           for (int i = 0; i < kPieces; ++i) {
             const int r = row_of(i), key = key0 + r;
             const uint4 v = from(r);
-            const float read = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
+            const float counts = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
             uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
-            if (key >= low || read < 0.f) {
+            if (counts != 1.f) {
+              w[0] = w[1] = w[2] = w[3] = 0u;
+            } else if (!INT8 && key >= low) {
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
                 const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
                 w[k] &= ~nan;
                 any |= nan;
               }
-              if (any != 0u && key < seen && !(read < 0.f)) atomicMin(nan_key + (unit & 7), key);
+              if (any != 0u && key < seen) atomicMin(nan_key + (unit & 7), key);
             }
             put(make_uint4(w[0], w[1], w[2], w[3]), r);
           }
@@ -597,13 +600,10 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
             for (int u = 0; u < 2; ++u) {
               const float4 f = sc(c * 2 + (P16 ? u : 0));
               part[u] = f.z * weigh16(v[c], u * 16, fmaxf(rf * f.x, 1e-37f), f.y - base, p[u]);
-              if (!plain && f.w == 0.f) {  // a page of zeros
-#pragma unroll
-                for (int q = 0; q < 8; ++q) p[u][q] = 0u;
-              }
             }
             l += part[0] + part[1];
             tmem_st8x2(s_tm + col0 / 2 + c * 16, p);
+            if (kChunks == 4 && c == 1) __syncwarp();
           }
           if constexpr (REP == 2) {  // the other copy's keys
             const uint32_t none[2][8] = {};
