@@ -758,18 +758,30 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 
 }  // namespace
 
+// Rows of a unit, from the rows of a (sequence, cache head); GPU time in us at d = 128, pages of 64:
+//   up to 8, 16: one or two groups of the few-row kernel (8 rows of 64 sequences 103.0 as one
+//     group, 106.0 as two, 145 as a tile; 16 rows 110 and 148);
+//   up to 64: a tile with its rows twice (40 rows of 16 sequences 32.5, in a tile of 128 34.4);
+//   up to 128: one tile (128 rows 29.0, in a unit of two tiles 32.7);
+//   above: a unit of two tiles, whose step costs 1.6 times one tile's, where that saves time (384
+//     rows do not: 124 and 121) and the CTAs have some 8 steps each to make good its longer
+//     start and larger merge (107 steps a CTA 212, with single tiles 267; 13 steps 47.5 and 52.5;
+//     7 steps 37.9 and 36.5; 3 steps 37.5 and 31.1).
 // lead: beginning one more unit costs a CTA 1 us (rows of up to 16, steps of 0.7 us) and 5 us (tiles,
 // steps of 1 to 2 us); counting it shares ragged batches out more evenly: drafts 39.9 us with
 // none, 37.0 with 4, 36.9 with 8; a chunk 243.3, 242.5, 247.0; single tokens of 64 sequences
 // 102.7 with none, 101.5 with 1, 101.5 with 4.
 AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
   AttnPlan p{};
-  p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 64 : rows <= 128 ? 128 : 256;
   p.log2_keys = 7;
-  p.lead = p.rows <= 16 ? 1 : 4;
-  p.units = static_cast<long long>(B) * HK * ((rows + p.rows - 1) / p.rows);
   p.cap_steps = (cap + 127) >> 7;
   if (p.cap_steps < 1) p.cap_steps = 1;
+  const long long heads = static_cast<long long>(B) * HK, one = (rows + 127) / 128, two = (rows + 255) / 256;
+  const long long long_runs = 8LL * sm_count();
+  const bool wide = two * 8 < one * 5 && (heads * two >= long_runs || heads * two * p.cap_steps >= long_runs);
+  p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 64 : wide ? 256 : 128;
+  p.lead = p.rows <= 16 ? 1 : 4;
+  p.units = heads * ((rows + p.rows - 1) / p.rows);
   const long long most = (p.rows > 16 ? 1LL : 2LL) * sm_count();  // CTAs that an SM holds
   p.ctas = static_cast<int>(p.units >= most || p.units * p.cap_steps >= most ? most : p.units * p.cap_steps);
   return p;
@@ -777,16 +789,16 @@ AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
 
 // Whether units are cut, from the sizes that the host knows (capacities, not lengths).
 // Cutting shares the steps out evenly but adds the merge and, with many rows, units that
-// begin within a CTA's run: worth about 6.5 steps (single tokens, steps of 0.7 us: 12 units
-// of 4 steps 10.4 us cut, 8.4 whole; of 8 steps 10.4 and 11.5; 64 units of 8 steps 15.1 and
-// 14.5; 192 of 8 steps 14.6 and 12.5, of 16 steps 18.5 both; 32 tiles of 8 steps 28.8 and 22.7,
-// of 16 steps 30.9 and 33.2). Beyond 16 steps unequal lengths may cost more than that, so
-// those are always cut.
+// begin within a CTA's run: worth about 6 steps (GPU time in us, cut and whole: single tokens,
+// 12 units of 4 steps 10.3, 10.2, of 8 steps 10.3, 12.3; 64 of 8 steps 12.5, 14.4; 192 of 16 steps,
+// which saves 5.9, 29.2, 26.0; 320 of 8 steps 26.7, 28.6; 32 tiles of 4 steps 22.6, 20.6, of 8
+// steps 24.7, 27.4; 256 tiles of 16 steps 82.7, 79.4). Beyond 16 steps unequal lengths may cost
+// more than that, so those are always cut.
 static bool attn_cut(const AttnPlan& p) {
   if (p.cap_steps <= 4) return false;
   if (p.cap_steps > 16) return true;
   const long long rounds = (p.units + p.ctas - 1) / p.ctas;
-  return static_cast<double>(rounds * p.cap_steps) - static_cast<double>(p.units * p.cap_steps) / p.ctas > 6.5;
+  return static_cast<double>(rounds * p.cap_steps) - static_cast<double>(p.units * p.cap_steps) / p.ctas > 6.1;
 }
 
 size_t cache_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width) {

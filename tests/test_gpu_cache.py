@@ -265,16 +265,16 @@ def test_scales_far_apart(fa):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("d,G,N", [(128, 1, 1), (64, 6, 2), (128, 8, 4), (64, 2, 60), (128, 4, 50)])
-def test_pages_of_zeros_beside_large_values(fa, d, G, N, fmt):
+@pytest.mark.parametrize("d,G,N,B", [(128, 1, 1, 1), (64, 6, 2, 1), (128, 8, 4, 1), (64, 2, 60, 1), (128, 4, 50, 1), (64, 4, 50, 640)])
+def test_pages_of_zeros_beside_large_values(fa, d, G, N, B, fmt):
     """Tokens whose V is zero take their share of the weights whatever the other pages' scale."""
     page, W = 32, 9
     cache = random_cache(fa, W, 2, page, d, fmt, seed=31)
     cache.v_scale[:] = 2.0 ** 30
     cache.v_scale[::2] = 0.0
     cache.v_scale[1] = 2.0 ** -30
-    table = torch.arange(W, dtype=torch.int32, device="cuda")[None]
-    check_batch(fa, queries(1, 2 * G, N, d, "bf16", 32), cache, table, [W * page - 3], [N])
+    table = torch.arange(W, dtype=torch.int32, device="cuda")[None].expand(B, -1)
+    check_batch(fa, queries(B, 2 * G, N, d, "bf16", 32), cache, table, [W * page - 3] * B, [N] * B)
 
 
 @pytest.mark.parametrize("mul", [2.0 ** -60, 2.0 ** 90])
@@ -421,6 +421,8 @@ def check_batch(fa, q, cache, table, lens, qlens, causal=True, **kw):
     (64, 16, 40, 20, 9, 170, 120),      # thousands of units of one step: their descriptions wrap
     (128, 64, 40, 20, 9, 170, 128), (128, 16, 32, 16, 1, 300, 100), (64, 32, 18, 2, 16, 8, 3000),
     (128, 128, 3, 1, 341, 3, 2500), (64, 64, 2, 1, 1000, 2, 4000), (128, 16, 8, 2, 260, 2, 1500), (64, 16, 5, 1, 700, 1, 900),
+    # enough steps for units of two tiles
+    (128, 64, 4, 2, 400, 3, 7000), (64, 16, 6, 2, 300, 2, 12000), (128, 128, 2, 1, 900, 3, 9000), (64, 32, 4, 4, 150, 320, 200),
 ])
 def test_many_units_and_long_chunks(fa, d, page, H, HK, N, B, longest, fmt, dt):
     g = torch.Generator().manual_seed(B + N)
@@ -439,20 +441,21 @@ def test_many_units_and_long_chunks(fa, d, page, H, HK, N, B, longest, fmt, dt):
     assert torch.isneginf(a[1]).equal(torch.isneginf(b[1]))
 
 
-@pytest.mark.parametrize("G,N", [(1, 3), (2, 12), (1, 40), (4, 60), (1, 400)])
-def test_nan_behind_a_row_has_no_effect_on_it(fa, G, N):
+@pytest.mark.parametrize("G,N,B", [(1, 3, 2), (2, 12, 2), (1, 40, 2), (4, 60, 2), (1, 400, 2), (2, 100, 640)])
+def test_nan_behind_a_row_has_no_effect_on_it(fa, G, N, B):
     """NaN in K and V at token t reaches the rows that see t, all of each of them, and no other row, in every
-    kernel; rows of other heads and sequences stay as they are."""
+    kernel (the last size fills units of two tiles); rows of other heads and sequences stay as they are."""
     L = max(N, 1) + 90
     m = filled(fa, 2, 2, 16, 64, "e4m3", [L, L], seed=20)
-    q = queries(2, 2 * G, N, 64, "bf16", 17)
-    i32 = torch.tensor([L, L], dtype=torch.int32, device="cuda")
-    want, wl = fa.cache_attention(q, m.cache, m.table.cuda(), i32)
+    table = torch.cat([m.table, m.table[:1].expand(B - 2, -1)]).cuda()
+    q = queries(B, 2 * G, N, 64, "bf16", 17)
+    i32 = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    want, wl = fa.cache_attention(q, m.cache, table, i32)
     at = [L - N + N // 2, L - 1]
     for n, t in zip("vk", at):
         m.codes[n][int(m.table[1, t // 16]), 1, t % 16, 3] = 0xff
         getattr(m.cache, n).view(torch.uint8).copy_(torch.from_numpy(m.codes[n]))
-    o, lse = fa.cache_attention(q, m.cache, m.table.cuda(), i32)
+    o, lse = fa.cache_attention(q, m.cache, table, i32)
     hit = torch.zeros_like(lse, dtype=torch.bool)
     hit[1, G:, N // 2:] = True
     assert torch.isnan(o[1, G:, N // 2:]).any(-1).all()
