@@ -197,16 +197,19 @@ template <int D, int NQ, bool INT8>
 __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, uint8_t* smem,
                                              const TileBars& b, const Watchdog& wd, int cw, int lane) {
   using L = TileLayout<D, NQ>;
-  // the row of the lane's i-th piece, and its chunk
-  constexpr int kRows = kKeys / L::kConvWarps, kPieces = kRows * D / 512;
+  // The lane's pieces: chunk ch of rows row0[e] + 8 g, e < kPer, g < kGroups, at constant
+  // distances of a piece with g = 0 (both swizzles repeat every 8 rows).
+  constexpr int kRows = kKeys / L::kConvWarps, kPer = D / 64, kGroups = kRows / 8;
   const int ch = D == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
-  auto row_of = [&](int i) {
-    if constexpr (D == 128) {
-      const int p = (lane >> 4) + 2 * (i & 1);
-      return cw * kRows + (i >> 1) * 8 + ((lane & 4) ? p ^ 5 : p);
-    }
-    return cw * kRows + i * 8 + (lane >> 2);
-  };
+  int row0[kPer];
+  uint32_t raw_at[kPer], half_at[kPer];  // in the raw and the fp16 tile; the second half's place is the first's ^ 16
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    const int p = D == 128 ? (lane >> 4) + 2 * e : lane >> 2, r = cw * kRows + (D == 128 && (lane & 4) ? p ^ 5 : p);
+    row0[e] = r;
+    raw_at[e] = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
+    half_at[e] = (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128 + (((ch & 3) * 2 ^ (r & 7)) << 4);
+  }
   int* const nan_key = reinterpret_cast<int*>(smem + L::oNan);
   int n = 0;  // steps converted
   for (int unit = 0;; ++unit) {
@@ -231,48 +234,47 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
           const float counts = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (lane & 7) * 16 + 12);
           check = (!INT8 && key0 + kKeys > low) || __any_sync(0xffffffffu, counts != 1.f);
         }
-        auto from = [&](int r) {
-          return lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
-        };
-        auto put = [&](const uint4& v, int r) {
+        auto put = [&](const uint4& v, int e, int g) {
           uint32_t w[8];
           decode4<INT8>(v.x, w[0], w[1]);
           decode4<INT8>(v.y, w[2], w[3]);
           decode4<INT8>(v.z, w[4], w[5]);
           decode4<INT8>(v.w, w[6], w[7]);
-          const uint32_t row = dst + (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128;
-          const int unit16 = (ch & 3) * 2 ^ (r & 7);
-          st_shared_v4(row + (unit16 << 4), w[0], w[1], w[2], w[3]);
-          st_shared_v4(row + ((unit16 ^ 1) << 4), w[4], w[5], w[6], w[7]);
+          st_shared_v4(dst + half_at[e] + g * 1024, w[0], w[1], w[2], w[3]);
+          st_shared_v4(dst + (half_at[e] ^ 16u) + g * 1024, w[4], w[5], w[6], w[7]);
         };
         if (!check) {
+          constexpr int kBatch = D / 16;  // loads in flight
 #pragma unroll 1
-          for (int i0 = 0; i0 < kPieces; i0 += D / 16) {
-            uint4 v[D / 16];
+          for (int g0 = 0; g0 < kGroups; g0 += kBatch / kPer) {
+            uint4 v[kBatch];
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) v[i] = from(row_of(i0 + i));
+            for (int i = 0; i < kBatch; ++i) v[i] = lds128(src + raw_at[i % kPer] + (g0 + i / kPer) * (8 * D));
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) put(v[i], row_of(i0 + i));
+            for (int i = 0; i < kBatch; ++i) put(v[i], i % kPer, g0 + i / kPer);
           }
         } else {
 #pragma unroll 1
-          for (int i = 0; i < kPieces; ++i) {
-            const int r = row_of(i), key = key0 + r;
-            const uint4 v = from(r);
-            const float counts = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
-            uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
-            if (counts != 1.f) {
-              w[0] = w[1] = w[2] = w[3] = 0u;
-            } else if (!INT8 && key >= low) {
+          for (int g = 0; g < kGroups; ++g) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                w[k] &= ~nan;
-                any |= nan;
+            for (int e = 0; e < kPer; ++e) {
+              const int r = row0[e] + g * 8, key = key0 + r;
+              const uint4 v = lds128(src + raw_at[e] + g * (8 * D));
+              const float counts = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
+              uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
+              if (counts != 1.f) {
+                w[0] = w[1] = w[2] = w[3] = 0u;
+              } else if (!INT8 && key >= low) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                  w[k] &= ~nan;
+                  any |= nan;
+                }
+                if (any != 0u && key < seen) atomicMin(nan_key + (unit & 7), key);
               }
-              if (any != 0u && key < seen) atomicMin(nan_key + (unit & 7), key);
+              put(make_uint4(w[0], w[1], w[2], w[3]), e, g);
             }
-            put(make_uint4(w[0], w[1], w[2], w[3]), r);
           }
         }
         fence_proxy_async_smem();
