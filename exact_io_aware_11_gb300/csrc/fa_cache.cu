@@ -11,7 +11,10 @@
 // repeated moves form a geometric series, at most one step in all.
 //
 // What bounds it: memory (2 bytes read and 1 written per element) for prompts,
-// latency for single tokens.
+// latency for single tokens. Measured (GPU time): prompts of 1021 to 4099 tokens, 5 sequences, 8
+// heads, d = 128, int8: 19.7 us, 4000 GB/s (bursts of four to five rounds of blocks); 4 of 8192,
+// e4m3: 37 us, 5450 GB/s; one token of 64 sequences 5.4 us; reading 16384 tokens of 16 heads back:
+// 36.9 us, 5450 GB/s.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -162,7 +165,7 @@ struct UnitAt {
   }
 };
 
-// Whole pages. A unit is one (sequence, page, head), K and V together; its page * d / 32
+// Whole pages (more than kFew tokens). A unit is one (sequence, page, head), K and V together; its page * d / 32
 // threads hold its rows in registers, 32 elements of each, so the page is read once:
 // the loads, the maxima over the unit, then the codes. 16 bytes in and 8 bytes out per
 // thread and piece, coalesced over the unit's rows. Beside the memory the instructions
@@ -293,7 +296,8 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
   }
 }
 
-// A few tokens (N <= kFew): one warp per (sequence, page, head) of K or V, a
+// A few tokens (N <= kFew; 8 tokens of 64 sequences 6.2 us, by whole pages 10.3; of 256 sequences
+// 10.1 and 24.7; of 4 5.5 and 6.2): one warp per (sequence, page, head) of K or V, a
 // row per lane group: lane l holds channels [4 l', 4 l' + 4) of a row, l' = l
 // modulo d / 4. The page's older rows are touched only when the scale grows.
 constexpr int kFew = 8;
@@ -360,7 +364,7 @@ __global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a,
 
 // Reading back: a thread takes 16 codes (one 16-byte load, two 16-byte
 // stores) of kRead rows a block's width apart, so that several loads are in
-// flight.
+// flight (16384 tokens of 16 heads: 1 row 37.0 us, 2 36.9, 4 42.1).
 constexpr int kRead = 2;
 template <bool FP16, bool INT8>
 __global__ void __launch_bounds__(256) cache_read_kernel(const CacheRows a, int tiles) {
@@ -422,6 +426,8 @@ cudaError_t write_variant(const CacheRows& a, cudaStream_t stream) {
     return launch_pdl(cache_write_few_kernel<FP16, INT8>, dim3((2 * n + 3) / 4), dim3(128), 0, stream, a, pages, 2 * n);
   }
   const int log2_t = a.c.log2_page + (a.c.d == 128 ? 7 : 6) - 5;
+  // a unit a block, of 128 threads at least: smaller blocks end and begin more evenly (19.7 us
+  // where blocks of 256 took 20.7)
   const int threads = log2_t > 8 ? 512 : log2_t > 7 ? 256 : 128;
   const unsigned per = static_cast<unsigned>(threads >> log2_t);
   return launch_pdl(cache_write_pages_kernel<FP16, INT8>, dim3((n + per - 1) / per), dim3(threads), 0, stream, a,

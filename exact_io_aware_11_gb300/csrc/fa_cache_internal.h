@@ -1,5 +1,5 @@
 // Launch descriptions of the rotary and cache entry points (fa_cache_api.cu)
-// and the kernels behind them (fa_rotary.cu, fa_cache.cu, fa_cache_attn.cu).
+// and the kernels behind them (fa_rotary.cu, fa_cache.cu, fa_cache_attn.cu, fa_cache_tile.cuh).
 #pragma once
 
 #include "fa.h"

@@ -18,7 +18,7 @@
 namespace fa {
 
 struct AttnGrid {
-  int B, HK, N, G, D;
+  int B, HK, N, G;
   int rows;       // query rows of a tile
   int row_tiles;  // tiles of N * G rows
   int log2_keys;  // keys of a step

@@ -3,7 +3,7 @@
 // tcgen05.
 //
 // Mathematics, units, shares and parts: as in fa_cache_attn.cu. A unit has NQ tiles of
-// 128 query rows (NQ = 2 above 128 rows), whose S = Q K^T and O += P V run as 128 x
+// 128 query rows, whose S = Q K^T and O += P V run as 128 x
 // 128 x d products with fp16 operands and fp32 accumulators in TMEM. A task is one
 // tile's step; task k uses S buffer k mod 2, and the issue order
 //   S(0) S(1) | PV(0) S(2) PV(1) S(3) ...
@@ -12,13 +12,21 @@
 //
 // Warps: 4 NQ softmax warps (a thread owns a query row, the TMEM lane of its
 // warp's quarter), 4 / NQ converter warps (codes to fp16 tiles in the swizzled form
-// the products read), the MMA issuer, the TMA producer. The codes are converted
-// unscaled: K's scale multiplies the scores and V's joins the exponent, both
+// the products read), the MMA issuer, 2 / NQ loaders (TMA copies of whole pages). The codes are
+// converted unscaled: K's scale multiplies the scores and V's joins the exponent, both
 // constant over 16 columns, so that the converters do nothing but convert.
 //
-// What bounds it: with 256 rows a step is 2048 cycles of products and as many of
-// exponentials, with 96 KB of shared-memory traffic for the conversion beside the 192 KB
-// that the products read; with few rows, the conversion and the cache itself.
+// What bounds it, and what it measured (GPU time, d = 128):
+//   Chunks (NQ = 2; 2048 tokens of 16 heads on 4 over 16384, e4m3, pages of 64): 212 us, 1215
+//   TFLOP/s with the merge. A step is 2048 cycles of products and takes some 3500: softmax,
+//   P V and the next S follow one another within a tile, and the two tiles cover each other only in
+//   part. Tensor pipe 55 %, issue slots 41 %, no other pipe above 35 %. Tried and slower, the chunk
+//   then at 230 us: one pass over the scores with the reference moved afterwards (304: spills) or
+//   chunk by chunk (326), and P handed over in halves (247). int8 codes take three instructions
+//   on the busiest pipe where e4m3 takes two conversions: 141 us where e4m3 takes 122 (2
+//   sequences of 1024 on 8192).
+//   Drafts (REP = 2; 5 tokens of 16 heads on 2, 16 sequences of 2000 to 16384, pages of 16): 35 us,
+//   of which 15 steps of 1 us (5 TB/s of codes), 5 us of start, 3 us of end and the merge's 4.
 #pragma once
 
 #include "fa_cache_internal.h"

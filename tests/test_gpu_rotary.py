@@ -49,6 +49,8 @@ def check(y, x, rot, pos, dt, back=False, tag=""):
 @pytest.mark.parametrize("B,H,HK,N,d,r,storage", [
     (1, 1, 1, 1, 64, 64, "bhnd"), (3, 4, 2, 7, 64, 64, "bnhd"), (2, 5, 1, 33, 128, 128, "packed"), (2, 3, 3, 5, 128, 64, "bnhd"),
     (1, 2, 1, 9, 64, 20, "bhnd"), (2, 2, 2, 4, 128, 2, "packed"), (1, 3, 2, 130, 64, 48, "bnhd"), (2, 16, 4, 600, 128, 96, "bhnd"),
+    # several heads to a thread, their number not a multiple of it
+    (2, 16, 3, 2100, 128, 96, "bhnd"), (2, 13, 2, 2100, 128, 128, "bnhd"), (1, 13, 2, 1500, 64, 20, "bnhd"),
 ])
 def test_forward_and_backward(fa, B, H, HK, N, d, r, storage, interleaved, dt):
     rot = fa.rotary_frequencies(r, interleaved=interleaved)
