@@ -3,11 +3,11 @@
 //
 // Mathematics: with codes kc, vc and scales ks, vs of each page,
 //   x_j = scale log2e ks (q . kc_j),  y_j = x_j + log2 vs_j,  M = max_j y_j,
-//   w_j = 2^(y_j - M + 11),  O = sum_j w_j vc_j / sum_j w_j / vs_j,
-//   LSE = (M - 11 + log2 sum_j w_j / vs_j) ln 2.
+//   w_j = 2^(y_j - M + 7),  O = sum_j w_j vc_j / sum_j w_j / vs_j,
+//   LSE = (M - 7 + log2 sum_j w_j / vs_j) ln 2.
 // Taking V's scale into the exponent keeps it out of the products, and the
 // running maximum then sits on the weight that V is really given: the weights are
-// rounded to fp16 (11 bits, against bf16's 8) and 2^25 below the largest one
+// rounded to fp16 (11 bits, against bf16's 8) and 2^21 below the reference
 // they still have all of them. The sum is formed from the unrounded weights. Codes of
 // either format are exact in fp16. A row of q is scaled by a power of two so that
 // its largest value lies in [2^14, 2^15): exact for every value within 2^-28 of it.
@@ -17,7 +17,7 @@
 // (128 keys, K and V: 32 KB at d = 128) with TMA copies of whole pages, and four
 // consumer warps, each with 32 keys of every stage and a softmax of its own, which
 // meet only when a unit ends. The reference maximum moves only when a weight
-// would pass 2^4, so that most tiles need no reduction across lanes. Products run
+// would pass 2^15, so that most tiles need no reduction across lanes. Products run
 // on the warp matrix instruction with keys (K) and channels (V) on its 16 rows and
 // the query rows on its 8 columns, so that a group of 8 query rows costs one pass
 // over the converted codes: the tcgen05 form needs 128 rows and would convert

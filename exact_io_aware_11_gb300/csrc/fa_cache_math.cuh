@@ -10,12 +10,15 @@
 namespace fa {
 
 constexpr float kLn2Cache = 0.69314718055994530942f;
-constexpr float kSlack = 4.f;                // log2 units a weight may stand above the reference
+// Log2 units a weight may stand above the reference before that moves (a chunk with 4 210.8 us, 6
+// 203.0, 8 201.3, 10 201.1: heavy-tailed scores move it often, and moving O costs a tile more than a
+// step's weights). Weights within 2^21 below the reference keep fp16's 11 bits.
+constexpr float kSlack = 8.f;
 constexpr float kBias = 15.f - kSlack;       // weights are at most 2^15
 constexpr float kMinScale = 0x1p-100f;       // a page whose V scale is not above it counts as zeros
 // V scale that stands in for a page of zeros, whose weights count in the sum alone. A weight whose
-// exponent lies 2^-137 below the reference is lost to the sum as well, so the stand-in is
-// near the scales that occur: pages of zeros keep 2^-47 of the sum beside scales up to 2^30.
+// exponent lies 2^-133 below the reference is lost to the sum as well, so the stand-in is
+// near the scales that occur: pages of zeros keep 2^-43 of the sum beside scales up to 2^30.
 constexpr float kZeroScale = 0x1p-60f;
 
 __device__ __forceinline__ float2 unpack16(uint32_t w, bool fp16) {

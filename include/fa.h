@@ -457,7 +457,7 @@ size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, 
  * chip (exactly) and the scales applied to the scores and the weights; pages
  * with a V scale of 2^-100 or less count as zeros. Where V scales of one sequence
  * differ by a factor r (a page of zeros standing for 2^-60), weights below
- * 2^-137 r of the largest are lost: r up to 2^90 costs nothing in 32 bits.
+ * 2^-133 r of the largest are lost: r up to 2^90 costs nothing in 32 bits.
  * Query rows that see no token, and rows i >= q_len[b], get O = 0, LSE = -inf.
  *   workspace : DEVICE, 16-byte aligned, contents ignored, or NULL with
  *               workspace_bytes = 0; with fewer bytes than

@@ -6,7 +6,7 @@ its rounding has one answer. A value read back is off by half a step of its type
 
 Attention's bounds, from what the kernel rounds (A = sum p |v|, E = sum |q k| scale, both of the
 row): the weights are rounded to fp16 (2^-12 each way, in the numerator alone: 2^-12 A) or
-flushed 2^-36 below the largest; a score is an fp32 sum of at most 128 exact products (128 *
+flushed 2^-32 below the largest; a score is an fp32 sum of at most 128 exact products (128 *
 2^-24 E = 2^-17 E at the very most) whose error moves every weight by that part, numerator and sum
 both, plus 2^-21 for the exponential and 2^-21 for fp32's argument near 2^5; sums of n weights
 add n 2^-24 at most (pairs of chunks: far less). O is rounded once: half a step. So
