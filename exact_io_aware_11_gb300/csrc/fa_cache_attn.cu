@@ -772,7 +772,7 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 //   up to 128: one tile (128 rows 29.0, in a unit of two tiles 32.7);
 //   above: a unit of two tiles, whose step costs 1.6 times one tile's, where that saves time (384
 //     rows do not: 124 and 121) and the CTAs have some 8 steps each to make good its longer
-//     start and larger merge (107 steps a CTA 212, with single tiles 267; 13 steps 47.5 and 52.5;
+//     start and larger merge (107 steps a CTA 212, with single tiles 267, before the last steps for speed; 13 steps 47.5 and 52.5;
 //     7 steps 37.9 and 36.5; 3 steps 37.5 and 31.1).
 // lead: beginning one more unit costs a CTA 1 us (rows of up to 16, steps of 0.7 us) and 5 us (tiles,
 // steps of 1 to 2 us); counting it shares ragged batches out more evenly: drafts 39.9 us with

@@ -17,14 +17,13 @@
 // constant over 16 columns, so that the converters do nothing but convert.
 //
 // What bounds it, and what it measured (GPU time, d = 128):
-//   Chunks (NQ = 2; 2048 tokens of 16 heads on 4 over 16384, e4m3, pages of 64): 212 us, 1215
-//   TFLOP/s with the merge. A step is 2048 cycles of products and takes some 3500: softmax,
+//   Chunks (NQ = 2; 2048 tokens of 16 heads on 4 over 16384, e4m3, pages of 64): 197 us, 1307
+//   TFLOP/s with the merge. A step is 2048 cycles of products and takes some 3200: softmax,
 //   P V and the next S follow one another within a tile, and the two tiles cover each other only in
-//   part. Tensor pipe 55 %, issue slots 41 %, no other pipe above 35 %. Tried and slower, the chunk
-//   then at 230 us: one pass over the scores with the reference moved afterwards (304: spills) or
-//   chunk by chunk (326), and P handed over in halves (247). int8 codes take three instructions
-//   on the busiest pipe where e4m3 takes two conversions: 141 us where e4m3 takes 122 (2
-//   sequences of 1024 on 8192).
+//   part. Tensor pipe 55 to 60 %, issue slots 41 %, no other pipe above 35 %. Tried and slower: one
+//   pass over the scores with the reference moved afterwards (304 us where two passes took 230:
+//   spills) or chunk by chunk (326). int8 codes take three instructions on the busiest pipe where
+//   e4m3 takes two conversions: 131 us where e4m3 takes 114 (2 sequences of 1024 on 8192).
 //   Drafts (REP = 2; 5 tokens of 16 heads on 2, 16 sequences of 2000 to 16384, pages of 16): 35 us,
 //   of which 15 steps of 1 us (5 TB/s of codes), 5 us of start, 3 us of end and the merge's 4.
 #pragma once
