@@ -766,14 +766,14 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 }  // namespace
 
 // Rows of a unit, from the rows of a (sequence, cache head); GPU time in us at d = 128, pages of 64:
-//   up to 8, 16: one or two groups of the few-row kernel (8 rows of 64 sequences 103.0 as one
-//     group, 106.0 as two, 145 as a tile; 16 rows 110 and 148);
-//   up to 64: a tile with its rows twice (40 rows of 16 sequences 32.5, in a tile of 128 34.4);
-//   up to 128: one tile (128 rows 29.0, in a unit of two tiles 32.7);
-//   above: a unit of two tiles, whose step costs 1.6 times one tile's, where that saves time (384
-//     rows do not: 124 and 121) and the CTAs have some 8 steps each to make good its longer
-//     start and larger merge (107 steps a CTA 212, with single tiles 267, before the last steps for speed; 13 steps 47.5 and 52.5;
-//     7 steps 37.9 and 36.5; 3 steps 37.5 and 31.1).
+//   up to 8, 16: one or two groups of the few-row kernel (8 rows of 64 sequences 103.2 as one
+//     group, 106.0 as two, 156 as a tile; 16 rows 110 and 158);
+//   up to 64: a tile with its rows twice (40 rows of 16 sequences 33.1, in a tile of 128 34.8);
+//   up to 128: one tile (128 rows 29.0, in a unit of two tiles 31.3);
+//   above: a unit of two tiles, whose step costs some 1.4 times one tile's, where the CTAs have about
+//     6 steps each to make good its longer start and larger merge (107 steps a CTA 198, with
+//     single tiles 266; 13 steps 45.6 and 51.3; 7 steps 37.1 and 36.9; 3 steps 36.3 and 31.6; 384
+//     rows, which leave half a tile empty, at 54 steps 112.9 and 118.7).
 // lead: beginning one more unit costs a CTA 1 us (rows of up to 16, steps of 0.7 us) and 5 us (tiles,
 // steps of 1 to 2 us); counting it shares ragged batches out more evenly: drafts 39.9 us with
 // none, 37.0 with 4, 36.9 with 8; a chunk 243.3, 242.5, 247.0; single tokens of 64 sequences
@@ -783,9 +783,8 @@ AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
   p.log2_keys = 7;
   p.cap_steps = (cap + 127) >> 7;
   if (p.cap_steps < 1) p.cap_steps = 1;
-  const long long heads = static_cast<long long>(B) * HK, one = (rows + 127) / 128, two = (rows + 255) / 256;
-  const long long long_runs = 8LL * sm_count();
-  const bool wide = two * 8 < one * 5 && (heads * two >= long_runs || heads * two * p.cap_steps >= long_runs);
+  const long long heads = static_cast<long long>(B) * HK, two = (rows + 255) / 256, enough = 6LL * sm_count();
+  const bool wide = rows > 128 && (heads * two >= enough || heads * two * p.cap_steps >= enough);
   p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 64 : wide ? 256 : 128;
   p.lead = p.rows <= 16 ? 1 : 4;
   p.units = heads * ((rows + p.rows - 1) / p.rows);

@@ -392,8 +392,8 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   using L = TileLayout<D, NQ>;
   // The weights are handed over in halves of 64 keys, so that P V begins under the second
   // half's exponentials: a chunk in e4m3 201.5 us as a whole, 196.7 in halves; in int8, where
-  // the converters are behind, 131.9 and 141.3.
-  constexpr bool kHalves = REP == 1 && !INT8;
+  // the converters are behind, 131.9 and 141.3; in units of one tile (384 rows) 118.7 and 130.2.
+  constexpr bool kHalves = NQ == 2 && !INT8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShare share;
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
