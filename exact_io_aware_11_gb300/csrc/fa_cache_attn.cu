@@ -25,7 +25,7 @@
 //
 // Measured (GPU time): one token of 64 sequences of 1000 to 8192, 32 heads on 8, d = 128, e4m3: 101
 // us, 5950 GB/s; the same with 32 heads on 32 (16 sequences of 8192) 92 us, 5800 GB/s; 64
-// sequences of 4096, 12 heads, d = 64: 90 us, 4450 GB/s, where scores and weights weigh twice as
+// sequences of 4096, 12 heads, d = 64: 75 us, 5370 GB/s, where scores and weights weigh twice as
 // much beside a row's bytes; one sequence of 131071, 16 heads on 4, int8: 33.5 us, 4000 GB/s, of which
 // 17 us stream at the memory's rate, 2 us share the steps out, 3 us bring the first tile and 4 us
 // merge; one of 1024, 12 heads, d = 64: 10.3 us, launches and latencies.
@@ -44,9 +44,15 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kTile = 32;                    // keys of a warp's tile
 constexpr int kKeys = kWarps * kTile;        // keys of a step
 
+// CTAs of the few-row kernel that an SM holds: at d = 64 with one group of rows its registers
+// leave room for a third, which hides more of the steps' latencies (64 sequences of 4096, 12
+// heads: 75 us, with two 90).
+constexpr int few_row_ctas(int d, int rows) { return d == 64 && rows <= 8 ? 3 : 2; }
+
 template <int D, int NT>
 struct Layout {
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kCtas = few_row_ctas(D, 8 * NT);  // on an SM
+  static constexpr int kStages = D == 128 ? 3 : kCtas == 3 ? 4 : 6;
   static constexpr int kMat = kKeys * D;               // K or V of a step
   static constexpr int kStage = 2 * kMat;
   static constexpr int kRing = kStages * kStage;
@@ -55,7 +61,7 @@ struct Layout {
   static constexpr int kQuery = kMerge + kWarps * 4 * D * 4;  // NT = 2: fragments of q, rows' factors
   static constexpr int kBars = kQuery + (NT > 1 ? NT * (D / 16) * 256 + NT * 32 : 0);
   static constexpr int kSmem = kBars + 2 * kStages * 8 + 1024;  // slack: 1024-byte alignment
-  static_assert(2 * (kSmem + 1024 + 1024) <= 228 * 1024, "two CTAs per SM");
+  static_assert(kCtas * (kSmem + 1024 + 1024) <= 228 * 1024, "kCtas CTAs on an SM");
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -213,7 +219,7 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
 
 // NT groups of 8 query rows per unit.
 template <int D, int NT, bool INT8>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
     cache_attn_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
   using L = Layout<D, NT>;
   constexpr int kStages = L::kStages;
@@ -778,7 +784,7 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 // steps of 1 to 2 us); counting it shares ragged batches out more evenly: drafts 39.9 us with
 // none, 37.0 with 4, 36.9 with 8; a chunk 243.3, 242.5, 247.0; single tokens of 64 sequences
 // 102.7 with none, 101.5 with 1, 101.5 with 4.
-AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
+AttnPlan attn_plan(int B, int HK, long long rows, long long cap, int d) {
   AttnPlan p{};
   p.log2_keys = 7;
   p.cap_steps = (cap + 127) >> 7;
@@ -788,7 +794,7 @@ AttnPlan attn_plan(int B, int HK, long long rows, long long cap) {
   p.rows = rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 64 ? 64 : wide ? 256 : 128;
   p.lead = p.rows <= 16 ? 1 : 4;
   p.units = heads * ((rows + p.rows - 1) / p.rows);
-  const long long most = (p.rows > 16 ? 1LL : 2LL) * sm_count();  // CTAs that an SM holds
+  const long long most = (p.rows > 16 ? 1LL : few_row_ctas(d, p.rows)) * sm_count();
   p.ctas = static_cast<int>(p.units >= most || p.units * p.cap_steps >= most ? most : p.units * p.cap_steps);
   return p;
 }
@@ -808,13 +814,13 @@ static bool attn_cut(const AttnPlan& p) {
 }
 
 size_t cache_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width) {
-  const AttnPlan p = attn_plan(B, HK, static_cast<long long>(N) * G, static_cast<long long>(table_width) * page);
+  const AttnPlan p = attn_plan(B, HK, static_cast<long long>(N) * G, static_cast<long long>(table_width) * page, d);
   return attn_cut(p) ? attn_workspace(p.ctas, p.rows, d).total : 0;
 }
 
 cudaError_t launch_cache_attention(const CacheAttnLaunch& a, cudaStream_t stream) {
   const long long rows = static_cast<long long>(a.N) * a.G, cap = static_cast<long long>(a.c.table_width) * a.c.page;
-  const AttnPlan p = attn_plan(a.B, a.c.H, rows, cap);
+  const AttnPlan p = attn_plan(a.B, a.c.H, rows, cap, a.c.d);
   AttnGrid g{};
   g.B = a.B;
   g.HK = a.c.H;

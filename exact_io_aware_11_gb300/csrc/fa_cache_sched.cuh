@@ -202,7 +202,7 @@ struct AttnPlan {
   int rows, log2_keys, ctas, lead;
   long long units, cap_steps;
 };
-AttnPlan attn_plan(int B, int HK, long long rows, long long cap);
+AttnPlan attn_plan(int B, int HK, long long rows, long long cap, int d);
 
 // Tiles of 64, 128 (g.rows) or 2 x 128 query rows on tcgen05 (fa_cache_tile.cuh), one
 // translation unit for each format.
