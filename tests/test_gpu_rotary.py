@@ -51,6 +51,8 @@ def check(y, x, rot, pos, dt, back=False, tag=""):
     (1, 2, 1, 9, 64, 20, "bhnd"), (2, 2, 2, 4, 128, 2, "packed"), (1, 3, 2, 130, 64, 48, "bnhd"), (2, 16, 4, 600, 128, 96, "bhnd"),
     # several heads to a thread, their number not a multiple of it
     (2, 16, 3, 2100, 128, 96, "bhnd"), (2, 13, 2, 2100, 128, 128, "bnhd"), (1, 13, 2, 1500, 64, 20, "bnhd"),
+    (2, 5, 2, 40, 128, 100, "packed"), (1, 11, 1, 70, 64, 62, "bnhd"), (3, 1, 1, 5, 128, 126, "bhnd"), (2, 4, 4, 9, 64, 34, "bhnd"),
+    (2, 13, 2, 2100, 128, 100, "bnhd"), (4, 30, 3, 1100, 64, 62, "bhnd"),
 ])
 def test_forward_and_backward(fa, B, H, HK, N, d, r, storage, interleaved, dt):
     rot = fa.rotary_frequencies(r, interleaved=interleaved)
