@@ -265,7 +265,7 @@ def test_scales_far_apart(fa):
 
 
 @pytest.mark.parametrize("fmt", ["e4m3", "int8"])
-@pytest.mark.parametrize("d,G,N,B", [(128, 1, 1, 1), (64, 6, 2, 1), (128, 8, 4, 1), (64, 2, 60, 1), (128, 4, 50, 1), (64, 4, 50, 640)])
+@pytest.mark.parametrize("d,G,N,B", [(128, 1, 1, 1), (64, 6, 2, 1), (128, 8, 4, 1), (64, 2, 60, 1), (128, 4, 50, 1), (128, 4, 9, 200), (64, 4, 50, 640)])
 def test_pages_of_zeros_beside_large_values(fa, d, G, N, B, fmt):
     """Tokens whose V is zero take their share of the weights whatever the other pages' scale."""
     page, W = 32, 9
@@ -441,10 +441,10 @@ def test_many_units_and_long_chunks(fa, d, page, H, HK, N, B, longest, fmt, dt):
     assert torch.isneginf(a[1]).equal(torch.isneginf(b[1]))
 
 
-@pytest.mark.parametrize("G,N,B", [(1, 3, 2), (2, 12, 2), (1, 40, 2), (4, 60, 2), (1, 400, 2), (2, 100, 640)])
+@pytest.mark.parametrize("G,N,B", [(1, 3, 2), (2, 12, 2), (1, 40, 2), (4, 60, 2), (1, 400, 2), (2, 12, 300), (1, 50, 300), (2, 100, 640)])
 def test_nan_behind_a_row_has_no_effect_on_it(fa, G, N, B):
     """NaN in K and V at token t reaches the rows that see t, all of each of them, and no other row, in every
-    kernel (the last size fills units of two tiles); rows of other heads and sequences stay as they are."""
+    kernel (the last three sizes: tiles with their rows twice, units of two tiles); rows of other heads and sequences stay as they are."""
     L = max(N, 1) + 90
     m = filled(fa, 2, 2, 16, 64, "e4m3", [L, L], seed=20)
     table = torch.cat([m.table, m.table[:1].expand(B - 2, -1)]).cuda()

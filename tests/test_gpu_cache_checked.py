@@ -29,9 +29,10 @@ def run_cases(fa):
         for G, N in ((1, 1), (3, 4), (2, 30), (4, 90)):
             q = torch.randn((B, HK * G, N, d), generator=g).to(torch.bfloat16).cuda()
             res += fa.cache_attention(q, cache, table, n)
-        q = torch.randn((640, HK * 4, 50, d), generator=g).to(torch.bfloat16).cuda()  # units of two tiles
-        many = fa.cache_attention(q, cache, table[:1].expand(640, -1), n[:1].repeat(640))
-        res += [t[::71] for t in many]
+        for N in (10, 50):  # tiles with their rows twice, units of two tiles
+            q = torch.randn((640, HK * 4, N, d), generator=g).to(torch.bfloat16).cuda()
+            many = fa.cache_attention(q, cache, table[:1].expand(640, -1), n[:1].repeat(640))
+            res += [t[::71] for t in many]
         torch.cuda.synchronize()
         assert fa.device_status() == fa.FA_OK
         out[i] = [t.cpu() for t in res]
