@@ -165,9 +165,9 @@ struct UnitAt {
   }
 };
 
-// Whole pages (more than kFew tokens). A unit is one (sequence, page, head), K and V together; its page * d / 32
-// threads hold its rows in registers, 32 elements of each, so the page is read once:
-// the loads, the maxima over the unit, then the codes. 16 bytes in and 8 bytes out per
+// Pages (more than kFew tokens). A unit is one (sequence, page, head), K and V together; its R d / 32
+// threads hold its R new rows in registers (R: a page, or the power of two that holds N), 32
+// elements of each, so they are read once: the loads, the maxima over the unit, then the codes. 16 bytes in and 8 bytes out per
 // thread and piece, coalesced over the unit's rows. Beside the memory the instructions
 // around few elements bind it, so K and V share a thread's place, places within the page
 // are 32-bit, and a thread's four pieces lie a constant stride apart.
@@ -194,7 +194,7 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
     hi = static_cast<int>(min(static_cast<long long>(a.c.page), sp.end - page0));
     if (lo < hi) page = page_of(a, b, pi);  // needed after the loads below, which do not wait for it
   }
-  const int row0 = t >> log2_chunks, row_step = 1 << (log2_t - log2_chunks);
+  const int row0 = lo + (t >> log2_chunks), row_step = 1 << (log2_t - log2_chunks);
   const long long at0 = b * a.st.b + h * a.st.h + (before + row0) * a.st.n + (t & ((1 << log2_chunks) - 1)) * 8;
   const long long src_step = row_step * a.st.n;
   uint4 x[2][4];
@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = row0 + k * row_step;
-      x[kv][k] = row >= lo && row < hi ? __ldg(reinterpret_cast<const uint4*>(src + k * src_step)) : make_uint4(0, 0, 0, 0);
+      x[kv][k] = row < hi ? __ldg(reinterpret_cast<const uint4*>(src + k * src_step)) : make_uint4(0, 0, 0, 0);
     }
   }
   const long long ph = static_cast<long long>(page) * a.c.H + h;
@@ -268,28 +268,32 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
   for (int kv = 0; kv < 2; ++kv) {
     const float s = fmaxf(s_old[kv], scale_for<INT8>(amax[kv]));
     const float inv = inverse(s);
-    uint8_t* const dst = a.c.code[kv] + (ph << a.c.log2_page) * a.c.d + t * 8;
-    if (finite && lo == 0 && hi == a.c.page) {  // a whole page of finite values
+    uint8_t* const dst = a.c.code[kv] + ((ph << a.c.log2_page) + lo) * a.c.d + t * 8;
+    if (finite) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         float v[2][4];
         values8<FP16>(x[kv][k], v);
-        *reinterpret_cast<uint2*>(dst + (k * 8 << log2_t)) =
-            make_uint2(encode4_finite<INT8>(v[0], inv), encode4_finite<INT8>(v[1], inv));
+        if (row0 + k * row_step < hi)
+          *reinterpret_cast<uint2*>(dst + (k * 8 << log2_t)) =
+              make_uint2(encode4_finite<INT8>(v[0], inv), encode4_finite<INT8>(v[1], inv));
       }
     } else {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int row = row0 + k * row_step;
-        uint2* const at = reinterpret_cast<uint2*>(dst + (k * 8 << log2_t));
-        if (row >= lo && row < hi) {
-          float v[2][4];
-          values8<FP16>(x[kv][k], v);
-          *at = make_uint2(encode4<INT8>(v[0], inv), encode4<INT8>(v[1], inv));
-        } else if (row < lo && s > s_old[kv]) {
-          const uint2 c = *at;
-          *at = make_uint2(move4<INT8>(c.x, s_old[kv] * inv), move4<INT8>(c.y, s_old[kv] * inv));
-        }
+        float v[2][4];
+        values8<FP16>(x[kv][k], v);
+        if (row0 + k * row_step < hi)
+          *reinterpret_cast<uint2*>(dst + (k * 8 << log2_t)) = make_uint2(encode4<INT8>(v[0], inv), encode4<INT8>(v[1], inv));
+      }
+    }
+    if (lo > 0 && s > s_old[kv]) {  // the page's older rows move to the new scale
+      uint8_t* const old = a.c.code[kv] + (ph << a.c.log2_page) * a.c.d + t * 8;
+#pragma unroll 1
+      for (int row = t >> log2_chunks, k = 0; row < lo; row += row_step, ++k) {
+        uint2* const at = reinterpret_cast<uint2*>(old + (k * 8 << log2_t));
+        const uint2 c = *at;
+        *at = make_uint2(move4<INT8>(c.x, s_old[kv] * inv), move4<INT8>(c.y, s_old[kv] * inv));
       }
     }
     if (t == 0) a.c.scale[kv][ph] = s;
@@ -425,7 +429,9 @@ cudaError_t write_variant(const CacheRows& a, cudaStream_t stream) {
   if (a.N <= kFew) {
     return launch_pdl(cache_write_few_kernel<FP16, INT8>, dim3((2 * n + 3) / 4), dim3(128), 0, stream, a, pages, 2 * n);
   }
-  const int log2_t = a.c.log2_page + (a.c.d == 128 ? 7 : 6) - 5;
+  int log2_rows = 4;
+  while (log2_rows < a.c.log2_page && (1 << log2_rows) < a.N) ++log2_rows;
+  const int log2_t = log2_rows + (a.c.d == 128 ? 7 : 6) - 5;
   // a unit a block, of 128 threads at least: smaller blocks end and begin more evenly (19.7 us
   // where blocks of 256 took 20.7)
   const int threads = log2_t > 8 ? 512 : log2_t > 7 ? 256 : 128;

@@ -794,7 +794,8 @@ AttnPlan attn_plan(int B, int HK, long long rows, long long cap, int d) {
   if (p.cap_steps < 1) p.cap_steps = 1;
   const long long heads = static_cast<long long>(B) * HK, two = (rows + 255) / 256, enough = 6LL * sm_count();
   const bool wide = rows > 128 && (heads * two >= enough || heads * two * p.cap_steps >= enough);
-  const bool brief = heads * p.cap_steps < 3LL * sm_count();  // as tiles of up to 64 rows
+  const long long groups = (rows + 15) / 16, s = p.cap_steps;
+  const bool brief = heads * s < 3LL * sm_count() || groups * (10 + 15 * s) < 100 + 22 * s;
   p.rows = rows <= 8 ? 8 : rows <= 16 || (rows <= 64 && brief) ? 16 : rows <= 64 ? 64 : wide ? 256 : 128;
   p.lead = p.rows <= 16 ? 1 : 4;
   p.units = heads * ((rows + p.rows - 1) / p.rows);
