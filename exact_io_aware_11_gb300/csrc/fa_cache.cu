@@ -167,10 +167,11 @@ struct UnitAt {
 
 // Pages (more than kFew tokens). A unit is one (sequence, page, head), K and V together; its R d / 32
 // threads hold its R new rows in registers (R: a page, or the power of two that holds N), 32
-// elements of each, so they are read once: the loads, the maxima over the unit, then the codes. 16 bytes in and 8 bytes out per
-// thread and piece, coalesced over the unit's rows. Beside the memory the instructions
-// around few elements bind it, so K and V share a thread's place, places within the page
-// are 32-bit, and a thread's four pieces lie a constant stride apart.
+// elements of each, so they are read once: the loads, the maxima over the unit, then the codes.
+// 16 bytes in and 8 bytes out per thread and piece, coalesced over the unit's rows. Beside the
+// memory the instructions around few elements bind it, so K and V share a thread's place, places
+// within the page are 32-bit, and a thread's four pieces lie a constant stride apart. 38 tokens of
+// 224 sequences, 12 heads, pages of 128 take 29 us with R = 64 and 60 with R = 128.
 template <bool FP16, bool INT8>
 __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows a, int log2_t, int pages_per_seq,
                                                                 unsigned units) {
@@ -300,8 +301,9 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
   }
 }
 
-// A few tokens (N <= kFew; 8 tokens of 64 sequences 6.2 us, by whole pages 10.3; of 256 sequences
-// 10.1 and 24.7; of 4 5.5 and 6.2): one warp per (sequence, page, head) of K or V, a
+// A few tokens (N <= kFew; us here and by the kernel above: 1 token of 64 sequences 5.5, 6.2; 8 tokens
+// of 4 5.1, 6.2, of 64 6.2, 6.2, of 256 8.4, 10.3 in e4m3 and 10.2, 10.1 in int8): one warp per
+// (sequence, page, head) of K or V, a
 // row per lane group: lane l holds channels [4 l', 4 l' + 4) of a row, l' = l
 // modulo d / 4. The page's older rows are touched only when the scale grows.
 constexpr int kFew = 8;

@@ -777,7 +777,7 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 //   up to 64: a tile with its rows twice (40 rows of 16 sequences 33.1, in a tile of 128 34.8) where
 //     the CTAs have 3 steps each; otherwise groups of 16, which start and end sooner though each
 //     reads the cache (2 steps a CTA, 32 rows: 18.8 in groups, 24.2 as tiles; 64 rows 22.7 and 26.4;
-//     7 steps 28.1 and 25.7; 27 steps, 94.3 and 73.8);
+//     7 steps 28.1 and 25.7; 54 steps 94.3 and 73.8; 1024 units of 4 steps 75.3 and 74.0);
 //   up to 128: one tile (128 rows 29.0, in a unit of two tiles 31.3);
 //   above: a unit of two tiles, whose step costs some 1.4 times one tile's, where the CTAs have about
 //     6 steps each to make good its longer start and larger merge (107 steps a CTA 198, with
@@ -794,8 +794,7 @@ AttnPlan attn_plan(int B, int HK, long long rows, long long cap, int d) {
   if (p.cap_steps < 1) p.cap_steps = 1;
   const long long heads = static_cast<long long>(B) * HK, two = (rows + 255) / 256, enough = 6LL * sm_count();
   const bool wide = rows > 128 && (heads * two >= enough || heads * two * p.cap_steps >= enough);
-  const long long groups = (rows + 15) / 16, s = p.cap_steps;
-  const bool brief = heads * s < 3LL * sm_count() || groups * (10 + 15 * s) < 100 + 22 * s;
+  const bool brief = heads * p.cap_steps < 3LL * sm_count();  // as tiles of up to 64 rows
   p.rows = rows <= 8 ? 8 : rows <= 16 || (rows <= 64 && brief) ? 16 : rows <= 64 ? 64 : wide ? 256 : 128;
   p.lead = p.rows <= 16 ? 1 : 4;
   p.units = heads * ((rows + p.rows - 1) / p.rows);
