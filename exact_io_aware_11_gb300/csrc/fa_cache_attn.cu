@@ -57,8 +57,8 @@ struct Layout {
   static constexpr int kStage = 2 * kMat;
   static constexpr int kRing = kStages * kStage;
   static constexpr int kScales = kRing;                // [stages][8 groups of 16 keys] ks, vs
-  static constexpr int kMerge = kScales + kStages * 64;  // four rows of every warp, fp32
-  static constexpr int kQuery = kMerge + kWarps * 4 * D * 4;  // NT = 2: fragments of q, rows' factors
+  static constexpr int kQuery = kScales + kStages * 64;  // NT = 2: fragments of q, rows' factors
+  static_assert(kWarps * 8 * NT * D * 4 <= kStage, "the warps' O of a unit fits a stage");
   static constexpr int kBars = kQuery + (NT > 1 ? NT * (D / 16) * 256 + NT * 32 : 0);
   static constexpr int kSmem = kBars + 2 * kStages * 8 + 1024;  // slack: 1024-byte alignment
   static_assert(kCtas * (kSmem + 1024 + 1024) <= 228 * 1024, "kCtas CTAs on an SM");
@@ -228,11 +228,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShare share;
   __shared__ long long part[kThreads / 32];
-  __shared__ float sm_m[kWarps][kRows], sm_l[kWarps][kRows];
+  __shared__ float sm_m[2][kWarps][kRows], sm_l[2][kWarps][kRows];  // of a unit, in turn
   __shared__ int abort_flag;
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
-  float* const merge = reinterpret_cast<float*>(smem + L::kMerge);
   uint64_t* const full = reinterpret_cast<uint64_t*>(smem + L::kBars);
   uint64_t* const empty = full + kStages;
   check_init(a.status);
@@ -256,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
   }
   if (g.split && threadIdx.x == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
   bool alive = true;  // no wait has given up
-  int stage = 0;
+  int stage = 0, turn = 0;
   uint32_t phase = 0;
 
   while (!cur.done(g)) {
@@ -468,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
         }
       }
       __syncwarp();  // every lane has read the stage
+      if (step + 1 == steps) break;  // the unit's last stage is kept: the warps join in it
       if (lane == 0) mbar_arrive(empty + stage);
       if (++stage == kStages) {
         stage = 0;
@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
     }
     cur.skip(g, steps);
 
-    // ---- join the warps' keys
+    // ---- join the warps' keys, through the last step's stage
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -488,70 +488,90 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
           m[n][k] = -INFINITY;
         }
         if (gq == 0) {
-          sm_m[warp][n * 8 + 2 * t + k] = m[n][k];
-          sm_l[warp][n * 8 + 2 * t + k] = l[n][k];
+          sm_m[turn][warp][n * 8 + 2 * t + k] = m[n][k];
+          sm_l[turn][warp][n * 8 + 2 * t + k] = l[n][k];
         }
       }
-    named_bar_sync(1, kWarps * 32);
+    named_bar_sync(1, kWarps * 32);  // also: every warp has read its part of the stage
     const bool last = step0 + steps == x.steps, whole = step0 == 0 && last;
     const int slot = 2 * blockIdx.x + (step0 == 0 ? 1 : 0);
     if (g.split && !whole && last && threadIdx.x == 0)
       g.record[blockIdx.x] =
           make_int4(x.b * g.row_tiles + x.row0 / g.rows, h, attn_cta_of(unit_first, share), 0);
+    // O of warp w, row r: D words at (w kRows + r) D; pair i of group gq at 2 (8 i + gq), and half the
+    // banks on for every other pair of rows, so that a warp's 64 words meet every bank twice
+    float* const merge = reinterpret_cast<float*>(smem + stage * L::kStage);
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {  // rows n * 8 + 2 t + k
-        {
-          const int r = n * 8 + 2 * t + k;
-          float M = sm_m[0][r];
+      for (int k = 0; k < 2; ++k) {
+        const int r = n * 8 + 2 * t + k;
+        float M = sm_m[turn][0][r];
 #pragma unroll
-          for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
-          const float f = ex2(m[n][k] - (M == -INFINITY ? 0.f : M));
-          float* const at = merge + (warp * 4 + t) * D + gq * (D / 8);
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[turn][w][r]);
+        const float f = ex2(m[n][k] - (M == -INFINITY ? 0.f : M));
+        float* const at = merge + (warp * kRows + r) * D;
 #pragma unroll
-          for (int i = 0; i < kM; ++i)
-            *reinterpret_cast<float2*>(at + 2 * i) = make_float2(o[i][n][k] * f, o[i][n][2 + k] * f);
-        }
-        named_bar_sync(1, kWarps * 32);
-        constexpr int kPer = D / 32;  // channels of a row per lane
-        const int d0 = lane * kPer, r = n * 8 + 2 * warp + k;
-        float M = sm_m[0][r];
-#pragma unroll
-        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[w][r]);
-        float sum = 0.f, acc[kPer];
-#pragma unroll
-        for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          sum = fmaf(sm_l[w][r], ex2(sm_m[w][r] - (M == -INFINITY ? 0.f : M)), sum);
-#pragma unroll
-          for (int d = 0; d < kPer; ++d) acc[d] += merge[(w * 4 + warp) * D + d0 + d];
-        }
-        const int row = x.row0 + r, i = row / g.G;
-        if (!whole) {
-          const long long pr = static_cast<long long>(slot) * g.rows + r;
-#pragma unroll
-          for (int d = 0; d < kPer; d += 2)
-            *reinterpret_cast<float2*>(g.o_part + pr * D + d0 + d) = make_float2(acc[d], acc[d + 1]);
-          if (lane == 0) {
-            g.m_part[pr] = M;
-            g.l_part[pr] = sum;
-          }
-        } else if (i < g.N) {
-          const bool none = sum == 0.f;  // a row that sees no key; NaN stays NaN
-          const float inv = none ? 0.f : 1.f / sum;
-          const int head = h * g.G + (row - i * g.G);
-          uint16_t* const dst = a.o + x.b * a.so.b + head * a.so.h + i * a.so.n + d0;
-#pragma unroll
-          for (int d = 0; d < kPer; d += 2)
-            *reinterpret_cast<uint32_t*>(dst + d) = none ? 0u : pack16(acc[d] * inv, acc[d + 1] * inv, a.fp16);
-          if (lane == 0)
-            a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + i] =
-                none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
-        }
-        named_bar_sync(1, kWarps * 32);
+        for (int i = 0; i < kM; ++i)
+          *reinterpret_cast<float2*>(at + ((16 * i + 2 * gq) ^ ((t & 1) << 4))) = make_float2(o[i][n][k] * f, o[i][n][2 + k] * f);
       }
+    named_bar_sync(1, kWarps * 32);
+    constexpr int kPer = D / 32;  // channels of a row per lane
+    const int d0 = lane * kPer;
+#pragma unroll
+    for (int j = 0; j < 2 * NT; ++j) {  // a warp joins every fourth row
+      const int r = warp + kWarps * j;
+      float M = sm_m[turn][0][r];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, sm_m[turn][w][r]);
+      float sum = 0.f, acc[kPer];
+#pragma unroll
+      for (int d = 0; d < kPer; ++d) acc[d] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        sum = fmaf(sm_l[turn][w][r], ex2(sm_m[turn][w][r] - (M == -INFINITY ? 0.f : M)), sum);
+#pragma unroll
+        for (int d = 0; d < kPer; d += 2) {
+          const int pair = (d0 + d) % (D / 8) / 2;
+          const float2 v = *reinterpret_cast<const float2*>(merge + (w * kRows + r) * D +
+                                                            ((16 * pair + 2 * (d0 / (D / 8))) ^ ((r >> 1 & 1) << 4)));
+          acc[d] += v.x;
+          acc[d + 1] += v.y;
+        }
+      }
+      const int row = x.row0 + r, i = row / g.G;
+      if (!whole) {
+        const long long pr = static_cast<long long>(slot) * g.rows + r;
+#pragma unroll
+        for (int d = 0; d < kPer; d += 2)
+          *reinterpret_cast<float2*>(g.o_part + pr * D + d0 + d) = make_float2(acc[d], acc[d + 1]);
+        if (lane == 0) {
+          g.m_part[pr] = M;
+          g.l_part[pr] = sum;
+        }
+      } else if (i < g.N) {
+        const bool none = sum == 0.f;  // a row that sees no key; NaN stays NaN
+        const float inv = none ? 0.f : 1.f / sum;
+        const int head = h * g.G + (row - i * g.G);
+        uint16_t* const dst = a.o + x.b * a.so.b + head * a.so.h + i * a.so.n + d0;
+#pragma unroll
+        for (int d = 0; d < kPer; d += 2)
+          *reinterpret_cast<uint32_t*>(dst + d) = none ? 0u : pack16(acc[d] * inv, acc[d + 1] * inv, a.fp16);
+        if (lane == 0)
+          a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + i] =
+              none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
+      }
+    }
+    // the stage goes back, and the statistics' other half is next: a warp that is a unit ahead
+    // has passed that unit's barriers, and with it all that read these
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(empty + stage);
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    turn ^= 1;
   }
 }
 
