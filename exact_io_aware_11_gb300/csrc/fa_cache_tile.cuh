@@ -191,29 +191,61 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     if (L::kLoaders == 1 || (i & 1) == loader) mbar_wait_drain(b.raw_full + i % L::kStg, (i / L::kStg) & 1, a.wait_limit);
 }
 
+// V's rows [row0, row0 + rows) of a step that holds keys which a row of queries may not see (from
+// `low` on), pages of zeros or groups of keys that were not read: such groups become zeros, and so do pages of
+// zeros but for their NaN codes. NaN codes at keys >= low are taken out, and the first such key < seen
+// is kept for the unit: the rows that see it become NaN. A call, because few steps come here: within the
+// converters' loop it cost every step (a chunk in int8 131 us, so 127).
+template <int D, bool INT8>
+__device__ __noinline__ void convert_checked(uint32_t src, uint32_t dst, const float4* scales, int row0, int rows, int key0,
+                                             int low, int seen, int* nan_key, int lane) {
+#pragma unroll 2
+  for (int i = lane; i < rows * (D / 16); i += 32) {  // pieces in tile_convert's order
+    const int ch = D == 128 ? (i & 3) | ((i >> 1) & 4) : i & 3;
+    const int p = D == 128 ? ((i >> 4) & 3) + 8 * (i >> 6) : i >> 2, r = row0 + (D == 128 && (i & 4) ? p ^ 5 : p), key = key0 + r;
+    const uint4 v = lds128(src + (D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4)));
+    const float counts = scales[r >> 4].w;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
+    if (counts != 1.f) {
+      const bool keep = !INT8 && counts == 0.f;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) w[k] &= keep ? __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+    }
+    if (!INT8 && key >= low) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+        w[k] &= ~nan;
+        any |= nan;
+      }
+      if (any != 0u && key < seen) atomicMin(nan_key, key);
+    }
+    const uint32_t at = dst + (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128 + (((ch & 3) * 2 ^ (r & 7)) << 4);
+    uint32_t h[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) decode4<INT8>(w[k], h[2 * k], h[2 * k + 1]);
+    st_shared_v4(at, h[0], h[1], h[2], h[3]);
+    st_shared_v4(at ^ 16u, h[4], h[5], h[6], h[7]);
+  }
+}
+
 // Converters: each warp takes its 32 (64) rows of every raw tile, 16 codes a lane at a
 // time. At d = 128 the 8 lanes of a shared-memory phase take four chunks of rows r
 // and r ^ 5: the rows differ in bit 2 (so their raw chunks, at c ^ (r & 7), fall
 // apart) and in bit 0 (so do the results, at 2 c ^ (r & 7)), and every bank is met
 // once in both directions.
-// Where a row of queries may not see a key of V (x.seen and the first row's limit
-// bound those keys), its NaN codes are taken out, and the first such key is kept
-// for the unit: the rows that see it become NaN. Pages of zeros, and groups of keys that were
-// not read, become zeros.
 template <int D, int NQ, bool INT8>
 __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, uint8_t* smem,
                                              const TileBars& b, const Watchdog& wd, int cw, int lane) {
   using L = TileLayout<D, NQ>;
-  // The lane's pieces: chunk ch of rows row0[e] + 8 g, e < kPer, g < kGroups, at constant
+  // The lane's pieces: chunk ch of its row of 8 + 8 g, e < kPer, g < kGroups, at constant
   // distances of a piece with g = 0 (both swizzles repeat every 8 rows).
   constexpr int kRows = kKeys / L::kConvWarps, kPer = D / 64, kGroups = kRows / 8;
   const int ch = D == 128 ? (lane & 3) | ((lane >> 1) & 4) : lane & 3;
-  int row0[kPer];
   uint32_t raw_at[kPer], half_at[kPer];  // in the raw and the fp16 tile; the second half's place is the first's ^ 16
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     const int p = D == 128 ? (lane >> 4) + 2 * e : lane >> 2, r = cw * kRows + (D == 128 && (lane & 4) ? p ^ 5 : p);
-    row0[e] = r;
     raw_at[e] = D == 128 ? r * 128 + ((ch ^ (r & 7)) << 4) : r * 64 + ((ch ^ ((r >> 1) & 3)) << 4);
     half_at[e] = (D == 128 ? (ch >> 2) * kChunkBytes : 0) + r * 128 + (((ch & 3) * 2 ^ (r & 7)) << 4);
   }
@@ -261,28 +293,8 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
             for (int i = 0; i < kBatch; ++i) put(v[i], i % kPer, g0 + i / kPer);
           }
         } else {
-#pragma unroll 1
-          for (int g = 0; g < kGroups; ++g) {
-#pragma unroll
-            for (int e = 0; e < kPer; ++e) {
-              const int r = row0[e] + g * 8, key = key0 + r;
-              const uint4 v = lds128(src + raw_at[e] + g * (8 * D));
-              const float counts = *reinterpret_cast<const float*>(smem + L::oScales + (n % kScaleSlots) * 128 + (r >> 4) * 16 + 12);
-              uint32_t w[4] = {v.x, v.y, v.z, v.w}, any = 0u;
-              if (counts != 1.f) {
-                w[0] = w[1] = w[2] = w[3] = 0u;
-              } else if (!INT8 && key >= low) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const uint32_t nan = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                  w[k] &= ~nan;
-                  any |= nan;
-                }
-                if (any != 0u && key < seen) atomicMin(nan_key + (unit & 7), key);
-              }
-              put(make_uint4(w[0], w[1], w[2], w[3]), e, g);
-            }
-          }
+          convert_checked<D, INT8>(src, dst, reinterpret_cast<const float4*>(smem + L::oScales + (n % kScaleSlots) * 128), cw * kRows,
+                                   kRows, key0, low, seen, nan_key + (unit & 7), lane);
         }
         fence_proxy_async_smem();
         __syncwarp();

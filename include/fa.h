@@ -455,7 +455,8 @@ size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, 
  * h / (Hq / H), Hq a multiple of H; num_pages * H * page_size < 2^31. N = 1 decodes, small N checks drafted
  * tokens, large N runs a chunk of a prompt. The 8-bit codes are converted on
  * chip (exactly) and the scales applied to the scores and the weights; pages
- * with a V scale of 2^-100 or less count as zeros. Where V scales of one sequence
+ * with a V scale of 2^-100 or less count as zeros, but for their NaN codes, which
+ * are NaN whatever the scale. Where V scales of one sequence
  * differ by a factor r (a page of zeros standing for 2^-60), weights below
  * 2^-133 r of the largest are lost: r up to 2^90 costs nothing in 32 bits.
  * Query rows that see no token, and rows i >= q_len[b], get O = 0, LSE = -inf.
