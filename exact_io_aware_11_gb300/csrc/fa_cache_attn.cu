@@ -116,12 +116,10 @@ __device__ __forceinline__ float load_query(const uint16_t* row, bool real, bool
 
 // A weight of zero does not mask a NaN. Where not every row of a unit sees all
 // of a tile (its keys may be leftovers behind the sequence's end), V's NaN codes
-// (e4m3 0x7f, 0xff) are taken out of it, and the rows that see one of them get a
-// NaN sum; `gone`: no row sees any (a page that was not read).
-// Lane: keys key, + 1, + 8, + 9.
-template <int NT, int W>
-__device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], bool gone, int key, const int (&lim)[NT][2],
-                                              float (&l)[NT][2]) {
+// (e4m3 0x7f, 0xff) are taken out of it; the first key that had one comes back, 0x7fffffff if there
+// was none. `gone`: no row sees any (a page that was not read). Lane: keys key, + 1, + 8, + 9.
+template <int W>
+__device__ __forceinline__ int take_out_nan(uint32_t (&v)[4][W], bool gone, int key) {
   int first = 0x7fffffff;
 #pragma unroll
   for (int k = 0; k < 4; ++k)
@@ -133,12 +131,29 @@ __device__ __forceinline__ void poison_unseen(uint32_t (&v)[4][W], bool gone, in
         first = min(first, key + (k & 1) + 8 * (k >> 1));
       }
     }
-  first = gone ? 0x7fffffff : __reduce_min_sync(0xffffffffu, first);
+  return gone ? 0x7fffffff : __reduce_min_sync(0xffffffffu, first);
+}
+// The rows of a unit that see such keys, of which `first` is the least, get NaN in the channels
+// that have it: in O, or in the part that the unit leaves, where this thread has just written them.
+// A call after the rows, because it is rare: code among theirs cost launches without any NaN 0.6 of 10 us.
+template <int D, int NT>
+__device__ __noinline__ void put_nan(const CacheAttnLaunch& a, int b, int row0, int kv, int ql, int h, int first,
+                                     float* o_part, int warp, int lane) {
+  constexpr int kPer = D / 32;
+  const int d0 = lane * kPer;
+  for (int r = warp; r < 8 * NT; r += kWarps) {
+    const int row = row0 + r, i = row / a.G, end = i >= ql ? 0 : a.causal ? kv - ql + i + 1 : kv;  // attn_limit
+    const unsigned nan = static_cast<unsigned>(seen_nan<1>(a.c, b, h, first, end, d0 & ~3)) >> (d0 & 3);
+    uint16_t* const o = a.o + b * a.so.b + (h * a.G + (row - i * a.G)) * a.so.h + i * a.so.n + d0;
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      if (first < lim[n][k]) l[n][k] = __int_as_float(0x7fffffff);
+    for (int d = 0; d < kPer; ++d) {
+      if (!(nan >> d & 1u)) continue;
+      if (o_part != nullptr)
+        o_part[r * D + d0 + d] = __int_as_float(0x7fffffff);
+      else
+        o[d] = 0x7fffu;  // NaN in bf16 and in fp16
+    }
+  }
 }
 
 // The producer warp: every step of the CTA's run, a stage each. Lane i < 8 looks
@@ -229,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
   __shared__ AttnShare share;
   __shared__ long long part[kThreads / 32];
   __shared__ float sm_m[2][kWarps][kRows], sm_l[2][kWarps][kRows];  // of a unit, in turn
+  __shared__ int sm_nan[2][kWarps];  // likewise: the warps' nan_key
   __shared__ int abort_flag;
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
@@ -321,6 +337,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
       l[n][0] = l[n][1] = 0.f;
     }
 
+    int nan_key = 0x7fffffff;  // first key of V with a NaN that was taken out
     int key0 = (step0 << g.log2_keys) + warp * kTile;
     for (int step = 0; step < steps; ++step, key0 += kKeys) {
       alive = alive && mbar_wait_warp(full + stage, phase, wd);
@@ -454,7 +471,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
               v[k][1] = w.y;
             }
           }
-          if (!INT8 && edge) poison_unseen(v, ks[u] < 0.f, key0 + u * 16 + 2 * t, lim, l);
+          if (!INT8 && (key0 + kTile > low || ks[u] < 0.f))
+            nan_key = min(nan_key, take_out_nan(v, ks[u] < 0.f, key0 + u * 16 + 2 * t));
 #pragma unroll
           for (int i = 0; i < kM; ++i) {
             const uint32_t sel = (i & 1) ? 0x7362 : 0x5140;
@@ -492,6 +510,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
           sm_l[turn][warp][n * 8 + 2 * t + k] = l[n][k];
         }
       }
+    if (!INT8 && lane == 0) sm_nan[turn][warp] = nan_key;
     named_bar_sync(1, kWarps * 32);  // also: every warp has read its part of the stage
     const bool last = step0 + steps == x.steps, whole = step0 == 0 && last;
     const int slot = 2 * blockIdx.x + (step0 == 0 ? 1 : 0);
@@ -561,6 +580,13 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
           a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + i] =
               none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
       }
+    }
+    if constexpr (!INT8) {
+      int first = sm_nan[turn][0];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) first = min(first, sm_nan[turn][w]);
+      if (first != 0x7fffffff)
+        put_nan<D, NT>(a, x.b, x.row0, x.kv, x.ql, h, first, whole ? nullptr : g.o_part + static_cast<long long>(slot) * g.rows * D, warp, lane);
     }
     // the stage goes back, and the statistics' other half is next: a warp that is a unit ahead
     // has passed that unit's barriers, and with it all that read these

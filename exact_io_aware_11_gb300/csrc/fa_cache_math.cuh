@@ -1,10 +1,11 @@
 // What the kernels of the attention over the cache share: the conversions of
-// 16-bit types and of the 8-bit codes, and the weights' reference.
+// 16-bit types and of the 8-bit codes, the weights' reference, NaN in V.
 #pragma once
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include "fa_cache_internal.h"
 #include "fa_ptx.cuh"
 
 namespace fa {
@@ -72,6 +73,27 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) 
         : "=r"(lo), "=r"(hi)
         : "r"(w));
   }
+}
+
+// Channels [c0, c0 + 4 W) of V, c0 a multiple of 4, that are NaN at one of the keys [first, end) of a
+// sequence and cache head: a bit each. For rows that see a NaN which was taken out of a tile because other
+// rows of the unit do not see all of its keys: at most a tile's keys and a unit's rows of them.
+template <int W>
+__device__ __forceinline__ unsigned long long seen_nan(const CacheView& c, int b, int h, int first, int end, int c0) {
+  unsigned long long bits = 0ull;
+#pragma unroll 1
+  for (int key = first; key < end; ++key) {
+    const int p = c.table[b * c.table_stride + (key >> c.log2_page)];
+    if (p < 0 || p >= c.num_pages) continue;  // not read
+    const long long row = ((static_cast<long long>(p) * c.H + h) << c.log2_page) + (key & (c.page - 1));
+    const uint32_t* const at = reinterpret_cast<const uint32_t*>(c.code[1] + row * c.d + c0);
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      const uint32_t nan = __vcmpeq4(at[w] & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x08040201u;  // a bit of each byte
+      bits |= static_cast<unsigned long long>(nan * 0x01010101u >> 24) << (4 * w);
+    }
+  }
+  return bits;
 }
 
 }  // namespace fa

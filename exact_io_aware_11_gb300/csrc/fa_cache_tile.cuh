@@ -194,8 +194,8 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
 // V's rows [row0, row0 + rows) of a step that holds keys which a row of queries may not see (from
 // `low` on), pages of zeros or groups of keys that were not read: such groups become zeros, and so do pages of
 // zeros but for their NaN codes. NaN codes at keys >= low are taken out, and the first such key < seen
-// is kept for the unit: the rows that see it become NaN. A call, because few steps come here: within the
-// converters' loop it cost every step (a chunk in int8 131 us, so 127).
+// is kept for the unit: the rows that see it look for the channels (seen_nan). A call, because few
+// steps come here: within the converters' loop it cost every step (a chunk in int8 131 us, so 127).
 template <int D, bool INT8>
 __device__ __noinline__ void convert_checked(uint32_t src, uint32_t dst, const float4* scales, int row0, int rows, int key0,
                                              int low, int seen, int* nan_key, int lane) {
@@ -341,6 +341,10 @@ __device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at,
     st_shared_v4(place(lane, i), half2_of(w.x), half2_of(w.y), half2_of(w.z), half2_of(w.w));
   }
   return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
+}
+
+static __device__ __noinline__ unsigned long long seen_nan64(const CacheView& c, int b, int h, int first, int end, int c0) {
+  return seen_nan<16>(c, b, h, first, end, c0);
 }
 
 // Writes 32 rows x 128 bytes, a lane's row as 8 pieces, to the rows' own places: through `box`
@@ -728,6 +732,13 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         m = M;
         if (!mbar_wait_warp<true>(b.rep_out + pair, 1, wd)) break;
       }
+      const TileUnit x = *ux;
+      const int r = t * 128 + rl, row = x.row0 + r, qi = row / g.G, head = x.h * g.G + (row - qi * g.G);
+      int nan_key = 0x7fffffff, end = 0;  // keys of V with a NaN that was taken out, and seen by this row
+      if (!INT8) {
+        nan_key = *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4);
+        end = unit_limit(g, x, r);
+      }
       // 64 channels of the row's O, from column 64 c
       auto read_o = [&](int c, uint32_t (&o)[2][32]) {
 #pragma unroll
@@ -747,11 +758,15 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
             }
           }
         }
+        if (!INT8 && nan_key < end) {
+          const unsigned long long nan = seen_nan64(a.c, x.b, x.h, nan_key, end, c * 64);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+#pragma unroll
+            for (int q = 0; q < 32; ++q)
+              if (nan >> (e * 32 + q) & 1ull) o[e][q] = 0x7fffffffu;
+        }
       };
-      const TileUnit x = *ux;
-      const int r = t * 128 + rl, row = x.row0 + r, qi = row / g.G, head = x.h * g.G + (row - qi * g.G);
-      if (!INT8 && *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4) < unit_limit(g, x, r))
-        l = __int_as_float(0x7fffffff);
       if (qi >= x.ql) {
         l = 0.f;
         m = -INFINITY;

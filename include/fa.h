@@ -460,6 +460,8 @@ size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, 
  * differ by a factor r (a page of zeros standing for 2^-60), weights below
  * 2^-133 r of the largest are lost: r up to 2^90 costs nothing in 32 bits.
  * Query rows that see no token, and rows i >= q_len[b], get O = 0, LSE = -inf.
+ * A NaN that a row sees in V is in that channel of its O alone, one in K or in q in
+ * all of its O and in its LSE; one that it does not see has no effect on it.
  *   workspace : DEVICE, 16-byte aligned, contents ignored, or NULL with
  *               workspace_bytes = 0; with fewer bytes than
  *               fa_cache_attention_workspace_bytes each (sequence, head) stays

@@ -52,3 +52,41 @@ def check(want, got, hit):
 def test_nan_that_every_row_sees(fa, G, N, B, d, scale):
     """On a page of zeros (cache_write makes one of a page whose finite values are all zero) as on any other."""
     check(*planted(fa, G, N, B, d, 16, [(1, 1, 3, 5, scale), (0, 0, 20, d - 1, scale)]))
+
+
+@pytest.mark.parametrize("scale", [0.0, None])
+@pytest.mark.parametrize("G,N,B,d", KERNELS)
+def test_nan_that_some_rows_see(fa, G, N, B, d, scale):
+    """Tokens from the first row's own to the last row's, several channels, beside the edge of what rows see."""
+    L = N + 90
+    at = [(1, 1, L - N + i, c, scale) for i, c in ((N // 2, 7), (N - 1, 0), (N // 3, d - 1), (0, 33), (N // 2, 8))]
+    check(*planted(fa, G, N, B, d, 16, at + [(0, 0, L - 1, 15, scale), (1, 0, 2, 3, scale)]))
+
+
+@pytest.mark.parametrize("split", [True, False])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("G,N,d", [(4, 2, 64), (2, 8, 128), (4, 12, 64), (2, 60, 128), (4, 100, 64), (4, 100, 128)])
+def test_nan_in_units_that_are_cut(fa, G, N, d, causal, split):
+    L = 6000
+    at = [(1, 1, t, c, s) for t, c, s in ((5, 1, None), (2999, 2, 0.0), (L - N + N // 2, 3, None), (L - 1, 4, 0.0), (L - 1, 63, 0.0))]
+    check(*planted(fa, G, N, 2, d, 64, at, causal=causal, split=split, L=L))
+
+
+def test_nan_beside_a_page_that_was_not_read(fa):
+    """A bad page's keys are masked; a NaN of the page beside it, in the same tile, is seen by every row."""
+    L, G = 4000, 2
+    for N in (2, 8, 60):
+        m = filled(fa, 1, 1, 16, 64, "e4m3", [L], seed=42)
+        table, q = m.table.cuda(), queries(1, G, N, 64, "bf16", 43)
+        bad = table.clone()
+        bad[0, 9] = -1
+        n = torch.tensor([L], dtype=torch.int32, device="cuda")
+        m.cache.v.view(torch.uint8)[int(table[0, 9])] = 0x7f      # what lies in the ring before is anything
+        want = fa.cache_attention(q, m.cache, bad, n)
+        m.cache.v.view(torch.uint8)[int(table[0, 8]), 0, 5, 11] = 0x7f
+        got = fa.cache_attention(q, m.cache, bad, n)
+        torch.cuda.synchronize()
+        assert fa.device_status() == fa.FA_ERR_BAD_PAGE
+        assert torch.isfinite(want[0]).all() and torch.isnan(got[0][..., 11]).all()
+        keep = [c for c in range(64) if c != 11]
+        assert torch.equal(got[0][..., keep], want[0][..., keep]) and torch.equal(got[1], want[1])
