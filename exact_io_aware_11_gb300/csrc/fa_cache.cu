@@ -84,7 +84,9 @@ __device__ __forceinline__ float scale_for(float amax) {
   e = max(e, 1);
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
-__device__ __forceinline__ float inverse(float s) { return s > 0.f ? __frcp_rn(s) : 0.f; }
+// What values are multiplied by to become codes. Of a page of scale 0 the finite ones are zeros,
+// and infinities and NaN have to stay what they are.
+__device__ __forceinline__ float inverse(float s) { return s > 0.f ? __frcp_rn(s) : 1.f; }
 
 // Two values to codes (ties to even, saturating), `lo` in the low byte.
 template <bool INT8>

@@ -411,7 +411,7 @@ typedef struct fa_cache_range {
  * ties to even. A power of two makes the division exact, and moving an e4m3 row
  * only shifts its exponent (values that become subnormal are rounded
  * again). Infinities are held as the largest code; NaN stays NaN in e4m3 and
- * becomes 0 in int8. Rows behind the last token keep what they hold. The page
+ * becomes 0 in int8; where all finite values are zero the scale is 0. Rows behind the last token keep what they hold. The page
  * table entries that a call writes through must name different pages. */
 int fa_cache_write(const fa_cache* cache, const void* k, const void* v, int B, int N,
                    const fa_cache_range* range, struct CUstream_st* stream);
