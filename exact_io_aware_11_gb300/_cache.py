@@ -244,7 +244,7 @@ def rotary_forward(q, rotary: Rotary, k=None, positions=None, offset: int = 0, o
     """q [B, H, N, d] with the first rotary.rotary_dim channels of each row turned to
     its position (fa_rotary_fwd); with k [B, Hk, N, d], (q, k) in one launch.
     positions: int32 [N] or [B, N] on the device, or None for offset + n.
-    out=q (k_out=k) rotates in place."""
+    out=q (k_out=k) rotates in place, also within slices of one packed projection."""
     return _on(_rotary, _device_of(q, "q"), stream, "fa_rotary_fwd", q, rotary, k, positions, int(offset), out, k_out)
 
 
@@ -316,7 +316,8 @@ def cache_write(cache: KVCache, k, v, page_table, start, count=None, stream=None
     start[b] + n (fa_cache_write). start, count: int32 [B]; start=None means 0,
     count=None all N rows. Where a page is shared by the old and the new tokens of a
     sequence, its older rows move to the page's new scale if that grew. The entries of
-    page_table that a call writes through must name different pages."""
+    page_table that a call writes through must name different pages. k and v share strides: where
+    they are slices of one projection, rotate k in place (rotary_forward's k_out=k)."""
     _on(_cache_rows, _check_cache(cache), stream, "fa_cache_write", cache, k, v, page_table, start, count)
 
 

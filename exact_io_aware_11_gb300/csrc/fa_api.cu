@@ -157,22 +157,22 @@ bool dense_strides(int B, int H, int N, int d, Strides* s) {
                       d, s);
 }
 
-// Whether two bf16 [B, H, N, d] tensors with the same strides `s` share an
-// element, their bases `a` and `b` (16-byte aligned) being given. Row starts
-// form the set P = {i_b sb + i_h sh + i_n sn}; the tensors overlap iff the
+// Whether two 16-bit tensors [B, Ha, N, d] and [B, Hb, N, d] with the same strides `s`
+// share an element, their bases `a` and `b` (16-byte aligned) being given. Row starts
+// form the sets {i_b sb + i_h sh + i_n sn}; the tensors overlap iff the
 // base difference (in elements) lies within d - 1 of some difference of two
-// row starts, sum_a k_a s_a with |k_a| < extent_a. The axes' strides nest
-// (each at least the one below times its extent, as make_strides requires),
+// row starts, sum_a k_a s_a with -extent_a(b) < k_a < extent_a(a). The axes' strides nest
+// (each at least the one below times its extent in either tensor, as make_strides requires),
 // so for every axis, largest stride first, only the coefficients next to
 // delta / stride can lead to a hit, and a search over those is exact. This
 // accepts interleaved views such as q, k, v of one packed [B, N, 3, H, d]
-// buffer, which a comparison of address spans would reject.
-bool strided_overlap(const void* a, const void* b, int B, int H, int N, int d, const Strides& s) {
+// or, with grouped heads, [B, N, Ha + 2 Hb, d] buffer, which a comparison of address spans would reject.
+bool strided_overlap(const void* a, const void* b, int B, int Ha, int Hb, int N, int d, const Strides& s) {
   const long long diff = static_cast<long long>(reinterpret_cast<uintptr_t>(b)) -
                          static_cast<long long>(reinterpret_cast<uintptr_t>(a));
   if (diff % 2 != 0) return true;  // not on the same element grid: be conservative
   const long long delta = diff / 2;
-  long long st[3] = {s.n, s.h, s.b}, ext[3] = {N, H, B};
+  long long st[3] = {s.n, s.h, s.b}, lo[3] = {1LL - N, 1LL - Hb, 1LL - B}, hi[3] = {N - 1LL, Ha - 1LL, B - 1LL};
   // axes of extent 1 never step; sort the rest by stride, largest first
   int ord[3] = {0, 1, 2};
   for (int x = 0; x < 3; ++x)
@@ -183,21 +183,20 @@ bool strided_overlap(const void* a, const void* b, int B, int H, int N, int d, c
         ord[y + 1] = t;
       }
   struct Rec {
-    static bool hit(const long long* st, const long long* ext, const int* ord, int lvl, long long r,
-                    int d) {
+    static bool hit(const long long* st, const long long* lo, const long long* hi, const int* ord, int lvl,
+                    long long r, int d) {
       if (lvl == 3) return r > -d && r < d;
       const int ax = ord[lvl];
-      if (ext[ax] <= 1 || st[ax] == 0) return hit(st, ext, ord, lvl + 1, r, d);
-      const long long lim = ext[ax] - 1;
+      if ((lo[ax] == 0 && hi[ax] == 0) || st[ax] == 0) return hit(st, lo, hi, ord, lvl + 1, r, d);
       long long k0 = r / st[ax];
       for (long long k = k0 - 1; k <= k0 + 1; ++k) {
-        if (k < -lim || k > lim) continue;
-        if (hit(st, ext, ord, lvl + 1, r - k * st[ax], d)) return true;
+        if (k < lo[ax] || k > hi[ax]) continue;
+        if (hit(st, lo, hi, ord, lvl + 1, r - k * st[ax], d)) return true;
       }
       return false;
     }
   };
-  return Rec::hit(st, ext, ord, 0, delta, d);
+  return Rec::hit(st, lo, hi, ord, 0, delta, d);
 }
 
 // Bytes from the first to one past the last element of a tensor with strides s.
@@ -346,7 +345,7 @@ int fwd_common(const void* q, const void* k, const void* v, void* o, float* lse,
   const size_t tb = span_bytes(B, H, N, d, lay, 2), lb = tensor_bytes(B, H, N, 1, 4);
   const void* ins[3] = {q, k, v};
   for (const void* in : ins)
-    if (strided_overlap(o, in, B, H, N, d, lay) || overlaps(lse, lb, in, tb) ||
+    if (strided_overlap(o, in, B, H, H, N, d, lay) || overlaps(lse, lb, in, tb) ||
         (split_ws && overlaps(split_ws, split_ws_bytes, in, tb)))
       return FA_ERR_INVALID_ARG;
   if (overlaps(o, tb, lse, lb)) return FA_ERR_INVALID_ARG;
@@ -430,11 +429,11 @@ int bwd_common(int stages, const BwdPtrs& p, int B, int H, int N, int d, int cau
     void* out = outs[x];
     if (!out) continue;
     for (const void* in : ins)
-      if (in && strided_overlap(out, in, B, H, N, d, lay)) return FA_ERR_INVALID_ARG;
+      if (in && strided_overlap(out, in, B, H, H, N, d, lay)) return FA_ERR_INVALID_ARG;
     if ((p.lse && overlaps(out, tb, p.lse, lb)) || overlaps(out, tb, p.ws, ws_used))
       return FA_ERR_INVALID_ARG;
     for (int y = x + 1; y < 3; ++y)
-      if (outs[y] && strided_overlap(out, outs[y], B, H, N, d, lay)) return FA_ERR_INVALID_ARG;
+      if (outs[y] && strided_overlap(out, outs[y], B, H, H, N, d, lay)) return FA_ERR_INVALID_ARG;
   }
   for (const void* in : ins)
     if (in && overlaps(p.ws, ws_used, in, tb)) return FA_ERR_INVALID_ARG;

@@ -36,11 +36,13 @@ int make_tensor(const void* p, int B, int H, int N, int d, const int64_t* s, Ten
   return FA_OK;
 }
 
-// Whether two tensors of a call may share an element: exactly where they have the same
-// shape and strides, by their address ranges otherwise.
+// Whether two tensors of a call, which differ in their heads at most, may share an element: exactly
+// where their strides are the same (of axes that both step), by their address ranges otherwise.
 bool tensors_meet(const Tensor& a, const Tensor& b) {
-  if (a.H == b.H && a.st.b == b.st.b && a.st.h == b.st.h && a.st.n == b.st.n)
-    return strided_overlap(a.p, b.p, a.B, a.H, a.N, a.d, a.st);
+  Strides st = a.st;
+  if (a.H == 1) st.h = b.st.h;
+  if ((a.B == 1 || st.b == b.st.b) && (b.H == 1 || st.h == b.st.h) && (a.N == 1 || st.n == b.st.n))
+    return strided_overlap(a.p, b.p, a.B, a.H, b.H, a.N, a.d, st);
   return ranges_meet(a.p, a.bytes(), b.p, b.bytes());
 }
 bool same_place(const Tensor& a, const Tensor& b) {

@@ -222,8 +222,8 @@ int device_status_word(int** status);
 // Strides of [B, H, N, d] tensors; false if they break the rules of fa.h.
 bool make_strides(int B, int H, int N, int d, long long sb, long long sh, long long sn, Strides* out);
 bool dense_strides(int B, int H, int N, int d, Strides* s);
-// Whether two 16-bit tensors with the same strides share an element.
-bool strided_overlap(const void* a, const void* b, int B, int H, int N, int d, const Strides& s);
+// Whether two 16-bit tensors of Ha and Hb heads with the same strides share an element.
+bool strided_overlap(const void* a, const void* b, int B, int Ha, int Hb, int N, int d, const Strides& s);
 size_t span_bytes(int B, int H, int N, int d, const Strides& s, size_t elem);
 
 // Launches `kern` with programmatic dependent launch allowed: the grid may be

@@ -356,8 +356,9 @@ typedef struct fa_rotary_options {
  *   a' = factor (a cos theta - b sin theta),  b' = factor (a sin theta + b cos theta).
  *   q [B, Hq, N, d] -> q_out;  k [B, Hk, N, d] -> k_out, or both NULL with Hk = 0.
  * d is 64 or 128. Angles, sines and products are in 32 bits, rounded once to
- * dtype. A tensor may be rotated in place (same pointer and strides);
- * any other overlap of an output is FA_ERR_INVALID_ARG. */
+ * dtype. A tensor may be rotated in place (same pointer and strides), also where q and k
+ * are slices of one packed projection; any other overlap of an output is
+ * FA_ERR_INVALID_ARG. */
 int fa_rotary_fwd(const void* q, void* q_out, const void* k, void* k_out, int B, int Hq, int Hk,
                   int N, int d, const fa_rotary_options* opt, struct CUstream_st* stream);
 
