@@ -84,6 +84,11 @@ __device__ __forceinline__ float scale_for(float amax) {
   e = max(e, 1);
   return __uint_as_float(static_cast<uint32_t>(e) << 23);
 }
+// The smallest power of two that is not below s. A page of another scale (a pool filled elsewhere) takes
+// one with its next tokens: x / s is then exact, and every path forms the same codes.
+__device__ __forceinline__ float ceil_power(float s) {
+  return __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0xff800000u);
+}
 // What values are multiplied by to become codes. Of a page of scale 0 the finite ones are zeros,
 // and infinities and NaN have to stay what they are.
 __device__ __forceinline__ float inverse(float s) { return s > 0.f ? __frcp_rn(s) : 1.f; }
@@ -269,7 +274,7 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
   if (log2_t == 5) __syncwarp();
 #pragma unroll
   for (int kv = 0; kv < 2; ++kv) {
-    const float s = fmaxf(s_old[kv], scale_for<INT8>(amax[kv]));
+    const float s = fmaxf(ceil_power(s_old[kv]), scale_for<INT8>(amax[kv]));
     const float inv = inverse(s);
     uint8_t* const dst = a.c.code[kv] + ((ph << a.c.log2_page) + lo) * a.c.d + t * 8;
     if (finite) {
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a,
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-  const float s = fmaxf(s_old, scale_for<INT8>(amax));
+  const float s = fmaxf(ceil_power(s_old), scale_for<INT8>(amax));
   const float inv = inverse(s);
   uint8_t* const dst = a.c.code[kv] + ((static_cast<long long>(page) * a.c.H + h) << a.c.log2_page) * a.c.d + ch;
   if (s > s_old && held) {

@@ -374,7 +374,8 @@ typedef enum { FA_CACHE_E4M3 = 0, FA_CACHE_INT8 = 1 } fa_cache_format;
  *   k, v             : DEVICE 8-bit codes [num_pages, H, page_size, d]
  *                      (e4m3, or int8), 16-byte aligned, contiguous;
  *   k_scale, v_scale : DEVICE fp32 [num_pages, H], one scale for each page and
- *                      head, finite and >= 0;
+ *                      head, 0 <= scale < 2^126 (fa_cache_write makes powers of two
+ *                      and zeros; a pool that was filled elsewhere may hold others);
  *   page_size        : 16, 32, 64 or 128 tokens;  d : 64 or 128.
  * Token t of a sequence lies in row t % page_size of the page that its page
  * table row names at t / page_size. */
@@ -408,7 +409,7 @@ typedef struct fa_cache_range {
  * the smallest power of two s with |x| <= s * 448 (e4m3) or s * 127 (int8) for
  * the finite values written to it, and no less than before where the page
  * already holds earlier tokens of this sequence (its rows before start[b]);
- * when it grows, those rows are moved to it. Codes are x / s to the nearest,
+ * when it grows (from another value to a power of two, too), those rows are moved to it. Codes are x / s to the nearest,
  * ties to even. A power of two makes the division exact, and moving an e4m3 row
  * only shifts its exponent (values that become subnormal are rounded
  * again). Infinities are held as the largest code; NaN stays NaN in e4m3 and

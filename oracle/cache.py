@@ -68,7 +68,8 @@ def write(codes, scale, x, table, start, count, page, fmt):
                 new = x[b, h, t0 - first:t1 - first]
                 a = np.abs(new[np.isfinite(new)])
                 old = scale[p, h] if held else 0.0
-                s = max(old, scale_for(a.max() if a.size else 0.0, fmt))
+                power = 2.0 ** np.ceil(np.log2(old)) if old > 0 else 0.0
+                s = max(power, scale_for(a.max() if a.size else 0.0, fmt))
                 inv = 1 / s if s > 0 else 1.0  # scale 0: zeros, infinities (the largest code) and NaN
                 if held and s > old:
                     codes[p, h, :held] = encode(decode(codes[p, h, :held], fmt) * (old * inv), fmt)
