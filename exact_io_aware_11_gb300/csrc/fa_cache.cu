@@ -148,14 +148,14 @@ struct Span {
 __device__ __forceinline__ Span span_of(const CacheRows& a, int b) {
   const long long room = static_cast<long long>(a.c.table_width) << a.c.log2_page;
   Span s;
-  s.first = a.start != nullptr ? max(0, __ldg(a.start + b)) : 0;
-  const int cnt = a.count != nullptr ? min(a.N, max(0, __ldg(a.count + b))) : a.N;
+  s.first = a.start != nullptr ? max(0, a.start[b]) : 0;
+  const int cnt = a.count != nullptr ? min(a.N, max(0, a.count[b])) : a.N;
   s.end = min(s.first + cnt, room);
   return s;
 }
 // The page that entry i of sequence b's table row names, or -1 (reported).
 __device__ __forceinline__ int page_of(const CacheRows& a, int b, long long i) {
-  const int p = __ldg(a.c.table + b * a.c.table_stride + i);
+  const int p = a.c.table[b * a.c.table_stride + i];
   if (p >= 0 && p < a.c.num_pages) return p;
   report_bad_page(a.status);
   return -1;
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(512) cache_write_pages_kernel(const CacheRows 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const int row = row0 + k * row_step;
-      x[kv][k] = row < hi ? __ldg(reinterpret_cast<const uint4*>(src + k * src_step)) : make_uint4(0, 0, 0, 0);
+      x[kv][k] = row < hi ? *reinterpret_cast<const uint4*>(src + k * src_step) : make_uint4(0, 0, 0, 0);
     }
   }
   const long long ph = static_cast<long long>(page) * a.c.H + h;
@@ -341,7 +341,7 @@ __global__ void __launch_bounds__(128) cache_write_few_kernel(const CacheRows a,
   for (int k = 0; k < kFew; ++k) {
     const long long tok = t0 + k * rows + sub;
     x[k] = make_uint2(0, 0);
-    if (tok < t1) x[k] = __ldg(reinterpret_cast<const uint2*>(src + (tok - sp.first) * a.st.n));
+    if (tok < t1) x[k] = *reinterpret_cast<const uint2*>(src + (tok - sp.first) * a.st.n);
   }
 #pragma unroll
   for (int k = 0; k < kFew; ++k) {

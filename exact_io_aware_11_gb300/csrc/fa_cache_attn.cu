@@ -95,7 +95,7 @@ __device__ __forceinline__ float load_query(const uint16_t* row, bool real, bool
   float mx = 0.f;
 #pragma unroll
   for (int v = 0; v < D / 32; ++v) {
-    const uint4 w = real ? __ldg(reinterpret_cast<const uint4*>(row + t * (D / 4)) + v) : make_uint4(0, 0, 0, 0);
+    const uint4 w = real ? reinterpret_cast<const uint4*>(row + t * (D / 4))[v] : make_uint4(0, 0, 0, 0);
     const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -181,7 +181,7 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
       s.want = group && key < ld.x.seen;
       s.h = ld.h;
       s.row = key & (c.page - 1);
-      if (s.want) s.pid = __ldg(c.table + ld.x.b * c.table_stride + (key >> c.log2_page));
+      if (s.want) s.pid = c.table[ld.x.b * c.table_stride + (key >> c.log2_page)];
       ld.next(g);
     }
     return s;
@@ -193,8 +193,8 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
-      s.ks = __ldg(c.scale[0] + ph);
-      s.vs = __ldg(c.scale[1] + ph);
+      s.ks = c.scale[0][ph];
+      s.vs = c.scale[1][ph];
     }
   };
   Step now = look(), next = look();

@@ -44,8 +44,8 @@ __device__ __forceinline__ AttnEntry attn_entry(const AttnGrid& g, int e) {
   AttnEntry x;
   x.b = e / g.row_tiles;
   x.row0 = (e - x.b * g.row_tiles) * g.rows;
-  x.kv = min(g.cap, max(0, __ldg(g.kv_len + x.b)));
-  x.ql = g.q_len != nullptr ? min(g.N, max(0, __ldg(g.q_len + x.b))) : g.N;
+  x.kv = min(g.cap, max(0, g.kv_len[x.b]));
+  x.ql = g.q_len != nullptr ? min(g.N, max(0, g.q_len[x.b])) : g.N;
   const int rows = min(g.rows, x.ql * g.G - x.row0);
   x.seen = 0;
   if (rows > 0) x.seen = g.causal ? max(0, x.kv - x.ql + (x.row0 + rows - 1) / g.G + 1) : x.kv;

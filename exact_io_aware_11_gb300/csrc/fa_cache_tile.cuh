@@ -131,7 +131,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       s.want = group && key < ld.x.seen;
       s.h = ld.h;
       s.row = key & (c.page - 1);
-      if (s.want) s.pid = __ldg(c.table + ld.x.b * c.table_stride + (key >> c.log2_page));
+      if (s.want) s.pid = c.table[ld.x.b * c.table_stride + (key >> c.log2_page)];
       ld.next(g);
     }
     return s;
@@ -143,8 +143,8 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
-      s.ks = __ldg(c.scale[0] + ph);
-      s.vs = __ldg(c.scale[1] + ph);
+      s.ks = c.scale[0][ph];
+      s.vs = c.scale[1][ph];
     }
   };
   Step now = look(), next = look();

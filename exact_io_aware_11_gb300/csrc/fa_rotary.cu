@@ -55,7 +55,7 @@ __device__ __forceinline__ void turn_of(unsigned long long turns, int p, float f
 }
 
 __device__ __forceinline__ int position(const RotaryLaunch& a, int b, int n) {
-  return a.pos != nullptr ? __ldg(a.pos + b * a.pos_b + n * a.pos_n)
+  return a.pos != nullptr ? a.pos[b * a.pos_b + n * a.pos_n]
                           : static_cast<int>(static_cast<unsigned>(a.offset) + static_cast<unsigned>(n));
 }
 
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 8) rotary_kernel(const RotaryLaunch 
     for (int i = 0; i < 8; ++i) {
       c[i] = 1.f;
       s[i] = 0.f;
-      if (i < pairs) turn_of(__ldg(a.turns + it.job * 8 + i), pos, a.fcos, a.fsin, c[i], s[i]);
+      if (i < pairs) turn_of(a.turns[it.job * 8 + i], pos, a.fcos, a.fsin, c[i], s[i]);
     }
   }
   for (int h0 = it.h0; h0 < it.heads; h0 += kBatch * hgroups) {
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kThreads) rotary_rows_kernel(const RotaryLaunc
       other[j][e] = ch < half ? ch + half : ch < a.r ? ch - half : -1;
       c[j][e] = 1.f;
       s[j][e] = 0.f;
-      if (ch < a.r) turn_of(__ldg(a.turns + min(ch, other[j][e])), pos, a.fcos, ch < half ? -a.fsin : a.fsin, c[j][e], s[j][e]);
+      if (ch < a.r) turn_of(a.turns[min(ch, other[j][e])], pos, a.fcos, ch < half ? -a.fsin : a.fsin, c[j][e], s[j][e]);
     }
   while (true) {
 #pragma unroll

@@ -1,4 +1,5 @@
 """Definitions and host-side checks of the cache's calls that need no GPU."""
+import os
 import warnings
 
 import numpy as np
@@ -74,3 +75,16 @@ def test_tensors_on_another_device_are_refused(monkeypatch):
             for odd in list(names):
                 with pytest.raises(ValueError):
                     call()
+
+
+def test_kernels_of_dependent_launches_read_coherently():
+    """These kernels may be set up while their predecessor on the stream (a write before a read, a
+    rotation in place before a write) still runs: what it writes is not read-only for their lifetime, as the
+    non-coherent load (__ldg, ld.global.nc) demands."""
+    csrc = os.path.join(os.path.dirname(fa.__file__), "csrc")
+    names = sorted(n for n in os.listdir(csrc) if n.startswith(("fa_cache", "fa_rotary")))
+    assert len(names) >= 9
+    for n in names:
+        with open(os.path.join(csrc, n)) as f:
+            text = f.read()
+        assert "__ldg" not in text and ".global.nc" not in text and "__restrict__" not in text, n
