@@ -359,7 +359,7 @@ def cache_attention(q, cache: KVCache, page_table, kv_len, q_len=None, causal: b
     token kv_len[b] - q_len[b] + i, so the newest tokens are written before the call. Rows
     that see no token, and rows i >= q_len[b], get O = 0 and LSE = -inf. `workspace`:
     uint8 of cache_attention_workspace_bytes(...) bytes, kept by the caller, allocated
-    here if None; split=False does without."""
+    here if None; split=False does without either."""
     return _on(_cache_attention, _check_cache(cache), stream, q, cache, page_table, kv_len, q_len, causal, scale, out, lse,
                workspace, split)
 
@@ -383,7 +383,7 @@ def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, ls
     if workspace is not None:
         if workspace.device != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
-        need = workspace.numel() * workspace.element_size()
+        need = workspace.numel() * workspace.element_size() if split else 0
     else:
         need = L.fa_cache_attention_workspace_bytes(cache._struct, B, H, N, pages) if split else 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None

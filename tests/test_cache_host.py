@@ -77,6 +77,26 @@ def test_tensors_on_another_device_are_refused(monkeypatch):
                     call()
 
 
+def test_split_false_uses_no_workspace(monkeypatch):
+    """Neither one that the caller gives nor one of its own."""
+    given = []
+
+    class Lib:
+        fa_cache_attention_workspace_bytes = staticmethod(lambda *a: 512)
+        fa_cache_attention = staticmethod(lambda *a: given.append(a[9]) or 0)  # workspace_bytes
+
+    monkeypatch.setattr(_cache, "_on", lambda call, device, stream, *args: call(*args))
+    monkeypatch.setattr(_cache, "_raw_stream", lambda index: None)
+    monkeypatch.setattr(_cache, "lib", Lib)
+    with warnings.catch_warnings(), FakeTensorMode():
+        warnings.simplefilter("ignore")  # of a fake tensor's data_ptr
+        t = lambda shape, dtype: torch.empty(shape, dtype=dtype, device="cuda:0")  # noqa: E731
+        cache = fa.KVCache(*(t((9, 2, 16, 64), torch.int8) for _ in "kv"), *(t((9, 2), torch.float32) for _ in "kv"))
+        for ws, split in ((None, True), (t((700,), torch.uint8), True), (None, False), (t((700,), torch.uint8), False)):
+            fa.cache_attention(t((3, 4, 5, 64), torch.bfloat16), cache, t((3, 4), torch.int32), t((3,), torch.int32), workspace=ws, split=split)
+    assert given == [512, 700, 0, 0]
+
+
 def test_kernels_of_dependent_launches_read_coherently():
     """These kernels may be set up while their predecessor on the stream (a write before a read, a
     rotation in place before a write) still runs: what it writes is not read-only for their lifetime, as the
