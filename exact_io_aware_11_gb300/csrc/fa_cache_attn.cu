@@ -1,5 +1,6 @@
-// Attention over the paged 8-bit cache, few query rows per cache head
-// (single tokens and drafted ones), and the merge of units that were cut.
+// Attention over the paged 8-bit cache in units of 8 or 16 query rows per cache head
+// (single tokens, drafted ones, up to 64 rows over short caches: attn_plan), and the merge of
+// units that were cut.
 //
 // Mathematics: with codes kc, vc and scales ks, vs of each page,
 //   x_j = scale log2e ks (q . kc_j),  y_j = x_j + log2 vs_j,  M = max_j y_j,
@@ -24,7 +25,7 @@
 // through shared memory.
 //
 // Measured (GPU time): one token of 64 sequences of 1000 to 8192, 32 heads on 8, d = 128, e4m3: 101
-// us, 5950 GB/s; the same with 32 heads on 32 (16 sequences of 8192) 92 us, 5800 GB/s; 64
+// to 102.6 us, 5900 GB/s; 16 heads on 16 (16 sequences of 8192) 92 us, 5840 GB/s; 64
 // sequences of 4096, 12 heads, d = 64: 75 us, 5370 GB/s, where scores and weights weigh twice as
 // much beside a row's bytes; one sequence of 131071, 16 heads on 4, int8: 33.5 us, 4000 GB/s, of which
 // 17 us stream at the memory's rate, 2 us share the steps out, 3 us bring the first tile and 4 us
@@ -826,8 +827,8 @@ AttnWorkspace attn_workspace(int ctas, int rows, int d) {
 //     7 steps 28.1 and 25.7; 54 steps 94.3 and 73.8; 1024 units of 4 steps 75.3 and 74.0);
 //   up to 128: one tile (128 rows 29.0, in a unit of two tiles 31.3);
 //   above: a unit of two tiles, whose step costs some 1.4 times one tile's, where the CTAs have about
-//     6 steps each to make good its longer start and larger merge (107 steps a CTA 198, with
-//     single tiles 266; 13 steps 45.6 and 51.3; 7 steps 37.1 and 36.9; 3 steps 36.3 and 31.6; 384
+//     6 steps each to make good its longer start and larger merge (107 steps a CTA 197, with
+//     single tiles 267; 13 steps 45.6 and 51.3; 7 steps 37.1 and 36.9; 3 steps 36.3 and 31.6; 384
 //     rows, which leave half a tile empty, at 54 steps 112.9 and 118.7).
 // lead: beginning one more unit costs a CTA 1 us (rows of up to 16, steps of 0.7 us) and 5 us (tiles,
 // steps of 1 to 2 us); counting it shares ragged batches out more evenly: drafts 39.9 us with

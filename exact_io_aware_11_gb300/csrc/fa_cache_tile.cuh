@@ -1,6 +1,6 @@
 // Attention over the paged 8-bit cache, many query rows per cache head (drafted
 // tokens of large groups, chunks of a prompt): tiles of 128 query rows on
-// tcgen05.
+// tcgen05. Which calls come here: attn_plan.
 //
 // Mathematics, units, shares and parts: as in fa_cache_attn.cu. A unit has NQ tiles of
 // 128 query rows, whose S = Q K^T and O += P V run as 128 x
@@ -17,15 +17,17 @@
 // constant over 16 columns, so that the converters do nothing but convert.
 //
 // What bounds it, and what it measured (GPU time, d = 128):
-//   Chunks (NQ = 2; 2048 tokens of 16 heads on 4 over 16384, e4m3, pages of 64): 197 us, 1307
+//   Chunks (NQ = 2; 2048 tokens of 16 heads on 4 over 16384, e4m3, pages of 64): 196 us, 1317
 //   TFLOP/s with the merge. A step is 2048 cycles of products and takes some 3200: softmax,
 //   P V and the next S follow one another within a tile, and the two tiles cover each other only in
-//   part. Tensor pipe 55 to 60 %, issue slots 41 %, no other pipe above 35 %. Tried and slower: one
+//   part. Tensor pipe 58 %, issue slots 45 %, no other pipe above 37 %. Tried and slower: one
 //   pass over the scores with the reference moved afterwards (304 us where two passes took 230:
 //   spills) or chunk by chunk (326). int8 codes take three instructions on the busiest pipe where
-//   e4m3 takes two conversions: 131 us where e4m3 takes 114 (2 sequences of 1024 on 8192).
+//   e4m3 takes two conversions: 127 us where e4m3 takes 113 (2 sequences of 1024 on 8192), 218 us for the
+//   chunk above. At d = 64 that chunk takes 187 us in either format: the exponentials of a step stay.
 //   Drafts (REP = 2; 5 tokens of 16 heads on 2, 16 sequences of 2000 to 16384, pages of 16): 35 us,
-//   of which 15 steps of 1 us (5 TB/s of codes), 5 us of start, 3 us of end and the merge's 4.
+//   of which 15 steps of 1 us (5 TB/s of codes), 5 us of start, 3 us of end and the merge's 4; 6 to 8
+//   are not accounted for.
 #pragma once
 
 #include "fa_cache_internal.h"
@@ -407,8 +409,8 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     cache_attn_tile_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
   using L = TileLayout<D, NQ>;
   // The weights are handed over in halves of 64 keys, so that P V begins under the second
-  // half's exponentials: a chunk in e4m3 201.5 us as a whole, 196.7 in halves; in int8, where
-  // the converters are behind, 131.9 and 141.3; in units of one tile (384 rows) 118.7 and 130.2.
+  // half's exponentials: a chunk in e4m3 207.0 us as a whole, 197.3 in halves; in int8, where
+  // the converters are behind, 219.4 and 221.3; in units of one tile (384 rows, e4m3) 118.7 and 130.2.
   constexpr bool kHalves = NQ == 2 && !INT8;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnShare share;

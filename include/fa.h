@@ -458,9 +458,12 @@ size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, 
  * tokens, large N runs a chunk of a prompt. The 8-bit codes are converted on
  * chip (exactly) and the scales applied to the scores and the weights; pages
  * with a V scale of 2^-100 or less count as zeros, but for their NaN codes, which
- * are NaN whatever the scale. Where V scales of one sequence
- * differ by a factor r (a page of zeros standing for 2^-60), weights below
- * 2^-133 r of the largest are lost: r up to 2^90 costs nothing in 32 bits.
+ * are NaN whatever the scale. A token's weight in the product with V, softmax weight times V
+ * scale, is rounded to fp16: 11 bits down to 2^-21 of the row's largest, below that 2^-32 of
+ * the largest. The sum is formed in 32 bits: where V scales of one sequence differ by a
+ * factor r (a page of zeros standing for 2^-60), weights below 2^-133 r of the largest are
+ * lost to it, so r up to 2^90 costs the sum and the LSE nothing; from r of 2^21 on the smaller
+ * page's values lose bits beside zeros of the larger one.
  * Query rows that see no token, and rows i >= q_len[b], get O = 0, LSE = -inf.
  * A NaN that a row sees in V is in that channel of its O alone, one in K or in q in
  * all of its O and in its LSE; one that it does not see has no effect on it.
