@@ -335,8 +335,6 @@ def _plain_reserve(s):
     free = (refs == 0).nonzero(as_tuple=True)[0]
     n = torch.cumsum(take, 0)  # pages taken up to here
     fail = torch.where(take & (n > free.numel()), b, S).amin() if b.numel() else torch.tensor(S, device="cuda")
-    ok = torch.ones(S, dtype=torch.int32, device="cuda")
-    ok[b[b >= fail]] = 0
     go = take & (b < fail)
     bt, kt, pt = b[go], k[go], p[go]
     dst = free[n[go] - 1]
@@ -345,7 +343,8 @@ def _plain_reserve(s):
     table[bt, kt] = dst.to(torch.int32)
     held = (pt >= 0) & (kt == start[bt] // page) & (start[bt] % page != 0)
     _move(s, pt[held], dst[held])
-    return ok
+    # once a row's pages are not there any more, the rows that need none are served alone
+    return (~(inside & ((table < 0) | (refs[table.clamp(min=0).long()] > 1))).any(1)).to(torch.int32)
 
 
 def _plain_compact(s):
