@@ -11,6 +11,8 @@ from ._lib import (FA_ERR_BAD_PAGE, FA_ERR_CUDA, FA_ERR_DEVICE_TIMEOUT, FA_ERR_I
                    status_string)
 from ._cache import (KVCache, Rotary, cache_attention, cache_attention_workspace_bytes, cache_read, cache_write,
                      rotary_backward, rotary_forward, rotary_frequencies)
+from ._pages import (cache_compact, cache_compact_workspace_bytes, cache_copy, cache_fork, cache_reserve,
+                     cache_reserve_workspace_bytes)
 
 __all__ = ["FA_ERR_CUDA", "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INVALID_ARG", "FA_ERR_UNSUPPORTED",
            "FA_OK", "AttentionOptions", "FaError", "attention_backward", "attention_forward",
@@ -19,4 +21,6 @@ __all__ = ["FA_ERR_CUDA", "FA_ERR_DEVICE_TIMEOUT", "FA_ERR_INVALID_ARG", "FA_ERR
            "device_status", "forward", "fwd_workspace_bytes", "lib", "library_path", "selftest_wait_timeout",
            "status_string",
            "FA_ERR_BAD_PAGE", "KVCache", "Rotary", "cache_attention", "cache_attention_workspace_bytes", "cache_read",
-           "cache_write", "rotary_backward", "rotary_forward", "rotary_frequencies"]
+           "cache_write", "rotary_backward", "rotary_forward", "rotary_frequencies",
+           "cache_compact", "cache_compact_workspace_bytes", "cache_copy", "cache_fork", "cache_reserve",
+           "cache_reserve_workspace_bytes"]

@@ -1,0 +1,171 @@
+"""Binding of the page entry points of libfa.so: pages of the 8-bit cache copied, shared
+between sequences, dealt out and moved together, in every layer of a model.
+
+As in _cache.py, every step runs in the CUDA kernels. A page table is int32 [rows, columns], -1
+where a row has no page; refs int32 [num_pages] counts the entries that name each page
+(0: free) and starts as zeros beside a table of -1.
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from ._cache import _I32, _I64, _SZ, CacheStruct, KVCache, _check_int, _check_lengths, _done, _on, _raw_stream
+from ._lib import _I, _P, SIGNATURES, lib
+
+
+class PageTableStruct(ctypes.Structure):
+    """fa_page_table of include/fa.h."""
+    _fields_ = [("entries", _P), ("stride", _I64), ("rows", _I), ("width", _I), ("refs", _P), ("num_pages", _I), ("page_size", _I)]
+
+
+_CACHES, _TABLE = ctypes.POINTER(CacheStruct), ctypes.POINTER(PageTableStruct)
+SIGNATURES["fa_cache_copy"] = (_I, [_CACHES, _I, _P, _P, _I, _P])
+SIGNATURES["fa_cache_fork"] = (_I, [_TABLE, _P, _P, _P])
+SIGNATURES["fa_cache_reserve_workspace_bytes"] = (_SZ, [_I, _I, _I])
+SIGNATURES["fa_cache_reserve"] = (_I, [_CACHES, _I, _TABLE, _P, _P, _I32, _P, _P, _SZ, _P])
+SIGNATURES["fa_cache_compact_workspace_bytes"] = (_SZ, [_I])
+SIGNATURES["fa_cache_compact"] = (_I, [_CACHES, _I, _TABLE, _P, _P, _P, _SZ, _P])
+
+
+def _layers(caches):
+    """The structs of one KVCache or a sequence of them, and the device they share."""
+    if isinstance(caches, KVCache):
+        return caches._struct, 1, caches.device
+    try:
+        caches = list(caches)
+    except TypeError:
+        caches = []
+    if not caches or not all(isinstance(c, KVCache) for c in caches):
+        raise ValueError("caches must be a KVCache or a sequence of them, one for each layer")
+    dev = caches[0].device
+    if any(c.device != dev for c in caches):
+        raise ValueError("the layers' caches are on different devices")
+    return (CacheStruct * len(caches))(*[c._struct for c in caches]), len(caches), dev
+
+
+def _table(t, refs, page_size, dev):
+    _check_int(t, "page_table", dev, 2)
+    _check_int(refs, "refs", dev, 1)
+    if t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError("page_table must be [rows, pages per row] with a contiguous last axis")
+    if not refs.is_contiguous():
+        raise ValueError("refs must be contiguous")
+    return PageTableStruct(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.shape[0], t.shape[1], refs.data_ptr(), refs.shape[0],
+                           page_size)
+
+
+def _workspace(workspace, need, dev):
+    """The caller's workspace, or a new one, and its bytes."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def _rows_out(t, n, what, dev):
+    if t is None:
+        return torch.empty(n, dtype=torch.int32, device=dev)
+    _check_int(t, what, dev, 1)
+    if t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous int32 [{n}]")
+    return t
+
+
+def cache_copy(caches, src, dst, stream=None) -> None:
+    """Copies page src[i] to page dst[i], codes and scales, in every layer's cache (fa_cache_copy): int32
+    [n] on the device; moves with -1 in either are left out. No page of dst may be another move's
+    source or destination."""
+    s, n, dev = _layers(caches)
+    _on(_copy, dev, stream, s, n, dev, src, dst)
+
+
+def _copy(s, layers, dev, src, dst):
+    for t, what in ((src, "src"), (dst, "dst")):
+        _check_int(t, what, dev, 1)
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+    if src.shape != dst.shape:
+        raise ValueError("src and dst must have the same length")
+    _done(lib().fa_cache_copy(s, layers, src.data_ptr(), dst.data_ptr(), src.shape[0], _raw_stream(dev.index)), "fa_cache_copy")
+
+
+def cache_fork(page_table, refs, page_size: int, parent=None, keep=None, stream=None) -> None:
+    """Rows of page_table become copies of other rows, all at once, in place (fa_cache_fork): row b
+    takes the pages of row parent[b] (-1: none, b: its own), of which those of the first keep[b]
+    tokens stay (None: all). refs follows, so rows that finish or are cut short give their pages back.
+    parent, keep: int32 [rows], one of them at least. Before a row writes into a page that it
+    shares, cache_reserve gives it its own."""
+    if not isinstance(page_table, torch.Tensor) or not page_table.is_cuda:
+        raise ValueError("page_table must be a CUDA tensor")
+    _on(_fork, page_table.device, stream, page_table, refs, int(page_size), parent, keep)
+
+
+def _fork(page_table, refs, page_size, parent, keep):
+    dev = page_table.device
+    t = _table(page_table, refs, page_size, dev)
+    if parent is None and keep is None:
+        raise ValueError("give parent, keep or both")
+    p, k = (_check_lengths(x, what, dev, t.rows) for x, what in ((parent, "parent"), (keep, "keep")))
+    _done(lib().fa_cache_fork(t, p, k, _raw_stream(dev.index)), "fa_cache_fork")
+
+
+def cache_reserve_workspace_bytes(cache: KVCache, rows: int, pages: int) -> int:
+    """Workspace bytes of cache_reserve for a page table of `rows` rows and `pages` columns."""
+    return lib().fa_cache_reserve_workspace_bytes(rows, pages, cache.k.shape[0])
+
+
+def cache_reserve(caches, page_table, refs, start, count, ok=None, workspace=None, stream=None):
+    """Gives row b a page of its own for each of the tokens start[b] + n, n < count[b], that are to be
+    written (fa_cache_reserve): free pages, the lowest first, where it has none; a copy, in every
+    layer, of a page that it shares and that holds earlier tokens of it. start: int32 [rows] or None for 0; count: int32
+    [rows] or one number for every row. Returns ok, int32 [rows]: 0 where pages ran out or the
+    tokens pass the table's width; such rows must not be written to. `workspace`: uint8 of
+    cache_reserve_workspace_bytes(...) bytes, allocated here if None."""
+    s, n, dev = _layers(caches)
+    return _on(_reserve, dev, stream, s, n, dev, page_table, refs, start, count, ok, workspace)
+
+
+def _page_size(s, layers):
+    return s.page_size if layers == 1 and isinstance(s, CacheStruct) else s[0].page_size
+
+
+def _reserve(s, layers, dev, page_table, refs, start, count, ok, workspace):
+    t = _table(page_table, refs, _page_size(s, layers), dev)
+    tokens = 0
+    if not isinstance(count, torch.Tensor):
+        if count is None or not 0 <= int(count) < 2 ** 31:
+            raise ValueError("count must be int32 [rows] or a number of tokens")
+        tokens, count = int(count), None
+    b, c = (_check_lengths(x, what, dev, t.rows) for x, what in ((start, "start"), (count, "count")))
+    ok = _rows_out(ok, t.rows, "ok", dev)
+    L = lib()
+    workspace, have = _workspace(workspace, L.fa_cache_reserve_workspace_bytes(t.rows, t.width, t.num_pages) if workspace is None else 0, dev)
+    _done(L.fa_cache_reserve(s, layers, t, b, c, tokens, ok.data_ptr(), workspace.data_ptr(), have, _raw_stream(dev.index)), "fa_cache_reserve")
+    return ok
+
+
+def cache_compact_workspace_bytes(cache: KVCache) -> int:
+    """Workspace bytes of cache_compact."""
+    return lib().fa_cache_compact_workspace_bytes(cache.k.shape[0])
+
+
+def cache_compact(caches, page_table, refs, where=None, live=None, workspace=None, stream=None):
+    """Moves the pages in use to the lowest numbers, in every layer, in page_table and in refs
+    (fa_cache_compact). Returns where, int32 [num_pages]: each page's new number, -1 for free ones (for other
+    tables that name pages), and live, int32 [1]: the pages in use. `workspace`: uint8 of
+    cache_compact_workspace_bytes(...) bytes, allocated here if None."""
+    s, n, dev = _layers(caches)
+    return _on(_compact, dev, stream, s, n, dev, page_table, refs, where, live, workspace)
+
+
+def _compact(s, layers, dev, page_table, refs, where, live, workspace):
+    t = _table(page_table, refs, _page_size(s, layers), dev)
+    where, live = _rows_out(where, t.num_pages, "where", dev), _rows_out(live, 1, "live", dev)
+    L = lib()
+    workspace, have = _workspace(workspace, L.fa_cache_compact_workspace_bytes(t.num_pages) if workspace is None else 0, dev)
+    _done(L.fa_cache_compact(s, layers, t, where.data_ptr(), live.data_ptr(), workspace.data_ptr(), have, _raw_stream(dev.index)),
+          "fa_cache_compact")
+    return where, live

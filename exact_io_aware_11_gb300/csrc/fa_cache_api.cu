@@ -1,6 +1,7 @@
 // C-ABI of the rotary and cache entry points (declared in include/fa.h):
 // argument validation and dispatch. Nothing is launched and nothing written
 // when an argument is refused.
+#include <algorithm>
 #include <climits>
 #include <cmath>
 #include <cstring>
@@ -225,6 +226,75 @@ int check_attention_sizes(const fa_cache* cache, int B, int Hq, int N, int table
   return FA_OK;
 }
 
+// ------------------------------------------------------------------ pages
+constexpr int kMaxLayers = 1024, kMaxTableRows = 16384;
+
+struct Range {
+  const void* p;
+  size_t n;
+};
+
+// The pools of a model's layers: all of one shape, no memory in common, and none with `others`.
+int check_layers(const fa_cache* caches, int layers, const Range* others, int n_others) {
+  if (caches == nullptr || layers < 1 || layers > kMaxLayers) return FA_ERR_INVALID_ARG;
+  for (int l = 0; l < layers; ++l) {
+    const fa_cache& c = caches[l];
+    const int st = check_cache_sizes(&c);
+    if (st != FA_OK) return st;
+    if (c.num_pages != caches->num_pages || c.H != caches->H || c.page_size != caches->page_size || c.d != caches->d ||
+        c.format != caches->format)
+      return FA_ERR_INVALID_ARG;
+    if (!c.k || !c.v || !c.k_scale || !c.v_scale || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(c.k_scale, 4) ||
+        !aligned(c.v_scale, 4))
+      return FA_ERR_INVALID_ARG;
+    for (int i = 0; i < n_others; ++i)
+      if (meets_cache(&c, others[i].p, others[i].n)) return FA_ERR_INVALID_ARG;
+  }
+  Range parts[4 * kMaxLayers];
+  int n = 0;
+  for (int l = 0; l < layers; ++l) {
+    const fa_cache& c = caches[l];
+    parts[n++] = {c.k, pool_bytes(&c)};
+    parts[n++] = {c.v, pool_bytes(&c)};
+    parts[n++] = {c.k_scale, scale_bytes(&c)};
+    parts[n++] = {c.v_scale, scale_bytes(&c)};
+  }
+  std::sort(parts, parts + n, [](const Range& a, const Range& b) { return reinterpret_cast<uintptr_t>(a.p) < reinterpret_cast<uintptr_t>(b.p); });
+  for (int i = 1; i < n; ++i)
+    if (ranges_meet(parts[i - 1].p, parts[i - 1].n, parts[i].p, parts[i].n)) return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+
+int check_page_table_sizes(int rows, int width, int num_pages, int page) {
+  if (rows < 1 || rows > kMaxTableRows || width < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
+  // entries are counted, and tokens, in 32 bits
+  if (static_cast<long long>(rows) * width > (1LL << 30) || static_cast<long long>(width) * page > INT_MAX - 1024)
+    return FA_ERR_INVALID_ARG;
+  return FA_OK;
+}
+int check_page_table(const fa_page_table* t, PageTable* v) {
+  if (t == nullptr) return FA_ERR_INVALID_ARG;
+  const int st = check_page_table_sizes(t->rows, t->width, t->num_pages, t->page_size);
+  if (st != FA_OK) return st;
+  if (t->entries == nullptr || t->refs == nullptr || !aligned(t->entries, 4) || !aligned(t->refs, 4)) return FA_ERR_INVALID_ARG;
+  // rows may not share entries: they are written
+  if (t->stride < 0 || t->stride > (1LL << 40) || (t->rows > 1 && t->stride < t->width)) return FA_ERR_INVALID_ARG;
+  *v = PageTable{t->entries, t->stride, t->rows, t->width, t->refs, t->num_pages, t->page_size};
+  return FA_OK;
+}
+
+// The table, the counts, then what a call reads or writes beside them; whether what it writes
+// (the first `written` of `r`) meets anything else.
+bool any_meet(const Range* r, int n, int written) {
+  for (int i = 0; i < written; ++i)
+    for (int j = i + 1; j < n; ++j)
+      if (ranges_meet(r[i].p, r[i].n, r[j].p, r[j].n)) return true;
+  return false;
+}
+Range table_range(const fa_page_table* t) { return {t->entries, table_bytes(t->rows, t->stride, t->width)}; }
+Range refs_range(const fa_page_table* t) { return {t->refs, static_cast<size_t>(t->num_pages) * 4}; }
+
 }  // namespace
 }  // namespace fa
 
@@ -314,6 +384,82 @@ int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache
   a.ws = static_cast<uint8_t*>(workspace);
   a.ws_bytes = workspace_bytes;
   return launch_cache_attention(a, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_cache_copy(const fa_cache* caches, int layers, const int32_t* src, const int32_t* dst, int n, struct CUstream_st* stream) {
+  if (n < 0 || (n > 0 && (src == nullptr || dst == nullptr)) || !aligned(src, 4) || !aligned(dst, 4)) return FA_ERR_INVALID_ARG;
+  const Range lists[2] = {{src, static_cast<size_t>(n) * 4}, {dst, static_cast<size_t>(n) * 4}};
+  int st = check_layers(caches, layers, lists, 2);
+  if (st != FA_OK || n == 0) return st;
+  PageCopyLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  if ((st = device_status_word(&a.status)) != FA_OK) return st;
+  a.src = src;
+  a.dst = dst;
+  a.n = n;
+  a.wait_limit = kWaitLimitCycles;
+  return launch_page_copy(a, caches, layers, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_cache_fork(const fa_page_table* table, const int32_t* parent, const int32_t* keep, struct CUstream_st* stream) {
+  PageForkLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  int st = check_page_table(table, &a.t);
+  if (st != FA_OK) return st;
+  if ((parent == nullptr && keep == nullptr) || !aligned(parent, 4) || !aligned(keep, 4)) return FA_ERR_INVALID_ARG;
+  const size_t len = static_cast<size_t>(table->rows) * 4;
+  const Range r[] = {table_range(table), refs_range(table), {parent, len}, {keep, len}};
+  if (any_meet(r, 4, 2)) return FA_ERR_INVALID_ARG;
+  if ((st = device_status_word(&a.status)) != FA_OK) return st;
+  a.parent = parent;
+  a.keep = keep;
+  return launch_page_fork(a, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_cache_reserve_workspace_bytes(int rows, int width, int num_pages) {
+  return check_page_table_sizes(rows, width, num_pages, 16) == FA_OK ? reserve_workspace(rows, width, num_pages) : 0;
+}
+
+int fa_cache_reserve(const fa_cache* caches, int layers, const fa_page_table* table, const int32_t* start, const int32_t* count,
+                     int tokens, int32_t* ok, void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
+  PageReserveLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  int st = check_page_table(table, &a.t);
+  if (st != FA_OK) return st;
+  if (ok == nullptr || !aligned(ok, 4) || !aligned(start, 4) || !aligned(count, 4) || tokens < 0) return FA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < reserve_workspace(table->rows, table->width, table->num_pages))
+    return FA_ERR_INVALID_ARG;
+  const size_t len = static_cast<size_t>(table->rows) * 4;
+  const Range r[] = {table_range(table), refs_range(table), {ok, len}, {workspace, workspace_bytes}, {start, len}, {count, len}};
+  if (any_meet(r, 6, 4)) return FA_ERR_INVALID_ARG;
+  if ((st = check_layers(caches, layers, r, 6)) != FA_OK) return st;
+  if (caches->num_pages != table->num_pages || caches->page_size != table->page_size) return FA_ERR_INVALID_ARG;
+  if ((st = device_status_word(&a.status)) != FA_OK) return st;
+  a.start = start;
+  a.count = count;
+  a.tokens = tokens;
+  a.ok = ok;
+  return launch_page_reserve(a, caches, layers, static_cast<uint8_t*>(workspace), stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_cache_compact_workspace_bytes(int num_pages) { return num_pages >= 1 ? compact_workspace(num_pages) : 0; }
+
+int fa_cache_compact(const fa_cache* caches, int layers, const fa_page_table* table, int32_t* where, int32_t* live,
+                     void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
+  PageCompactLaunch a;
+  std::memset(&a, 0, sizeof(a));
+  int st = check_page_table(table, &a.t);
+  if (st != FA_OK) return st;
+  if (where == nullptr || live == nullptr || !aligned(where, 4) || !aligned(live, 4)) return FA_ERR_INVALID_ARG;
+  if (workspace == nullptr || !aligned(workspace, 16) || workspace_bytes < compact_workspace(table->num_pages)) return FA_ERR_INVALID_ARG;
+  const Range r[] = {table_range(table), refs_range(table), {where, static_cast<size_t>(table->num_pages) * 4}, {live, 4}, {workspace, workspace_bytes}};
+  if (any_meet(r, 5, 5)) return FA_ERR_INVALID_ARG;
+  if ((st = check_layers(caches, layers, r, 5)) != FA_OK) return st;
+  if (caches->num_pages != table->num_pages || caches->page_size != table->page_size) return FA_ERR_INVALID_ARG;
+  if ((st = device_status_word(&a.status)) != FA_OK) return st;
+  a.where = where;
+  a.live = live;
+  return launch_page_compact(a, caches, layers, static_cast<uint8_t*>(workspace), stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // extern "C"

@@ -73,6 +73,72 @@ struct CacheAttnLaunch {
 cudaError_t launch_cache_attention(const CacheAttnLaunch& a, cudaStream_t stream);
 size_t cache_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width);
 
+// A page table with the counts of its pages' users (fa_page_table).
+struct PageTable {
+  int* entry;
+  long long stride;
+  int rows, width;
+  int* refs;
+  int num_pages, page;
+};
+
+constexpr int kCopyLayers = 64;  // layers of a launch
+struct PageCopyLaunch {
+  const int* src;
+  const int* dst;
+  const int* count;  // moves (device), nullptr: n
+  int n, num_pages, H, layers, piece;
+  long long page_bytes;  // codes of a page, K or V
+  int* status;
+  long long wait_limit;
+  struct Layer {
+    uint8_t* code[2];
+    float* scale[2];
+  } layer[kCopyLayers];
+};
+// a: src, dst, count, n, status, wait_limit; the rest comes from the caches.
+cudaError_t launch_page_copy(PageCopyLaunch a, const fa_cache* caches, int layers, cudaStream_t stream);
+
+struct PageForkLaunch {
+  PageTable t;
+  const int* parent;
+  const int* keep;
+  int* status;
+  int log2_cols;  // of a CTA
+};
+cudaError_t launch_page_fork(PageForkLaunch a, cudaStream_t stream);
+
+struct PageReserveLaunch {
+  PageTable t;
+  const int* start;
+  const int* count;
+  int tokens;  // of every row, where count is nullptr
+  int* ok;
+  int* status;
+  // workspace
+  int* moves;  // pages to be copied
+  int* slots;  // exchanges between the CTAs
+  int* src;    // [rows]
+  int* dst;
+  int* list;   // free pages
+};
+size_t reserve_workspace(int rows, int width, int num_pages);
+cudaError_t launch_page_reserve(PageReserveLaunch a, const fa_cache* caches, int layers, uint8_t* ws, cudaStream_t stream);
+
+struct PageCompactLaunch {
+  PageTable t;
+  int* where;
+  int* live;
+  int* status;
+  // workspace
+  int* moves;
+  int* slots;
+  int* src;
+  int* dst;
+};
+size_t compact_workspace(int num_pages);
+cudaError_t launch_page_compact(PageCompactLaunch a, const fa_cache* caches, int layers, uint8_t* ws, cudaStream_t stream);
+
 bool encode_code_rows(CUtensorMap* map, const void* base, long long rows, int d, int box_rows);
 
 // Records a page table entry out of range (fa_device_status).

@@ -1,0 +1,583 @@
+// The pages of the 8-bit cache: copying them in every layer, sequences that share them
+// (fa_cache_fork), pages for tokens to come (fa_cache_reserve), and moving the pages in use
+// together (fa_cache_compact). What these do is counting and copying; the definitions are in fa.h.
+//
+// refs[p] counts the table entries that name page p; a page is free where it is 0. The counts
+// change by integer adds, whose order does not matter, so that every call has one result.
+#include "fa_cache_internal.h"
+#include "fa_ptx.cuh"
+
+namespace fa {
+namespace {
+
+__device__ __forceinline__ bool is_page(int p, int num_pages) { return p >= 0 && p < num_pages; }
+
+// ------------------------------------------------------------------ copying
+// Every (move, layer, K or V) is a run of contiguous codes, cut into pieces. A CTA's first warp sends
+// its pieces through a ring in shared memory with bulk copies (no registers, no cache lines held); the
+// other warps copy the scales. Bound: memory, two bytes moved per code.
+constexpr int kCopyWarps = 4, kCopyStages = 8, kCopyAhead = 5;  // pieces that are loaded ahead
+constexpr int kCopySmem(int piece) { return kCopyStages * piece + 128; }
+
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(__cvta_generic_to_global(dst)),
+               "r"(smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+// Move m's pages; false where there is none.
+__device__ __forceinline__ bool move_of(const PageCopyLaunch& a, int m, int* src, int* dst) {
+  *src = a.src[m];
+  *dst = a.dst[m];
+  if (*src == -1 || *dst == -1 || *src == *dst) return false;
+  if (is_page(*src, a.num_pages) && is_page(*dst, a.num_pages)) return true;
+  report_bad_page(a.status);
+  return false;
+}
+
+__global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid_constant__ PageCopyLaunch a) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ __align__(8) uint64_t full[kCopyStages];
+  __shared__ int abort_flag;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kCopyStages; ++i) mbar_init(full + i, 1);
+    abort_flag = 0;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  grid_dep_wait();
+  grid_dep_launch();
+  const int n = a.count != nullptr ? min(a.n, *a.count) : a.n;
+  const int per_layer = 2, tensors = a.layers * per_layer;
+  if (warp > 0) {  // scales
+    const long long items = static_cast<long long>(n) * tensors;
+    for (long long i = blockIdx.x * (kCopyWarps - 1LL) + warp - 1; i < items; i += gridDim.x * (kCopyWarps - 1LL)) {
+      const int m = static_cast<int>(i / tensors), t = static_cast<int>(i - static_cast<long long>(m) * tensors);
+      int src, dst;
+      if (!move_of(a, m, &src, &dst)) continue;
+      float* const s = a.layer[t >> 1].scale[t & 1];
+      for (int h = lane; h < a.H; h += 32) s[static_cast<long long>(dst) * a.H + h] = s[static_cast<long long>(src) * a.H + h];
+    }
+    return;
+  }
+  const int pieces = static_cast<int>(a.page_bytes / a.piece);
+  const long long items = static_cast<long long>(n) * tensors * pieces;
+  const Watchdog wd{a.wait_limit, a.status, &abort_flag};
+  // Lane l looks up the warp's pieces l, l + 32, ...; lane 0 issues them.
+  const uint8_t* from = nullptr;
+  uint8_t* to = nullptr;
+  auto look = [&](long long k) {
+    const long long i = blockIdx.x + k * gridDim.x;
+    from = nullptr;
+    if (i >= items) return;
+    const long long mt = i / pieces;
+    const int part = static_cast<int>(i - mt * pieces), m = static_cast<int>(mt / tensors), t = static_cast<int>(mt - static_cast<long long>(m) * tensors);
+    int src, dst;
+    if (!move_of(a, m, &src, &dst)) return;
+    uint8_t* const c = a.layer[t >> 1].code[t & 1] + static_cast<long long>(part) * a.piece;
+    from = c + src * a.page_bytes;
+    to = c + dst * a.page_bytes;
+  };
+  const long long mine = items > blockIdx.x ? (items - blockIdx.x + gridDim.x - 1) / gridDim.x : 0;
+  long long loaded = 0, stored = 0;    // pieces
+  unsigned long long go[kCopyAhead];   // where the pieces that are loaded go to, in turn
+  // Lane 0 keeps the destinations; every lane walks the same loop.
+  bool ok = true;
+  for (long long k0 = 0; k0 < mine && ok; k0 += 32) {
+    look(k0 + lane);
+    const int batch = static_cast<int>(min(32LL, mine - k0));
+    for (int j = 0; j < batch && ok; ++j) {
+      const unsigned long long f = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(from), j);
+      const unsigned long long d = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(to), j);
+      if (f == 0ull) continue;  // no move
+      const int st = static_cast<int>(loaded % kCopyStages);
+      if (lane == 0) {
+        // the store that used the stage before has read it: at most the latest few have not
+        if (loaded >= kCopyStages) bulk_wait_read<kCopyStages - kCopyAhead - 1>();
+        mbar_expect_tx(full + st, a.piece);
+        bulk_load(smem + st * a.piece, reinterpret_cast<const void*>(f), a.piece, full + st);
+      }
+      __syncwarp();
+      // the destinations move up; [0] is the oldest piece that is not stored once the ring is full
+      const bool drain = loaded - stored == kCopyAhead;
+      if (drain) {
+        const int os = static_cast<int>(stored % kCopyStages);
+        ok = mbar_wait_warp(full + os, static_cast<uint32_t>(stored / kCopyStages) & 1u, wd);
+        if (ok) {
+          if (lane == 0) {
+            bulk_store(reinterpret_cast<void*>(go[0]), smem + os * a.piece, a.piece);
+            bulk_commit();
+          }
+          ++stored;
+#pragma unroll
+          for (int i = 0; i + 1 < kCopyAhead; ++i) go[i] = go[i + 1];
+        }
+      }
+      const int at = static_cast<int>(loaded - stored);
+#pragma unroll
+      for (int i = 0; i < kCopyAhead; ++i)
+        if (i == at) go[i] = d;
+      ++loaded;
+    }
+  }
+  for (; stored < loaded; ++stored) {
+    const int os = static_cast<int>(stored % kCopyStages);
+    const bool landed = mbar_wait_drain(full + os, static_cast<uint32_t>(stored / kCopyStages) & 1u, a.wait_limit);
+    if (!landed) {
+      ok = false;
+      if (lane == 0) watchdog_fire(a.status, &abort_flag);
+    }
+    if (ok && lane == 0) {
+      bulk_store(reinterpret_cast<void*>(go[0]), smem + os * a.piece, a.piece);
+      bulk_commit();
+    }
+    ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+#pragma unroll
+    for (int i = 0; i + 1 < kCopyAhead; ++i) go[i] = go[i + 1];
+  }
+  if (lane == 0) bulk_wait0();
+}
+
+// ------------------------------------------------------------------ forking
+// A CTA takes some columns of every row, so that rows can be exchanged in place: all of the
+// old entries that go to other rows are read into shared memory before any is written.
+constexpr int kForkThreads = 512, kForkWords = 16384;
+
+__global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const __grid_constant__ PageForkLaunch a) {
+  extern __shared__ int stage[];  // [rows][cols]
+  grid_dep_wait();
+  grid_dep_launch();
+  const PageTable& t = a.t;
+  const int c0 = blockIdx.x << a.log2_cols, cols = 1 << a.log2_cols;
+  const int n = t.rows << a.log2_cols;
+  // columns of row b that stay
+  auto kept = [&](int b) {
+    if (a.keep == nullptr) return t.width;
+    const long long k = max(0, a.keep[b]);
+    return static_cast<int>(min(static_cast<long long>(t.width), (k + t.page - 1) / t.page));
+  };
+  auto parent_of = [&](int b) {
+    if (a.parent == nullptr) return b;
+    const int p = a.parent[b];
+    if (p >= -1 && p < t.rows) return p;
+    if (c0 == 0) report_bad_page(a.status);
+    return b;  // such a row stays as it is, but for `keep`
+  };
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int b = i >> a.log2_cols, c = c0 + (i & (cols - 1));
+    if (c >= t.width) continue;
+    const int p = parent_of(b);
+    if (p == b) continue;
+    int e = -1;
+    if (p >= 0 && c < kept(b)) e = t.entry[p * t.stride + c];
+    if (e != -1 && !is_page(e, t.num_pages)) {
+      report_bad_page(a.status);
+      e = -1;
+    }
+    stage[i] = e;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kForkThreads) {
+    const int b = i >> a.log2_cols, c = c0 + (i & (cols - 1));
+    if (c >= t.width) continue;
+    const int p = parent_of(b);
+    int* const at = t.entry + b * t.stride + c;
+    if (p == b && c < kept(b)) continue;
+    const int now = p == b ? -1 : stage[i], old = *at;
+    if (old == now) continue;
+    *at = now;
+    if (now >= 0) atomicAdd(t.refs + now, 1);
+    if (is_page(old, t.num_pages))
+      atomicAdd(t.refs + old, -1);
+    else if (old != -1)
+      report_bad_page(a.status);
+  }
+}
+
+// ------------------------------------------------------------------ a cluster of CTAs that counts
+constexpr int kCluster = 8, kCountThreads = 512;
+
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ int load_l2(const int* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(__cvta_generic_to_global(p)) : "memory");
+  return v;
+}
+
+// Exclusive prefix of v over the CTA's threads, and the sum. `part`: kCountThreads / 32 words.
+__device__ __forceinline__ int block_scan(int v, int* part, int* total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = v;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += u;
+  }
+  __syncthreads();  // part's last values have been read
+  if (lane == 31) part[warp] = incl;
+  __syncthreads();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int w = 0; w < kCountThreads / 32; ++w) {
+    const int p = part[w];
+    if (w < warp) before += p;
+    sum += p;
+  }
+  *total = sum;
+  return before + incl - v;
+}
+// Each CTA's v, exchanged through `slot` (kCluster words of global memory, written by nobody
+// else meanwhile): what the CTAs before this one have, and all. A barrier of the cluster.
+__device__ __forceinline__ int cluster_scan(int v, int* slot, int rank, int* total) {
+  if (threadIdx.x == 0) slot[rank] = v;
+  cluster_sync();
+  int before = 0, sum = 0;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) {
+    const int x = load_l2(slot + r);
+    if (r < rank) before += x;
+    sum += x;
+  }
+  *total = sum;
+  return before;
+}
+// The CTA's share of the pages.
+struct PageSlice {
+  int first, end;
+};
+__device__ __forceinline__ PageSlice page_slice(int num_pages, int rank) {
+  const int per = ((num_pages + kCluster - 1) / kCluster + 3) & ~3;
+  const long long f = static_cast<long long>(per) * rank;
+  return PageSlice{static_cast<int>(min(f, static_cast<long long>(num_pages))),
+                   static_cast<int>(min(f + per, static_cast<long long>(num_pages)))};
+}
+// Pages p of the slice with want(p, refs[p]), counted.
+template <typename Want>
+__device__ __forceinline__ int count_pages(const PageSlice& s, const int* refs, int* part, Want want) {
+  int mine = 0, total;
+  for (int p = s.first + threadIdx.x; p < s.end; p += kCountThreads) mine += want(p, load_l2(refs + p)) ? 1 : 0;
+  block_scan(mine, part, &total);
+  return total;
+}
+// The same pages, in order: the k-th, from `rank0` on, goes to list[k] where k < most.
+template <typename Want>
+__device__ __forceinline__ void list_pages(const PageSlice& s, const int* refs, int* part, int rank0, int most, int* list, Want want) {
+  for (int p0 = s.first; p0 < s.end && rank0 < most; p0 += 4 * kCountThreads) {
+    const int p = p0 + 4 * threadIdx.x;
+    int w = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (p + i < s.end && want(p + i, load_l2(refs + p + i))) w |= 1 << i;
+    int total;
+    int k = rank0 + block_scan(__popc(w), part, &total);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (w >> i & 1) {
+        if (k < most) list[k] = p + i;
+        ++k;
+      }
+    rank0 += total;
+  }
+}
+
+// ------------------------------------------------------------------ reserving
+// The items are the columns of the rows' ranges, in the order of rows. Who copies a page that
+// several of them write to: all but the last one, which keeps it if nobody outside the call has it.
+// That is found in refs itself: every item takes itself off its page's count; where nothing
+// is left the last item, by an atomic minimum of -(2^30 + its number), keeps the page.
+// Bound: latency, some five round trips to memory between barriers of the cluster.
+constexpr int kReserveRows = 16384 / kCluster;  // of a CTA
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads)
+    page_reserve_kernel(const __grid_constant__ PageReserveLaunch a) {
+  __shared__ int first_item[kReserveRows + 1];  // of each of the CTA's rows
+  __shared__ int first_col[kReserveRows];
+  __shared__ int part[kCountThreads / 32];
+  __shared__ int fail_row;
+  const PageTable& t = a.t;
+  const int rank = blockIdx.x;  // the grid is one cluster
+  const int per = (t.rows + kCluster - 1) / kCluster, row0 = min(t.rows, rank * per), rows = min(t.rows, row0 + per) - row0;
+  grid_dep_wait();
+  if (threadIdx.x == 0) {
+    fail_row = t.rows;
+    if (rank == 0) *a.moves = 0;
+  }
+  // ---- the rows' ranges
+  int items = 0;
+  for (int r0 = 0; r0 < rows; r0 += kCountThreads) {
+    const int r = r0 + threadIdx.x, b = row0 + r;
+    int n = 0;
+    if (r < rows) {
+      const long long s = a.start != nullptr ? a.start[b] : 0;
+      const long long c = max(0, a.count != nullptr ? a.count[b] : a.tokens);
+      const bool fits = c == 0 || (s >= 0 && s + c <= static_cast<long long>(t.width) * t.page);
+      const int col = fits && c > 0 ? static_cast<int>(s / t.page) : 0;
+      if (fits && c > 0) n = static_cast<int>((s + c + t.page - 1) / t.page) - col;
+      first_col[r] = col;
+      a.ok[b] = fits ? 1 : 0;
+    }
+    int total;
+    const int k = block_scan(n, part, &total);
+    if (r < rows) first_item[r] = items + k;
+    items += total;
+  }
+  if (threadIdx.x == 0) first_item[rows] = items;
+  __syncthreads();
+  struct Item {
+    int r, col, entry, code;
+    bool page;  // entry names a page
+  };
+  auto item = [&](int i) {
+    int lo = 0, hi = rows;  // the last row with first_item <= i
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      (first_item[mid] <= i ? lo : hi) = mid;
+    }
+    Item x;
+    x.r = lo;
+    x.col = first_col[lo] + i - first_item[lo];
+    x.entry = t.entry[(row0 + lo) * t.stride + x.col];
+    x.page = is_page(x.entry, t.num_pages);
+    x.code = -(1 << 30) - ((row0 + lo) * t.width + x.col);
+    return x;
+  };
+  // ---- every item off its page's count
+  for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    const Item x = item(i);
+    if (x.page)
+      atomicAdd(t.refs + x.entry, -1);
+    else if (x.entry != -1)
+      report_bad_page(a.status);
+  }
+  cluster_sync();
+  // ---- pages that nobody else has: the last item keeps them
+  for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    const Item x = item(i);
+    if (x.page && load_l2(t.refs + x.entry) <= 0) atomicMin(t.refs + x.entry, x.code);
+  }
+  cluster_sync();
+  auto takes = [&](const Item& x) { return !x.page || load_l2(t.refs + x.entry) != x.code; };
+  int mine = 0, need, wanted, have, all_free = 0, free_before = 0;
+  for (int i = threadIdx.x; i < items; i += kCountThreads) mine += takes(item(i)) ? 1 : 0;
+  block_scan(mine, part, &need);
+  const int before = cluster_scan(need, a.slots, rank, &wanted);
+  int f = t.rows;  // the first row that fails
+  if (wanted > 0) {  // the same in every CTA
+    auto is_free = [](int, int refs) { return refs == 0; };
+    const PageSlice s = page_slice(t.num_pages, rank);
+    have = count_pages(s, t.refs, part, is_free);
+    free_before = cluster_scan(have, a.slots + kCluster, rank, &all_free);
+    if (wanted > all_free) {
+      int k0 = before;
+      for (int i0 = 0; i0 < items; i0 += kCountThreads) {
+        const int i = i0 + threadIdx.x;
+        Item x{};
+        const bool take = i < items && (x = item(i), takes(x));
+        int total;
+        const int k = k0 + block_scan(take ? 1 : 0, part, &total);
+        if (take && k >= all_free) atomicMin(&fail_row, row0 + x.r);
+        k0 += total;
+      }
+      __syncthreads();
+      if (threadIdx.x == 0) a.slots[2 * kCluster + rank] = fail_row;
+      cluster_sync();
+#pragma unroll
+      for (int r = 0; r < kCluster; ++r) f = min(f, load_l2(a.slots + 2 * kCluster + r));
+    }
+    list_pages(s, t.refs, part, free_before, min(wanted, all_free), a.list, is_free);
+    cluster_sync();
+  }
+  // ---- pages dealt out
+  int k0 = before;
+  for (int i0 = 0; i0 < items; i0 += kCountThreads) {
+    const int i = i0 + threadIdx.x;
+    Item x{};
+    bool take = false, keeps = false;
+    if (i < items) {
+      x = item(i);
+      take = takes(x);
+      keeps = !take;
+    }
+    int total;
+    const int k = k0 + block_scan(take ? 1 : 0, part, &total), b = row0 + x.r;
+    if (keeps) t.refs[x.entry] = b < f ? 1 : 0;  // (below, the rows that fail come back to their pages' counts)
+    if (take && b < f) {
+      const int p = load_l2(a.list + k);
+      t.entry[b * t.stride + x.col] = p;
+      t.refs[p] = 1;
+      // earlier tokens of the sequence in the page
+      if (x.page && i == first_item[x.r] && (a.start != nullptr ? a.start[b] : 0) % t.page != 0) {
+        const int m = atomicAdd(a.moves, 1);
+        a.src[m] = x.entry;
+        a.dst[m] = p;
+      }
+    }
+    k0 += total;
+  }
+  if (f < t.rows) {
+    cluster_sync();
+    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+      const Item x = item(i);
+      if (x.page && row0 + x.r >= f) atomicAdd(t.refs + x.entry, 1);
+    }
+    cluster_sync();
+    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+      const Item x = item(i);
+      if (row0 + x.r >= f && (!x.page || load_l2(t.refs + x.entry) != 1)) a.ok[row0 + x.r] = 0;
+    }
+  }
+  grid_dep_launch();
+}
+
+// ------------------------------------------------------------------ compacting
+// L pages are in use. The k-th of them with a number >= L goes to the k-th free number below L, so
+// that no page is read and written, and no more pages move than have to.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads)
+    page_compact_kernel(const __grid_constant__ PageCompactLaunch a) {
+  __shared__ int part[kCountThreads / 32];
+  const int rank = blockIdx.x, P = a.t.num_pages;
+  int* const refs = a.t.refs;
+  grid_dep_wait();
+  const PageSlice s = page_slice(P, rank);
+  int live, moves, holes;
+  cluster_scan(count_pages(s, refs, part, [](int, int r) { return r != 0; }), a.slots, rank, &live);
+  auto mover = [live](int p, int r) { return p >= live && r != 0; };
+  auto hole = [live](int p, int r) { return p < live && r == 0; };
+  const int m0 = cluster_scan(count_pages(s, refs, part, mover), a.slots + kCluster, rank, &moves);
+  const int h0 = cluster_scan(count_pages(s, refs, part, hole), a.slots + 2 * kCluster, rank, &holes);
+  list_pages(s, refs, part, m0, moves, a.src, mover);
+  list_pages(s, refs, part, h0, moves, a.dst, hole);
+  for (int p = s.first + threadIdx.x; p < s.end; p += kCountThreads) a.where[p] = load_l2(refs + p) != 0 ? p : -1;
+  if (rank == 0 && threadIdx.x == 0) {
+    *a.live = live;
+    *a.moves = moves;
+  }
+  cluster_sync();
+  for (int k = rank * kCountThreads + threadIdx.x; k < moves; k += kCluster * kCountThreads) {
+    const int from = load_l2(a.src + k), to = load_l2(a.dst + k);
+    a.where[from] = to;
+    refs[to] = load_l2(refs + from);
+    refs[from] = 0;
+  }
+  grid_dep_launch();
+}
+
+__global__ void __launch_bounds__(256) page_rename_kernel(const __grid_constant__ PageCompactLaunch a) {
+  grid_dep_wait();
+  grid_dep_launch();
+  const PageTable& t = a.t;
+  const long long n = static_cast<long long>(t.rows) * t.width;
+  for (long long i = blockIdx.x * 256LL + threadIdx.x; i < n; i += gridDim.x * 256LL) {
+    const long long b = i / t.width;
+    int* const at = t.entry + b * t.stride + (i - b * t.width);
+    const int e = *at;
+    if (is_page(e, t.num_pages))
+      *at = a.where[e];
+    else if (e != -1)
+      report_bad_page(a.status);
+  }
+}
+
+size_t words(long long n) { return align256(static_cast<size_t>(n) * 4); }
+
+}  // namespace
+
+cudaError_t launch_page_copy(PageCopyLaunch a, const fa_cache* caches, int layers, cudaStream_t stream) {
+  const fa_cache& c = caches[0];
+  a.page_bytes = static_cast<long long>(c.H) * c.page_size * c.d;
+  a.H = c.H;
+  a.num_pages = c.num_pages;
+  for (int l0 = 0; l0 < layers; l0 += kCopyLayers) {
+    a.layers = layers - l0 < kCopyLayers ? layers - l0 : kCopyLayers;
+    for (int l = 0; l < a.layers; ++l) {
+      const fa_cache& x = caches[l0 + l];
+      a.layer[l] = PageCopyLaunch::Layer{{static_cast<uint8_t*>(x.k), static_cast<uint8_t*>(x.v)}, {x.k_scale, x.v_scale}};
+    }
+    // pieces of 16 KB, smaller ones where there would be few
+    const long long runs = static_cast<long long>(a.n) * a.layers * 2;
+    long long piece = a.page_bytes;
+    while (piece > 16384 || (piece > 2048 && runs * (a.page_bytes / piece) < 4LL * sm_count())) {
+      if (piece % 2 == 0 && (piece / 2) % 128 == 0) {
+        piece /= 2;
+        continue;
+      }
+      // an odd number of heads: a multiple of 1024 bytes that divides the page
+      long long best = 1024;
+      for (long long p = 2048; p < piece && p <= 16384; p += 1024)
+        if (a.page_bytes % p == 0) best = p;
+      piece = best;
+      break;
+    }
+    a.piece = static_cast<int>(piece);
+    const long long items = runs * (a.page_bytes / piece);
+    const int grid = static_cast<int>(items < sm_count() ? items : sm_count());
+    static std::atomic<unsigned long long> smem_set{0};
+    cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_copy_kernel), kCopySmem(16384));
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(page_copy_kernel, dim3(grid), dim3(kCopyWarps * 32), kCopySmem(a.piece), stream, a);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+cudaError_t launch_page_fork(PageForkLaunch a, cudaStream_t stream) {
+  // 32 columns a CTA, fewer where the staged entries would not fit or most SMs would be idle
+  a.log2_cols = 5;
+  while (a.log2_cols > 0 && ((a.t.rows << a.log2_cols) > kForkWords ||
+                             (a.log2_cols > 3 && (a.t.width >> a.log2_cols) < sm_count())))
+    --a.log2_cols;
+  const int smem = (a.t.rows << a.log2_cols) * 4;
+  static std::atomic<unsigned long long> smem_set{0};
+  const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_fork_kernel), kForkWords * 4);
+  if (e != cudaSuccess) return e;
+  const int grid = (a.t.width + (1 << a.log2_cols) - 1) >> a.log2_cols;
+  return launch_pdl(page_fork_kernel, dim3(grid), dim3(kForkThreads), smem, stream, a);
+}
+
+size_t reserve_workspace(int rows, int width, int num_pages) {
+  const long long most = static_cast<long long>(rows) * width;  // pages that a call can take
+  return 256 + 2 * words(rows) + words(most < num_pages ? most : num_pages);
+}
+cudaError_t launch_page_reserve(PageReserveLaunch a, const fa_cache* caches, int layers, uint8_t* ws, cudaStream_t stream) {
+  a.moves = reinterpret_cast<int*>(ws);
+  a.slots = a.moves + 8;
+  a.src = reinterpret_cast<int*>(ws + 256);
+  a.dst = reinterpret_cast<int*>(ws + 256 + words(a.t.rows));
+  a.list = reinterpret_cast<int*>(ws + 256 + 2 * words(a.t.rows));
+  cudaError_t e = launch_pdl(page_reserve_kernel, dim3(kCluster), dim3(kCountThreads), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  PageCopyLaunch c{};
+  c.src = a.src;
+  c.dst = a.dst;
+  c.n = a.t.rows;
+  c.count = a.moves;
+  c.status = a.status;
+  c.wait_limit = kWaitLimitCycles;
+  return launch_page_copy(c, caches, layers, stream);
+}
+
+size_t compact_workspace(int num_pages) { return 256 + 2 * words(num_pages / 2 + 1); }
+cudaError_t launch_page_compact(PageCompactLaunch a, const fa_cache* caches, int layers, uint8_t* ws, cudaStream_t stream) {
+  a.moves = reinterpret_cast<int*>(ws);
+  a.slots = a.moves + 8;
+  a.src = reinterpret_cast<int*>(ws + 256);
+  a.dst = reinterpret_cast<int*>(ws + 256 + words(a.t.num_pages / 2 + 1));
+  cudaError_t e = launch_pdl(page_compact_kernel, dim3(kCluster), dim3(kCountThreads), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  const long long n = static_cast<long long>(a.t.rows) * a.t.width, blocks = (n + 255) / 256, most = 4LL * sm_count();
+  e = launch_pdl(page_rename_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, stream, a);
+  if (e != cudaSuccess) return e;
+  PageCopyLaunch c{};
+  c.src = a.src;
+  c.dst = a.dst;
+  c.n = a.t.num_pages / 2 > 0 ? a.t.num_pages / 2 : 1;
+  c.count = a.moves;
+  c.status = a.status;
+  c.wait_limit = kWaitLimitCycles;
+  return launch_page_copy(c, caches, layers, stream);
+}
+
+}  // namespace fa

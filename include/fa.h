@@ -475,11 +475,84 @@ int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache
                        int N, const fa_cache_attention_options* opt, void* workspace,
                        size_t workspace_bytes, struct CUstream_st* stream);
 
+/* ------------------------------------------------------------------------
+ * The pages of a cache, dealt out on the device: sequences that share pages,
+ * pages for tokens to come, copies. One page table serves every layer of a
+ * model: its entries name a page in each layer's pool, so these calls take the
+ * pools of all `layers` (fa_cache each; HOST array, read before the call returns; same
+ * num_pages, H, page_size, d and format, no memory in common).
+ * Calls that share a table or counts must be ordered on the GPU. Results do not depend on
+ * the order in which threads run.
+ * ------------------------------------------------------------------------ */
+
+/* A page table and how many of its entries name each page.
+ *   entries   : DEVICE int32, row b at b * stride, width entries: a page, or -1 for none;
+ *               rows * width <= 2^30, rows <= 16384, stride >= width;
+ *   refs      : DEVICE int32 [num_pages]: entries that name page p, plus whatever the
+ *               caller adds for users of its own. A page is free where it is 0. */
+typedef struct fa_page_table {
+  int32_t* entries;
+  int64_t stride;
+  int rows, width;
+  int32_t* refs;
+  int num_pages, page_size;
+} fa_page_table;
+
+/* Copies page src[i] to page dst[i], i < n, codes and scales, K and V, in every layer.
+ *   src, dst : DEVICE int32 [n]; a move with -1 in either is left out. No dst may be another
+ *              move's src or dst. Others out of range are left out and reported
+ *              as FA_ERR_BAD_PAGE. */
+int fa_cache_copy(const fa_cache* caches, int layers, const int32_t* src, const int32_t* dst, int n,
+                  struct CUstream_st* stream);
+
+/* Rows of the table become copies of other rows, all at once and in place:
+ *   parent : DEVICE int32 [rows]: row b takes the entries that row parent[b] had before the
+ *            call; -1 empties it; parent[b] = b leaves it as it is. NULL: every row its own. A parent
+ *            out of range counts as b and is reported (FA_ERR_BAD_PAGE);
+ *   keep   : DEVICE int32 [rows], or NULL: of the new row only the entries of its first
+ *            keep[b] tokens stay (negative: none), the others become -1.
+ * With that, refs gains the entries that were made and loses those that are gone: samples of one
+ * prompt, beams in any order, a prompt taken up at an earlier token, finished
+ * sequences and rejected drafts. A page that several rows name holds the same
+ * tokens for all of them; before one of them writes on, fa_cache_reserve gives it its own.
+ * An entry out of range becomes -1 where it is copied or dropped, and is reported. */
+int fa_cache_fork(const fa_page_table* table, const int32_t* parent, const int32_t* keep, struct CUstream_st* stream);
+
+size_t fa_cache_reserve_workspace_bytes(int rows, int width, int num_pages);
+
+/* Sees to it that row b has a page of its own for each of the tokens start[b] + n,
+ * n < count[b], before they are written. In the order of rows and columns: an entry of -1 gets
+ * the lowest page that was free before the call and is not taken yet; an entry whose page other entries
+ * name as well gets such a page instead, with the page's contents copied in every
+ * layer where it holds earlier tokens of the row (its first column, start[b] not at the
+ * page's beginning). refs follows.
+ *   start : DEVICE int32 [rows], or NULL for 0;
+ *   count : DEVICE int32 [rows], or NULL for `tokens` >= 0 in every row (negative: 0);
+ *   ok    : DEVICE int32 [rows], written: 1 where the row has what it needs, 0 otherwise.
+ * A row whose tokens start below 0 or pass the table's width is left as it is (ok 0). If there are too few free
+ * pages, the first row that lacks one is left as it is, and from there on no pages are dealt out: a later
+ * row is ok if it needs none. Rows that are not ok must not be written to. An entry out of
+ * range is reported (FA_ERR_BAD_PAGE) and treated as -1.
+ *   workspace : DEVICE, 16-byte aligned, fa_cache_reserve_workspace_bytes at least. */
+int fa_cache_reserve(const fa_cache* caches, int layers, const fa_page_table* table, const int32_t* start, const int32_t* count,
+                     int tokens, int32_t* ok, void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
+size_t fa_cache_compact_workspace_bytes(int num_pages);
+
+/* Moves the L pages in use to the numbers below L: the k-th page in use with a number >= L takes
+ * the k-th free one below L, in every layer, in refs and in the table.
+ *   where : DEVICE int32 [num_pages], written: the page's new number, -1 for free ones (for
+ *           tables and lists that the caller has besides);
+ *   live  : DEVICE int32 [1], written: L.
+ *   workspace : DEVICE, 16-byte aligned, fa_cache_compact_workspace_bytes at least. */
+int fa_cache_compact(const fa_cache* caches, int layers, const fa_page_table* table, int32_t* where, int32_t* live,
+                     void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
 /* Device-side status of the current device: FA_OK, or FA_ERR_DEVICE_TIMEOUT
  * if a bounded wait inside a kernel gave up since the last call, or (in a
  * library built with FA_CHECKS=1) FA_ERR_DEVICE_CHECK if a TMA copy failed
  * its coordinate or alignment check and was skipped, or FA_ERR_BAD_PAGE
- * if a page table entry was out of range. Reading clears it. Call only after synchronising the streams that ran the
+ * if a page table entry (or a row's parent) was out of range. Reading clears it. Call only after synchronising the streams that ran the
  * kernels. Returns FA_ERR_CUDA if the status word cannot be read. */
 int fa_device_status(void);
 
