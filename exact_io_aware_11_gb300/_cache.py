@@ -58,6 +58,10 @@ SIGNATURES["fa_cache_attention_workspace_bytes"] = (_SZ, [ctypes.POINTER(CacheSt
 SIGNATURES["fa_cache_attention"] = (_I, [_P, _P, _P, ctypes.POINTER(CacheStruct), _I, _I, _I,
                                          ctypes.POINTER(CacheAttentionOptions), _P, _SZ, _P])
 
+SIGNATURES["fa_cache_attention_shared_workspace_bytes"] = (_SZ, [ctypes.POINTER(CacheStruct), _I, _I, _I, _I, _I])
+SIGNATURES["fa_cache_attention_shared"] = (_I, [_P, _P, _P, ctypes.POINTER(CacheStruct), _I, _I, _I,
+                                                ctypes.POINTER(CacheAttentionOptions), _P, _P, _I, _P, _SZ, _P])
+
 # These calls are made once per layer and token: the checks below read each attribute once,
 # and the stream comes from the binding that torch.cuda.current_stream wraps (0.1 us against 2).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
@@ -364,7 +368,8 @@ def cache_attention(q, cache: KVCache, page_table, kv_len, q_len=None, causal: b
                workspace, split)
 
 
-def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, lse, workspace, split):
+def _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse):
+    """What both attention calls check and allocate: out, lse and the arguments that describe them."""
     dev = cache.device
     n, qs = _rows(q, "q", dev)
     B, H, N, d = n
@@ -379,16 +384,61 @@ def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, ls
         lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
     elif lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, H, N] on the tensors' device")
-    L = lib()
-    if workspace is not None:
-        if workspace.device != dev or not workspace.is_contiguous():
-            raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
-        need = workspace.numel() * workspace.element_size() if split else 0
-    else:
-        need = L.fa_cache_attention_workspace_bytes(cache._struct, B, H, N, pages) if split else 0
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
     opt = CacheAttentionOptions(table, table_stride, pages, kl, ql, 1 if causal else 0, _DTYPES[q.dtype],
                                 d ** -0.5 if scale is None else scale, *qs, *os)
-    _done(L.fa_cache_attention(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache._struct, B, H, N, opt,
-                               workspace.data_ptr() if need else None, need, _raw_stream(dev.index)), "fa_cache_attention")
+    return o, lse, opt, (q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache._struct, B, H, N, opt)
+
+
+def _check_workspace(workspace, dev):
+    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
+    return workspace.numel() * workspace.element_size()
+
+
+def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, lse, workspace, split):
+    dev = cache.device
+    o, lse, opt, args = _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse)
+    L = lib()
+    if workspace is not None:
+        need = _check_workspace(workspace, dev) if split else 0
+    else:
+        need = L.fa_cache_attention_workspace_bytes(cache._struct, *args[4:7], opt.table_width) if split else 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _done(L.fa_cache_attention(*args, workspace.data_ptr() if need else None, need, _raw_stream(dev.index)), "fa_cache_attention")
+    return o, lse
+
+
+def cache_attention_shared_workspace_bytes(cache: KVCache, B: int, heads: int, N: int, pages: int, groups: int) -> int:
+    """Workspace bytes of cache_attention_shared, for q [B, heads, N, d], a page table of `pages`
+    columns and `groups` groups."""
+    return _on(lib().fa_cache_attention_shared_workspace_bytes, _check_cache(cache), None, cache._struct, B, heads, N, pages, groups)
+
+
+def cache_attention_shared(q, cache: KVCache, page_table, kv_len, prefix_of, prefix_len, q_len=None, causal: bool = True,
+                           scale: float | None = None, out=None, lse=None, workspace=None, stream=None):
+    """cache_attention of a batch whose sequences share prefixes, whose keys are read once for all of a
+    group (fa_cache_attention_shared): the same O, LSE. prefix_of: int32 [B], each sequence's group (-1: none);
+    prefix_len: int32 [groups], tokens that a group shares, in the same pages (whole pages count).
+    page_table's rows and kv_len are the whole sequences', prefix included, as cache_fork
+    leaves them. `workspace`: uint8 of cache_attention_shared_workspace_bytes(...) bytes, allocated here if None."""
+    return _on(_cache_attention_shared, _check_cache(cache), stream, q, cache, page_table, kv_len, prefix_of, prefix_len, q_len, causal,
+               scale, out, lse, workspace)
+
+
+def _cache_attention_shared(q, cache, page_table, kv_len, prefix_of, prefix_len, q_len, causal, scale, out, lse, workspace):
+    dev = cache.device
+    o, lse, opt, args = _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse)
+    of = _check_lengths(prefix_of, "prefix_of", dev, args[4])
+    _check_int(prefix_len, "prefix_len", dev, 1)
+    groups = prefix_len.shape[0]
+    if of is None or groups < 1 or not prefix_len.is_contiguous():
+        raise ValueError("prefix_of must be int32 [B] and prefix_len contiguous int32 [groups]")
+    L = lib()
+    if workspace is not None:
+        need = _check_workspace(workspace, dev)
+    else:
+        need = L.fa_cache_attention_shared_workspace_bytes(cache._struct, *args[4:7], opt.table_width, groups)
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    _done(L.fa_cache_attention_shared(*args, of, prefix_len.data_ptr(), groups, workspace.data_ptr() if need else None, need,
+                                      _raw_stream(dev.index)), "fa_cache_attention_shared")
     return o, lse

@@ -226,13 +226,76 @@ int check_attention_sizes(const fa_cache* cache, int B, int Hq, int N, int table
   return FA_OK;
 }
 
-// ------------------------------------------------------------------ pages
-constexpr int kMaxLayers = 1024, kMaxTableRows = 16384;
-
 struct Range {
   const void* p;
   size_t n;
 };
+
+// Checks a call of the attention and describes its launch. more: what else it reads.
+int make_attention(const void* q, void* o, float* lse, const fa_cache* cache, int B, int Hq, int N,
+                   const fa_cache_attention_options* opt, void* workspace, size_t workspace_bytes, const Range* more, int n_more,
+                   CacheAttnLaunch* launch) {
+  if (opt == nullptr) return FA_ERR_INVALID_ARG;
+  CacheAttnLaunch& a = *launch;
+  std::memset(&a, 0, sizeof(a));
+  int st = check_cache(cache, opt->page_table, opt->table_stride, opt->table_width, &a.c);
+  if (st != FA_OK) return st;
+  if ((st = check_attention_sizes(cache, B, Hq, N, opt->table_width)) != FA_OK) return st;
+  if (opt->dtype != FA_BF16 && opt->dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
+  if (opt->causal != 0 && opt->causal != 1) return FA_ERR_INVALID_ARG;
+  const float scale_log2 = opt->scale * 1.4426950408889634f;
+  if (!std::isfinite(scale_log2) || !(opt->scale > 0.f)) return FA_ERR_INVALID_ARG;
+  if (opt->kv_len == nullptr || !aligned(opt->kv_len, 4) || !aligned(opt->q_len, 4)) return FA_ERR_INVALID_ARG;
+  if (lse == nullptr || !aligned(lse, 16)) return FA_ERR_INVALID_ARG;
+  if ((workspace == nullptr && workspace_bytes != 0) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
+  Tensor tq, to;
+  if ((st = make_tensor(q, B, Hq, N, cache->d, opt->q_stride, &tq)) != FA_OK) return st;
+  if ((st = make_tensor(o, B, Hq, N, cache->d, opt->o_stride, &to)) != FA_OK) return st;
+  const size_t lse_bytes = static_cast<size_t>(B) * Hq * N * 4, len = static_cast<size_t>(B) * 4;
+  const size_t tab = table_bytes(B, opt->table_stride, opt->table_width);
+  if (tensors_meet(to, tq) || ranges_meet(lse, lse_bytes, q, tq.bytes()) || ranges_meet(lse, lse_bytes, o, to.bytes()))
+    return FA_ERR_INVALID_ARG;
+  const struct {
+    const void* p;
+    size_t n;
+  } outs[] = {{o, to.bytes()}, {lse, lse_bytes}, {workspace, workspace_bytes}};
+  for (const auto& x : outs) {
+    for (int i = 0; i < n_more; ++i)
+      if (ranges_meet(x.p, x.n, more[i].p, more[i].n)) return FA_ERR_INVALID_ARG;
+    if (meets_cache(cache, x.p, x.n) || ranges_meet(x.p, x.n, opt->page_table, tab) ||
+        ranges_meet(x.p, x.n, opt->kv_len, len) || ranges_meet(x.p, x.n, opt->q_len, len))
+      return FA_ERR_INVALID_ARG;
+  }
+  if (ranges_meet(workspace, workspace_bytes, q, tq.bytes()) || ranges_meet(workspace, workspace_bytes, o, to.bytes()) ||
+      ranges_meet(workspace, workspace_bytes, lse, lse_bytes))
+    return FA_ERR_INVALID_ARG;
+  if ((st = device_status_word(&a.status)) != FA_OK) return st;
+  a.q = static_cast<const uint16_t*>(q);
+  a.o = static_cast<uint16_t*>(o);
+  a.lse = lse;
+  a.sq = tq.rows();
+  a.so = to.rows();
+  a.B = B;
+  a.Hq = Hq;
+  a.N = N;
+  a.G = Hq / cache->H;
+  a.fp16 = opt->dtype == FA_FP16;
+  a.causal = opt->causal;
+  a.scale_log2 = scale_log2;
+  a.kv_len = opt->kv_len;
+  a.q_len = opt->q_len;
+  a.wait_limit = kWaitLimitCycles;
+  const long long pool_rows = static_cast<long long>(cache->num_pages) * cache->H * cache->page_size;
+  if (!encode_code_rows(&a.tm[0], cache->k, pool_rows, cache->d, cache->page_size) ||
+      !encode_code_rows(&a.tm[1], cache->v, pool_rows, cache->d, cache->page_size))
+    return FA_ERR_CUDA;
+  a.ws = static_cast<uint8_t*>(workspace);
+  a.ws_bytes = workspace_bytes;
+  return FA_OK;
+}
+
+// ------------------------------------------------------------------ pages
+constexpr int kMaxLayers = 1024, kMaxTableRows = 16384;
 
 // The pools of a model's layers: all of one shape, no memory in common, and none with `others`.
 int check_layers(const fa_cache* caches, int layers, const Range* others, int n_others) {
@@ -330,60 +393,30 @@ size_t fa_cache_attention_workspace_bytes(const fa_cache* cache, int B, int Hq, 
 int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache, int B, int Hq, int N,
                        const fa_cache_attention_options* opt, void* workspace, size_t workspace_bytes,
                        struct CUstream_st* stream) {
-  if (opt == nullptr) return FA_ERR_INVALID_ARG;
   CacheAttnLaunch a;
-  std::memset(&a, 0, sizeof(a));
-  int st = check_cache(cache, opt->page_table, opt->table_stride, opt->table_width, &a.c);
+  const int st = make_attention(q, o, lse, cache, B, Hq, N, opt, workspace, workspace_bytes, nullptr, 0, &a);
   if (st != FA_OK) return st;
-  if ((st = check_attention_sizes(cache, B, Hq, N, opt->table_width)) != FA_OK) return st;
-  if (opt->dtype != FA_BF16 && opt->dtype != FA_FP16) return FA_ERR_UNSUPPORTED;
-  if (opt->causal != 0 && opt->causal != 1) return FA_ERR_INVALID_ARG;
-  const float scale_log2 = opt->scale * 1.4426950408889634f;
-  if (!std::isfinite(scale_log2) || !(opt->scale > 0.f)) return FA_ERR_INVALID_ARG;
-  if (opt->kv_len == nullptr || !aligned(opt->kv_len, 4) || !aligned(opt->q_len, 4)) return FA_ERR_INVALID_ARG;
-  if (lse == nullptr || !aligned(lse, 16)) return FA_ERR_INVALID_ARG;
-  if ((workspace == nullptr && workspace_bytes != 0) || !aligned(workspace, 16)) return FA_ERR_INVALID_ARG;
-  Tensor tq, to;
-  if ((st = make_tensor(q, B, Hq, N, cache->d, opt->q_stride, &tq)) != FA_OK) return st;
-  if ((st = make_tensor(o, B, Hq, N, cache->d, opt->o_stride, &to)) != FA_OK) return st;
-  const size_t lse_bytes = static_cast<size_t>(B) * Hq * N * 4, len = static_cast<size_t>(B) * 4;
-  const size_t tab = table_bytes(B, opt->table_stride, opt->table_width);
-  if (tensors_meet(to, tq) || ranges_meet(lse, lse_bytes, q, tq.bytes()) || ranges_meet(lse, lse_bytes, o, to.bytes()))
-    return FA_ERR_INVALID_ARG;
-  const struct {
-    const void* p;
-    size_t n;
-  } outs[] = {{o, to.bytes()}, {lse, lse_bytes}, {workspace, workspace_bytes}};
-  for (const auto& x : outs)
-    if (meets_cache(cache, x.p, x.n) || ranges_meet(x.p, x.n, opt->page_table, tab) ||
-        ranges_meet(x.p, x.n, opt->kv_len, len) || ranges_meet(x.p, x.n, opt->q_len, len))
-      return FA_ERR_INVALID_ARG;
-  if (ranges_meet(workspace, workspace_bytes, q, tq.bytes()) || ranges_meet(workspace, workspace_bytes, o, to.bytes()) ||
-      ranges_meet(workspace, workspace_bytes, lse, lse_bytes))
-    return FA_ERR_INVALID_ARG;
-  if ((st = device_status_word(&a.status)) != FA_OK) return st;
-  a.q = static_cast<const uint16_t*>(q);
-  a.o = static_cast<uint16_t*>(o);
-  a.lse = lse;
-  a.sq = tq.rows();
-  a.so = to.rows();
-  a.B = B;
-  a.Hq = Hq;
-  a.N = N;
-  a.G = Hq / cache->H;
-  a.fp16 = opt->dtype == FA_FP16;
-  a.causal = opt->causal;
-  a.scale_log2 = scale_log2;
-  a.kv_len = opt->kv_len;
-  a.q_len = opt->q_len;
-  a.wait_limit = kWaitLimitCycles;
-  const long long pool_rows = static_cast<long long>(cache->num_pages) * cache->H * cache->page_size;
-  if (!encode_code_rows(&a.tm[0], cache->k, pool_rows, cache->d, cache->page_size) ||
-      !encode_code_rows(&a.tm[1], cache->v, pool_rows, cache->d, cache->page_size))
-    return FA_ERR_CUDA;
-  a.ws = static_cast<uint8_t*>(workspace);
-  a.ws_bytes = workspace_bytes;
   return launch_cache_attention(a, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
+}
+
+size_t fa_cache_attention_shared_workspace_bytes(const fa_cache* cache, int B, int Hq, int N, int table_width, int groups) {
+  if (check_attention_sizes(cache, B, Hq, N, table_width) != FA_OK || groups < 1 || groups > kSharedGroups) return 0;
+  return shared_attention_workspace(B, cache->H, Hq / cache->H, N, cache->d, cache->page_size, table_width, groups);
+}
+
+int fa_cache_attention_shared(const void* q, void* o, float* lse, const fa_cache* cache, int B, int Hq, int N,
+                              const fa_cache_attention_options* opt, const int32_t* prefix_of, const int32_t* prefix_len, int groups,
+                              void* workspace, size_t workspace_bytes, struct CUstream_st* stream) {
+  if (groups < 1 || groups > kSharedGroups || prefix_of == nullptr || prefix_len == nullptr || !aligned(prefix_of, 4) ||
+      !aligned(prefix_len, 4) || B < 1)
+    return FA_ERR_INVALID_ARG;
+  const Range more[2] = {{prefix_of, static_cast<size_t>(B) * 4}, {prefix_len, static_cast<size_t>(groups) * 4}};
+  CacheAttnLaunch a;
+  const int st = make_attention(q, o, lse, cache, B, Hq, N, opt, workspace, workspace_bytes, more, 2, &a);
+  if (st != FA_OK) return st;
+  if (workspace_bytes < shared_attention_workspace(B, cache->H, a.G, N, cache->d, cache->page_size, opt->table_width, groups))
+    return FA_ERR_INVALID_ARG;
+  return launch_shared_attention(a, prefix_of, prefix_len, groups, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_cache_copy(const fa_cache* caches, int layers, const int32_t* src, const int32_t* dst, int n, struct CUstream_st* stream) {

@@ -1,5 +1,6 @@
 // Launch descriptions of the rotary and cache entry points (fa_cache_api.cu)
-// and the kernels behind them (fa_rotary.cu, fa_cache.cu, fa_cache_attn.cu, fa_cache_tile.cuh).
+// and the kernels behind them (fa_rotary.cu, fa_cache.cu, fa_cache_attn.cu, fa_cache_rows.cuh,
+// fa_cache_tile.cuh, fa_cache_shared.cu, fa_cache_pages.cu).
 #pragma once
 
 #include "fa.h"
@@ -72,6 +73,10 @@ struct CacheAttnLaunch {
 };
 cudaError_t launch_cache_attention(const CacheAttnLaunch& a, cudaStream_t stream);
 size_t cache_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width);
+constexpr int kSharedGroups = 2048;  // groups of a call with shared prefixes
+cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* prefix_of, const int32_t* prefix_len, int groups,
+                                    cudaStream_t stream);
+size_t shared_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width, int groups);
 
 // A page table with the counts of its pages' users (fa_page_table).
 struct PageTable {

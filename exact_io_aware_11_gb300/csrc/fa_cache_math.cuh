@@ -76,14 +76,14 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t& lo, uint32_t& hi) 
 }
 
 // Channels [c0, c0 + 4 W) of V, c0 a multiple of 4, that are NaN at one of the keys [first, end) of a
-// sequence and cache head: a bit each. For rows that see a NaN which was taken out of a tile because other
+// sequence and cache head, from entry `tab` of the page table on: a bit each. For rows that see a NaN which was taken out of a tile because other
 // rows of the unit do not see all of its keys: at most a tile's keys and a unit's rows of them.
 template <int W>
-__device__ __forceinline__ unsigned long long seen_nan(const CacheView& c, int b, int h, int first, int end, int c0) {
+__device__ __forceinline__ unsigned long long seen_nan(const CacheView& c, long long tab, int h, int first, int end, int c0) {
   unsigned long long bits = 0ull;
 #pragma unroll 1
   for (int key = first; key < end; ++key) {
-    const int p = c.table[b * c.table_stride + (key >> c.log2_page)];
+    const int p = c.table[tab + (key >> c.log2_page)];
     if (p < 0 || p >= c.num_pages) continue;  // not read
     const long long row = ((static_cast<long long>(p) * c.H + h) << c.log2_page) + (key & (c.page - 1));
     const uint32_t* const at = reinterpret_cast<const uint32_t*>(c.code[1] + row * c.d + c0);

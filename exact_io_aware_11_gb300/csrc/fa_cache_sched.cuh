@@ -17,10 +17,12 @@
 
 namespace fa {
 
+struct SharedEntry;
+
 struct AttnGrid {
   int B, HK, N, G;
   int rows;       // query rows of a tile
-  int row_tiles;  // tiles of N * G rows
+  int row_tiles;  // tiles of N * G rows (one sequence's)
   int log2_keys;  // keys of a step
   int cap;        // tokens a page table row has room for
   int causal, split;
@@ -32,6 +34,12 @@ struct AttnGrid {
   float* m_part;  // [2 C][rows]
   float* l_part;
   float* o_part;  // [2 C][rows][D]; tiles: [2 C][rows / 32][D / 4][32 rows][4]
+  // shared prefixes (fa_cache_shared.cu): the entries, made on the device before, the sequences of
+  // the groups, and per unit the CTAs that its parts come from: {-1, 0} where a slot 2 C + unit has it whole
+  const SharedEntry* entry;
+  const int* entries;
+  const int* member;
+  int2* unit_parts;
 };
 
 // One (sequence, row tile).
@@ -40,16 +48,48 @@ struct AttnEntry {
   int seen;             // tokens the tile's last row sees
   int steps;
 };
-__device__ __forceinline__ AttnEntry attn_entry(const AttnGrid& g, int e) {
-  AttnEntry x;
-  x.b = e / g.row_tiles;
-  x.row0 = (e - x.b * g.row_tiles) * g.rows;
-  x.kv = min(g.cap, max(0, g.kv_len[x.b]));
-  x.ql = g.q_len != nullptr ? min(g.N, max(0, g.q_len[x.b])) : g.N;
-  const int rows = min(g.rows, x.ql * g.G - x.row0);
-  x.seen = 0;
-  if (rows > 0) x.seen = g.causal ? max(0, x.kv - x.ql + (x.row0 + rows - 1) / g.G + 1) : x.kv;
-  x.steps = max(1, (x.seen + (1 << g.log2_keys) - 1) >> g.log2_keys);
+// An entry of a list: its keys begin at column `col` of b's row of the page table, and kv and seen
+// count from there. list >= 0: the rows are those of all `count` sequences member[list],
+// member[list + 1], ..., one sequence after another, over the same keys, of which all
+// see every one. list < 0: count 1 where no part of b's rows comes from elsewhere.
+struct __align__(16) SharedEntry : AttnEntry {
+  int list, count, col, pad[3];
+};
+__device__ __forceinline__ int first_column(const AttnEntry&) { return 0; }
+__device__ __forceinline__ int first_column(const SharedEntry& x) { return x.col; }
+template <bool SH>
+struct AttnEntryOf {
+  using type = AttnEntry;
+};
+template <>
+struct AttnEntryOf<true> {
+  using type = SharedEntry;
+};
+template <bool SH>
+__device__ __forceinline__ typename AttnEntryOf<SH>::type attn_entry(const AttnGrid& g, int e) {
+  typename AttnEntryOf<SH>::type x;
+  if constexpr (SH) {
+    const int4* const p = reinterpret_cast<const int4*>(g.entry + e);
+    const int4 u = __ldcg(p), v = __ldcg(p + 1);
+    x.b = u.x;
+    x.row0 = u.y;
+    x.kv = u.z;
+    x.ql = u.w;
+    x.seen = v.x;
+    x.steps = v.y;
+    x.list = v.z;
+    x.count = v.w;
+    x.col = __ldcg(reinterpret_cast<const int*>(p + 2));
+  } else {
+    x.b = e / g.row_tiles;
+    x.row0 = (e - x.b * g.row_tiles) * g.rows;
+    x.kv = min(g.cap, max(0, g.kv_len[x.b]));
+    x.ql = g.q_len != nullptr ? min(g.N, max(0, g.q_len[x.b])) : g.N;
+    const int rows = min(g.rows, x.ql * g.G - x.row0);
+    x.seen = 0;
+    if (rows > 0) x.seen = g.causal ? max(0, x.kv - x.ql + (x.row0 + rows - 1) / g.G + 1) : x.kv;
+    x.steps = max(1, (x.seen + (1 << g.log2_keys) - 1) >> g.log2_keys);
+  }
   return x;
 }
 // Tokens that row r of the tile sees.
@@ -59,10 +99,45 @@ __device__ __forceinline__ int attn_limit(const AttnGrid& g, const AttnEntry& x,
   return g.causal ? max(0, x.kv - x.ql + i + 1) : x.kv;
 }
 
+// Row r of an entry's tile. exists: it has a place in O and LSE; real: it stands for a query;
+// limit: the keys that it sees, from the entry's first on.
+struct AttnRow {
+  int b, i, head, limit;  // sequence, query row, head of the cache head's group
+  bool exists, real;
+};
+template <typename X>
+__device__ __forceinline__ AttnRow shared_row(const AttnGrid& g, const X& x, int r) {
+  AttnRow y;
+  int row = x.row0 + r, ql = x.ql;
+  y.b = x.b;
+  y.exists = true;
+  if (x.list >= 0) {
+    const int rows = g.N * g.G, m = row / rows;
+    y.exists = m < x.count;
+    row -= m * rows;
+    if (y.exists) {
+      y.b = __ldcg(g.member + x.list + m);
+      ql = g.q_len != nullptr ? min(g.N, max(0, g.q_len[y.b])) : g.N;
+    }
+  }
+  y.i = row / g.G;
+  y.head = row - y.i * g.G;
+  y.exists = y.exists && y.i < g.N;
+  y.real = y.exists && y.i < ql;
+  y.limit = !y.real ? 0 : x.list >= 0 || !g.causal ? x.kv : max(0, x.kv - ql + y.i + 1);
+  return y;
+}
+
+template <bool SH>
+__device__ __forceinline__ int attn_entries(const AttnGrid& g) {
+  return SH ? __ldcg(g.entries) : g.B * g.row_tiles;
+}
+
 // A CTA's place in the list: unit (e, h) at `step`, which is `pos` places from the
 // list's start; the CTA's run lasts until `end`.
+template <bool SH>
 struct AttnCursor {
-  AttnEntry x;
+  typename AttnEntryOf<SH>::type x;
   int e, h, step;
   long long pos, end;
   __device__ __forceinline__ bool done(const AttnGrid& g) const {
@@ -88,7 +163,7 @@ struct AttnCursor {
     pos += g.lead;
     if (++h == g.HK) {
       h = 0;
-      if (++e < g.B * g.row_tiles) x = attn_entry(g, e);
+      if (++e < attn_entries<SH>(g)) x = attn_entry<SH>(g, e);
     }
   }
 };
@@ -98,7 +173,10 @@ struct AttnShare {
   long long first;  // the first place of `entry`
   long long each;
   int extra, ctas, entry;
-  AttnEntry x;      // of `entry`
+};
+template <bool SH>
+struct AttnShareOf : AttnShare {
+  typename AttnEntryOf<SH>::type x;  // of `entry`
 };
 
 // n / d for n that mostly fits 32 bits (a 64-bit division takes some 400 cycles).
@@ -112,14 +190,14 @@ __device__ __forceinline__ long long attn_start(const AttnShare& s, int c) {
 
 // This CTA's cursor. Called by the whole CTA of kThreads threads; `sh` and
 // `part` (kThreads / 32 words) are shared memory.
-template <int kThreads>
-__device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* sh, long long* part) {
-  const int E = g.B * g.row_tiles, per = (E + kThreads - 1) / kThreads;
+template <int kThreads, bool SH>
+__device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShareOf<SH>* sh, long long* part) {
+  const int E = attn_entries<SH>(g), per = (E + kThreads - 1) / kThreads;
   const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
-  AttnEntry own{};  // the thread's only entry, where it has just one
+  typename AttnEntryOf<SH>::type own{};  // the thread's only entry, where it has just one
   long long mine = 0;
   for (int e = e0; e < e1; ++e) {
-    own = attn_entry(g, e);
+    own = attn_entry<SH>(g, e);
     mine += own.steps + g.lead;
   }
   long long incl = mine;
@@ -142,14 +220,14 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
   total *= g.HK;
   AttnShare d{};
   d.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  d.each = attn_div(total, d.ctas);
+  d.each = SH && total == 0 ? 0 : attn_div(total, d.ctas);  // (a list may be empty)
   d.extra = static_cast<int>(total - d.each * d.ctas);
   const int c = blockIdx.x;
   const long long s0 = c < d.ctas ? attn_start(d, c) : total;
   long long p = before * g.HK;
   if (s0 >= p && s0 < p + mine * g.HK) {
     for (int e = e0; e < e1; ++e) {
-      const AttnEntry x = per == 1 ? own : attn_entry(g, e);
+      const typename AttnEntryOf<SH>::type x = per == 1 ? own : attn_entry<SH>(g, e);
       const long long n = static_cast<long long>(x.steps + g.lead) * g.HK;
       if (s0 < p + n) {
         sh->entry = e;
@@ -166,7 +244,7 @@ __device__ __forceinline__ AttnCursor attn_share(const AttnGrid& g, AttnShare* s
     sh->ctas = d.ctas;
   }
   __syncthreads();
-  AttnCursor cur;
+  AttnCursor<SH> cur;
   cur.e = sh->entry;
   cur.h = 0;
   cur.step = 0;
@@ -210,5 +288,8 @@ cudaError_t launch_cache_attention_tiles_e4m3(const CacheAttnLaunch& a, const At
                                               cudaStream_t stream);
 cudaError_t launch_cache_attention_tiles_int8(const CacheAttnLaunch& a, const AttnGrid& g, int ctas,
                                               cudaStream_t stream);
+// The same over a list of entries (AttnGrid::entry).
+cudaError_t launch_shared_tiles_e4m3(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream);
+cudaError_t launch_shared_tiles_int8(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream);
 
 }  // namespace fa

@@ -1,0 +1,409 @@
+// Attention over the paged 8-bit cache for a batch whose sequences share prefixes
+// (fa_cache_attention_shared). It is the attention of fa_cache_attention, row by row; only who reads
+// the keys changes.
+//
+// Mathematics: the softmax of a row over [prefix | own tokens] is joined from parts over any runs of its
+// keys: with m_q, l_q, O_q of part q and M = max m_q, O = sum 2^(m_q - M) O_q / sum 2^(m_q - M) l_q.
+// So the rows of all of a group's sequences stand together in tiles over the prefix, whose keys
+// are then read once for all of them, and each sequence's rows go over its own tokens.
+//
+// Four launches: the plan (one CTA: who belongs to which group, the lists of entries), the tile
+// kernel (fa_cache_tile.cuh) over list A, prefixes of groups with more than 16 rows to a cache
+// head; the kernel for the sequences' own tokens over list B, with few rows (fa_cache_rows.cuh) also
+// the prefixes of small groups; and the join. Parts are in 32 bits.
+#include "fa_cache_rows.cuh"
+
+namespace fa {
+namespace {
+
+constexpr int kPlanThreads = 1024, kMaxGroups = kSharedGroups;
+
+struct PlanLaunch {
+  int B, groups, N, G, page, cap, causal;
+  int rows_a, rows_b, tiles_b, few;  // few: list B's kernel takes few rows
+  const int32_t* of;
+  const int32_t* len;
+  const int32_t* kv_len;
+  const int32_t* q_len;
+  // workspace
+  int* entries;      // of A, of B
+  SharedEntry* entry_a;
+  SharedEntry* entry_b;
+  int* member;       // [B]
+  int4* seq;         // [B] where the sequence's part over the prefix is: list (0 none, 1 A, 2 B), its
+                     // first row in the group, the group's first entry
+};
+
+__device__ __forceinline__ SharedEntry make_entry(int b, int row0, int kv, int ql, int seen, int list, int count, int col) {
+  SharedEntry x;
+  x.b = b;
+  x.row0 = row0;
+  x.kv = kv;
+  x.ql = ql;
+  x.seen = seen;
+  x.steps = max(1, (seen + 127) >> 7);
+  x.list = list;
+  x.count = count;
+  x.col = col;
+  x.pad[0] = x.pad[1] = x.pad[2] = 0;
+  return x;
+}
+
+// Tokens of a group's prefix in whole pages.
+__device__ __forceinline__ int prefix_tokens(const PlanLaunch& a, int g) {
+  return min(max(0, a.len[g]), a.cap) / a.page * a.page;
+}
+struct Sequence {
+  int kv, ql, group, prefix;  // group -1: on its own
+};
+// A sequence counts as one of its group where every one of its rows sees the whole prefix.
+__device__ __forceinline__ Sequence sequence(const PlanLaunch& a, int b) {
+  Sequence s;
+  s.kv = min(a.cap, max(0, a.kv_len[b]));
+  s.ql = a.q_len != nullptr ? min(a.N, max(0, a.q_len[b])) : a.N;
+  s.group = a.of[b];
+  s.prefix = 0;
+  if (s.group >= 0 && s.group < a.groups && s.ql > 0) s.prefix = prefix_tokens(a, s.group);
+  if (s.prefix == 0 || (a.causal ? s.kv - s.ql + 1 : s.kv) < s.prefix) {
+    s.group = -1;
+    s.prefix = 0;
+  }
+  return s;
+}
+
+__global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ PlanLaunch a) {
+  __shared__ int count[kMaxGroups], start[kMaxGroups], base[kMaxGroups], first[kMaxGroups];
+  __shared__ int rank[kPlanThreads];
+  __shared__ int sums[3][kPlanThreads / 32];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = a.N * a.G;
+  grid_dep_wait();
+  for (int g = tid; g < a.groups; g += kPlanThreads) count[g] = 0;
+  // ---- each sequence's place in its group, in the order of the batch
+  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    rank[tid] = b < a.B ? sequence(a, b).group : -1;
+    __syncthreads();
+    if (warp == 0)
+      for (int c = 0; c < kPlanThreads && b0 + c < a.B; c += 32) {
+        const int g = rank[c + lane];
+        const unsigned same = __match_any_sync(0xffffffffu, g);
+        const int before = g >= 0 ? count[g] : 0, r = before + __popc(same & ((1u << lane) - 1));
+        __syncwarp();
+        if (g >= 0) {
+          if (lane == __ffs(same) - 1) count[g] = before + __popc(same);
+          if (r == 0) first[g] = b0 + c + lane;
+          rank[c + lane] = r;
+        }
+        __syncwarp();
+      }
+    __syncthreads();
+    if (b < a.B) a.seq[b] = make_int4(0, rank[tid], 0, 0);
+    __syncthreads();
+  }
+  // ---- groups: their sequences' places in the list, their entries
+  int at_member = 0, at_a = 0, at_b = a.B * a.tiles_b;  // list B begins with the sequences' own tokens
+  for (int g0 = 0; g0 < a.groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    int n = g < a.groups ? count[g] : 0;
+    if (n < 2) n = 0;  // alone, it shares nothing
+    const long long rows = static_cast<long long>(n) * NG;
+    const bool small = a.few && rows <= 16;
+    const int per = small ? a.rows_b : a.rows_a, tiles = static_cast<int>((rows + per - 1) / per);
+    int v[3] = {n, small ? 0 : tiles, small ? tiles : 0}, incl[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      incl[k] = v[k];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, incl[k], o);
+        if (lane >= o) incl[k] += u;
+      }
+      if (lane == 31) sums[k][warp] = incl[k];
+    }
+    __syncthreads();
+    int total[3];
+#pragma unroll
+    for (int k = 0; k < 3; ++k) {
+      int before = 0, sum = 0;
+      for (int w = 0; w < kPlanThreads / 32; ++w) {
+        if (w < warp) before += sums[k][w];
+        sum += sums[k][w];
+      }
+      incl[k] += before - v[k];  // exclusive
+      total[k] = sum;
+    }
+    if (g < a.groups) {
+      count[g] = n;
+      start[g] = at_member + incl[0];
+      base[g] = small ? at_b + incl[2] : at_a + incl[1];
+      if (n > 0) {
+        const int tokens = prefix_tokens(a, g);
+        SharedEntry* const to = small ? a.entry_b : a.entry_a;
+        for (int t = 0; t < tiles; ++t) to[base[g] + t] = make_entry(first[g], t * per, tokens, 0, tokens, start[g], n, 0);
+      }
+    }
+    at_member += total[0];
+    at_a += total[1];
+    at_b += total[2];
+    __syncthreads();
+  }
+  if (tid == 0) {
+    a.entries[0] = at_a;
+    a.entries[1] = at_b;
+  }
+  // ---- sequences: their own tokens
+  for (int b = tid; b < a.B; b += kPlanThreads) {
+    const Sequence s = sequence(a, b);
+    int4 to = make_int4(0, 0, 0, 0);
+    int prefix = 0;
+    if (s.group >= 0 && count[s.group] > 0) {
+      const int r = a.seq[b].y;
+      prefix = s.prefix;
+      a.member[start[s.group] + r] = b;
+      to = make_int4(a.few && static_cast<long long>(count[s.group]) * NG <= 16 ? 2 : 1, r * NG, base[s.group], 0);
+    }
+    a.seq[b] = to;
+    const int kv = s.kv - prefix;
+    for (int t = 0; t < a.tiles_b; ++t) {
+      const int row0 = t * a.rows_b, rows = min(a.rows_b, s.ql * a.G - row0);
+      const int seen = rows <= 0 ? 0 : a.causal ? max(0, kv - s.ql + (row0 + rows - 1) / a.G + 1) : kv;
+      a.entry_b[b * a.tiles_b + t] = make_entry(b, row0, kv, s.ql, seen, -1, to.x == 0 ? 1 : 0, prefix / a.page);
+    }
+  }
+  grid_dep_launch();
+}
+
+// One list's parts, as the kernels leave them.
+struct JoinList {
+  const int2* unit_parts;
+  const float* m;
+  const float* l;
+  const float* o;
+  int rows, ctas, tiles;  // tiles: O in the tile kernel's order
+};
+struct JoinLaunch {
+  JoinList list[2];  // A, B
+  const int4* seq;
+  int rows_b, tiles_b, HK;
+};
+
+// The parts of every row of O whose units have not written it: a warp a row, a lane 4 channels. Bound:
+// latency and the L2 cache (a part is 4 D + 8 bytes a row).
+template <int D>
+__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
+  constexpr int kBatch = 4;
+  const int lane = threadIdx.x & 31;
+  grid_dep_wait();
+  grid_dep_launch();
+  const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
+  if (row >= static_cast<long long>(a.B) * a.Hq * a.N) return;
+  const int bh = static_cast<int>(row / a.N), i = static_cast<int>(row - static_cast<long long>(bh) * a.N);
+  const int b = bh / a.Hq, head = bh - b * a.Hq, hk = head / a.G, r = i * a.G + head - hk * a.G;
+  const int4 s = j.seq[b];
+  const int tile = r / j.rows_b, own = (b * j.tiles_b + tile) * j.HK + hk;
+  const int2 parts = j.list[1].unit_parts[own];
+  if (s.x == 0 && parts.x < 0) return;  // straight from its unit
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float sum = 0.f, M = -INFINITY;
+  auto add = [&](const JoinList& x, int unit, int row_in_unit, int2 p) {
+    const int first = p.x < 0 ? 0 : p.x, last = p.x < 0 ? 0 : p.y;
+    for (int q0 = first; q0 <= last; q0 += kBatch) {
+      float mq[kBatch], lq[kBatch];
+      float4 v[kBatch];
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        mq[k] = -INFINITY;
+        lq[k] = 0.f;
+        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int q = q0 + k;
+        if (q <= last) {
+          const int slot = p.x < 0 ? 2 * x.ctas + unit : 2 * q + (q == first ? 1 : 0);
+          const long long pr = static_cast<long long>(slot) * x.rows + row_in_unit;
+          mq[k] = x.m[pr];
+          lq[k] = x.l[pr];
+          if (lane < D / 4)
+            v[k] = x.tiles ? reinterpret_cast<const float4*>(x.o)[((pr >> 5) * (D / 4) + lane) * 32 + (pr & 31)]
+                           : reinterpret_cast<const float4*>(x.o)[pr * (D / 4) + lane];
+        }
+      }
+      float Mn = M;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, mq[k]);
+      const float zero = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - zero);
+      M = Mn;
+      sum *= e;
+      acc.x *= e;
+      acc.y *= e;
+      acc.z *= e;
+      acc.w *= e;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        const float f = ex2(mq[k] - zero);
+        sum = fmaf(lq[k], f, sum);
+        acc.x = fmaf(v[k].x, f, acc.x);
+        acc.y = fmaf(v[k].y, f, acc.y);
+        acc.z = fmaf(v[k].z, f, acc.z);
+        acc.w = fmaf(v[k].w, f, acc.w);
+      }
+    }
+  };
+  if (s.x != 0) {
+    const JoinList& x = j.list[s.x - 1];
+    const int at = s.y + r, t = at / x.rows, unit = (s.z + t) * j.HK + hk;
+    add(x, unit, at - t * x.rows, x.unit_parts[unit]);
+  }
+  add(j.list[1], own, r - tile * j.rows_b, parts);
+  const bool none = sum == 0.f;  // a row that sees no key; NaN stays NaN
+  const float inv = none ? 0.f : 1.f / sum;
+  if (lane < D / 4) {
+    uint2 w = make_uint2(0u, 0u);
+    if (!none) w = make_uint2(pack16(acc.x * inv, acc.y * inv, a.fp16), pack16(acc.z * inv, acc.w * inv, a.fp16));
+    *reinterpret_cast<uint2*>(a.o + b * a.so.b + head * a.so.h + i * a.so.n + lane * 4) = w;
+  }
+  if (lane == 0) a.lse[row] = none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
+}
+
+// Rows of a unit and CTAs of both lists, and the workspace.
+struct SharedPlan {
+  bool plain;  // as fa_cache_attention
+  int rows_a, rows_b, tiles_b, ctas_a, ctas_b, lead_b;
+  long long max_a, max_b;  // entries
+  size_t entry_a, entry_b, member, seq, unit_a, unit_b, m_a, l_a, o_a, m_b, l_b, o_b, total;
+};
+SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_width, int groups) {
+  SharedPlan p{};
+  const long long NG = static_cast<long long>(N) * G, cap = static_cast<long long>(table_width) * page;
+  p.plain = NG > 128 || B < 2;
+  if (p.plain) {
+    p.total = cache_attention_workspace(B, HK, G, N, d, page, table_width);
+    return p;
+  }
+  const AttnPlan own = attn_plan(B, HK, NG, cap, d);
+  const AttnPlan pre = attn_plan(groups < B ? groups : B, HK, (B + groups - 1) / groups * NG, cap, d);
+  const bool few = own.rows <= 16;
+  p.rows_b = own.rows;
+  p.lead_b = own.lead;
+  p.tiles_b = static_cast<int>((NG + p.rows_b - 1) / p.rows_b);
+  p.rows_a = pre.rows <= 16 ? 64 : pre.rows;
+  const long long pairs = groups < B / 2 ? groups : B / 2;  // groups of two and more
+  p.max_a = B * NG / p.rows_a + pairs;
+  p.max_b = static_cast<long long>(B) * p.tiles_b + (few ? B * NG / p.rows_b + pairs : 0);
+  const long long sms = sm_count(), most_b = few ? static_cast<long long>(few_row_ctas(d, p.rows_b)) * sms : sms;
+  const long long steps = (cap + 127) / 128;
+  p.ctas_a = static_cast<int>(p.max_a * HK >= sms || p.max_a * HK * steps >= sms ? sms : p.max_a * HK * steps);
+  p.ctas_b = static_cast<int>(p.max_b * HK >= most_b || p.max_b * HK * steps >= most_b ? most_b : p.max_b * HK * steps);
+  size_t at = 256;
+  auto take = [&](size_t bytes) {
+    const size_t here = at;
+    at += align256(bytes);
+    return here;
+  };
+  p.entry_a = take(p.max_a * sizeof(SharedEntry));
+  p.entry_b = take(p.max_b * sizeof(SharedEntry));
+  p.member = take(static_cast<size_t>(B) * 4);
+  p.seq = take(static_cast<size_t>(B) * 16);
+  p.unit_a = take(p.max_a * HK * 8);
+  p.unit_b = take(p.max_b * HK * 8);
+  const size_t parts_a = (2LL * p.ctas_a + p.max_a * HK) * p.rows_a, parts_b = (2LL * p.ctas_b + p.max_b * HK) * p.rows_b;
+  p.m_a = take(parts_a * 4);
+  p.l_a = take(parts_a * 4);
+  p.o_a = take(parts_a * d * 4);
+  p.m_b = take(parts_b * 4);
+  p.l_b = take(parts_b * 4);
+  p.o_b = take(parts_b * d * 4);
+  p.total = at;
+  return p;
+}
+
+template <int D, bool INT8>
+cudaError_t launch_shared(const CacheAttnLaunch& a, const AttnGrid& ga, const AttnGrid& gb, const SharedPlan& p, const JoinLaunch& j,
+                          cudaStream_t stream) {
+  auto tiles = [&](const AttnGrid& g, int ctas) {
+    return INT8 ? launch_shared_tiles_int8(a, g, ctas, stream) : launch_shared_tiles_e4m3(a, g, ctas, stream);
+  };
+  cudaError_t e = tiles(ga, p.ctas_a);
+  if (e != cudaSuccess) return e;
+  e = p.rows_b > 16  ? tiles(gb, p.ctas_b)
+      : p.rows_b > 8 ? launch_rows<D, 2, INT8, true>(a, gb, p.ctas_b, stream)
+                     : launch_rows<D, 1, INT8, true>(a, gb, p.ctas_b, stream);
+  if (e != cudaSuccess) return e;
+  const long long rows = static_cast<long long>(a.B) * a.Hq * a.N;
+  return launch_pdl(shared_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, a, j);
+}
+
+}  // namespace
+
+size_t shared_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width, int groups) {
+  return shared_plan(B, HK, G, N, d, page, table_width, groups).total;
+}
+
+cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* prefix_of, const int32_t* prefix_len, int groups,
+                                    cudaStream_t stream) {
+  const SharedPlan p = shared_plan(a.B, a.c.H, a.G, a.N, a.c.d, a.c.page, a.c.table_width, groups);
+  if (p.plain) return launch_cache_attention(a, stream);
+  const int cap = a.c.table_width * a.c.page;
+  PlanLaunch pl{};
+  pl.B = a.B;
+  pl.groups = groups;
+  pl.N = a.N;
+  pl.G = a.G;
+  pl.page = a.c.page;
+  pl.cap = cap;
+  pl.causal = a.causal;
+  pl.rows_a = p.rows_a;
+  pl.rows_b = p.rows_b;
+  pl.tiles_b = p.tiles_b;
+  pl.few = p.rows_b <= 16;
+  pl.of = prefix_of;
+  pl.len = prefix_len;
+  pl.kv_len = a.kv_len;
+  pl.q_len = a.q_len;
+  pl.entries = reinterpret_cast<int*>(a.ws);
+  pl.entry_a = reinterpret_cast<SharedEntry*>(a.ws + p.entry_a);
+  pl.entry_b = reinterpret_cast<SharedEntry*>(a.ws + p.entry_b);
+  pl.member = reinterpret_cast<int*>(a.ws + p.member);
+  pl.seq = reinterpret_cast<int4*>(a.ws + p.seq);
+  cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pl);
+  if (e != cudaSuccess) return e;
+  AttnGrid g{};
+  g.B = a.B;
+  g.HK = a.c.H;
+  g.N = a.N;
+  g.G = a.G;
+  g.log2_keys = 7;
+  g.cap = cap;
+  g.causal = a.causal;
+  g.split = 1;
+  g.kv_len = a.kv_len;
+  g.q_len = a.q_len;
+  g.member = pl.member;
+  AttnGrid ga = g, gb = g;
+  ga.rows = p.rows_a;
+  ga.lead = 4;
+  ga.entry = pl.entry_a;
+  ga.entries = pl.entries;
+  ga.unit_parts = reinterpret_cast<int2*>(a.ws + p.unit_a);
+  ga.m_part = reinterpret_cast<float*>(a.ws + p.m_a);
+  ga.l_part = reinterpret_cast<float*>(a.ws + p.l_a);
+  ga.o_part = reinterpret_cast<float*>(a.ws + p.o_a);
+  gb.rows = p.rows_b;
+  gb.lead = p.lead_b;
+  gb.entry = pl.entry_b;
+  gb.entries = pl.entries + 1;
+  gb.unit_parts = reinterpret_cast<int2*>(a.ws + p.unit_b);
+  gb.m_part = reinterpret_cast<float*>(a.ws + p.m_b);
+  gb.l_part = reinterpret_cast<float*>(a.ws + p.l_b);
+  gb.o_part = reinterpret_cast<float*>(a.ws + p.o_b);
+  JoinLaunch j{};
+  j.list[0] = JoinList{ga.unit_parts, ga.m_part, ga.l_part, ga.o_part, p.rows_a, p.ctas_a, 1};
+  j.list[1] = JoinList{gb.unit_parts, gb.m_part, gb.l_part, gb.o_part, p.rows_b, p.ctas_b, p.rows_b > 16};
+  j.seq = pl.seq;
+  j.rows_b = p.rows_b;
+  j.tiles_b = p.tiles_b;
+  j.HK = a.c.H;
+  if (a.c.d == 128)
+    return a.c.int8 ? launch_shared<128, true>(a, ga, gb, p, j, stream) : launch_shared<128, false>(a, ga, gb, p, j, stream);
+  return a.c.int8 ? launch_shared<64, true>(a, ga, gb, p, j, stream) : launch_shared<64, false>(a, ga, gb, p, j, stream);
+}
+
+}  // namespace fa

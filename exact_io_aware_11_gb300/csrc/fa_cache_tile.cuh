@@ -2,7 +2,7 @@
 // tokens of large groups, chunks of a prompt): tiles of 128 query rows on
 // tcgen05. Which calls come here: attn_plan.
 //
-// Mathematics, units, shares and parts: as in fa_cache_attn.cu. A unit has NQ tiles of
+// Mathematics, units, shares and parts: as in fa_cache_rows.cuh. A unit has NQ tiles of
 // 128 query rows, whose S = Q K^T and O += P V run as 128 x
 // 128 x d products with fp16 operands and fp32 accumulators in TMEM. A task is one
 // tile's step; task k uses S buffer k mod 2, and the issue order
@@ -41,7 +41,7 @@ constexpr int kKeys = 128;
 constexpr int kChunkBytes = 128 * 128;  // 128 rows x 64 fp16 columns, 128-byte swizzle
 constexpr int kScaleSlots = 8;          // steps whose scales are kept
 
-template <int D, int NQ>
+template <int D, int NQ, bool SH = false>
 struct TileLayout {
   // NQ = 2: 12 warps, so that a softmax thread can hold a step's 128 scores (168 registers)
   static constexpr int kConvWarps = NQ == 2 ? 2 : 4;
@@ -58,13 +58,14 @@ struct TileLayout {
   // describes a unit three steps before it issues K(n), for which K(n - kStg / 2) is
   // converted, so the scores of the step two before that are formed, so the weights of
   // the step NQ = 1: two, NQ = 2: one before that are done; that step's unit may still be read.
-  static constexpr int kUnits = kStg <= 2 ? 8 : 16;
+  static constexpr int kUnits = kStg <= 2 ? 8 : SH && kStg <= 4 ? 10 : 16;
   static_assert(3 + kStg / 2 + 2 + (NQ == 1 ? 2 : 1) < kUnits, "a unit's description outlives its use");
   static constexpr int oUnits = oNan + 32;
-  static constexpr int oBars = oUnits + kUnits * 32;
+  static constexpr int kUnitBytes = SH ? 48 : 32;
+  static constexpr int oBars = oUnits + kUnits * kUnitBytes;
   static constexpr int kBars = 2 * kStg + 17 + kUnits + 7;
   static constexpr int kSmem = oBars + kBars * 8 + 16 + 1024;
-  static_assert(kSmem + sizeof(AttnShare) + 16 <= 227 * 1024, "shared memory of one CTA");
+  static_assert(kSmem + sizeof(AttnShareOf<SH>) + 16 <= 227 * 1024, "shared memory of one CTA");
   static constexpr uint32_t cO = 256;                   // TMEM column of O
 };
 
@@ -74,6 +75,19 @@ struct __align__(16) TileUnit {
   int b, row0, h, first;  // sequence, first row, cache head, first step
   int steps, kv, ql, seen_last;  // seen: tokens the last row sees; top bit: the unit ends here
 };
+// A list's (AttnGrid::entry): rows, first column and number as AttnEntry has them.
+struct __align__(16) TileUnitShared : TileUnit {
+  int list, count, col, unit;
+};
+template <bool SH>
+struct TileUnitOf {
+  using type = TileUnit;
+};
+template <>
+struct TileUnitOf<true> {
+  using type = TileUnitShared;
+};
+static_assert(sizeof(TileUnit) == 32 && sizeof(TileUnitShared) == 48, "TileLayout::kUnitBytes");
 __device__ __forceinline__ int unit_limit(const AttnGrid& g, const TileUnit& x, int r) {
   const int i = (x.row0 + r) / g.G;
   if (i >= x.ql) return 0;
@@ -95,11 +109,12 @@ struct TileBars {
 // With NQ = 1 K and V have a warp each: a step of 16-token pages is 16 copies, which take one
 // warp some 75 cycles each to issue. K's also describes the units to the other warps (TileLayout::kUnits), and
 // writes the record of a cut unit that the CTA ends, well before that end.
-template <int D, int NQ>
-__device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor ld,
+template <int D, int NQ, bool SH>
+__device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor<SH> ld,
                                              const AttnShare& share, uint8_t* smem, const TileBars& b,
                                              const Watchdog& wd, int loader, int lane) {
-  using L = TileLayout<D, NQ>;
+  using L = TileLayout<D, NQ, SH>;
+  using Unit = typename TileUnitOf<SH>::type;
   const CacheView& c = a.c;
   const int rows = min(c.page, kKeys), per_page = rows >> 4;
   const bool group = lane < kKeys / 16, leader = group && lane % per_page == 0;
@@ -110,9 +125,9 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
   };
   int units = 0;
   bool first = true;
-  auto describe = [&](const TileUnit& u) {
+  auto describe = [&](const Unit& u) {
     if (lane == 0) {
-      *reinterpret_cast<TileUnit*>(smem + L::oUnits + units % L::kUnits * 32) = u;
+      *reinterpret_cast<Unit*>(smem + L::oUnits + units % L::kUnits * L::kUnitBytes) = u;
       mbar_arrive(b.ufull + units % L::kUnits);
     }
     ++units;
@@ -123,9 +138,25 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       if (loader == 0 && (first || ld.step == 0)) {
         const int steps = ld.run(g);
         const bool ends = ld.step + steps == ld.x.steps;
-        describe(TileUnit{ld.x.b, ld.x.row0, ld.h, ld.step, steps, ld.x.kv, ld.x.ql,
-                          static_cast<int>(static_cast<unsigned>(ld.x.seen) | (ends ? 0x80000000u : 0u))});
-        if (ld.step > 0 && ends && g.split && lane == 0)
+        Unit u;
+        u.b = ld.x.b;
+        u.row0 = ld.x.row0;
+        u.h = ld.h;
+        u.first = ld.step;
+        u.steps = steps;
+        u.kv = ld.x.kv;
+        u.ql = ld.x.ql;
+        u.seen_last = static_cast<int>(static_cast<unsigned>(ld.x.seen) | (ends ? 0x80000000u : 0u));
+        if constexpr (SH) {
+          u.list = ld.x.list;
+          u.count = ld.x.count;
+          u.col = ld.x.col;
+          u.unit = ld.e * g.HK + ld.h;
+          if (ends && lane == 0)
+            g.unit_parts[u.unit] = ld.step > 0 ? make_int2(attn_cta_of(ld.pos - ld.step, share), blockIdx.x) : make_int2(-1, 0);
+        }
+        describe(u);
+        if (!SH && ld.step > 0 && ends && g.split && lane == 0)
           g.record[blockIdx.x] = make_int4(ld.e, ld.h, attn_cta_of(ld.pos - ld.step, share), 0);
         first = false;
       }
@@ -133,7 +164,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       s.want = group && key < ld.x.seen;
       s.h = ld.h;
       s.row = key & (c.page - 1);
-      if (s.want) s.pid = c.table[ld.x.b * c.table_stride + (key >> c.log2_page)];
+      if (s.want) s.pid = c.table[ld.x.b * c.table_stride + first_column(ld.x) + (key >> c.log2_page)];
       ld.next(g);
     }
     return s;
@@ -188,7 +219,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     scales(next);  // before the next load of a page id: waiting for one waits for all of its kind
     third = look();
   }
-  if (loader == 0) describe(TileUnit{0, 0, 0, 0, 0, 0, 0, 0});
+  if (loader == 0) describe(Unit{});
   for (int i = max(0, issued - L::kStg); i < issued; ++i)  // copies in flight land before the CTA exits
     if (L::kLoaders == 1 || (i & 1) == loader) mbar_wait_drain(b.raw_full + i % L::kStg, (i / L::kStg) & 1, a.wait_limit);
 }
@@ -236,10 +267,11 @@ __device__ __noinline__ void convert_checked(uint32_t src, uint32_t dst, const f
 // and r ^ 5: the rows differ in bit 2 (so their raw chunks, at c ^ (r & 7), fall
 // apart) and in bit 0 (so do the results, at 2 c ^ (r & 7)), and every bank is met
 // once in both directions.
-template <int D, int NQ, bool INT8>
+template <int D, int NQ, bool INT8, bool SH>
 __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, uint8_t* smem,
                                              const TileBars& b, const Watchdog& wd, int cw, int lane) {
-  using L = TileLayout<D, NQ>;
+  using L = TileLayout<D, NQ, SH>;
+  using Unit = typename TileUnitOf<SH>::type;
   // The lane's pieces: chunk ch of its row of 8 + 8 g, e < kPer, g < kGroups, at constant
   // distances of a piece with g = 0 (both swizzles repeat every 8 rows).
   constexpr int kRows = kKeys / L::kConvWarps, kPer = D / 64, kGroups = kRows / 8;
@@ -255,12 +287,17 @@ __device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const Att
   int n = 0;  // steps converted
   for (int unit = 0;; ++unit) {
     if (!mbar_wait_warp(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) return;
-    const TileUnit x = *reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32);
+    const Unit x = *reinterpret_cast<const Unit*>(smem + L::oUnits + unit % L::kUnits * L::kUnitBytes);
     if (x.steps == 0) return;
     // slot of the unit three on; the one five back, which used it, has ended (a unit
     // has a step at least, and K(n) waits for the scores of step n - 2)
     if (cw == 0 && lane == 0) nan_key[(unit + 3) & 7] = 0x7fffffff;
-    const int seen = x.seen_last & 0x7fffffff, low = unit_limit(g, x, 0);
+    const int seen = x.seen_last & 0x7fffffff;
+    int low;
+    if constexpr (SH)
+      low = x.list >= 0 ? x.kv : unit_limit(g, x, 0);
+    else
+      low = unit_limit(g, x, 0);
     int key0 = x.first << g.log2_keys;
     for (const int end = n + x.steps; n < end; ++n, key0 += kKeys) {
 #pragma unroll
@@ -345,8 +382,8 @@ __device__ __forceinline__ float tile_queries(const uint16_t* q, long long q_at,
   return __uint_as_float(static_cast<uint32_t>(e - 14) << 23);
 }
 
-static __device__ __noinline__ unsigned long long seen_nan64(const CacheView& c, int b, int h, int first, int end, int c0) {
-  return seen_nan<16>(c, b, h, first, end, c0);
+static __device__ __noinline__ unsigned long long seen_nan64(const CacheView& c, long long tab, int h, int first, int end, int c0) {
+  return seen_nan<16>(c, tab, h, first, end, c0);
 }
 
 // Writes 32 rows x 128 bytes, a lane's row as 8 pieces, to the rows' own places: through `box`
@@ -404,16 +441,19 @@ __device__ __forceinline__ float weigh16(const uint32_t (&v)[32], int c0, float 
 // otherwise). REP = 2 (units of up to 64 rows): the rows stand in the tile twice, and each
 // copy's warps take half of a step's keys, with weights of zero for the others; a unit ends
 // with the copies joined. All four softmax warps then work, each on half the columns.
-template <int D, int NQ, int REP, bool INT8, bool P16>
-__global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
+// SH: the units are a list's, and their rows' parts are joined afterwards, but where a sequence
+// shares nothing (AttnGrid::entry).
+template <int D, int NQ, int REP, bool INT8, bool P16, bool SH>
+__global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
     cache_attn_tile_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
-  using L = TileLayout<D, NQ>;
+  using L = TileLayout<D, NQ, SH>;
+  using Unit = typename TileUnitOf<SH>::type;
   // The weights are handed over in halves of 64 keys, so that P V begins under the second
   // half's exponentials: a chunk in e4m3 207.0 us as a whole, 197.3 in halves; in int8, where
   // the converters are behind, 219.4 and 221.3; in units of one tile (384 rows, e4m3) 118.7 and 130.2.
   constexpr bool kHalves = NQ == 2 && !INT8;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ AttnShare share;
+  __shared__ AttnShareOf<SH> share;
   uint8_t* const smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   TileBars b;
@@ -477,13 +517,13 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   grid_dep_wait();
   grid_dep_launch();
   // its barriers publish the above; the slots of the scales are not in use yet
-  AttnCursor cur = attn_share<L::kThreads>(g, &share, reinterpret_cast<long long*>(smem + L::oScales));
+  AttnCursor<SH> cur = attn_share<L::kThreads, SH>(g, &share, reinterpret_cast<long long*>(smem + L::oScales));
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const Watchdog wd{a.wait_limit, a.status, abort_flag};
   if (warp >= L::kLoad) {
-    if (g.split && warp == L::kLoad && lane == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
-    tile_produce<D, NQ>(a, g, cur, share, smem, b, wd, warp - L::kLoad, lane);
+    if (!SH && g.split && warp == L::kLoad && lane == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
+    tile_produce<D, NQ, SH>(a, g, cur, share, smem, b, wd, warp - L::kLoad, lane);
   } else if (warp == L::kMma) {
     // ------------------------------------------------------------ MMA issuer (whole warp)
     constexpr uint32_t kIdS = idesc_f16(128, 128, false), kIdO = idesc_f16(128, D, true);
@@ -494,7 +534,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     bool ok = true;
     for (int unit = 0; ok; ++unit) {
       if (!mbar_wait_spin_w(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) break;
-      const int steps = reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32)->steps, tasks = steps * NQ;
+      const int steps = reinterpret_cast<const Unit*>(smem + L::oUnits + unit % L::kUnits * L::kUnitBytes)->steps, tasks = steps * NQ;
       if (steps == 0) break;
       for (int t = 0; ok && t < NQ; ++t) ok = mbar_wait_spin_w(b.qfull + t, unit & 1, wd);
       if (!ok) break;
@@ -545,7 +585,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     mbar_wait_drain(b.fin, 0, a.wait_limit);
     __syncwarp();
   } else if (warp >= L::kConv && warp < L::kMma) {
-    tile_convert<D, NQ, INT8>(a, g, smem, b, wd, warp - L::kConv, lane);
+    tile_convert<D, NQ, INT8, SH>(a, g, smem, b, wd, warp - L::kConv, lane);
   } else if (warp < L::kConv) {
     // ------------------------------------------------------------ softmax
     static_assert(REP == 1 || NQ == 1, "copies of rows stand in one tile");
@@ -560,27 +600,37 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
     int task = t, step_n = 0;  // of this tile; steps so far (for the slots of the scales)
     for (int unit = 0;; ++unit) {
       if (!mbar_wait_warp<true>(b.ufull + unit % L::kUnits, (unit / L::kUnits) & 1, wd)) break;
-      const TileUnit* const ux = reinterpret_cast<const TileUnit*>(smem + L::oUnits + unit % L::kUnits * 32);
+      const Unit* const ux = reinterpret_cast<const Unit*>(smem + L::oUnits + unit % L::kUnits * L::kUnitBytes);
       const int steps = ux->steps;
       if (steps == 0) break;
       int lim, low;
       float rf;
       bool live;
       {
-        const TileUnit x = *ux;
+        const Unit x = *ux;
         if (REP == 2 && unit > 0 && !mbar_wait_warp<true>(b.rep_done, (unit - 1) & 1, wd)) break;
-        const int row = x.row0 + t * 128 + rl, qi = row / g.G;
-        lim = unit_limit(g, x, t * 128 + rl);
+        bool real;
+        long long at;
+        if constexpr (SH) {
+          const AttnRow y = shared_row(g, x, t * 128 + rl);
+          lim = y.limit;
+          real = y.real;
+          at = real ? y.b * a.sq.b + static_cast<long long>(x.h * g.G + y.head) * a.sq.h + y.i * a.sq.n : -1;
+        } else {
+          const int row = x.row0 + t * 128 + rl, qi = row / g.G;
+          lim = unit_limit(g, x, t * 128 + rl);
+          real = qi < x.ql;
+          at = real ? x.b * a.sq.b + static_cast<long long>(x.h * g.G + (row - qi * g.G)) * a.sq.h + qi * a.sq.n : -1;
+        }
         // The warp's 32 rows of queries to fp16, scaled by a power of two each, into the
         // swizzled tile (the last unit's scores are done: its last P V was awaited).
-        const long long at = qi < x.ql ? x.b * a.sq.b + static_cast<long long>(x.h * g.G + (row - qi * g.G)) * a.sq.h + qi * a.sq.n : -1;
         rf = a.scale_log2 * tile_queries<D>(a.q, at, a.fp16, q_at, lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(b.qfull + t);
         live = __any_sync(0xffffffffu, lim > 0);  // rows of this warp see keys
         // rows that stand for no query (their q is zero) do not make a step an edge
-        low = __reduce_min_sync(0xffffffffu, qi < x.ql ? lim : 0x7fffffff) - (x.first << g.log2_keys) - col0;
+        low = __reduce_min_sync(0xffffffffu, real ? lim : 0x7fffffff) - (x.first << g.log2_keys) - col0;
         lim -= (x.first << g.log2_keys) + col0;  // both from here on relative to the step's first key of these columns
       }
       float m = -INFINITY, l = 0.f;
@@ -734,12 +784,33 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
         m = M;
         if (!mbar_wait_warp<true>(b.rep_out + pair, 1, wd)) break;
       }
-      const TileUnit x = *ux;
-      const int r = t * 128 + rl, row = x.row0 + r, qi = row / g.G, head = x.h * g.G + (row - qi * g.G);
+      const Unit x = *ux;
+      const int r = t * 128 + rl;
+      int ob, qi, head, limit = 0;  // the row's place in O, and (SH) the keys it sees
+      bool real, row_ok;
+      if constexpr (SH) {
+        const AttnRow y = shared_row(g, x, r);
+        ob = y.b;
+        qi = y.i;
+        head = x.h * g.G + y.head;
+        real = y.real;
+        row_ok = y.exists;
+        limit = y.limit;
+      } else {
+        const int row = x.row0 + r;
+        ob = x.b;
+        qi = row / g.G;
+        head = x.h * g.G + (row - qi * g.G);
+        real = qi < x.ql;
+        row_ok = qi < g.N;
+      }
       int nan_key = 0x7fffffff, end = 0;  // keys of V with a NaN that was taken out, and seen by this row
       if (!INT8) {
         nan_key = *reinterpret_cast<volatile int*>(smem + L::oNan + (unit & 7) * 4);
-        end = unit_limit(g, x, r);
+        if constexpr (SH)
+          end = limit;
+        else
+          end = unit_limit(g, x, r);
       }
       // 64 channels of the row's O, from column 64 c
       auto read_o = [&](int c, uint32_t (&o)[2][32]) {
@@ -761,7 +832,9 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
           }
         }
         if (!INT8 && nan_key < end) {
-          const unsigned long long nan = seen_nan64(a.c, x.b, x.h, nan_key, end, c * 64);
+          long long tab = x.b * a.c.table_stride;
+          if constexpr (SH) tab += x.col;
+          const unsigned long long nan = seen_nan64(a.c, tab, x.h, nan_key, end, c * 64);
 #pragma unroll
           for (int e = 0; e < 2; ++e)
 #pragma unroll
@@ -769,14 +842,16 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
               if (nan >> (e * 32 + q) & 1ull) o[e][q] = 0x7fffffffu;
         }
       };
-      if (qi >= x.ql) {
+      if (!real) {
         l = 0.f;
         m = -INFINITY;
       }
-      const bool none = l == 0.f, row_ok = qi < g.N;
-      if (x.first == 0 && x.seen_last < 0) {  // the whole unit
+      const bool none = l == 0.f, whole = x.first == 0 && x.seen_last < 0;
+      bool direct = whole;  // straight to O and LSE
+      if constexpr (SH) direct = whole && x.list < 0 && x.count == 1;
+      if (direct) {
         const float inv = none ? 0.f : 1.f / l;
-        uint16_t* const dst = a.o + x.b * a.so.b + static_cast<long long>(head) * a.so.h + qi * a.so.n;
+        uint16_t* const dst = a.o + ob * a.so.b + static_cast<long long>(head) * a.so.h + qi * a.so.n;
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t o[2][32];
@@ -795,10 +870,14 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
           store_rows(box + (REP == 2 ? c * 8192 : 0), w, row_ok ? reinterpret_cast<uint8_t*>(dst + c * 64) : nullptr, lane);
         }
         if (row_ok)
-          a.lse[(static_cast<long long>(x.b) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
+          a.lse[(static_cast<long long>(ob) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
       } else {
         // a part, in the order of the registers: 512 bytes a warp and store
-        const long long pr = static_cast<long long>(2 * blockIdx.x + (x.first == 0 ? 1 : 0)) * g.rows + r;
+        int slot = 2 * blockIdx.x + (x.first == 0 ? 1 : 0);
+        if constexpr (SH) {
+          if (whole) slot = 2 * gridDim.x + x.unit;
+        }
+        const long long pr = static_cast<long long>(slot) * g.rows + r;
         if (row_ok) {
           g.m_part[pr] = m;
           g.l_part[pr] = l;
@@ -831,27 +910,27 @@ __global__ void __launch_bounds__(TileLayout<D, NQ>::kThreads, 1)
   }
 }
 
-template <int D, int NQ, int REP, bool INT8, bool P16>
+template <int D, int NQ, int REP, bool INT8, bool P16, bool SH>
 cudaError_t launch_tile_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  using L = TileLayout<D, NQ>;
-  auto kern = cache_attn_tile_kernel<D, NQ, REP, INT8, P16>;
+  using L = TileLayout<D, NQ, SH>;
+  auto kern = cache_attn_tile_kernel<D, NQ, REP, INT8, P16, SH>;
   static std::atomic<unsigned long long> smem_set{0};
   const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(kern), L::kSmem);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(ctas), dim3(L::kThreads), L::kSmem, stream, a, g);
 }
 
-template <int D, bool INT8, bool P16>
+template <int D, bool INT8, bool P16, bool SH>
 cudaError_t launch_tile_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  if (g.rows == 64) return launch_tile_variant<D, 1, 2, INT8, P16>(a, g, ctas, stream);
-  return g.rows == 128 ? launch_tile_variant<D, 1, 1, INT8, P16>(a, g, ctas, stream)
-                       : launch_tile_variant<D, 2, 1, INT8, P16>(a, g, ctas, stream);
+  if (g.rows == 64) return launch_tile_variant<D, 1, 2, INT8, P16, SH>(a, g, ctas, stream);
+  return g.rows == 128 ? launch_tile_variant<D, 1, 1, INT8, P16, SH>(a, g, ctas, stream)
+                       : launch_tile_variant<D, 2, 1, INT8, P16, SH>(a, g, ctas, stream);
 }
 
-template <int D, bool INT8>
+template <int D, bool INT8, bool SH = false>
 cudaError_t launch_tiles(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
-  return a.c.page == 16 ? launch_tile_rows<D, INT8, true>(a, g, ctas, stream)
-                        : launch_tile_rows<D, INT8, false>(a, g, ctas, stream);
+  return a.c.page == 16 ? launch_tile_rows<D, INT8, true, SH>(a, g, ctas, stream)
+                        : launch_tile_rows<D, INT8, false, SH>(a, g, ctas, stream);
 }
 
 }  // namespace

@@ -475,6 +475,26 @@ int fa_cache_attention(const void* q, void* o, float* lse, const fa_cache* cache
                        int N, const fa_cache_attention_options* opt, void* workspace,
                        size_t workspace_bytes, struct CUstream_st* stream);
 
+size_t fa_cache_attention_shared_workspace_bytes(const fa_cache* cache, int B, int Hq, int N, int table_width, int groups);
+
+/* fa_cache_attention where sequences of the batch begin with the same tokens, in the same pages: their keys
+ * are read once for all of them. O and LSE are those of fa_cache_attention with the same arguments (up to
+ * the order of sums).
+ *   prefix_of  : DEVICE int32 [B]: the group (0 .. groups - 1) of sequence b, any other number: none;
+ *                the sequences of a group may stand anywhere in the batch;
+ *   prefix_len : DEVICE int32 [groups]: tokens that the group shares. The whole pages of them count:
+ *                the first prefix_len / page_size entries of the page table's row must be the same
+ *                in all of the group's sequences (as fa_cache_fork leaves them; read from one of them);
+ *   groups     : 1 .. 2048. With about B / groups sequences to a group the work is divided best.
+ * The lengths of prefixes and sequences may be any: a sequence whose rows do not all see the whole
+ * prefix, and one that is alone in its group, goes by itself. Calls of more than 128 query rows to a cache
+ * head and sequence (N * Hq / H) share nothing, because their products bound them.
+ *   workspace : DEVICE, 16-byte aligned, fa_cache_attention_shared_workspace_bytes at least, contents
+ *               ignored. Calls that share it must be ordered on the GPU. */
+int fa_cache_attention_shared(const void* q, void* o, float* lse, const fa_cache* cache, int B, int Hq, int N,
+                              const fa_cache_attention_options* opt, const int32_t* prefix_of, const int32_t* prefix_len, int groups,
+                              void* workspace, size_t workspace_bytes, struct CUstream_st* stream);
+
 /* ------------------------------------------------------------------------
  * The pages of a cache, dealt out on the device: sequences that share pages,
  * pages for tokens to come, copies. One page table serves every layer of a
