@@ -282,6 +282,7 @@ class KVCache:
         self.device, self.heads, self.page_size, self.head_dim = k.device, H, page, d
         self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, H, page, d,
                                    _FORMATS[k.dtype])
+        self._bytes = bytes(self._struct)  # several layers' structs are put together from these
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, head_dim: int, page_size: int = 64, dtype=torch.float8_e4m3fn, device="cuda"):

@@ -11,7 +11,7 @@ import ctypes
 
 import torch
 
-from ._cache import _I32, _I64, _SZ, CacheStruct, KVCache, _check_int, _check_lengths, _done, _on, _raw_stream
+from ._cache import _I32, _I64, _SZ, KVCache, _check_int, _check_lengths, _done, _on, _raw_stream
 from ._lib import _I, _P, SIGNATURES, lib
 
 
@@ -20,7 +20,7 @@ class PageTableStruct(ctypes.Structure):
     _fields_ = [("entries", _P), ("stride", _I64), ("rows", _I), ("width", _I), ("refs", _P), ("num_pages", _I), ("page_size", _I)]
 
 
-_CACHES, _TABLE = ctypes.POINTER(CacheStruct), ctypes.POINTER(PageTableStruct)
+_CACHES, _TABLE = ctypes.c_char_p, ctypes.POINTER(PageTableStruct)  # a host array of fa_cache, as bytes
 SIGNATURES["fa_cache_copy"] = (_I, [_CACHES, _I, _P, _P, _I, _P])
 SIGNATURES["fa_cache_fork"] = (_I, [_TABLE, _P, _P, _P])
 SIGNATURES["fa_cache_reserve_workspace_bytes"] = (_SZ, [_I, _I, _I])
@@ -30,30 +30,34 @@ SIGNATURES["fa_cache_compact"] = (_I, [_CACHES, _I, _TABLE, _P, _P, _P, _SZ, _P]
 
 
 def _layers(caches):
-    """The structs of one KVCache or a sequence of them, and the device they share."""
+    """One KVCache or a sequence of them as the C calls take them: structs, their number, the
+    first one."""
     if isinstance(caches, KVCache):
-        return caches._struct, 1, caches.device
+        return caches._bytes, 1, caches
     try:
         caches = list(caches)
-    except TypeError:
+        structs = b"".join([c._bytes for c in caches])
+    except (TypeError, AttributeError):
         caches = []
-    if not caches or not all(isinstance(c, KVCache) for c in caches):
+    if not caches:
         raise ValueError("caches must be a KVCache or a sequence of them, one for each layer")
-    dev = caches[0].device
-    if any(c.device != dev for c in caches):
-        raise ValueError("the layers' caches are on different devices")
-    return (CacheStruct * len(caches))(*[c._struct for c in caches]), len(caches), dev
+    first = caches[0]
+    index = first.device.index
+    for c in caches:
+        if c.device.index != index:
+            raise ValueError("the layers' caches are on different devices")
+    return structs, len(caches), first
 
 
 def _table(t, refs, page_size, dev):
     _check_int(t, "page_table", dev, 2)
     _check_int(refs, "refs", dev, 1)
-    if t.shape[0] < 1 or t.shape[1] < 1 or (t.shape[1] > 1 and t.stride(1) != 1):
+    (rows, width), (stride, one) = t.shape, t.stride()
+    if rows < 1 or width < 1 or (width > 1 and one != 1):
         raise ValueError("page_table must be [rows, pages per row] with a contiguous last axis")
     if not refs.is_contiguous():
         raise ValueError("refs must be contiguous")
-    return PageTableStruct(t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.shape[0], t.shape[1], refs.data_ptr(), refs.shape[0],
-                           page_size)
+    return PageTableStruct(t.data_ptr(), stride if rows > 1 else 0, rows, width, refs.data_ptr(), refs.shape[0], page_size)
 
 
 def _workspace(workspace, need, dev):
@@ -78,8 +82,8 @@ def cache_copy(caches, src, dst, stream=None) -> None:
     """Copies page src[i] to page dst[i], codes and scales, in every layer's cache (fa_cache_copy): int32
     [n] on the device; moves with -1 in either are left out. No page of dst may be another move's
     source or destination."""
-    s, n, dev = _layers(caches)
-    _on(_copy, dev, stream, s, n, dev, src, dst)
+    s, n, first = _layers(caches)
+    _on(_copy, first.device, stream, s, n, first.device, src, dst)
 
 
 def _copy(s, layers, dev, src, dst):
@@ -124,16 +128,13 @@ def cache_reserve(caches, page_table, refs, start, count, ok=None, workspace=Non
     [rows] or one number for every row. Returns ok, int32 [rows]: 0 where pages ran out or the
     tokens pass the table's width; such rows must not be written to. `workspace`: uint8 of
     cache_reserve_workspace_bytes(...) bytes, allocated here if None."""
-    s, n, dev = _layers(caches)
-    return _on(_reserve, dev, stream, s, n, dev, page_table, refs, start, count, ok, workspace)
+    s, n, first = _layers(caches)
+    return _on(_reserve, first.device, stream, s, n, first, page_table, refs, start, count, ok, workspace)
 
 
-def _page_size(s, layers):
-    return s.page_size if layers == 1 and isinstance(s, CacheStruct) else s[0].page_size
-
-
-def _reserve(s, layers, dev, page_table, refs, start, count, ok, workspace):
-    t = _table(page_table, refs, _page_size(s, layers), dev)
+def _reserve(s, layers, first, page_table, refs, start, count, ok, workspace):
+    dev = first.device
+    t = _table(page_table, refs, first.page_size, dev)
     tokens = 0
     if not isinstance(count, torch.Tensor):
         if count is None or not 0 <= int(count) < 2 ** 31:
@@ -157,12 +158,13 @@ def cache_compact(caches, page_table, refs, where=None, live=None, workspace=Non
     (fa_cache_compact). Returns where, int32 [num_pages]: each page's new number, -1 for free ones (for other
     tables that name pages), and live, int32 [1]: the pages in use. `workspace`: uint8 of
     cache_compact_workspace_bytes(...) bytes, allocated here if None."""
-    s, n, dev = _layers(caches)
-    return _on(_compact, dev, stream, s, n, dev, page_table, refs, where, live, workspace)
+    s, n, first = _layers(caches)
+    return _on(_compact, first.device, stream, s, n, first, page_table, refs, where, live, workspace)
 
 
-def _compact(s, layers, dev, page_table, refs, where, live, workspace):
-    t = _table(page_table, refs, _page_size(s, layers), dev)
+def _compact(s, layers, first, page_table, refs, where, live, workspace):
+    dev = first.device
+    t = _table(page_table, refs, first.page_size, dev)
     where, live = _rows_out(where, t.num_pages, "where", dev), _rows_out(live, 1, "live", dev)
     L = lib()
     workspace, have = _workspace(workspace, L.fa_cache_compact_workspace_bytes(t.num_pages) if workspace is None else 0, dev)

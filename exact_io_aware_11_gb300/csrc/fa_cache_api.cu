@@ -295,7 +295,7 @@ int make_attention(const void* q, void* o, float* lse, const fa_cache* cache, in
 }
 
 // ------------------------------------------------------------------ pages
-constexpr int kMaxLayers = 1024, kMaxTableRows = 16384;
+constexpr int kMaxLayers = 1024;
 
 // The pools of a model's layers: all of one shape, no memory in common, and none with `others`.
 int check_layers(const fa_cache* caches, int layers, const Range* others, int n_others) {
@@ -329,7 +329,7 @@ int check_layers(const fa_cache* caches, int layers, const Range* others, int n_
 }
 
 int check_page_table_sizes(int rows, int width, int num_pages, int page) {
-  if (rows < 1 || rows > kMaxTableRows || width < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
+  if (rows < 1 || rows > kPageTableRows || width < 1 || num_pages < 1) return FA_ERR_INVALID_ARG;
   if (page != 16 && page != 32 && page != 64 && page != 128) return FA_ERR_UNSUPPORTED;
   // entries are counted, and tokens, in 32 bits
   if (static_cast<long long>(rows) * width > (1LL << 30) || static_cast<long long>(width) * page > INT_MAX - 1024)

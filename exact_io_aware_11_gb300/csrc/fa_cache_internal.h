@@ -78,6 +78,7 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
                                     cudaStream_t stream);
 size_t shared_attention_workspace(int B, int HK, int G, int N, int d, int page, int table_width, int groups);
 
+constexpr int kPageTableRows = 16384;  // at most
 // A page table with the counts of its pages' users (fa_page_table).
 struct PageTable {
   int* entry;

@@ -284,86 +284,148 @@ __device__ __forceinline__ void list_pages(const PageSlice& s, const int* refs, 
 }
 
 // ------------------------------------------------------------------ reserving
-// The items are the columns of the rows' ranges, in the order of rows. Who copies a page that
-// several of them write to: all but the last one, which keeps it if nobody outside the call has it.
-// That is found in refs itself: every item takes itself off its page's count; where nothing
-// is left the last item, by an atomic minimum of -(2^30 + its number), keeps the page.
-// Bound: latency, some five round trips to memory between barriers of the cluster.
-constexpr int kReserveRows = 16384 / kCluster;  // of a CTA
+// The items are the columns of the rows' ranges, in the order of rows; each CTA has an equal run of them. An
+// item without a page takes one, an item whose page has no other user keeps it. Who copies a page that several
+// items write to: all but the last one, which keeps it if nobody outside the call has it. That is
+// found in refs itself: every such item takes itself off its page's count; where nothing is left the last
+// item, by an atomic minimum of -(2^30 + its number), keeps the page.
+// Bound: latency, four to eight round trips to memory between barriers of the cluster.
+constexpr int kItemCache = 4096;  // items of a CTA that are kept in shared memory
+enum : int { kTakes = 0, kOwn = 1, kShared = 2, kKeeps = 3 };  // kShared: takes one, once the keepers are known
+constexpr int reserve_smem(int rows) { return kItemCache * 8 + (2 * rows + 1) * 4; }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads)
     page_reserve_kernel(const __grid_constant__ PageReserveLaunch a) {
-  __shared__ int first_item[kReserveRows + 1];  // of each of the CTA's rows
-  __shared__ int first_col[kReserveRows];
+  extern __shared__ int2 cache[];  // row and state, entry
   __shared__ int part[kCountThreads / 32];
-  __shared__ int fail_row;
+  __shared__ int fail_row, any_shared;
   const PageTable& t = a.t;
   const int rank = blockIdx.x;  // the grid is one cluster
-  const int per = (t.rows + kCluster - 1) / kCluster, row0 = min(t.rows, rank * per), rows = min(t.rows, row0 + per) - row0;
+  int* const first_item = reinterpret_cast<int*>(cache + kItemCache);  // [rows + 1]
+  int* const first_col = first_item + t.rows + 1;                      // [rows]
   grid_dep_wait();
   if (threadIdx.x == 0) {
     fail_row = t.rows;
+    any_shared = 0;
     if (rank == 0) *a.moves = 0;
   }
-  // ---- the rows' ranges
-  int items = 0;
-  for (int r0 = 0; r0 < rows; r0 += kCountThreads) {
-    const int r = r0 + threadIdx.x, b = row0 + r;
+  // ---- the rows' ranges: every CTA has all of them
+  int all_items = 0;
+  for (int r0 = 0; r0 < t.rows; r0 += kCountThreads) {
+    const int b = r0 + threadIdx.x;
     int n = 0;
-    if (r < rows) {
+    if (b < t.rows) {
       const long long s = a.start != nullptr ? a.start[b] : 0;
       const long long c = max(0, a.count != nullptr ? a.count[b] : a.tokens);
       const bool fits = c == 0 || (s >= 0 && s + c <= static_cast<long long>(t.width) * t.page);
       const int col = fits && c > 0 ? static_cast<int>(s / t.page) : 0;
       if (fits && c > 0) n = static_cast<int>((s + c + t.page - 1) / t.page) - col;
-      first_col[r] = col;
-      a.ok[b] = fits ? 1 : 0;
+      first_col[b] = col;
+      if (rank == 0) a.ok[b] = fits ? 1 : 0;
     }
     int total;
     const int k = block_scan(n, part, &total);
-    if (r < rows) first_item[r] = items + k;
-    items += total;
+    if (b < t.rows) first_item[b] = all_items + k;
+    all_items += total;
   }
-  if (threadIdx.x == 0) first_item[rows] = items;
+  if (threadIdx.x == 0) first_item[t.rows] = all_items;
   __syncthreads();
+  const int item0 = static_cast<int>(static_cast<long long>(all_items) * rank / kCluster);
+  const int items = static_cast<int>(static_cast<long long>(all_items) * (rank + 1) / kCluster) - item0;
   struct Item {
-    int r, col, entry, code;
-    bool page;  // entry names a page
+    int row, col, entry, state;
   };
-  auto item = [&](int i) {
-    int lo = 0, hi = rows;  // the last row with first_item <= i
+  auto row_of = [&](int i) {  // the last row with first_item <= i
+    int lo = 0, hi = t.rows;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       (first_item[mid] <= i ? lo : hi) = mid;
     }
+    return lo;
+  };
+  auto column = [&](int row, int i) { return first_col[row] + item0 + i - first_item[row]; };
+  auto item = [&](int i) {
     Item x;
-    x.r = lo;
-    x.col = first_col[lo] + i - first_item[lo];
-    x.entry = t.entry[(row0 + lo) * t.stride + x.col];
-    x.page = is_page(x.entry, t.num_pages);
-    x.code = -(1 << 30) - ((row0 + lo) * t.width + x.col);
+    if (i < kItemCache) {
+      const int2 v = cache[i];
+      x.row = v.x >> 2;
+      x.state = v.x & 3;
+      x.entry = v.y;
+      x.col = column(x.row, i);
+    } else {
+      x.row = row_of(item0 + i);
+      x.col = column(x.row, i);
+      x.entry = t.entry[x.row * t.stride + x.col];
+      x.state = is_page(x.entry, t.num_pages) ? kShared : kTakes;
+    }
     return x;
   };
-  // ---- every item off its page's count
-  for (int i = threadIdx.x; i < items; i += kCountThreads) {
-    const Item x = item(i);
-    if (x.page)
-      atomicAdd(t.refs + x.entry, -1);
-    else if (x.entry != -1)
-      report_bad_page(a.status);
+  auto code = [&](int i) { return -(1 << 30) - (item0 + i); };
+  // ---- what each item has
+  constexpr int kAtOnce = 4;
+  int mine = 0;
+  for (int i0 = 0; i0 < items; i0 += kAtOnce * kCountThreads) {
+    int row[kAtOnce], entry[kAtOnce], refs[kAtOnce];
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + k * kCountThreads + threadIdx.x;
+      row[k] = 0;
+      entry[k] = -1;
+      if (i < items) {
+        row[k] = row_of(item0 + i);
+        entry[k] = t.entry[row[k] * t.stride + column(row[k], i)];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) refs[k] = is_page(entry[k], t.num_pages) ? load_l2(t.refs + entry[k]) : 0;
+#pragma unroll
+    for (int k = 0; k < kAtOnce; ++k) {
+      const int i = i0 + k * kCountThreads + threadIdx.x;
+      if (i >= items) continue;
+      int state = kTakes;
+      if (is_page(entry[k], t.num_pages))
+        state = i < kItemCache && refs[k] == 1 ? kOwn : kShared;
+      else if (entry[k] != -1)
+        report_bad_page(a.status);
+      if (state == kTakes) ++mine;
+      if (state == kShared) any_shared = 1;
+      if (i < kItemCache) cache[i] = make_int2(row[k] << 2 | state, entry[k]);
+    }
   }
-  cluster_sync();
-  // ---- pages that nobody else has: the last item keeps them
-  for (int i = threadIdx.x; i < items; i += kCountThreads) {
-    const Item x = item(i);
-    if (x.page && load_l2(t.refs + x.entry) <= 0) atomicMin(t.refs + x.entry, x.code);
-  }
-  cluster_sync();
-  auto takes = [&](const Item& x) { return !x.page || load_l2(t.refs + x.entry) != x.code; };
-  int mine = 0, need, wanted, have, all_free = 0, free_before = 0;
-  for (int i = threadIdx.x; i < items; i += kCountThreads) mine += takes(item(i)) ? 1 : 0;
+  int need, wanted, have, all_free = 0, free_before = 0;
   block_scan(mine, part, &need);
-  const int before = cluster_scan(need, a.slots, rank, &wanted);
+  if (threadIdx.x == 0) a.slots[3 * kCluster + rank] = any_shared;
+  int before = cluster_scan(need, a.slots, rank, &wanted);
+  bool shared = false;
+#pragma unroll
+  for (int r = 0; r < kCluster; ++r) shared |= load_l2(a.slots + 3 * kCluster + r) != 0;
+  // whether item i takes a page; final once `shared` has been dealt with
+  auto takes = [&](const Item& x, int i) {
+    return x.state == kTakes || (x.state == kShared && (i < kItemCache || load_l2(t.refs + x.entry) != code(i)));
+  };
+  if (shared) {
+    // ---- such items off their pages' counts; pages that nobody else has: the last item keeps them
+    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+      const Item x = item(i);
+      if (x.state == kShared) atomicAdd(t.refs + x.entry, -1);
+    }
+    cluster_sync();
+    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+      const Item x = item(i);
+      if (x.state == kShared && load_l2(t.refs + x.entry) <= 0) atomicMin(t.refs + x.entry, code(i));
+    }
+    cluster_sync();
+    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+      const Item x = item(i);
+      if (x.state != kShared) continue;
+      if (load_l2(t.refs + x.entry) != code(i))
+        ++mine;
+      else if (i < kItemCache)
+        cache[i].x = x.row << 2 | kKeeps;
+    }
+    block_scan(mine, part, &need);
+    before = cluster_scan(need, a.slots + 4 * kCluster, rank, &wanted);
+  }
   int f = t.rows;  // the first row that fails
   if (wanted > 0) {  // the same in every CTA
     auto is_free = [](int, int refs) { return refs == 0; };
@@ -375,10 +437,10 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
       for (int i0 = 0; i0 < items; i0 += kCountThreads) {
         const int i = i0 + threadIdx.x;
         Item x{};
-        const bool take = i < items && (x = item(i), takes(x));
+        const bool take = i < items && (x = item(i), takes(x, i));
         int total;
         const int k = k0 + block_scan(take ? 1 : 0, part, &total);
-        if (take && k >= all_free) atomicMin(&fail_row, row0 + x.r);
+        if (take && k >= all_free) atomicMin(&fail_row, x.row);
         k0 += total;
       }
       __syncthreads();
@@ -391,42 +453,44 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
     cluster_sync();
   }
   // ---- pages dealt out
-  int k0 = before;
-  for (int i0 = 0; i0 < items; i0 += kCountThreads) {
-    const int i = i0 + threadIdx.x;
-    Item x{};
-    bool take = false, keeps = false;
-    if (i < items) {
-      x = item(i);
-      take = takes(x);
-      keeps = !take;
-    }
-    int total;
-    const int k = k0 + block_scan(take ? 1 : 0, part, &total), b = row0 + x.r;
-    if (keeps) t.refs[x.entry] = b < f ? 1 : 0;  // (below, the rows that fail come back to their pages' counts)
-    if (take && b < f) {
-      const int p = load_l2(a.list + k);
-      t.entry[b * t.stride + x.col] = p;
-      t.refs[p] = 1;
-      // earlier tokens of the sequence in the page
-      if (x.page && i == first_item[x.r] && (a.start != nullptr ? a.start[b] : 0) % t.page != 0) {
-        const int m = atomicAdd(a.moves, 1);
-        a.src[m] = x.entry;
-        a.dst[m] = p;
+  if (shared || wanted > 0) {
+    int k0 = before;
+    for (int i0 = 0; i0 < items; i0 += kCountThreads) {
+      const int i = i0 + threadIdx.x;
+      Item x{};
+      bool take = false;
+      if (i < items) {
+        x = item(i);
+        take = takes(x, i);
       }
+      int total;
+      const int k = k0 + block_scan(take ? 1 : 0, part, &total), b = x.row;
+      // (below, the rows that fail come back to their pages' counts)
+      if (!take && (x.state == kKeeps || x.state == kShared)) t.refs[x.entry] = b < f ? 1 : 0;
+      if (take && b < f) {
+        const int p = load_l2(a.list + k);
+        t.entry[b * t.stride + x.col] = p;
+        t.refs[p] = 1;
+        // earlier tokens of the sequence in the page
+        if (x.state == kShared && x.col == first_col[b] && (a.start != nullptr ? a.start[b] : 0) % t.page != 0) {
+          const int m = atomicAdd(a.moves, 1);
+          a.src[m] = x.entry;
+          a.dst[m] = p;
+        }
+      }
+      k0 += total;
     }
-    k0 += total;
   }
   if (f < t.rows) {
     cluster_sync();
     for (int i = threadIdx.x; i < items; i += kCountThreads) {
       const Item x = item(i);
-      if (x.page && row0 + x.r >= f) atomicAdd(t.refs + x.entry, 1);
+      if ((x.state == kShared || x.state == kKeeps) && x.row >= f) atomicAdd(t.refs + x.entry, 1);
     }
     cluster_sync();
     for (int i = threadIdx.x; i < items; i += kCountThreads) {
       const Item x = item(i);
-      if (row0 + x.r >= f && (!x.page || load_l2(t.refs + x.entry) != 1)) a.ok[row0 + x.r] = 0;
+      if (x.row >= f && x.state != kOwn && (x.state == kTakes || load_l2(t.refs + x.entry) != 1)) a.ok[x.row] = 0;
     }
   }
   grid_dep_launch();
@@ -547,7 +611,10 @@ cudaError_t launch_page_reserve(PageReserveLaunch a, const fa_cache* caches, int
   a.src = reinterpret_cast<int*>(ws + 256);
   a.dst = reinterpret_cast<int*>(ws + 256 + words(a.t.rows));
   a.list = reinterpret_cast<int*>(ws + 256 + 2 * words(a.t.rows));
-  cudaError_t e = launch_pdl(page_reserve_kernel, dim3(kCluster), dim3(kCountThreads), 0, stream, a);
+  static std::atomic<unsigned long long> smem_set{0};
+  cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_reserve_kernel), reserve_smem(kPageTableRows));
+  if (e != cudaSuccess) return e;
+  e = launch_pdl(page_reserve_kernel, dim3(kCluster), dim3(kCountThreads), reserve_smem(a.t.rows), stream, a);
   if (e != cudaSuccess) return e;
   PageCopyLaunch c{};
   c.src = a.src;

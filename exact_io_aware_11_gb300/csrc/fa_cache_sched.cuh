@@ -33,7 +33,7 @@ struct AttnGrid {
   int4* record;   // [C]: entry, head, first CTA of a cut unit that c ends; entry -1: none
   float* m_part;  // [2 C][rows]
   float* l_part;
-  float* o_part;  // [2 C][rows][D]; tiles: [2 C][rows / 32][D / 4][32 rows][4]
+  float* o_part;  // [2 C][rows][D]; tiles (but not a list's): [2 C][rows / 32][D / 4][32 rows][4]
   // shared prefixes (fa_cache_shared.cu): the entries, made on the device before, the sequences of
   // the groups, and per unit the CTAs that its parts come from: {-1, 0} where a slot 2 C + unit has it whole
   const SharedEntry* entry;

@@ -179,7 +179,7 @@ struct JoinList {
   const float* m;
   const float* l;
   const float* o;
-  int rows, ctas, tiles;  // tiles: O in the tile kernel's order
+  int rows, ctas;
 };
 struct JoinLaunch {
   JoinList list[2];  // A, B
@@ -187,72 +187,91 @@ struct JoinLaunch {
   int rows_b, tiles_b, HK;
 };
 
-// The parts of every row of O whose units have not written it: a warp a row, a lane 4 channels. Bound:
-// latency and the L2 cache (a part is 4 D + 8 bytes a row).
+// The parts of every row of O whose units have not written it: a warp a row. Lane q looks up the
+// q-th part and its weight, then each lane sums 4 channels, eight parts in flight. Bound: latency
+// and the L2 cache (a part is 4 D + 8 bytes a row).
 template <int D>
 __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8;
   const int lane = threadIdx.x & 31;
-  grid_dep_wait();
-  grid_dep_launch();
   const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
-  if (row >= static_cast<long long>(a.B) * a.Hq * a.N) return;
   const int bh = static_cast<int>(row / a.N), i = static_cast<int>(row - static_cast<long long>(bh) * a.N);
   const int b = bh / a.Hq, head = bh - b * a.Hq, hk = head / a.G, r = i * a.G + head - hk * a.G;
-  const int4 s = j.seq[b];
   const int tile = r / j.rows_b, own = (b * j.tiles_b + tile) * j.HK + hk;
+  grid_dep_wait();
+  grid_dep_launch();
+  if (row >= static_cast<long long>(a.B) * a.Hq * a.N) return;
+  const int4 s = j.seq[b];
   const int2 parts = j.list[1].unit_parts[own];
   if (s.x == 0 && parts.x < 0) return;  // straight from its unit
+  // the prefix's parts, then the row's own; each list's first CTA, and how many
+  const JoinList& pl = j.list[s.x == 2 ? 1 : 0];
+  int unit = 0, at = 0, first = 0, n = 0;
+  bool whole = false;
+  if (s.x != 0) {
+    const int x = s.y + r, t = x / pl.rows;
+    unit = (s.z + t) * j.HK + hk;
+    at = x - t * pl.rows;
+    const int2 p = pl.unit_parts[unit];
+    whole = p.x < 0;
+    first = whole ? 0 : p.x;
+    n = whole ? 1 : p.y - p.x + 1;
+  }
+  const int all = n + (parts.x < 0 ? 1 : parts.y - parts.x + 1);
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f, M = -INFINITY;
-  auto add = [&](const JoinList& x, int unit, int row_in_unit, int2 p) {
-    const int first = p.x < 0 ? 0 : p.x, last = p.x < 0 ? 0 : p.y;
-    for (int q0 = first; q0 <= last; q0 += kBatch) {
-      float mq[kBatch], lq[kBatch];
-      float4 v[kBatch];
+  for (int q0 = 0; q0 < all; q0 += 32) {
+    // this lane's part
+    const int q = q0 + lane;
+    const float* o = nullptr;
+    float m = -INFINITY, l = 0.f;
+    if (q < all) {
+      const JoinList& x = q < n ? pl : j.list[1];
+      long long pr;
+      if (q < n)
+        pr = static_cast<long long>(whole ? 2 * x.ctas + unit : 2 * (first + q) + (q == 0 ? 1 : 0)) * x.rows + at;
+      else
+        pr = static_cast<long long>(parts.x < 0 ? 2 * x.ctas + own : 2 * (parts.x + q - n) + (q == n ? 1 : 0)) * x.rows + (r - tile * j.rows_b);
+      m = x.m[pr];
+      l = x.l[pr];
+      o = x.o + pr * D;
+    }
+    const int count = min(32, all - q0);
+    // the first parts' values are on their way while their weights are formed
+    float4 v[kBatch];
+    auto load = [&](int k0) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        mq[k] = -INFINITY;
-        lq[k] = 0.f;
-        v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int q = q0 + k;
-        if (q <= last) {
-          const int slot = p.x < 0 ? 2 * x.ctas + unit : 2 * q + (q == first ? 1 : 0);
-          const long long pr = static_cast<long long>(slot) * x.rows + row_in_unit;
-          mq[k] = x.m[pr];
-          lq[k] = x.l[pr];
-          if (lane < D / 4)
-            v[k] = x.tiles ? reinterpret_cast<const float4*>(x.o)[((pr >> 5) * (D / 4) + lane) * 32 + (pr & 31)]
-                           : reinterpret_cast<const float4*>(x.o)[pr * (D / 4) + lane];
-        }
+        const float4* const p = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + k) & 31));
+        v[k] = k0 + k < count && lane < D / 4 ? p[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      float Mn = M;
+    };
+    load(0);
+    float Mn = fmaxf(M, m);
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) Mn = fmaxf(Mn, mq[k]);
-      const float zero = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - zero);
-      M = Mn;
-      sum *= e;
-      acc.x *= e;
-      acc.y *= e;
-      acc.z *= e;
-      acc.w *= e;
+    for (int w = 16; w > 0; w >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, w));
+    const float zero = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - zero), f = ex2(m - zero);
+    M = Mn;
+    float part = l * f;
+#pragma unroll
+    for (int w = 16; w > 0; w >>= 1) part += __shfl_xor_sync(0xffffffffu, part, w);
+    sum = sum * e + part;
+    acc.x *= e;
+    acc.y *= e;
+    acc.z *= e;
+    acc.w *= e;
+    for (int k0 = 0; k0 < count; k0 += kBatch) {
+      if (k0 > 0) load(k0);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float f = ex2(mq[k] - zero);
-        sum = fmaf(lq[k], f, sum);
-        acc.x = fmaf(v[k].x, f, acc.x);
-        acc.y = fmaf(v[k].y, f, acc.y);
-        acc.z = fmaf(v[k].z, f, acc.z);
-        acc.w = fmaf(v[k].w, f, acc.w);
+        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
+        acc.x = fmaf(v[k].x, w, acc.x);
+        acc.y = fmaf(v[k].y, w, acc.y);
+        acc.z = fmaf(v[k].z, w, acc.z);
+        acc.w = fmaf(v[k].w, w, acc.w);
       }
     }
-  };
-  if (s.x != 0) {
-    const JoinList& x = j.list[s.x - 1];
-    const int at = s.y + r, t = at / x.rows, unit = (s.z + t) * j.HK + hk;
-    add(x, unit, at - t * x.rows, x.unit_parts[unit]);
   }
-  add(j.list[1], own, r - tile * j.rows_b, parts);
   const bool none = sum == 0.f;  // a row that sees no key; NaN stays NaN
   const float inv = none ? 0.f : 1.f / sum;
   if (lane < D / 4) {
@@ -395,8 +414,8 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   gb.l_part = reinterpret_cast<float*>(a.ws + p.l_b);
   gb.o_part = reinterpret_cast<float*>(a.ws + p.o_b);
   JoinLaunch j{};
-  j.list[0] = JoinList{ga.unit_parts, ga.m_part, ga.l_part, ga.o_part, p.rows_a, p.ctas_a, 1};
-  j.list[1] = JoinList{gb.unit_parts, gb.m_part, gb.l_part, gb.o_part, p.rows_b, p.ctas_b, p.rows_b > 16};
+  j.list[0] = JoinList{ga.unit_parts, ga.m_part, ga.l_part, ga.o_part, p.rows_a, p.ctas_a};
+  j.list[1] = JoinList{gb.unit_parts, gb.m_part, gb.l_part, gb.o_part, p.rows_b, p.ctas_b};
   j.seq = pl.seq;
   j.rows_b = p.rows_b;
   j.tiles_b = p.tiles_b;

@@ -872,7 +872,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
         if (row_ok)
           a.lse[(static_cast<long long>(ob) * a.Hq + head) * g.N + qi] = none ? -INFINITY : (m - kBias + log2f(l)) * kLn2Cache;
       } else {
-        // a part, in the order of the registers: 512 bytes a warp and store
+        // a part, in the order of the registers (512 bytes a warp and store)
         int slot = 2 * blockIdx.x + (x.first == 0 ? 1 : 0);
         if constexpr (SH) {
           if (whole) slot = 2 * gridDim.x + x.unit;
@@ -887,7 +887,17 @@ __global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
         for (int c = 0; c < D / 64; ++c) {
           uint32_t o[2][32];
           read_o(c, o);
-          if (row_ok) {  // rows that see nothing leave zeros: their accumulators hold whatever P was
+          if constexpr (SH) {  // whole rows, which are joined one by one
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              uint4 w[8];
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                w[v] = none ? make_uint4(0, 0, 0, 0) : make_uint4(o[e][4 * v], o[e][4 * v + 1], o[e][4 * v + 2], o[e][4 * v + 3]);
+              store_rows(box + (REP == 2 ? c * 8192 + e * 4096 : 0), w,
+                         row_ok ? reinterpret_cast<uint8_t*>(g.o_part + pr * D + c * 64 + e * 32) : nullptr, lane);
+            }
+          } else if (row_ok) {  // rows that see nothing leave zeros: their accumulators hold whatever P was
 #pragma unroll
             for (int v = 0; v < 16; ++v) {
               const uint32_t* const w = o[v >> 3] + (v & 7) * 4;

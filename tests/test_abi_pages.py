@@ -30,7 +30,7 @@ def layers_of(a):
         if l == a["layer"]:
             c.update(a["cache"])
         pools.append(_cache.CacheStruct(c["k"], c["v"], c["ks"], c["vs"], c["P"], c["H"], c["page"], c["d"], c["fmt"]))
-    return (_cache.CacheStruct * len(pools))(*pools) if a["pools"] else None
+    return b"".join(bytes(p) for p in pools) if a["pools"] else None
 
 
 def table_of(a):
