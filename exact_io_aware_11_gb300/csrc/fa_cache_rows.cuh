@@ -89,16 +89,22 @@ __device__ __forceinline__ uint32_t tile_offset(int r, int c) {
   return r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
 }
 
-// One row of queries in fp16, scaled by a power of two (its inverse comes
-// back): lane t of the row's four holds channels [D/4 t, D/4 (t + 1)).
+// One row of queries as it lies in memory, zeros where it is none: lane t of the row's four has channels
+// [D/4 t, D/4 (t + 1)).
+template <int D, bool SH>
+__device__ __forceinline__ void load_query(const uint16_t* row, bool real, int t, uint4 (&w)[D / 32]) {
+#pragma unroll
+  for (int v = 0; v < D / 32; ++v)
+    w[v] = real ? attn_load<SH>(reinterpret_cast<const uint4*>(row + t * (D / 4)) + v) : make_uint4(0, 0, 0, 0);
+}
+// The same in fp16, scaled by a power of two (its inverse comes back).
 template <int D>
-__device__ __forceinline__ float load_query(const uint16_t* row, bool real, bool fp16, int t, uint32_t (&q)[D / 8]) {
+__device__ __forceinline__ float scale_query(const uint4 (&raw)[D / 32], bool fp16, uint32_t (&q)[D / 8]) {
   float x[D / 4];
   float mx = 0.f;
 #pragma unroll
   for (int v = 0; v < D / 32; ++v) {
-    const uint4 w = real ? reinterpret_cast<const uint4*>(row + t * (D / 4))[v] : make_uint4(0, 0, 0, 0);
-    const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    const uint32_t ww[4] = {raw[v].x, raw[v].y, raw[v].z, raw[v].w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 f = unpack16(ww[i], fp16);
@@ -210,7 +216,7 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
       s.want = group && key < ld.x.seen;
       s.h = ld.h;
       s.row = key & (c.page - 1);
-      if (s.want) s.pid = c.table[ld.x.b * c.table_stride + first_column(ld.x) + (key >> c.log2_page)];
+      if (s.want) s.pid = attn_load<SH>(c.table + ld.x.b * c.table_stride + first_column(ld.x) + (key >> c.log2_page));
       ld.next(g);
     }
     return s;
@@ -222,8 +228,8 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
-      s.ks = c.scale[0][ph];
-      s.vs = c.scale[1][ph];
+      s.ks = attn_load<SH>(c.scale[0] + ph);
+      s.vs = attn_load<SH>(c.scale[1] + ph);
     }
   };
   Step now = look(), next = look();
@@ -291,18 +297,39 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
     tma_prefetch_desc(&a.tm[0]);
     tma_prefetch_desc(&a.tm[1]);
   }
-  grid_dep_wait();
+  attn_wait<SH>(g, false);
   grid_dep_launch();
   const Watchdog wd{a.wait_limit, a.status, &abort_flag};
   AttnCursor<SH> cur = attn_share<kThreads, SH>(g, &share, part);  // its barriers publish the above
   if (warp == kWarps) {
     produce<D, NT, SH>(a, g, cur, smem, full, empty, wd, lane);
+    attn_wait<SH>(g, true);
     return;
   }
   if (!SH && g.split && threadIdx.x == 0) g.record[blockIdx.x] = make_int4(-1, 0, 0, 0);
   bool alive = true;  // no wait has given up
   int stage = 0, turn = 0;
   uint32_t phase = 0;
+
+  // The queries of the cursor's unit, this lane's part of group n of 8 rows
+  auto query = [&](int n, uint4 (&w)[D / 32]) {
+    const int r = n * 8 + gq;
+    if constexpr (SH) {
+      const AttnRow y = shared_row(g, cur.x, r);
+      load_query<D, SH>(a.q + y.b * a.sq.b + static_cast<long long>(cur.h * g.G + y.head) * a.sq.h + y.i * a.sq.n, y.real, t, w);
+    } else {
+      const int row = cur.x.row0 + r, i = row / g.G;
+      load_query<D, SH>(a.q + cur.x.b * a.sq.b + static_cast<long long>(cur.h * g.G + (row - i * g.G)) * a.sq.h + i * a.sq.n,
+                        i < cur.x.ql, t, w);
+    }
+  };
+  // A list's units are short (a sequence's own tokens): their queries are loaded a unit ahead (64 sequences of 50 to 2000
+  // tokens 38.1 -> 36.4 us; 64 of 1000 to 8192, which is not a list, 100.2 -> 101.1: registers). Two groups of
+  // rows leave no registers for it (200 bytes of spills at d = 128).
+  constexpr bool kAhead = SH && NT == 1;
+  uint4 ahead[kAhead ? D / 32 : 1];
+  if constexpr (kAhead)
+    if (!cur.done(g)) query(0, ahead);
 
   while (!cur.done(g)) {
     // ---- a unit (or the CTA's part of one)
@@ -317,24 +344,23 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
     float* const rfs = reinterpret_cast<float*>(smem + L::kQuery + NT * (D / 16) * 256);
     float rf[NT][2];
     int lim[NT][2];
-    auto query = [&](int n, uint32_t (&w)[D / 8]) {
-      if constexpr (SH) {
-        const AttnRow y = shared_row(g, x, n * 8 + gq);
-        const uint16_t* row = a.q + y.b * a.sq.b + static_cast<long long>(h * g.G + y.head) * a.sq.h + y.i * a.sq.n;
-        return load_query<D>(row, y.real, a.fp16, t, w) * a.scale_log2;
-      }
-      const int r = x.row0 + n * 8 + gq, i = r / g.G;
-      const uint16_t* row = a.q + x.b * a.sq.b + static_cast<long long>(h * g.G + (r - i * g.G)) * a.sq.h + i * a.sq.n;
-      return load_query<D>(row, i < x.ql, a.fp16, t, w) * a.scale_log2;
-    };
     if constexpr (NT == 1) {
-      const float f = query(0, q);
+      uint4 raw[D / 32];
+      if constexpr (kAhead) {
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) raw[i] = ahead[kAhead ? i : 0];
+      } else {
+        query(0, raw);
+      }
+      const float f = scale_query<D>(raw, a.fp16, q) * a.scale_log2;
       rf[0][0] = __shfl_sync(0xffffffffu, f, 2 * t * 4);
       rf[0][1] = __shfl_sync(0xffffffffu, f, (2 * t + 1) * 4);
     } else {
       if (warp < NT) {
+        uint4 raw[D / 32];
+        query(warp, raw);
         uint32_t w[D / 8];
-        const float f = query(warp, w);
+        const float f = scale_query<D>(raw, a.fp16, w) * a.scale_log2;
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) qs[(warp * (D / 16) + i) * 32 + lane] = make_uint2(w[2 * i], w[2 * i + 1]);
         if (t == 0) rfs[warp * 8 + gq] = f;
@@ -534,6 +560,8 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
       }
     }
     cur.skip(g, steps);
+    if constexpr (kAhead)
+      if (!cur.done(g)) query(0, ahead);  // the next unit's, on their way while this one ends
 
     // ---- join the warps' keys, through the last step's stage
 #pragma unroll

@@ -14,6 +14,7 @@
 #pragma once
 
 #include "fa_cache_internal.h"
+#include "fa_ptx.cuh"
 
 namespace fa {
 
@@ -37,9 +38,10 @@ struct AttnGrid {
   // shared prefixes (fa_cache_shared.cu): the entries, made on the device before, the sequences of
   // the groups, and per unit the CTAs that its parts come from: {-1, 0} where a slot 2 C + unit has it whole
   const SharedEntry* entry;
-  const int* entries;
+  const int* entries;  // how many, and the CTAs that work on them
   const int* member;
   int2* unit_parts;
+  int late;  // the kernel runs beside the one before it, and waits for it at its end (shared_wait)
 };
 
 // One (sequence, row tile).
@@ -117,7 +119,7 @@ __device__ __forceinline__ AttnRow shared_row(const AttnGrid& g, const X& x, int
     row -= m * rows;
     if (y.exists) {
       y.b = __ldcg(g.member + x.list + m);
-      ql = g.q_len != nullptr ? min(g.N, max(0, g.q_len[y.b])) : g.N;
+      ql = g.q_len != nullptr ? min(g.N, max(0, __ldcg(g.q_len + y.b))) : g.N;
     }
   }
   y.i = row / g.G;
@@ -219,8 +221,10 @@ __device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShar
   before += incl - mine;
   total *= g.HK;
   AttnShare d{};
-  d.ctas = static_cast<int>(min(static_cast<long long>(gridDim.x), total));
-  d.each = SH && total == 0 ? 0 : attn_div(total, d.ctas);  // (a list may be empty)
+  int ctas = gridDim.x;
+  if constexpr (SH) ctas = min(ctas, __ldcg(g.entries + 1));
+  d.ctas = static_cast<int>(min(static_cast<long long>(ctas), total));
+  d.each = SH && d.ctas == 0 ? 0 : attn_div(total, d.ctas);  // (a list may be empty)
   d.extra = static_cast<int>(total - d.each * d.ctas);
   const int c = blockIdx.x;
   const long long s0 = c < d.ctas ? attn_start(d, c) : total;
@@ -272,6 +276,24 @@ __device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShar
 __device__ __forceinline__ int attn_cta_of(long long s, const AttnShare& d) {
   const long long longer = d.extra * (d.each + 1);  // steps of the CTAs that have one more
   return static_cast<int>(s < longer ? attn_div(s, d.each + 1) : d.extra + attn_div(s - longer, d.each));
+}
+
+// Loads of what earlier kernels wrote. A list's kernel may start without having waited for them itself (it was
+// let go by one that had), so it reads past the L1 cache.
+template <bool SH, typename T>
+__device__ __forceinline__ T attn_load(const T* p) {
+  if constexpr (SH) return __ldcg(p);
+  return *p;
+}
+// At the start (end false) and at the end of a kernel: the wait for the kernels before it.
+template <bool SH>
+__device__ __forceinline__ void attn_wait(const AttnGrid& g, bool end) {
+  if constexpr (SH) {
+    if ((g.late != 0) != end) return;
+  } else if (end) {
+    return;
+  }
+  grid_dep_wait();
 }
 
 // Keys of a step and rows of a tile of the kernel that a call of `rows` = N * G

@@ -11,6 +11,14 @@
 // kernel (fa_cache_tile.cuh) over list A, prefixes of groups with more than 16 rows to a cache
 // head; the kernel for the sequences' own tokens over list B, with few rows (fa_cache_rows.cuh) also
 // the prefixes of small groups; and the join. Parts are in 32 bits.
+//
+// The two lists run beside each other, because one is bound by products and latencies and the other by
+// memory: the plan gives each as many SMs as its share of the estimated cost, the
+// other CTAs of list A's kernel leave at once, and list B's kernel, let go by them, begins there without
+// waiting (its own wait, for list A's kernel, comes at its end, so that the join's covers both).
+// It may: list A's CTAs let it go after their wait for the plan, whose writes, and all
+// before them, are in the L2 cache then, where it reads (attn_load). It cannot keep a CTA of list A from running,
+// as they have all begun.
 #include "fa_cache_rows.cuh"
 
 namespace fa {
@@ -21,12 +29,14 @@ constexpr int kPlanThreads = 1024, kMaxGroups = kSharedGroups;
 struct PlanLaunch {
   int B, groups, N, G, page, cap, causal;
   int rows_a, rows_b, tiles_b, few;  // few: list B's kernel takes few rows
+  int HK, sms, ctas_a, per_sm_b;        // CTAs of list A's kernel, of list B's that an SM holds
+  int step_a, start_a, step_b, start_b;  // what an SM takes for a step and for beginning a unit, in ns
   const int32_t* of;
   const int32_t* len;
   const int32_t* kv_len;
   const int32_t* q_len;
   // workspace
-  int* entries;      // of A, of B
+  int* entries;      // of list A, its CTAs; of list B, its CTAs
   SharedEntry* entry_a;
   SharedEntry* entry_b;
   int* member;       // [B]
@@ -49,42 +59,58 @@ __device__ __forceinline__ SharedEntry make_entry(int b, int row0, int kv, int q
   return x;
 }
 
-// Tokens of a group's prefix in whole pages.
-__device__ __forceinline__ int prefix_tokens(const PlanLaunch& a, int g) {
-  return min(max(0, a.len[g]), a.cap) / a.page * a.page;
-}
 struct Sequence {
   int kv, ql, group, prefix;  // group -1: on its own
 };
 // A sequence counts as one of its group where every one of its rows sees the whole prefix.
-__device__ __forceinline__ Sequence sequence(const PlanLaunch& a, int b) {
+__device__ __forceinline__ Sequence sequence(const PlanLaunch& a, const int* tokens, int group, int kv_len, int q_len) {
   Sequence s;
-  s.kv = min(a.cap, max(0, a.kv_len[b]));
-  s.ql = a.q_len != nullptr ? min(a.N, max(0, a.q_len[b])) : a.N;
-  s.group = a.of[b];
+  s.kv = min(a.cap, max(0, kv_len));
+  s.ql = min(a.N, max(0, q_len));
+  s.group = group;
   s.prefix = 0;
-  if (s.group >= 0 && s.group < a.groups && s.ql > 0) s.prefix = prefix_tokens(a, s.group);
+  if (s.group >= 0 && s.group < a.groups && s.ql > 0) s.prefix = tokens[s.group];
   if (s.prefix == 0 || (a.causal ? s.kv - s.ql + 1 : s.kv) < s.prefix) {
     s.group = -1;
     s.prefix = 0;
   }
   return s;
 }
+__device__ __forceinline__ Sequence sequence(const PlanLaunch& a, const int* tokens, int b) {
+  return sequence(a, tokens, a.of[b], a.kv_len[b], a.q_len != nullptr ? a.q_len[b] : a.N);
+}
 
+// A block of as many threads as there are sequences or groups, 1024 at most; what is said of a
+// sequence stays in its thread's registers where each has one.
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_constant__ PlanLaunch a) {
   __shared__ int count[kMaxGroups], start[kMaxGroups], base[kMaxGroups], first[kMaxGroups];
+  __shared__ int tokens[kMaxGroups];  // of the prefixes, in whole pages
   __shared__ int rank[kPlanThreads];
   __shared__ int sums[3][kPlanThreads / 32];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, NG = a.N * a.G;
+  __shared__ unsigned long long cost[2];  // of the lists, in ns of an SM
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, threads = blockDim.x, NG = a.N * a.G;
+  const bool one = a.B <= threads;
+  if (tid < 2) cost[tid] = 0ull;
+  unsigned long long cost_a = 0ull, cost_b = 0ull;
   grid_dep_wait();
-  for (int g = tid; g < a.groups; g += kPlanThreads) count[g] = 0;
+  grid_dep_launch();
+  // (a sequence's group and lengths are on their way at the same time)
+  Sequence own{};
+  int group = tid < a.B ? a.of[tid] : -1, kv_len = tid < a.B ? a.kv_len[tid] : 0, q_len = a.q_len != nullptr && tid < a.B ? a.q_len[tid] : a.N;
+  for (int g = tid; g < a.groups; g += threads) {
+    count[g] = 0;
+    tokens[g] = min(max(0, a.len[g]), a.cap) / a.page * a.page;
+  }
+  __syncthreads();
   // ---- each sequence's place in its group, in the order of the batch
-  for (int b0 = 0; b0 < a.B; b0 += kPlanThreads) {
+  for (int b0 = 0; b0 < a.B; b0 += threads) {
     const int b = b0 + tid;
-    rank[tid] = b < a.B ? sequence(a, b).group : -1;
+    own.group = -1;
+    if (b < a.B) own = b0 == 0 ? sequence(a, tokens, group, kv_len, q_len) : sequence(a, tokens, b);
+    rank[tid] = own.group;
     __syncthreads();
     if (warp == 0)
-      for (int c = 0; c < kPlanThreads && b0 + c < a.B; c += 32) {
+      for (int c = 0; c < threads && b0 + c < a.B; c += 32) {
         const int g = rank[c + lane];
         const unsigned same = __match_any_sync(0xffffffffu, g);
         const int before = g >= 0 ? count[g] : 0, r = before + __popc(same & ((1u << lane) - 1));
@@ -97,19 +123,22 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
         __syncwarp();
       }
     __syncthreads();
-    if (b < a.B) a.seq[b] = make_int4(0, rank[tid], 0, 0);
-    __syncthreads();
+    if (!one) {
+      if (b < a.B) a.seq[b] = make_int4(0, rank[tid], 0, 0);
+      __syncthreads();
+    }
   }
   // ---- groups: their sequences' places in the list, their entries
   int at_member = 0, at_a = 0, at_b = a.B * a.tiles_b;  // list B begins with the sequences' own tokens
-  for (int g0 = 0; g0 < a.groups; g0 += kPlanThreads) {
+  for (int g0 = 0; g0 < a.groups; g0 += threads) {
     const int g = g0 + tid;
     int n = g < a.groups ? count[g] : 0;
     if (n < 2) n = 0;  // alone, it shares nothing
     const long long rows = static_cast<long long>(n) * NG;
     const bool small = a.few && rows <= 16;
     const int per = small ? a.rows_b : a.rows_a, tiles = static_cast<int>((rows + per - 1) / per);
-    int v[3] = {n, small ? 0 : tiles, small ? tiles : 0}, incl[3];
+    const int v[3] = {n, small ? 0 : tiles, small ? tiles : 0};
+    int incl[3], total[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       incl[k] = v[k];
@@ -121,11 +150,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       if (lane == 31) sums[k][warp] = incl[k];
     }
     __syncthreads();
-    int total[3];
 #pragma unroll
     for (int k = 0; k < 3; ++k) {
       int before = 0, sum = 0;
-      for (int w = 0; w < kPlanThreads / 32; ++w) {
+      for (int w = 0; w < threads >> 5; ++w) {
         if (w < warp) before += sums[k][w];
         sum += sums[k][w];
       }
@@ -137,9 +165,14 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       start[g] = at_member + incl[0];
       base[g] = small ? at_b + incl[2] : at_a + incl[1];
       if (n > 0) {
-        const int tokens = prefix_tokens(a, g);
+        const int seen = tokens[g];
         SharedEntry* const to = small ? a.entry_b : a.entry_a;
-        for (int t = 0; t < tiles; ++t) to[base[g] + t] = make_entry(first[g], t * per, tokens, 0, tokens, start[g], n, 0);
+        const unsigned long long steps = static_cast<unsigned long long>(tiles) * ((seen + 127) >> 7);
+        if (small)
+          cost_b += steps * a.step_b + static_cast<unsigned long long>(tiles) * a.start_b;
+        else
+          cost_a += steps * a.step_a + static_cast<unsigned long long>(tiles) * a.start_a;
+        for (int t = 0; t < tiles; ++t) to[base[g] + t] = make_entry(first[g], t * per, seen, 0, seen, start[g], n, 0);
       }
     }
     at_member += total[0];
@@ -147,17 +180,13 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     at_b += total[2];
     __syncthreads();
   }
-  if (tid == 0) {
-    a.entries[0] = at_a;
-    a.entries[1] = at_b;
-  }
   // ---- sequences: their own tokens
-  for (int b = tid; b < a.B; b += kPlanThreads) {
-    const Sequence s = sequence(a, b);
+  for (int b = tid; b < a.B; b += threads) {
+    const Sequence s = one ? own : sequence(a, tokens, b);
     int4 to = make_int4(0, 0, 0, 0);
     int prefix = 0;
     if (s.group >= 0 && count[s.group] > 0) {
-      const int r = a.seq[b].y;
+      const int r = one ? rank[tid] : a.seq[b].y;
       prefix = s.prefix;
       a.member[start[s.group] + r] = b;
       to = make_int4(a.few && static_cast<long long>(count[s.group]) * NG <= 16 ? 2 : 1, r * NG, base[s.group], 0);
@@ -168,9 +197,33 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
       const int row0 = t * a.rows_b, rows = min(a.rows_b, s.ql * a.G - row0);
       const int seen = rows <= 0 ? 0 : a.causal ? max(0, kv - s.ql + (row0 + rows - 1) / a.G + 1) : kv;
       a.entry_b[b * a.tiles_b + t] = make_entry(b, row0, kv, s.ql, seen, -1, to.x == 0 ? 1 : 0, prefix / a.page);
+      cost_b += static_cast<unsigned long long>(max(1, (seen + 127) >> 7)) * a.step_b + a.start_b;
     }
   }
-  grid_dep_launch();
+  // ---- how many SMs each list has
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    cost_a += __shfl_xor_sync(0xffffffffu, cost_a, o);
+    cost_b += __shfl_xor_sync(0xffffffffu, cost_b, o);
+  }
+  if (lane == 0) {
+    atomicAdd(&cost[0], cost_a);
+    atomicAdd(&cost[1], cost_b);
+  }
+  __syncthreads();
+  if (tid == 0) {
+    // list A's CTAs take some 3 us more for their beginning and end; both end together where cost_a / n + 3 us
+    // = cost_b / (sms - n)
+    const float fa = static_cast<float>(cost[0]) * a.HK, fb = static_cast<float>(cost[1]) * a.HK;
+    float x = a.sms * fa / (fa + fb);
+#pragma unroll 1
+    for (int k = 0; k < 4; ++k) x = fa / fmaxf((fa + fb + 3000.f * x) / a.sms - 3000.f, fa / a.sms);
+    const int n = at_a == 0 ? 0 : max(1, min(min(a.ctas_a, a.sms - 1), static_cast<int>(x + 0.5f)));
+    a.entries[0] = at_a;
+    a.entries[1] = n;
+    a.entries[2] = at_b;
+    a.entries[3] = (a.sms - n) * a.per_sm_b;
+  }
 }
 
 // One list's parts, as the kernels leave them.
@@ -188,11 +241,11 @@ struct JoinLaunch {
 };
 
 // The parts of every row of O whose units have not written it: a warp a row. Lane q looks up the
-// q-th part and its weight, then each lane sums 4 channels, eight parts in flight. Bound: latency
+// q-th part and its weight, then each lane sums 4 channels, four parts in flight. Bound: latency
 // and the L2 cache (a part is 4 D + 8 bytes a row).
 template <int D>
-__global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
-  constexpr int kBatch = 8;
+__global__ void __launch_bounds__(256, 4) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
+  constexpr int kBatch = 4;
   const int lane = threadIdx.x & 31;
   const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
   const int bh = static_cast<int>(row / a.N), i = static_cast<int>(row - static_cast<long long>(bh) * a.N);
@@ -282,32 +335,57 @@ __global__ void __launch_bounds__(256) shared_join_kernel(const __grid_constant_
   if (lane == 0) a.lse[row] = none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
 }
 
+// What a step and the beginning of a unit take of an SM, in ns, both lists at work (least squares over the CTAs of 64
+// to 256 sequences with 50 to 2000 tokens of their own behind prefixes of 8192 to 32768; two or three CTAs of
+// few rows share an SM).
+struct ListCost {
+  int step, start;
+};
+ListCost tile_cost(int d, int rows) {
+  if (rows == 256) return ListCost{d == 128 ? 1800 : 1500, 9000};
+  return ListCost{rows == 128 ? (d == 128 ? 1570 : 1250) : d == 128 ? 1080 : 930, 4000};
+}
+ListCost few_cost(int d, int rows) {
+  if (d == 128) return rows <= 8 ? ListCost{430, 1100} : ListCost{530, 2000};
+  return rows <= 8 ? ListCost{300, 400} : ListCost{410, 1100};
+}
+
 // Rows of a unit and CTAs of both lists, and the workspace.
 struct SharedPlan {
-  bool plain;  // as fa_cache_attention
-  int rows_a, rows_b, tiles_b, ctas_a, ctas_b, lead_b;
+  bool plain;   // as fa_cache_attention
+  bool only_b;  // list A is empty: no group has more than 16 rows
+  int rows_a, rows_b, tiles_b, ctas_a, ctas_b, lead_a, lead_b;
   long long max_a, max_b;  // entries
   size_t entry_a, entry_b, member, seq, unit_a, unit_b, m_a, l_a, o_a, m_b, l_b, o_b, total;
 };
 SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_width, int groups) {
   SharedPlan p{};
   const long long NG = static_cast<long long>(N) * G, cap = static_cast<long long>(table_width) * page;
-  p.plain = NG > 128 || B < 2;
+  const AttnPlan own = attn_plan(B, HK, NG, cap, d);
+  const bool few = own.rows <= 16;
+  // Sharing takes some 20 us whatever there is to do (the plan, a tile kernel's beginning and end, the join): not
+  // where the table has room for few steps a CTA without it. GPU time in us, shared and plain, one group
+  // with 128 tokens of its own a sequence: 8 rows at d = 128, 15 steps 24.7, 22.6, 28 steps 28.1, 33.0; at d = 64 7 steps 21.1,
+  // 16.5, 14 steps 24.4, 25.5; 16 rows, 8 steps 28.4, 24.0, 14 steps 29.6, 30.8; 40 rows, 14 steps 35.8, 27.8, 27 steps 44.1, 42.3; 80 rows,
+  // 28 steps 43.0, 32.3, 55 steps 51.1, 49.6.
+  const long long sms = sm_count(), most_b = few ? static_cast<long long>(few_row_ctas(d, own.rows)) * sms : sms;
+  const bool brief = own.units * own.cap_steps <= (few ? (own.rows > 8 ? 13 : d == 64 ? 11 : 18) : NG <= 64 ? 29 : 58) * most_b;
+  p.plain = NG > 128 || B < 2 || brief;
   if (p.plain) {
     p.total = cache_attention_workspace(B, HK, G, N, d, page, table_width);
     return p;
   }
-  const AttnPlan own = attn_plan(B, HK, NG, cap, d);
-  const AttnPlan pre = attn_plan(groups < B ? groups : B, HK, (B + groups - 1) / groups * NG, cap, d);
-  const bool few = own.rows <= 16;
   p.rows_b = own.rows;
-  p.lead_b = own.lead;
+  p.lead_b = !few ? own.lead : d == 64 && p.rows_b <= 8 ? 2 : 3;
+  p.lead_a = p.rows_a == 256 ? 6 : 3;
+  p.only_b = few && B * NG <= 16;
   p.tiles_b = static_cast<int>((NG + p.rows_b - 1) / p.rows_b);
-  p.rows_a = pre.rows <= 16 ? 64 : pre.rows;
+  // (with the other SMs at work on list B, few steps a CTA are no reason for smaller tiles)
+  const long long rows_of_group = (B + groups - 1) / groups * NG;
+  p.rows_a = rows_of_group <= 64 ? 64 : rows_of_group <= 128 ? 128 : 256;
   const long long pairs = groups < B / 2 ? groups : B / 2;  // groups of two and more
   p.max_a = B * NG / p.rows_a + pairs;
   p.max_b = static_cast<long long>(B) * p.tiles_b + (few ? B * NG / p.rows_b + pairs : 0);
-  const long long sms = sm_count(), most_b = few ? static_cast<long long>(few_row_ctas(d, p.rows_b)) * sms : sms;
   const long long steps = (cap + 127) / 128;
   p.ctas_a = static_cast<int>(p.max_a * HK >= sms || p.max_a * HK * steps >= sms ? sms : p.max_a * HK * steps);
   p.ctas_b = static_cast<int>(p.max_b * HK >= most_b || p.max_b * HK * steps >= most_b ? most_b : p.max_b * HK * steps);
@@ -340,7 +418,7 @@ cudaError_t launch_shared(const CacheAttnLaunch& a, const AttnGrid& ga, const At
   auto tiles = [&](const AttnGrid& g, int ctas) {
     return INT8 ? launch_shared_tiles_int8(a, g, ctas, stream) : launch_shared_tiles_e4m3(a, g, ctas, stream);
   };
-  cudaError_t e = tiles(ga, p.ctas_a);
+  cudaError_t e = p.only_b ? cudaSuccess : tiles(ga, p.ctas_a);
   if (e != cudaSuccess) return e;
   e = p.rows_b > 16  ? tiles(gb, p.ctas_b)
       : p.rows_b > 8 ? launch_rows<D, 2, INT8, true>(a, gb, p.ctas_b, stream)
@@ -373,6 +451,15 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   pl.rows_b = p.rows_b;
   pl.tiles_b = p.tiles_b;
   pl.few = p.rows_b <= 16;
+  pl.HK = a.c.H;
+  pl.sms = sm_count();
+  pl.ctas_a = p.ctas_a;
+  pl.per_sm_b = pl.few ? few_row_ctas(a.c.d, p.rows_b) : 1;
+  const ListCost ca = tile_cost(a.c.d, p.rows_a), cb = pl.few ? few_cost(a.c.d, p.rows_b) : tile_cost(a.c.d, p.rows_b);
+  pl.step_a = ca.step;
+  pl.start_a = ca.start;
+  pl.step_b = cb.step;
+  pl.start_b = cb.start;
   pl.of = prefix_of;
   pl.len = prefix_len;
   pl.kv_len = a.kv_len;
@@ -382,7 +469,8 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   pl.entry_b = reinterpret_cast<SharedEntry*>(a.ws + p.entry_b);
   pl.member = reinterpret_cast<int*>(a.ws + p.member);
   pl.seq = reinterpret_cast<int4*>(a.ws + p.seq);
-  cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pl);
+  const int most = a.B > groups ? a.B : groups, threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
+  cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(threads), 0, stream, pl);
   if (e != cudaSuccess) return e;
   AttnGrid g{};
   g.B = a.B;
@@ -398,7 +486,7 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   g.member = pl.member;
   AttnGrid ga = g, gb = g;
   ga.rows = p.rows_a;
-  ga.lead = 4;
+  ga.lead = p.lead_a;
   ga.entry = pl.entry_a;
   ga.entries = pl.entries;
   ga.unit_parts = reinterpret_cast<int2*>(a.ws + p.unit_a);
@@ -408,7 +496,8 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   gb.rows = p.rows_b;
   gb.lead = p.lead_b;
   gb.entry = pl.entry_b;
-  gb.entries = pl.entries + 1;
+  gb.entries = pl.entries + 2;
+  gb.late = p.only_b ? 0 : 1;
   gb.unit_parts = reinterpret_cast<int2*>(a.ws + p.unit_b);
   gb.m_part = reinterpret_cast<float*>(a.ws + p.m_b);
   gb.l_part = reinterpret_cast<float*>(a.ws + p.l_b);

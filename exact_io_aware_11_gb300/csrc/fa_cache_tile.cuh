@@ -164,7 +164,7 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       s.want = group && key < ld.x.seen;
       s.h = ld.h;
       s.row = key & (c.page - 1);
-      if (s.want) s.pid = c.table[ld.x.b * c.table_stride + first_column(ld.x) + (key >> c.log2_page)];
+      if (s.want) s.pid = attn_load<SH>(c.table + ld.x.b * c.table_stride + first_column(ld.x) + (key >> c.log2_page));
       ld.next(g);
     }
     return s;
@@ -176,8 +176,17 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
     if (good) {
       const int ph = s.pid * c.H + s.h;
       s.row += ph << c.log2_page;
-      s.ks = c.scale[0][ph];
-      s.vs = c.scale[1][ph];
+      s.ks = attn_load<SH>(c.scale[0] + ph);
+      s.vs = attn_load<SH>(c.scale[1] + ph);
+      // The ring holds a step or two, which does not cover the way from memory while another kernel
+      // keeps that busy: the pages come to the L2 cache two steps before.
+      if constexpr (SH) {
+        if (leader) {
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv)
+            if (L::kLoaders == 1 || kv == loader) l2_prefetch(c.code[kv] + static_cast<long long>(s.row) * D, rows * D);
+        }
+      }
     }
   };
   Step now = look(), next = look();
@@ -514,7 +523,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
     tmem_relinquish();
   }
   tc_fence_before();
-  grid_dep_wait();
+  attn_wait<SH>(g, false);
   grid_dep_launch();
   // its barriers publish the above; the slots of the scales are not in use yet
   AttnCursor<SH> cur = attn_share<L::kThreads, SH>(g, &share, reinterpret_cast<long long*>(smem + L::oScales));
@@ -918,6 +927,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
+  attn_wait<SH>(g, true);
 }
 
 template <int D, int NQ, int REP, bool INT8, bool P16, bool SH>

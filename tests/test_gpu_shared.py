@@ -18,13 +18,14 @@ def i32(x):
     return None if x is None else torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
 
 
-def batch(fa, of, prefix, own, HK, page, d, fmt, seed=0, spread=2):
+def batch(fa, of, prefix, own, HK, page, d, fmt, seed=0, spread=2, wide=True):
     """Sequences b of group of[b] (-1: none) with the whole pages of prefix[of[b]] tokens in common and own[b] tokens behind
-    them; every page holds finite values."""
+    them; every page holds finite values. A call whose table has room for few tokens is that of cache_attention: `wide` gives it
+    room for 2^18, so that all is shared that can be."""
     rng = np.random.default_rng(seed)
     shared = [p // page for p in prefix]
     lens = [own[b] + (shared[g] * page if 0 <= g < len(prefix) else 0) for b, g in enumerate(of)]
-    W = max(1, -(-max(lens) // page)) + 1
+    W = (1 << 18) // page if wide else max(1, -(-max(lens) // page)) + 1
     P = sum(shared) + sum(-(-n // page) for n in own) + 5
     m = Model(fa, P, HK, page, d, fmt, 1, 1, seed)
     for n in "kv":
@@ -95,12 +96,12 @@ def test_sizes(fa, B, groups, HK, G, N, prefix, own, d, page, fmt):
 
 
 @pytest.mark.parametrize("N,G", [(1, 1), (5, 4), (1, 12), (30, 3)])
-@pytest.mark.parametrize("causal", [True, False])
-def test_any_lengths(fa, N, G, causal):
+@pytest.mark.parametrize("causal,wide", [(True, True), (False, True), (True, False)])
+def test_any_lengths(fa, N, G, causal, wide):
     """Padded rows, sequences that end within or before their prefix, prefixes past the table or negative, no tokens at all."""
     of = [0, 0, 0, 0, 0, 0, 1, 1, 2, 2, 3, 3, -9, 99]
     prefix = [330, 10 ** 9, -5, 15]
-    m, lens = batch(fa, of, [330, 64, 0, 0], [N + 20, N, 1, 40, 7, 30, N + 1, N + 1, 30, 5, 40, 41, 8, 50], 2, 32, 128, "e4m3", seed=3)
+    m, lens = batch(fa, of, [330, 64, 0, 0], [N + 20, N, 1, 40, 7, 30, N + 1, N + 1, 30, 5, 40, 41, 8, 50], 2, 32, 128, "e4m3", seed=3, wide=wide)
     m.table[7] = m.table[6]                              # group 1: the whole table is shared
     lens[7] = lens[6]
     qlens = [N, min(N, 2), N, 0, N // 2, N + 7, N, N, N, 1, N, 0, N, N]
@@ -182,6 +183,7 @@ def test_outputs_workspace_and_a_table_in_a_wider_one(fa):
     of, prefix = [0, 0, 1, 0, 1], [200, 90]
     m, lens = batch(fa, of, prefix, [30, 1, 17, 64, 5], 2, 16, 64, "int8", seed=6)
     W = m.table.shape[1]
+    assert W == 1 << 14
     wide = torch.full((5, W + 9), 10 ** 8, dtype=torch.int32)
     wide[:, 4:4 + W] = m.table
     q = queries(5, 6, 1, 64, "fp16", 11, "bnhd")
@@ -206,7 +208,7 @@ def test_offsets_past_32_bits(fa):
     g = torch.Generator(device="cuda").manual_seed(1)
     for t in (cache.k, cache.v):
         t[P - 9:] = torch.randint(-9, 10, (9, HK, page, d), generator=g, device="cuda", dtype=torch.int8)
-    table = torch.full((20, 9), -1, dtype=torch.int32)
+    table = torch.full((20, 300), -1, dtype=torch.int32)
     table[:, :7] = torch.arange(P - 7, P)
     table[:, 7] = P - 8
     table = table.cuda()
@@ -223,11 +225,23 @@ def test_offsets_past_32_bits(fa):
     assert torch.equal(cache.k[dst], cache.k[src]) and torch.equal(cache.v[dst], cache.v[src])
 
 
+def test_few_tokens_are_the_plain_attention(fa):
+    """Where the table has room for few tokens, and where a sequence has more than 128 rows to a cache head, nothing is shared."""
+    of, prefix = [0] * 6, [96]
+    for N, wide in ((1, False), (130, True)):
+        m, lens = batch(fa, of, prefix, [N + 7 * b for b in range(6)], 1, 32, 64, "e4m3", seed=8, wide=wide)
+        q, table = queries(6, 1, N, 64, "bf16", 13), m.table.cuda()
+        o, lse = check_shared(fa, m, q, lens, of, prefix)
+        want = fa.cache_attention(q, m.cache, table, i32(lens))
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert fa.cache_attention_shared_workspace_bytes(m.cache, 6, 1, N, table.shape[1], 1) == fa.cache_attention_workspace_bytes(m.cache, 6, 1, N, table.shape[1])
+
+
 # ------------------------------------------------------------------ together
 def test_a_serving_run(fa):
     """Prompts written, samples forked from them, tokens written and attended over by both attentions, some samples dropped, the
     pool moved together in between, in two layers: every sequence reads back what was written to it."""
-    page, HK, H, d, P, S, W = 16, 2, 4, 64, 200, 12, 14
+    page, HK, H, d, P, S, W = 16, 2, 4, 64, 200, 12, 9000
     caches = [fa.KVCache.empty(P, HK, d, page, dtype=torch.int8) for _ in range(2)]
     table, refs = torch.full((S, W), -1, dtype=torch.int32, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda")
     rng = np.random.default_rng(0)
@@ -302,7 +316,7 @@ def test_a_serving_run(fa):
 def test_a_captured_step_is_replayed_with_other_lengths(fa, groups):
     """Reserve, write and attend in one graph, replayed token by token; the sequences' pages come from the pool as they grow.
     A second graph shares the workspaces and runs after the first."""
-    B, HK, H, d, page, P, W = 6, 2, 8, 64, 16, 120, 12
+    B, HK, H, d, page, P, W = 6, 2, 8, 64, 16, 120, 9000
     cache = fa.KVCache.empty(P, HK, d, page)
     table, refs = torch.full((B, W), -1, dtype=torch.int32, device="cuda"), torch.zeros(P, dtype=torch.int32, device="cuda")
     of = [b % groups for b in range(B)]
