@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 
 import torch
 
@@ -59,8 +60,7 @@ SIGNATURES["fa_cache_attention"] = (_I, [_P, _P, _P, ctypes.POINTER(CacheStruct)
                                          ctypes.POINTER(CacheAttentionOptions), _P, _SZ, _P])
 
 SIGNATURES["fa_cache_attention_shared_workspace_bytes"] = (_SZ, [ctypes.POINTER(CacheStruct), _I, _I, _I, _I, _I])
-SIGNATURES["fa_cache_attention_shared"] = (_I, [_P, _P, _P, ctypes.POINTER(CacheStruct), _I, _I, _I,
-                                                ctypes.POINTER(CacheAttentionOptions), _P, _P, _I, _P, _SZ, _P])
+SIGNATURES["fa_cache_attention_shared"] = (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _SZ, _P])  # structs as bytes
 
 # These calls are made once per layer and token: the checks below read each attribute once,
 # and the stream comes from the binding that torch.cuda.current_stream wraps (0.1 us against 2).
@@ -102,6 +102,19 @@ def _rows(t, what, device=None, dtype=None):
 def _check_int(t, what, device, dim):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.device != device or t.dim() != dim:
         raise ValueError(f"{what} must be an int32 tensor of {dim} dimension(s) on the tensors' device")
+
+
+_OPTIONS = struct.Struct("@PqiPPiifqqqqqq")  # CacheAttentionOptions (packed in a quarter of the constructor's time)
+assert _OPTIONS.size == ctypes.sizeof(CacheAttentionOptions)
+
+
+def _ints(t, what, index, n):
+    """The address of a contiguous int32 vector of n values (None: any) on device `index`."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index or t.dim() != 1:
+        raise ValueError(f"{what} must be an int32 vector on the tensors' device")
+    if (n is not None and t.shape[0] != n) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and have {n} values")
+    return t.data_ptr()
 
 
 def _check_lengths(t, what, device, B):
@@ -283,6 +296,7 @@ class KVCache:
         self._struct = CacheStruct(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), P, H, page, d,
                                    _FORMATS[k.dtype])
         self._bytes = bytes(self._struct)  # several layers' structs are put together from these
+        self._index = k.device.index
 
     @classmethod
     def empty(cls, num_pages: int, heads: int, head_dim: int, page_size: int = 64, dtype=torch.float8_e4m3fn, device="cuda"):
@@ -369,8 +383,7 @@ def cache_attention(q, cache: KVCache, page_table, kv_len, q_len=None, causal: b
                workspace, split)
 
 
-def _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse):
-    """What both attention calls check and allocate: out, lse and the arguments that describe them."""
+def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, lse, workspace, split):
     dev = cache.device
     n, qs = _rows(q, "q", dev)
     B, H, N, d = n
@@ -385,27 +398,18 @@ def _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse
         lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
     elif lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, H, N] on the tensors' device")
-    opt = CacheAttentionOptions(table, table_stride, pages, kl, ql, 1 if causal else 0, _DTYPES[q.dtype],
-                                d ** -0.5 if scale is None else scale, *qs, *os)
-    return o, lse, opt, (q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache._struct, B, H, N, opt)
-
-
-def _check_workspace(workspace, dev):
-    if not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
-    return workspace.numel() * workspace.element_size()
-
-
-def _cache_attention(q, cache, page_table, kv_len, q_len, causal, scale, out, lse, workspace, split):
-    dev = cache.device
-    o, lse, opt, args = _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse)
     L = lib()
     if workspace is not None:
-        need = _check_workspace(workspace, dev) if split else 0
+        if workspace.device != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
+        need = workspace.numel() * workspace.element_size() if split else 0
     else:
-        need = L.fa_cache_attention_workspace_bytes(cache._struct, *args[4:7], opt.table_width) if split else 0
+        need = L.fa_cache_attention_workspace_bytes(cache._struct, B, H, N, pages) if split else 0
         workspace = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
-    _done(L.fa_cache_attention(*args, workspace.data_ptr() if need else None, need, _raw_stream(dev.index)), "fa_cache_attention")
+    opt = CacheAttentionOptions(table, table_stride, pages, kl, ql, 1 if causal else 0, _DTYPES[q.dtype],
+                                d ** -0.5 if scale is None else scale, *qs, *os)
+    _done(L.fa_cache_attention(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache._struct, B, H, N, opt,
+                               workspace.data_ptr() if need else None, need, _raw_stream(dev.index)), "fa_cache_attention")
     return o, lse
 
 
@@ -427,19 +431,30 @@ def cache_attention_shared(q, cache: KVCache, page_table, kv_len, prefix_of, pre
 
 
 def _cache_attention_shared(q, cache, page_table, kv_len, prefix_of, prefix_len, q_len, causal, scale, out, lse, workspace):
-    dev = cache.device
-    o, lse, opt, args = _attention_args(q, cache, page_table, kv_len, q_len, causal, scale, out, lse)
-    of = _check_lengths(prefix_of, "prefix_of", dev, args[4])
-    _check_int(prefix_len, "prefix_len", dev, 1)
-    groups = prefix_len.shape[0]
-    if of is None or groups < 1 or not prefix_len.is_contiguous():
-        raise ValueError("prefix_of must be int32 [B] and prefix_len contiguous int32 [groups]")
+    dev, index = cache.device, cache._index
+    n, qs = _rows(q, "q", dev)
+    B, H, N, d = n
+    if d != cache.head_dim or H % cache.heads:
+        raise ValueError("q must have the cache's d and a multiple of its heads")
+    table, table_stride, pages = _check_table(page_table, dev, B)
+    kl, of = _ints(kv_len, "kv_len", index, B), _ints(prefix_of, "prefix_of", index, B)
+    ql = None if q_len is None else _ints(q_len, "q_len", index, B)
+    pl, groups = _ints(prefix_len, "prefix_len", index, None), prefix_len.shape[0]
+    o, os = _out(out, q, n, "out", dev)
+    if lse is None:
+        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
+    elif lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
+        raise ValueError("lse must be contiguous float32 [B, H, N] on the tensors' device")
     L = lib()
-    if workspace is not None:
-        need = _check_workspace(workspace, dev)
-    else:
-        need = L.fa_cache_attention_shared_workspace_bytes(cache._struct, *args[4:7], opt.table_width, groups)
+    if workspace is None:
+        need = L.fa_cache_attention_shared_workspace_bytes(cache._struct, B, H, N, pages, groups)
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    _done(L.fa_cache_attention_shared(*args, of, prefix_len.data_ptr(), groups, workspace.data_ptr() if need else None, need,
-                                      _raw_stream(dev.index)), "fa_cache_attention_shared")
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
+    else:
+        need = workspace.numel() * workspace.element_size()
+    opt = _OPTIONS.pack(table, table_stride, pages, kl, ql or 0, 1 if causal else 0, _DTYPES[q.dtype],
+                        d ** -0.5 if scale is None else scale, *qs, *os)
+    _done(L.fa_cache_attention_shared(q.data_ptr(), o.data_ptr(), lse.data_ptr(), cache._bytes, B, H, N, opt, of, pl, groups,
+                                      workspace.data_ptr() if need else None, need, _raw_stream(index)), "fa_cache_attention_shared")
     return o, lse

@@ -8,10 +8,11 @@ where a row has no page; refs int32 [num_pages] counts the entries that name eac
 from __future__ import annotations
 
 import ctypes
+import struct
 
 import torch
 
-from ._cache import _I32, _I64, _SZ, KVCache, _check_int, _check_lengths, _done, _on, _raw_stream
+from ._cache import _I32, _I64, _SZ, KVCache, _done, _ints, _on, _raw_stream
 from ._lib import _I, _P, SIGNATURES, lib
 
 
@@ -20,7 +21,9 @@ class PageTableStruct(ctypes.Structure):
     _fields_ = [("entries", _P), ("stride", _I64), ("rows", _I), ("width", _I), ("refs", _P), ("num_pages", _I), ("page_size", _I)]
 
 
-_CACHES, _TABLE = ctypes.c_char_p, ctypes.POINTER(PageTableStruct)  # a host array of fa_cache, as bytes
+_CACHES = _TABLE = ctypes.c_char_p  # a host array of fa_cache, a fa_page_table, as bytes
+_PACK = struct.Struct("@PqiiPii")    # PageTableStruct
+assert _PACK.size == ctypes.sizeof(PageTableStruct)
 SIGNATURES["fa_cache_copy"] = (_I, [_CACHES, _I, _P, _P, _I, _P])
 SIGNATURES["fa_cache_fork"] = (_I, [_TABLE, _P, _P, _P])
 SIGNATURES["fa_cache_reserve_workspace_bytes"] = (_SZ, [_I, _I, _I])
@@ -42,22 +45,26 @@ def _layers(caches):
     if not caches:
         raise ValueError("caches must be a KVCache or a sequence of them, one for each layer")
     first = caches[0]
-    index = first.device.index
+    index = first._index
     for c in caches:
-        if c.device.index != index:
+        if c._index != index:
             raise ValueError("the layers' caches are on different devices")
     return structs, len(caches), first
 
 
-def _table(t, refs, page_size, dev):
-    _check_int(t, "page_table", dev, 2)
-    _check_int(refs, "refs", dev, 1)
-    (rows, width), (stride, one) = t.shape, t.stride()
+def _table(t, refs, page_size, index):
+    """The fa_page_table of a table and its counts, the table's rows and columns, and the pages."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index or t.dim() != 2:
+        raise ValueError("page_table must be an int32 tensor of 2 dimensions on the tensors' device")
+    counts = _ints(refs, "refs", index, None)
+    (rows, width), (stride, one), pages = t.shape, t.stride(), refs.shape[0]
     if rows < 1 or width < 1 or (width > 1 and one != 1):
         raise ValueError("page_table must be [rows, pages per row] with a contiguous last axis")
-    if not refs.is_contiguous():
-        raise ValueError("refs must be contiguous")
-    return PageTableStruct(t.data_ptr(), stride if rows > 1 else 0, rows, width, refs.data_ptr(), refs.shape[0], page_size)
+    return _PACK.pack(t.data_ptr(), stride if rows > 1 else 0, rows, width, counts, pages, page_size), rows, width, pages
+
+
+def _maybe(t, what, index, n):
+    return None if t is None else _ints(t, what, index, n)
 
 
 def _workspace(workspace, need, dev):
@@ -72,9 +79,7 @@ def _workspace(workspace, need, dev):
 def _rows_out(t, n, what, dev):
     if t is None:
         return torch.empty(n, dtype=torch.int32, device=dev)
-    _check_int(t, what, dev, 1)
-    if t.shape[0] != n or not t.is_contiguous():
-        raise ValueError(f"{what} must be contiguous int32 [{n}]")
+    _ints(t, what, dev.index, n)
     return t
 
 
@@ -83,17 +88,13 @@ def cache_copy(caches, src, dst, stream=None) -> None:
     [n] on the device; moves with -1 in either are left out. No page of dst may be another move's
     source or destination."""
     s, n, first = _layers(caches)
-    _on(_copy, first.device, stream, s, n, first.device, src, dst)
+    _on(_copy, first.device, stream, s, n, first._index, src, dst)
 
 
-def _copy(s, layers, dev, src, dst):
-    for t, what in ((src, "src"), (dst, "dst")):
-        _check_int(t, what, dev, 1)
-        if not t.is_contiguous():
-            raise ValueError(f"{what} must be contiguous")
-    if src.shape != dst.shape:
-        raise ValueError("src and dst must have the same length")
-    _done(lib().fa_cache_copy(s, layers, src.data_ptr(), dst.data_ptr(), src.shape[0], _raw_stream(dev.index)), "fa_cache_copy")
+def _copy(s, layers, index, src, dst):
+    a = _ints(src, "src", index, None)
+    n = src.shape[0]
+    _done(lib().fa_cache_copy(s, layers, a, _ints(dst, "dst", index, n), n, _raw_stream(index)), "fa_cache_copy")
 
 
 def cache_fork(page_table, refs, page_size: int, parent=None, keep=None, stream=None) -> None:
@@ -108,12 +109,11 @@ def cache_fork(page_table, refs, page_size: int, parent=None, keep=None, stream=
 
 
 def _fork(page_table, refs, page_size, parent, keep):
-    dev = page_table.device
-    t = _table(page_table, refs, page_size, dev)
+    index = page_table.get_device()
+    t, rows, _, _ = _table(page_table, refs, page_size, index)
     if parent is None and keep is None:
         raise ValueError("give parent, keep or both")
-    p, k = (_check_lengths(x, what, dev, t.rows) for x, what in ((parent, "parent"), (keep, "keep")))
-    _done(lib().fa_cache_fork(t, p, k, _raw_stream(dev.index)), "fa_cache_fork")
+    _done(lib().fa_cache_fork(t, _maybe(parent, "parent", index, rows), _maybe(keep, "keep", index, rows), _raw_stream(index)), "fa_cache_fork")
 
 
 def cache_reserve_workspace_bytes(cache: KVCache, rows: int, pages: int) -> int:
@@ -133,18 +133,18 @@ def cache_reserve(caches, page_table, refs, start, count, ok=None, workspace=Non
 
 
 def _reserve(s, layers, first, page_table, refs, start, count, ok, workspace):
-    dev = first.device
-    t = _table(page_table, refs, first.page_size, dev)
+    dev, index = first.device, first._index
+    t, rows, width, pages = _table(page_table, refs, first.page_size, index)
     tokens = 0
     if not isinstance(count, torch.Tensor):
         if count is None or not 0 <= int(count) < 2 ** 31:
             raise ValueError("count must be int32 [rows] or a number of tokens")
         tokens, count = int(count), None
-    b, c = (_check_lengths(x, what, dev, t.rows) for x, what in ((start, "start"), (count, "count")))
-    ok = _rows_out(ok, t.rows, "ok", dev)
+    b, c = _maybe(start, "start", index, rows), _maybe(count, "count", index, rows)
+    ok = _rows_out(ok, rows, "ok", dev)
     L = lib()
-    workspace, have = _workspace(workspace, L.fa_cache_reserve_workspace_bytes(t.rows, t.width, t.num_pages) if workspace is None else 0, dev)
-    _done(L.fa_cache_reserve(s, layers, t, b, c, tokens, ok.data_ptr(), workspace.data_ptr(), have, _raw_stream(dev.index)), "fa_cache_reserve")
+    workspace, have = _workspace(workspace, L.fa_cache_reserve_workspace_bytes(rows, width, pages) if workspace is None else 0, dev)
+    _done(L.fa_cache_reserve(s, layers, t, b, c, tokens, ok.data_ptr(), workspace.data_ptr(), have, _raw_stream(index)), "fa_cache_reserve")
     return ok
 
 
@@ -163,11 +163,11 @@ def cache_compact(caches, page_table, refs, where=None, live=None, workspace=Non
 
 
 def _compact(s, layers, first, page_table, refs, where, live, workspace):
-    dev = first.device
-    t = _table(page_table, refs, first.page_size, dev)
-    where, live = _rows_out(where, t.num_pages, "where", dev), _rows_out(live, 1, "live", dev)
+    dev, index = first.device, first._index
+    t, _, _, pages = _table(page_table, refs, first.page_size, index)
+    where, live = _rows_out(where, pages, "where", dev), _rows_out(live, 1, "live", dev)
     L = lib()
-    workspace, have = _workspace(workspace, L.fa_cache_compact_workspace_bytes(t.num_pages) if workspace is None else 0, dev)
-    _done(L.fa_cache_compact(s, layers, t, where.data_ptr(), live.data_ptr(), workspace.data_ptr(), have, _raw_stream(dev.index)),
+    workspace, have = _workspace(workspace, L.fa_cache_compact_workspace_bytes(pages) if workspace is None else 0, dev)
+    _done(L.fa_cache_compact(s, layers, t, where.data_ptr(), live.data_ptr(), workspace.data_ptr(), have, _raw_stream(index)),
           "fa_cache_compact")
     return where, live

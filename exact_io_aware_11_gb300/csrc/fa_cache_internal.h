@@ -123,7 +123,6 @@ struct PageReserveLaunch {
   int* status;
   // workspace
   int* moves;  // pages to be copied
-  int* slots;  // exchanges between the CTAs
   int* src;    // [rows]
   int* dst;
   int* list;   // free pages
@@ -138,7 +137,6 @@ struct PageCompactLaunch {
   int* status;
   // workspace
   int* moves;
-  int* slots;
   int* src;
   int* dst;
 };

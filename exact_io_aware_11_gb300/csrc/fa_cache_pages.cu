@@ -195,11 +195,17 @@ __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const __grid_co
   }
 }
 
-// ------------------------------------------------------------------ a cluster of CTAs that counts
-constexpr int kCluster = 8, kCountThreads = 512;
+// ------------------------------------------------------------------ CTAs that count
+// One CTA for pools of up to 8192 pages, a cluster of eight for others.
+constexpr int kCluster = 8, kSmallPool = 8192;
+constexpr int count_threads(int ctas) { return ctas == 1 ? 1024 : 512; }
 
+template <int C>
 __device__ __forceinline__ void cluster_sync() {
-  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+  if constexpr (C == 1)
+    __syncthreads();
+  else
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ int load_l2(const int* p) {
   int v;
@@ -207,7 +213,8 @@ __device__ __forceinline__ int load_l2(const int* p) {
   return v;
 }
 
-// Exclusive prefix of v over the CTA's threads, and the sum. `part`: kCountThreads / 32 words.
+// Exclusive prefix of v over the CTA's threads, and the sum. `part`: a word a warp.
+template <int C>
 __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = v;
@@ -219,25 +226,37 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
   __syncthreads();  // part's last values have been read
   if (lane == 31) part[warp] = incl;
   __syncthreads();
-  int before = 0, sum = 0;
+  int p = lane < count_threads(C) / 32 ? part[lane] : 0, sum = p;
 #pragma unroll
-  for (int w = 0; w < kCountThreads / 32; ++w) {
-    const int p = part[w];
-    if (w < warp) before += p;
-    sum += p;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += u;
   }
-  *total = sum;
-  return before + incl - v;
+  *total = __shfl_sync(0xffffffffu, sum, 31);
+  return __shfl_sync(0xffffffffu, sum - p, warp) + incl - v;
 }
-// Each CTA's v, exchanged through `slot` (kCluster words of global memory, written by nobody
-// else meanwhile): what the CTAs before this one have, and all. A barrier of the cluster.
+// Each CTA's v written to `slot` (a word a CTA of shared memory, used once) of all; a barrier of the cluster.
+template <int C>
+__device__ __forceinline__ void exchange(int v, int* slot, int rank) {
+  if constexpr (C > 1) {
+    if (threadIdx.x < C) {
+      uint32_t to;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(to) : "r"(smem_u32(slot + rank)), "r"(threadIdx.x));
+      asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(to), "r"(v) : "memory");
+    }
+  } else if (threadIdx.x == 0) {
+    slot[0] = v;
+  }
+  cluster_sync<C>();
+}
+// What the CTAs before this one have of v, and all.
+template <int C>
 __device__ __forceinline__ int cluster_scan(int v, int* slot, int rank, int* total) {
-  if (threadIdx.x == 0) slot[rank] = v;
-  cluster_sync();
+  exchange<C>(v, slot, rank);
   int before = 0, sum = 0;
 #pragma unroll
-  for (int r = 0; r < kCluster; ++r) {
-    const int x = load_l2(slot + r);
+  for (int r = 0; r < C; ++r) {
+    const int x = slot[r];
     if (r < rank) before += x;
     sum += x;
   }
@@ -248,31 +267,33 @@ __device__ __forceinline__ int cluster_scan(int v, int* slot, int rank, int* tot
 struct PageSlice {
   int first, end;
 };
+template <int C>
 __device__ __forceinline__ PageSlice page_slice(int num_pages, int rank) {
-  const int per = ((num_pages + kCluster - 1) / kCluster + 3) & ~3;
+  const int per = ((num_pages + C - 1) / C + 3) & ~3;
   const long long f = static_cast<long long>(per) * rank;
   return PageSlice{static_cast<int>(min(f, static_cast<long long>(num_pages))),
                    static_cast<int>(min(f + per, static_cast<long long>(num_pages)))};
 }
 // Pages p of the slice with want(p, refs[p]), counted.
-template <typename Want>
+template <int C, typename Want>
 __device__ __forceinline__ int count_pages(const PageSlice& s, const int* refs, int* part, Want want) {
   int mine = 0, total;
-  for (int p = s.first + threadIdx.x; p < s.end; p += kCountThreads) mine += want(p, load_l2(refs + p)) ? 1 : 0;
-  block_scan(mine, part, &total);
+#pragma unroll 4
+  for (int p = s.first + threadIdx.x; p < s.end; p += count_threads(C)) mine += want(p, load_l2(refs + p)) ? 1 : 0;
+  block_scan<C>(mine, part, &total);
   return total;
 }
 // The same pages, in order: the k-th, from `rank0` on, goes to list[k] where k < most.
-template <typename Want>
+template <int C, typename Want>
 __device__ __forceinline__ void list_pages(const PageSlice& s, const int* refs, int* part, int rank0, int most, int* list, Want want) {
-  for (int p0 = s.first; p0 < s.end && rank0 < most; p0 += 4 * kCountThreads) {
+  for (int p0 = s.first; p0 < s.end && rank0 < most; p0 += 4 * count_threads(C)) {
     const int p = p0 + 4 * threadIdx.x;
     int w = 0;
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (p + i < s.end && want(p + i, load_l2(refs + p + i))) w |= 1 << i;
     int total;
-    int k = rank0 + block_scan(__popc(w), part, &total);
+    int k = rank0 + block_scan<C>(__popc(w), part, &total);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (w >> i & 1) {
@@ -294,15 +315,19 @@ constexpr int kItemCache = 4096;  // items of a CTA that are kept in shared memo
 enum : int { kTakes = 0, kOwn = 1, kShared = 2, kKeeps = 3 };  // kShared: takes one, once the keepers are known
 constexpr int reserve_smem(int rows) { return kItemCache * 8 + (2 * rows + 1) * 4; }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads)
+template <int C>
+__global__ void __launch_bounds__(count_threads(C), 1)
     page_reserve_kernel(const __grid_constant__ PageReserveLaunch a) {
   extern __shared__ int2 cache[];  // row and state, entry
-  __shared__ int part[kCountThreads / 32];
+  constexpr int kThreads = count_threads(C);
+  __shared__ int part[kThreads / 32];
+  __shared__ int slots[5][C];  // of the exchanges
   __shared__ int fail_row, any_shared;
   const PageTable& t = a.t;
-  const int rank = blockIdx.x;  // the grid is one cluster
+  const int rank = C == 1 ? 0 : blockIdx.x;  // the grid is one cluster
   int* const first_item = reinterpret_cast<int*>(cache + kItemCache);  // [rows + 1]
   int* const first_col = first_item + t.rows + 1;                      // [rows]
+  cluster_sync<C>();  // every CTA has begun: its shared memory may be written to
   grid_dep_wait();
   if (threadIdx.x == 0) {
     fail_row = t.rows;
@@ -311,7 +336,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
   }
   // ---- the rows' ranges: every CTA has all of them
   int all_items = 0;
-  for (int r0 = 0; r0 < t.rows; r0 += kCountThreads) {
+  for (int r0 = 0; r0 < t.rows; r0 += kThreads) {
     const int b = r0 + threadIdx.x;
     int n = 0;
     if (b < t.rows) {
@@ -324,14 +349,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
       if (rank == 0) a.ok[b] = fits ? 1 : 0;
     }
     int total;
-    const int k = block_scan(n, part, &total);
+    const int k = block_scan<C>(n, part, &total);
     if (b < t.rows) first_item[b] = all_items + k;
     all_items += total;
   }
   if (threadIdx.x == 0) first_item[t.rows] = all_items;
   __syncthreads();
-  const int item0 = static_cast<int>(static_cast<long long>(all_items) * rank / kCluster);
-  const int items = static_cast<int>(static_cast<long long>(all_items) * (rank + 1) / kCluster) - item0;
+  const int item0 = static_cast<int>(static_cast<long long>(all_items) * rank / C);
+  const int items = static_cast<int>(static_cast<long long>(all_items) * (rank + 1) / C) - item0;
   struct Item {
     int row, col, entry, state;
   };
@@ -364,11 +389,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
   // ---- what each item has
   constexpr int kAtOnce = 4;
   int mine = 0;
-  for (int i0 = 0; i0 < items; i0 += kAtOnce * kCountThreads) {
+  for (int i0 = 0; i0 < items; i0 += kAtOnce * kThreads) {
     int row[kAtOnce], entry[kAtOnce], refs[kAtOnce];
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int i = i0 + k * kCountThreads + threadIdx.x;
+      const int i = i0 + k * kThreads + threadIdx.x;
       row[k] = 0;
       entry[k] = -1;
       if (i < items) {
@@ -380,7 +405,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
     for (int k = 0; k < kAtOnce; ++k) refs[k] = is_page(entry[k], t.num_pages) ? load_l2(t.refs + entry[k]) : 0;
 #pragma unroll
     for (int k = 0; k < kAtOnce; ++k) {
-      const int i = i0 + k * kCountThreads + threadIdx.x;
+      const int i = i0 + k * kThreads + threadIdx.x;
       if (i >= items) continue;
       int state = kTakes;
       if (is_page(entry[k], t.num_pages))
@@ -393,29 +418,36 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
     }
   }
   int need, wanted, have, all_free = 0, free_before = 0;
-  block_scan(mine, part, &need);
-  if (threadIdx.x == 0) a.slots[3 * kCluster + rank] = any_shared;
-  int before = cluster_scan(need, a.slots, rank, &wanted);
+  block_scan<C>(mine, part, &need);
+  // (need is at most the pages of the table's rows, 2^30: a bit is left for any_shared)
+  exchange<C>(need | (any_shared != 0 ? 1 << 31 : 0), slots[0], rank);
+  int before = 0;
   bool shared = false;
+  wanted = 0;
 #pragma unroll
-  for (int r = 0; r < kCluster; ++r) shared |= load_l2(a.slots + 3 * kCluster + r) != 0;
+  for (int r = 0; r < C; ++r) {
+    const int v = slots[0][r];
+    shared |= v < 0;
+    if (r < rank) before += v & 0x7fffffff;
+    wanted += v & 0x7fffffff;
+  }
   // whether item i takes a page; final once `shared` has been dealt with
   auto takes = [&](const Item& x, int i) {
     return x.state == kTakes || (x.state == kShared && (i < kItemCache || load_l2(t.refs + x.entry) != code(i)));
   };
   if (shared) {
     // ---- such items off their pages' counts; pages that nobody else has: the last item keeps them
-    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    for (int i = threadIdx.x; i < items; i += kThreads) {
       const Item x = item(i);
       if (x.state == kShared) atomicAdd(t.refs + x.entry, -1);
     }
-    cluster_sync();
-    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    cluster_sync<C>();
+    for (int i = threadIdx.x; i < items; i += kThreads) {
       const Item x = item(i);
       if (x.state == kShared && load_l2(t.refs + x.entry) <= 0) atomicMin(t.refs + x.entry, code(i));
     }
-    cluster_sync();
-    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    cluster_sync<C>();
+    for (int i = threadIdx.x; i < items; i += kThreads) {
       const Item x = item(i);
       if (x.state != kShared) continue;
       if (load_l2(t.refs + x.entry) != code(i))
@@ -423,39 +455,38 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
       else if (i < kItemCache)
         cache[i].x = x.row << 2 | kKeeps;
     }
-    block_scan(mine, part, &need);
-    before = cluster_scan(need, a.slots + 4 * kCluster, rank, &wanted);
+    block_scan<C>(mine, part, &need);
+    before = cluster_scan<C>(need, slots[1], rank, &wanted);
   }
   int f = t.rows;  // the first row that fails
   if (wanted > 0) {  // the same in every CTA
     auto is_free = [](int, int refs) { return refs == 0; };
-    const PageSlice s = page_slice(t.num_pages, rank);
-    have = count_pages(s, t.refs, part, is_free);
-    free_before = cluster_scan(have, a.slots + kCluster, rank, &all_free);
+    const PageSlice s = page_slice<C>(t.num_pages, rank);
+    have = count_pages<C>(s, t.refs, part, is_free);
+    free_before = cluster_scan<C>(have, slots[2], rank, &all_free);
     if (wanted > all_free) {
       int k0 = before;
-      for (int i0 = 0; i0 < items; i0 += kCountThreads) {
+      for (int i0 = 0; i0 < items; i0 += kThreads) {
         const int i = i0 + threadIdx.x;
         Item x{};
         const bool take = i < items && (x = item(i), takes(x, i));
         int total;
-        const int k = k0 + block_scan(take ? 1 : 0, part, &total);
+        const int k = k0 + block_scan<C>(take ? 1 : 0, part, &total);
         if (take && k >= all_free) atomicMin(&fail_row, x.row);
         k0 += total;
       }
       __syncthreads();
-      if (threadIdx.x == 0) a.slots[2 * kCluster + rank] = fail_row;
-      cluster_sync();
+      exchange<C>(fail_row, slots[3], rank);
 #pragma unroll
-      for (int r = 0; r < kCluster; ++r) f = min(f, load_l2(a.slots + 2 * kCluster + r));
+      for (int r = 0; r < C; ++r) f = min(f, slots[3][r]);
     }
-    list_pages(s, t.refs, part, free_before, min(wanted, all_free), a.list, is_free);
-    cluster_sync();
+    list_pages<C>(s, t.refs, part, free_before, min(wanted, all_free), a.list, is_free);
+    cluster_sync<C>();
   }
   // ---- pages dealt out
   if (shared || wanted > 0) {
     int k0 = before;
-    for (int i0 = 0; i0 < items; i0 += kCountThreads) {
+    for (int i0 = 0; i0 < items; i0 += kThreads) {
       const int i = i0 + threadIdx.x;
       Item x{};
       bool take = false;
@@ -464,7 +495,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
         take = takes(x, i);
       }
       int total;
-      const int k = k0 + block_scan(take ? 1 : 0, part, &total), b = x.row;
+      const int k = k0 + block_scan<C>(take ? 1 : 0, part, &total), b = x.row;
       // (below, the rows that fail come back to their pages' counts)
       if (!take && (x.state == kKeeps || x.state == kShared)) t.refs[x.entry] = b < f ? 1 : 0;
       if (take && b < f) {
@@ -482,13 +513,13 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
     }
   }
   if (f < t.rows) {
-    cluster_sync();
-    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    cluster_sync<C>();
+    for (int i = threadIdx.x; i < items; i += kThreads) {
       const Item x = item(i);
       if ((x.state == kShared || x.state == kKeeps) && x.row >= f) atomicAdd(t.refs + x.entry, 1);
     }
-    cluster_sync();
-    for (int i = threadIdx.x; i < items; i += kCountThreads) {
+    cluster_sync<C>();
+    for (int i = threadIdx.x; i < items; i += kThreads) {
       const Item x = item(i);
       if (x.row >= f && x.state != kOwn && (x.state == kTakes || load_l2(t.refs + x.entry) != 1)) a.ok[x.row] = 0;
     }
@@ -499,28 +530,32 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads
 // ------------------------------------------------------------------ compacting
 // L pages are in use. The k-th of them with a number >= L goes to the k-th free number below L, so
 // that no page is read and written, and no more pages move than have to.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kCountThreads)
+template <int C>
+__global__ void __launch_bounds__(count_threads(C), 1)
     page_compact_kernel(const __grid_constant__ PageCompactLaunch a) {
-  __shared__ int part[kCountThreads / 32];
-  const int rank = blockIdx.x, P = a.t.num_pages;
+  constexpr int kThreads = count_threads(C);
+  __shared__ int part[kThreads / 32];
+  __shared__ int slots[3][C];
+  const int rank = C == 1 ? 0 : blockIdx.x, P = a.t.num_pages;
   int* const refs = a.t.refs;
+  cluster_sync<C>();  // every CTA has begun: its shared memory may be written to
   grid_dep_wait();
-  const PageSlice s = page_slice(P, rank);
+  const PageSlice s = page_slice<C>(P, rank);
   int live, moves, holes;
-  cluster_scan(count_pages(s, refs, part, [](int, int r) { return r != 0; }), a.slots, rank, &live);
+  cluster_scan<C>(count_pages<C>(s, refs, part, [](int, int r) { return r != 0; }), slots[0], rank, &live);
   auto mover = [live](int p, int r) { return p >= live && r != 0; };
   auto hole = [live](int p, int r) { return p < live && r == 0; };
-  const int m0 = cluster_scan(count_pages(s, refs, part, mover), a.slots + kCluster, rank, &moves);
-  const int h0 = cluster_scan(count_pages(s, refs, part, hole), a.slots + 2 * kCluster, rank, &holes);
-  list_pages(s, refs, part, m0, moves, a.src, mover);
-  list_pages(s, refs, part, h0, moves, a.dst, hole);
-  for (int p = s.first + threadIdx.x; p < s.end; p += kCountThreads) a.where[p] = load_l2(refs + p) != 0 ? p : -1;
+  const int m0 = cluster_scan<C>(count_pages<C>(s, refs, part, mover), slots[1], rank, &moves);
+  const int h0 = cluster_scan<C>(count_pages<C>(s, refs, part, hole), slots[2], rank, &holes);
+  list_pages<C>(s, refs, part, m0, moves, a.src, mover);
+  list_pages<C>(s, refs, part, h0, moves, a.dst, hole);
+  for (int p = s.first + threadIdx.x; p < s.end; p += kThreads) a.where[p] = load_l2(refs + p) != 0 ? p : -1;
   if (rank == 0 && threadIdx.x == 0) {
     *a.live = live;
     *a.moves = moves;
   }
-  cluster_sync();
-  for (int k = rank * kCountThreads + threadIdx.x; k < moves; k += kCluster * kCountThreads) {
+  cluster_sync<C>();
+  for (int k = rank * kThreads + threadIdx.x; k < moves; k += C * kThreads) {
     const int from = load_l2(a.src + k), to = load_l2(a.dst + k);
     a.where[from] = to;
     refs[to] = load_l2(refs + from);
@@ -543,6 +578,24 @@ __global__ void __launch_bounds__(256) page_rename_kernel(const __grid_constant_
     else if (e != -1)
       report_bad_page(a.status);
   }
+}
+
+// Launches a kernel of one CTA or of one cluster.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_counting(void (*kern)(KArgs...), int ctas, size_t smem, cudaStream_t stream, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(ctas);
+  cfg.blockDim = dim3(count_threads(ctas));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim = {static_cast<unsigned>(ctas), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = ctas > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<KArgs>(args)...);
 }
 
 size_t words(long long n) { return align256(static_cast<size_t>(n) * 4); }
@@ -607,14 +660,15 @@ size_t reserve_workspace(int rows, int width, int num_pages) {
 }
 cudaError_t launch_page_reserve(PageReserveLaunch a, const fa_cache* caches, int layers, uint8_t* ws, cudaStream_t stream) {
   a.moves = reinterpret_cast<int*>(ws);
-  a.slots = a.moves + 8;
   a.src = reinterpret_cast<int*>(ws + 256);
   a.dst = reinterpret_cast<int*>(ws + 256 + words(a.t.rows));
   a.list = reinterpret_cast<int*>(ws + 256 + 2 * words(a.t.rows));
-  static std::atomic<unsigned long long> smem_set{0};
-  cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_reserve_kernel), reserve_smem(kPageTableRows));
+  const bool small = a.t.num_pages <= kSmallPool;
+  auto kern = small ? page_reserve_kernel<1> : page_reserve_kernel<kCluster>;
+  static std::atomic<unsigned long long> smem_set[2];
+  cudaError_t e = set_smem_once(smem_set[small], reinterpret_cast<const void*>(kern), reserve_smem(kPageTableRows));
   if (e != cudaSuccess) return e;
-  e = launch_pdl(page_reserve_kernel, dim3(kCluster), dim3(kCountThreads), reserve_smem(a.t.rows), stream, a);
+  e = launch_counting(kern, small ? 1 : kCluster, reserve_smem(a.t.rows), stream, a);
   if (e != cudaSuccess) return e;
   PageCopyLaunch c{};
   c.src = a.src;
@@ -629,10 +683,10 @@ cudaError_t launch_page_reserve(PageReserveLaunch a, const fa_cache* caches, int
 size_t compact_workspace(int num_pages) { return 256 + 2 * words(num_pages / 2 + 1); }
 cudaError_t launch_page_compact(PageCompactLaunch a, const fa_cache* caches, int layers, uint8_t* ws, cudaStream_t stream) {
   a.moves = reinterpret_cast<int*>(ws);
-  a.slots = a.moves + 8;
   a.src = reinterpret_cast<int*>(ws + 256);
   a.dst = reinterpret_cast<int*>(ws + 256 + words(a.t.num_pages / 2 + 1));
-  cudaError_t e = launch_pdl(page_compact_kernel, dim3(kCluster), dim3(kCountThreads), 0, stream, a);
+  const bool small = a.t.num_pages <= kSmallPool;
+  cudaError_t e = launch_counting(small ? page_compact_kernel<1> : page_compact_kernel<kCluster>, small ? 1 : kCluster, 0, stream, a);
   if (e != cudaSuccess) return e;
   const long long n = static_cast<long long>(a.t.rows) * a.t.width, blocks = (n + 255) / 256, most = 4LL * sm_count();
   e = launch_pdl(page_rename_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)), dim3(256), 0, stream, a);

@@ -34,7 +34,7 @@ def layers_of(a):
 
 
 def table_of(a):
-    return _pages.PageTableStruct(a["tab"], a["ts"], a["rows"], a["tw"], a["refs"], a["P"], a["page"]) if a["table"] else None
+    return bytes(_pages.PageTableStruct(a["tab"], a["ts"], a["rows"], a["tw"], a["refs"], a["P"], a["page"])) if a["table"] else None
 
 
 BASE = dict(layers=2, layer=1, cache={}, pools=True, n_layers=None, src=at(0), dst=at(1), n=5, tab=at(2), ts=8, rows=4, tw=8, refs=at(3),
