@@ -16,7 +16,8 @@ __device__ __forceinline__ bool is_page(int p, int num_pages) { return p >= 0 &&
 // Every (move, layer, K or V) is a run of contiguous codes, cut into pieces. A CTA's first warp sends
 // its pieces through a ring in shared memory with bulk copies (no registers, no cache lines held); the
 // other warps copy the scales. Bound: memory, two bytes moved per code.
-constexpr int kCopyWarps = 4, kCopyStages = 8, kCopyAhead = 5;  // pieces that are loaded ahead
+constexpr int kCopyWarps = 4, kCopyStages = 6, kCopyAhead = 4;  // pieces that are loaded ahead
+constexpr int kCopyPiece = 32768;  // at most
 constexpr int kCopySmem(int piece) { return kCopyStages * piece + 128; }
 
 __device__ __forceinline__ void bulk_store(void* dst, const void* src, uint32_t bytes) {
@@ -140,57 +141,48 @@ __global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid
 }
 
 // ------------------------------------------------------------------ forking
-// A CTA takes some columns of every row, so that rows can be exchanged in place: all of the
-// old entries that go to other rows are read into shared memory before any is written.
+// A CTA takes some columns of every row, so that rows can be exchanged in place: all that the new
+// entries are made from is read into shared memory before any is written. Bound: latency (the parent, its entry, the
+// store), for large tables memory.
 constexpr int kForkThreads = 512, kForkWords = 16384;
 
 __global__ void __launch_bounds__(kForkThreads) page_fork_kernel(const __grid_constant__ PageForkLaunch a) {
-  extern __shared__ int stage[];  // [rows][cols]
+  extern __shared__ int2 stage[];  // [rows][cols]: an entry as it was, as it will be
   grid_dep_wait();
   grid_dep_launch();
   const PageTable& t = a.t;
   const int c0 = blockIdx.x << a.log2_cols, cols = 1 << a.log2_cols;
   const int n = t.rows << a.log2_cols;
-  // columns of row b that stay
-  auto kept = [&](int b) {
-    if (a.keep == nullptr) return t.width;
-    const long long k = max(0, a.keep[b]);
-    return static_cast<int>(min(static_cast<long long>(t.width), (k + t.page - 1) / t.page));
-  };
-  auto parent_of = [&](int b) {
-    if (a.parent == nullptr) return b;
-    const int p = a.parent[b];
-    if (p >= -1 && p < t.rows) return p;
-    if (c0 == 0) report_bad_page(a.status);
-    return b;  // such a row stays as it is, but for `keep`
-  };
+#pragma unroll 2
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
     const int b = i >> a.log2_cols, c = c0 + (i & (cols - 1));
     if (c >= t.width) continue;
-    const int p = parent_of(b);
-    if (p == b) continue;
-    int e = -1;
-    if (p >= 0 && c < kept(b)) e = t.entry[p * t.stride + c];
-    if (e != -1 && !is_page(e, t.num_pages)) {
-      report_bad_page(a.status);
-      e = -1;
+    int p = a.parent != nullptr ? a.parent[b] : b;
+    const int keep = a.keep != nullptr ? a.keep[b] : 0, old = t.entry[b * t.stride + c];
+    if (p < -1 || p >= t.rows) {  // such a row stays as it is, but for `keep`
+      if (c0 == 0) report_bad_page(a.status);
+      p = b;
     }
-    stage[i] = e;
+    const bool kept = p >= 0 && (a.keep == nullptr || static_cast<long long>(c) * t.page < keep);
+    int now = -1;
+    if (kept) now = p == b ? old : t.entry[p * t.stride + c];
+    if (p != b && now != -1 && !is_page(now, t.num_pages)) {
+      report_bad_page(a.status);
+      now = -1;
+    }
+    stage[i] = make_int2(old, now);
   }
   __syncthreads();
   for (int i = threadIdx.x; i < n; i += kForkThreads) {
     const int b = i >> a.log2_cols, c = c0 + (i & (cols - 1));
     if (c >= t.width) continue;
-    const int p = parent_of(b);
-    int* const at = t.entry + b * t.stride + c;
-    if (p == b && c < kept(b)) continue;
-    const int now = p == b ? -1 : stage[i], old = *at;
-    if (old == now) continue;
-    *at = now;
-    if (now >= 0) atomicAdd(t.refs + now, 1);
-    if (is_page(old, t.num_pages))
-      atomicAdd(t.refs + old, -1);
-    else if (old != -1)
+    const int2 e = stage[i];
+    if (e.x == e.y) continue;
+    t.entry[b * t.stride + c] = e.y;
+    if (e.y >= 0) atomicAdd(t.refs + e.y, 1);
+    if (is_page(e.x, t.num_pages))
+      atomicAdd(t.refs + e.x, -1);
+    else if (e.x != -1)
       report_bad_page(a.status);
   }
 }
@@ -237,7 +229,7 @@ __device__ __forceinline__ int block_scan(int v, int* part, int* total) {
 }
 // Each CTA's v written to `slot` (a word a CTA of shared memory, used once) of all; a barrier of the cluster.
 template <int C>
-__device__ __forceinline__ void exchange(int v, int* slot, int rank) {
+__device__ __forceinline__ void write_slot(int v, int* slot, int rank) {
   if constexpr (C > 1) {
     if (threadIdx.x < C) {
       uint32_t to;
@@ -247,12 +239,15 @@ __device__ __forceinline__ void exchange(int v, int* slot, int rank) {
   } else if (threadIdx.x == 0) {
     slot[0] = v;
   }
+}
+template <int C>
+__device__ __forceinline__ void exchange(int v, int* slot, int rank) {
+  write_slot<C>(v, slot, rank);
   cluster_sync<C>();
 }
-// What the CTAs before this one have of v, and all.
+// What the CTAs before this one have in `slot`, and all.
 template <int C>
-__device__ __forceinline__ int cluster_scan(int v, int* slot, int rank, int* total) {
-  exchange<C>(v, slot, rank);
+__device__ __forceinline__ int sum_slots(const int* slot, int rank, int* total) {
   int before = 0, sum = 0;
 #pragma unroll
   for (int r = 0; r < C; ++r) {
@@ -262,6 +257,11 @@ __device__ __forceinline__ int cluster_scan(int v, int* slot, int rank, int* tot
   }
   *total = sum;
   return before;
+}
+template <int C>
+__device__ __forceinline__ int cluster_scan(int v, int* slot, int rank, int* total) {
+  exchange<C>(v, slot, rank);
+  return sum_slots<C>(slot, rank, total);
 }
 // The CTA's share of the pages.
 struct PageSlice {
@@ -417,10 +417,15 @@ __global__ void __launch_bounds__(count_threads(C), 1)
       if (i < kItemCache) cache[i] = make_int2(row[k] << 2 | state, entry[k]);
     }
   }
-  int need, wanted, have, all_free = 0, free_before = 0;
+  int need, wanted, all_free;
+  auto is_free = [](int, int refs) { return refs == 0; };
+  const PageSlice s = page_slice<C>(t.num_pages, rank);
+  const int have = count_pages<C>(s, t.refs, part, is_free);
   block_scan<C>(mine, part, &need);
   // (need is at most the pages of the table's rows, 2^30: a bit is left for any_shared)
+  write_slot<C>(have, slots[2], rank);
   exchange<C>(need | (any_shared != 0 ? 1 << 31 : 0), slots[0], rank);
+  const int free_before = sum_slots<C>(slots[2], rank, &all_free);
   int before = 0;
   bool shared = false;
   wanted = 0;
@@ -460,10 +465,6 @@ __global__ void __launch_bounds__(count_threads(C), 1)
   }
   int f = t.rows;  // the first row that fails
   if (wanted > 0) {  // the same in every CTA
-    auto is_free = [](int, int refs) { return refs == 0; };
-    const PageSlice s = page_slice<C>(t.num_pages, rank);
-    have = count_pages<C>(s, t.refs, part, is_free);
-    free_before = cluster_scan<C>(have, slots[2], rank, &all_free);
     if (wanted > all_free) {
       int k0 = before;
       for (int i0 = 0; i0 < items; i0 += kThreads) {
@@ -486,27 +487,36 @@ __global__ void __launch_bounds__(count_threads(C), 1)
   // ---- pages dealt out
   if (shared || wanted > 0) {
     int k0 = before;
-    for (int i0 = 0; i0 < items; i0 += kThreads) {
-      const int i = i0 + threadIdx.x;
-      Item x{};
-      bool take = false;
-      if (i < items) {
-        x = item(i);
-        take = takes(x, i);
+    for (int i0 = 0; i0 < items; i0 += kAtOnce * kThreads) {
+      Item x[kAtOnce];
+      int take = 0;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int i = i0 + kAtOnce * threadIdx.x + k;
+        x[k].state = kOwn;
+        if (i >= items) continue;
+        x[k] = item(i);
+        if (takes(x[k], i)) take |= 1 << k;
       }
-      int total;
-      const int k = k0 + block_scan<C>(take ? 1 : 0, part, &total), b = x.row;
-      // (below, the rows that fail come back to their pages' counts)
-      if (!take && (x.state == kKeeps || x.state == kShared)) t.refs[x.entry] = b < f ? 1 : 0;
-      if (take && b < f) {
-        const int p = load_l2(a.list + k);
-        t.entry[b * t.stride + x.col] = p;
-        t.refs[p] = 1;
-        // earlier tokens of the sequence in the page
-        if (x.state == kShared && x.col == first_col[b] && (a.start != nullptr ? a.start[b] : 0) % t.page != 0) {
-          const int m = atomicAdd(a.moves, 1);
-          a.src[m] = x.entry;
-          a.dst[m] = p;
+      int total, at = k0 + block_scan<C>(__popc(take), part, &total), page[kAtOnce];
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k)
+        if (take >> k & 1) page[k] = x[k].row < f ? load_l2(a.list + at++) : -1;
+#pragma unroll
+      for (int k = 0; k < kAtOnce; ++k) {
+        const int b = x[k].row, p = page[k];
+        if (!(take >> k & 1)) {
+          // (below, the rows that fail come back to their pages' counts)
+          if (x[k].state == kKeeps || x[k].state == kShared) t.refs[x[k].entry] = b < f ? 1 : 0;
+        } else if (b < f && is_page(p, t.num_pages)) {  // (it is one, if refs counts the entries)
+          t.entry[b * t.stride + x[k].col] = p;
+          t.refs[p] = 1;
+          // earlier tokens of the sequence in the page
+          if (x[k].state == kShared && x[k].col == first_col[b] && (a.start != nullptr ? a.start[b] : 0) % t.page != 0) {
+            const int m = atomicAdd(a.moves, 1);
+            a.src[m] = x[k].entry;
+            a.dst[m] = p;
+          }
         }
       }
       k0 += total;
@@ -613,17 +623,17 @@ cudaError_t launch_page_copy(PageCopyLaunch a, const fa_cache* caches, int layer
       const fa_cache& x = caches[l0 + l];
       a.layer[l] = PageCopyLaunch::Layer{{static_cast<uint8_t*>(x.k), static_cast<uint8_t*>(x.v)}, {x.k_scale, x.v_scale}};
     }
-    // pieces of 16 KB, smaller ones where there would be few
+    // pieces of 32 KB (500 pages of 64 KB in 8 layers 166.8 us, of 16 KB 169.0), smaller ones where there would be few
     const long long runs = static_cast<long long>(a.n) * a.layers * 2;
     long long piece = a.page_bytes;
-    while (piece > 16384 || (piece > 2048 && runs * (a.page_bytes / piece) < 4LL * sm_count())) {
+    while (piece > kCopyPiece || (piece > 2048 && runs * (a.page_bytes / piece) < 4LL * sm_count())) {
       if (piece % 2 == 0 && (piece / 2) % 128 == 0) {
         piece /= 2;
         continue;
       }
       // an odd number of heads: a multiple of 1024 bytes that divides the page
       long long best = 1024;
-      for (long long p = 2048; p < piece && p <= 16384; p += 1024)
+      for (long long p = 2048; p < piece && p <= kCopyPiece; p += 1024)
         if (a.page_bytes % p == 0) best = p;
       piece = best;
       break;
@@ -632,7 +642,7 @@ cudaError_t launch_page_copy(PageCopyLaunch a, const fa_cache* caches, int layer
     const long long items = runs * (a.page_bytes / piece);
     const int grid = static_cast<int>(items < sm_count() ? items : sm_count());
     static std::atomic<unsigned long long> smem_set{0};
-    cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_copy_kernel), kCopySmem(16384));
+    cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_copy_kernel), kCopySmem(kCopyPiece));
     if (e != cudaSuccess) return e;
     e = launch_pdl(page_copy_kernel, dim3(grid), dim3(kCopyWarps * 32), kCopySmem(a.piece), stream, a);
     if (e != cudaSuccess) return e;
@@ -641,14 +651,13 @@ cudaError_t launch_page_copy(PageCopyLaunch a, const fa_cache* caches, int layer
 }
 
 cudaError_t launch_page_fork(PageForkLaunch a, cudaStream_t stream) {
-  // 32 columns a CTA, fewer where the staged entries would not fit or most SMs would be idle
+  // 32 columns a CTA, fewer where the staged entries would not fit or most SMs would be idle (256 rows of 66: 7.6 us with 8
+  // columns, 2.4 with one)
   a.log2_cols = 5;
-  while (a.log2_cols > 0 && ((a.t.rows << a.log2_cols) > kForkWords ||
-                             (a.log2_cols > 3 && (a.t.width >> a.log2_cols) < sm_count())))
-    --a.log2_cols;
-  const int smem = (a.t.rows << a.log2_cols) * 4;
+  while (a.log2_cols > 0 && ((a.t.rows << a.log2_cols) > kForkWords || (a.t.width >> a.log2_cols) < sm_count())) --a.log2_cols;
+  const int smem = (a.t.rows << a.log2_cols) * 8;
   static std::atomic<unsigned long long> smem_set{0};
-  const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_fork_kernel), kForkWords * 4);
+  const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(page_fork_kernel), kForkWords * 8);
   if (e != cudaSuccess) return e;
   const int grid = (a.t.width + (1 << a.log2_cols) - 1) >> a.log2_cols;
   return launch_pdl(page_fork_kernel, dim3(grid), dim3(kForkThreads), smem, stream, a);
