@@ -83,13 +83,13 @@ __device__ __forceinline__ unsigned long long seen_nan(const CacheView& c, long 
   unsigned long long bits = 0ull;
 #pragma unroll 1
   for (int key = first; key < end; ++key) {
-    const int p = c.table[tab + (key >> c.log2_page)];
+    const int p = __ldcg(c.table + tab + (key >> c.log2_page));
     if (p < 0 || p >= c.num_pages) continue;  // not read
     const long long row = ((static_cast<long long>(p) * c.H + h) << c.log2_page) + (key & (c.page - 1));
     const uint32_t* const at = reinterpret_cast<const uint32_t*>(c.code[1] + row * c.d + c0);
 #pragma unroll
     for (int w = 0; w < W; ++w) {
-      const uint32_t nan = __vcmpeq4(at[w] & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x08040201u;  // a bit of each byte
+      const uint32_t nan = __vcmpeq4(__ldcg(at + w) & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x08040201u;  // a bit of each byte
       bits |= static_cast<unsigned long long>(nan * 0x01010101u >> 24) << (4 * w);
     }
   }

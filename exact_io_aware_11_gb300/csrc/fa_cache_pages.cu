@@ -41,6 +41,7 @@ __global__ void __launch_bounds__(kCopyWarps * 32) page_copy_kernel(const __grid
   __shared__ __align__(8) uint64_t full[kCopyStages];
   __shared__ int abort_flag;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  check_init(a.status);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kCopyStages; ++i) mbar_init(full + i, 1);
     abort_flag = 0;

@@ -371,6 +371,8 @@ SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_w
   const long long sms = sm_count(), most_b = few ? static_cast<long long>(few_row_ctas(d, own.rows)) * sms : sms;
   const bool brief = own.units * own.cap_steps <= (few ? (own.rows > 8 ? 13 : d == 64 ? 11 : 18) : NG <= 64 ? 29 : 58) * most_b;
   p.plain = NG > 128 || B < 2 || brief;
+  // units are numbered in 32 bits
+  p.plain = p.plain || (static_cast<long long>(B) * (NG / 8 + 2) + groups) * HK > (1LL << 30);
   if (p.plain) {
     p.total = cache_attention_workspace(B, HK, G, N, d, page, table_width);
     return p;

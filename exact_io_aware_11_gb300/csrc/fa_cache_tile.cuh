@@ -178,15 +178,6 @@ __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const Att
       s.row += ph << c.log2_page;
       s.ks = attn_load<SH>(c.scale[0] + ph);
       s.vs = attn_load<SH>(c.scale[1] + ph);
-      // The ring holds a step or two, which does not cover the way from memory while another kernel
-      // keeps that busy: the pages come to the L2 cache two steps before.
-      if constexpr (SH) {
-        if (leader) {
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv)
-            if (L::kLoaders == 1 || kv == loader) l2_prefetch(c.code[kv] + static_cast<long long>(s.row) * D, rows * D);
-        }
-      }
     }
   };
   Step now = look(), next = look();

@@ -148,7 +148,7 @@ def check_reserve(fa, caches, table, refs, page, start, count, **kw):
 
 
 @pytest.mark.parametrize("B,W,P,page,spare", [(1, 1, 2, 16, 1), (6, 9, 60, 16, 20), (64, 40, 2500, 64, 900), (40, 30, 700, 32, 0), (300, 20, 4000, 16, 30),
-                                              (50, 100, 5000, 128, 60), (50, 100, 9000, 16, 30), (16384, 3, 20000, 16, 4000), (3, 4000, 12100, 16, 9000)])
+                                              (50, 100, 5000, 128, 60), (50, 100, 9000, 16, 30), (16384, 3, 20000, 16, 4000), (16384, 1, 8192, 16, 900), (3, 4000, 12100, 16, 9000)])
 @pytest.mark.parametrize("kind", ["token", "draft", "prompt"])
 def test_reserve(fa, B, W, P, page, spare, kind):
     """Rows with pages of their own and shared ones, at the start of pages and within them; enough free pages, and too few."""

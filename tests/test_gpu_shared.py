@@ -113,6 +113,15 @@ def test_any_lengths(fa, N, G, causal, wide):
     assert fa.device_status() == fa.FA_OK
 
 
+@pytest.mark.parametrize("G,N,B", [(4, 1, 3), (4, 1, 30), (3, 20, 4)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_nothing_behind_the_prefix(fa, G, N, B, causal):
+    """Sequences that end with their prefix: single tokens (and, without causality, any rows) see all of it."""
+    of, prefix = [b % 2 for b in range(B)], [256, 320]
+    m, lens = batch(fa, of, prefix, [0 if b % 3 else N + b for b in range(B)], 2, 64, 64, "e4m3", seed=9)
+    check_shared(fa, m, queries(B, 2 * G, N, 64, "bf16", 14), lens, of, prefix, causal=causal)
+
+
 def test_group_hint_of_another_size(fa):
     """`groups` far from the groups in use: all in one of 64, and as many groups as sequences."""
     B = 40
