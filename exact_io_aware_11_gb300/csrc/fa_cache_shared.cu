@@ -251,21 +251,25 @@ __global__ void __launch_bounds__(256, 4) shared_join_kernel(const __grid_consta
   const int bh = static_cast<int>(row / a.N), i = static_cast<int>(row - static_cast<long long>(bh) * a.N);
   const int b = bh / a.Hq, head = bh - b * a.Hq, hk = head / a.G, r = i * a.G + head - hk * a.G;
   const int tile = r / j.rows_b, own = (b * j.tiles_b + tile) * j.HK + hk;
-  grid_dep_wait();
-  grid_dep_launch();
-  if (row >= static_cast<long long>(a.B) * a.Hq * a.N) return;
-  const int4 s = j.seq[b];
-  const int2 parts = j.list[1].unit_parts[own];
-  if (s.x == 0 && parts.x < 0) return;  // straight from its unit
-  // the prefix's parts, then the row's own; each list's first CTA, and how many
-  const JoinList& pl = j.list[s.x == 2 ? 1 : 0];
-  int unit = 0, at = 0, first = 0, n = 0;
-  bool whole = false;
+  const bool row_ok = row < static_cast<long long>(a.B) * a.Hq * a.N;
+  // (the plan's writes are in the L2 cache long since: this kernel was let go by list B's, that by list A's)
+  const int4 s = row_ok ? __ldcg(j.seq + b) : make_int4(0, 0, 0, 0);
+  const JoinList& pl = j.list[s.x == 2 ? 1 : 0];  // where the prefix's parts are
+  int unit = 0, at = 0;
   if (s.x != 0) {
     const int x = s.y + r, t = x / pl.rows;
     unit = (s.z + t) * j.HK + hk;
     at = x - t * pl.rows;
-    const int2 p = pl.unit_parts[unit];
+  }
+  grid_dep_wait();
+  grid_dep_launch();
+  if (!row_ok) return;
+  const int2 parts = j.list[1].unit_parts[own], p = s.x != 0 ? pl.unit_parts[unit] : make_int2(0, 0);
+  if (s.x == 0 && parts.x < 0) return;  // straight from its unit
+  // the prefix's parts, then the row's own; each list's first CTA, and how many
+  int first = 0, n = 0;
+  bool whole = false;
+  if (s.x != 0) {
     whole = p.x < 0;
     first = whole ? 0 : p.x;
     n = whole ? 1 : p.y - p.x + 1;
