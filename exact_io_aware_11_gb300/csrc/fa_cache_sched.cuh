@@ -180,15 +180,23 @@ template <bool SH>
 struct AttnShareOf : AttnShare {
   typename AttnEntryOf<SH>::type x;  // of `entry`
 };
+// A list's division is even to the place: CTA c starts at floor(c * total / ctas), so that the
+// boundaries of equal units are boundaries of CTAs where there is a whole number of these to a unit.
+template <>
+struct AttnShareOf<true> : AttnShare {
+  SharedEntry x;
+  long long total;
+};
 
 // n / d for n that mostly fits 32 bits (a 64-bit division takes some 400 cycles).
 __device__ __forceinline__ long long attn_div(long long n, long long d) {
   if (((n | d) >> 32) == 0) return static_cast<unsigned>(n) / static_cast<unsigned>(d);
   return n / d;
 }
-__device__ __forceinline__ long long attn_start(const AttnShare& s, int c) {
+__device__ __forceinline__ long long attn_start(const AttnShareOf<false>& s, int c) {
   return c * s.each + min(c, s.extra);
 }
+__device__ __forceinline__ long long attn_start(const AttnShareOf<true>& s, int c) { return attn_div(c * s.total, s.ctas); }
 
 // This CTA's cursor. Called by the whole CTA of kThreads threads; `sh` and
 // `part` (kThreads / 32 words) are shared memory.
@@ -220,12 +228,16 @@ __device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShar
   }
   before += incl - mine;
   total *= g.HK;
-  AttnShare d{};
+  AttnShareOf<SH> d{};
   int ctas = gridDim.x;
   if constexpr (SH) ctas = min(ctas, __ldcg(g.entries + 1));
   d.ctas = static_cast<int>(min(static_cast<long long>(ctas), total));
-  d.each = SH && d.ctas == 0 ? 0 : attn_div(total, d.ctas);  // (a list may be empty)
-  d.extra = static_cast<int>(total - d.each * d.ctas);
+  if constexpr (SH) {
+    d.total = total;
+  } else {
+    d.each = attn_div(total, d.ctas);
+    d.extra = static_cast<int>(total - d.each * d.ctas);
+  }
   const int c = blockIdx.x;
   const long long s0 = c < d.ctas ? attn_start(d, c) : total;
   long long p = before * g.HK;
@@ -243,8 +255,12 @@ __device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShar
     }
   }
   if (threadIdx.x == 0) {
-    sh->each = d.each;
-    sh->extra = d.extra;
+    if constexpr (SH) {
+      sh->total = d.total;
+    } else {
+      sh->each = d.each;
+      sh->extra = d.extra;
+    }
     sh->ctas = d.ctas;
   }
   __syncthreads();
@@ -273,7 +289,10 @@ __device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShar
 }
 
 // The CTA whose run holds place s.
-__device__ __forceinline__ int attn_cta_of(long long s, const AttnShare& d) {
+__device__ __forceinline__ int attn_cta_of(long long s, const AttnShareOf<true>& d) {
+  return static_cast<int>(attn_div((s + 1) * d.ctas - 1, d.total));
+}
+__device__ __forceinline__ int attn_cta_of(long long s, const AttnShareOf<false>& d) {
   const long long longer = d.extra * (d.each + 1);  // steps of the CTAs that have one more
   return static_cast<int>(s < longer ? attn_div(s, d.each + 1) : d.extra + attn_div(s - longer, d.each));
 }

@@ -111,7 +111,7 @@ struct TileBars {
 // writes the record of a cut unit that the CTA ends, well before that end.
 template <int D, int NQ, bool SH>
 __device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor<SH> ld,
-                                             const AttnShare& share, uint8_t* smem, const TileBars& b,
+                                             const AttnShareOf<SH>& share, uint8_t* smem, const TileBars& b,
                                              const Watchdog& wd, int loader, int lane) {
   using L = TileLayout<D, NQ, SH>;
   using Unit = typename TileUnitOf<SH>::type;
