@@ -378,22 +378,24 @@ SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_w
   SharedPlan p{};
   const long long NG = static_cast<long long>(N) * G, cap = static_cast<long long>(table_width) * page;
   const AttnPlan own = attn_plan(B, HK, NG, cap, d);
-  const bool few = own.rows <= 16;
+  const long long sms = sm_count(), slots = own.rows <= 16 ? few_row_ctas(d, own.rows) * sms : sms;
   // Sharing takes some 20 us whatever there is to do (the plan, a tile kernel's beginning and end, the join): not
   // where the table has room for few steps a CTA without it. GPU time in us, shared and plain, one group
   // with 128 tokens of its own a sequence: 8 rows at d = 128, 15 steps 24.7, 22.6, 28 steps 28.1, 33.0; at d = 64 7 steps 21.1,
   // 16.5, 14 steps 24.4, 25.5; 16 rows, 8 steps 28.4, 24.0, 14 steps 29.6, 30.8; 40 rows, 14 steps 35.8, 27.8, 27 steps 44.1, 42.3; 80 rows,
   // 28 steps 43.0, 32.3, 55 steps 51.1, 49.6.
-  const long long sms = sm_count(), most_b = few ? static_cast<long long>(few_row_ctas(d, own.rows)) * sms : sms;
-  const bool brief = own.units * own.cap_steps <= (few ? (own.rows > 8 ? 13 : d == 64 ? 11 : 18) : NG <= 64 ? 29 : 58) * most_b;
-  p.plain = NG > 128 || B < 2 || brief;
+  const long long enough = NG <= 8 ? (d == 64 ? 11 : 18) : NG <= 16 ? 13 : NG <= 64 ? 29 : 58;
+  p.plain = NG > 128 || B < 2 || own.units * own.cap_steps <= enough * slots;
   // units are numbered in 32 bits
   p.plain = p.plain || (static_cast<long long>(B) * (NG / 8 + 2) + groups) * HK > (1LL << 30);
   if (p.plain) {
     p.total = cache_attention_workspace(B, HK, G, N, d, page, table_width);
     return p;
   }
-  p.rows_b = own.rows;
+  // Own tokens are short: up to 32 rows go as groups of 16, which begin in a quarter of a tile's time
+  // (20 rows of 64 sequences with 50 to 1000 tokens, 109.1 us in tiles, 93.9; 32 rows 149.2, 123.7; 32 rows of 32 sequences with 3000 to 6000 139.9, 134.3).
+  const bool few = NG <= 32;
+  p.rows_b = NG <= 8 ? 8 : few ? 16 : NG <= 64 ? 64 : 128;
   p.lead_b = !few ? own.lead : d == 64 && p.rows_b <= 8 ? 2 : 3;
   p.lead_a = p.rows_a == 256 ? 6 : 3;
   p.only_b = few && B * NG <= 16;
@@ -404,7 +406,7 @@ SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_w
   const long long pairs = groups < B / 2 ? groups : B / 2;  // groups of two and more
   p.max_a = B * NG / p.rows_a + pairs;
   p.max_b = static_cast<long long>(B) * p.tiles_b + (few ? B * NG / p.rows_b + pairs : 0);
-  const long long steps = (cap + 127) / 128;
+  const long long steps = (cap + 127) / 128, most_b = few ? few_row_ctas(d, p.rows_b) * sms : sms;
   p.ctas_a = static_cast<int>(p.max_a * HK >= sms || p.max_a * HK * steps >= sms ? sms : p.max_a * HK * steps);
   p.ctas_b = static_cast<int>(p.max_b * HK >= most_b || p.max_b * HK * steps >= most_b ? most_b : p.max_b * HK * steps);
   size_t at = 256;
