@@ -411,11 +411,12 @@ int fa_cache_attention_shared(const void* q, void* o, float* lse, const fa_cache
       !aligned(prefix_len, 4) || B < 1)
     return FA_ERR_INVALID_ARG;
   const Range more[2] = {{prefix_of, static_cast<size_t>(B) * 4}, {prefix_len, static_cast<size_t>(groups) * 4}};
+  if (opt != nullptr && check_attention_sizes(cache, B, Hq, N, opt->table_width) == FA_OK &&
+      workspace_bytes < shared_attention_workspace(B, cache->H, Hq / cache->H, N, cache->d, cache->page_size, opt->table_width, groups))
+    return FA_ERR_INVALID_ARG;
   CacheAttnLaunch a;
   const int st = make_attention(q, o, lse, cache, B, Hq, N, opt, workspace, workspace_bytes, more, 2, &a);
   if (st != FA_OK) return st;
-  if (workspace_bytes < shared_attention_workspace(B, cache->H, a.G, N, cache->d, cache->page_size, opt->table_width, groups))
-    return FA_ERR_INVALID_ARG;
   return launch_shared_attention(a, prefix_of, prefix_len, groups, stream) == cudaSuccess ? FA_OK : FA_ERR_CUDA;
 }
 
