@@ -169,6 +169,19 @@ def test_reserve(fa, B, W, P, page, spare, kind):
     check_reserve(fa, caches, table, refs, page, start, count)
 
 
+@pytest.mark.parametrize("B,W,P", [(150, 64, 8192), (150, 64, 5000), (900, 50, 30000), (900, 50, 20000)])
+def test_reserve_more_items_than_are_kept_on_chip(fa, B, W, P):
+    """Every column of every row: some 10000 items for one CTA, 45000 for a cluster, most of them of shared pages."""
+    rng = np.random.default_rng(B + P)
+    page = 16
+    table, refs, _ = random_table(rng, B, W, P // 3, page, shared=0.9)
+    refs = np.concatenate([refs, np.zeros(P - len(refs), np.int32)])
+    start, count = rng.integers(0, 20, B), np.full(B, W * page - 20)
+    refs[rng.choice(np.nonzero(refs)[0], 50)] += 1    # pages that the caller holds besides
+    ok, moves = check_reserve(fa, pools(fa, 1, P, 1, page, 64), table, refs, page, start, count)
+    assert len(moves) > 5
+
+
 def test_reserve_by_hand(fa):
     """Three rows share a partly filled page and all write on: the last one keeps it. Pages go in order."""
     caches = pools(fa, 3, 8, 2, 16, 64)
