@@ -256,3 +256,85 @@ def test_compact_bad_entries_are_left(fa):
     where, live = fa.cache_compact(caches, t, r)
     assert t.tolist() == [[0, 77, -1, -3]] and r.tolist() == [1, 0, 0, 0, 0, 0] and where.tolist() == [-1] * 5 + [0] and live.item() == 1
     assert fa.device_status() == fa.FA_ERR_BAD_PAGE
+
+
+# ------------------------------------------------------------------ streams and graphs
+def test_captured_calls_follow_the_tensors(fa):
+    """Fork, reserve, copy and compact in one graph, replayed with other parents, lengths and moves, on a stream of its own."""
+    B, W, P, page = 8, 12, 120, 16
+    rng = np.random.default_rng(3)
+    caches = pools(fa, 2, P, 2, page, 64)
+    table, refs, _ = random_table(rng, B, W, P // 2, page)
+    refs = np.concatenate([refs, np.zeros(P - len(refs), np.int32)])
+    t, r = i32(table), i32(refs)
+    parent, keep, start, count, src, dst = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B, B, B, B, 2, 2))
+    ok, where, live = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in (B, P, 1))
+    ws = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in (fa.cache_reserve_workspace_bytes(caches[0], B, W), fa.cache_compact_workspace_bytes(caches[0]))]
+
+    def step():
+        fa.cache_fork(t, r, page, parent=parent, keep=keep)
+        fa.cache_reserve(caches, t, r, start, count, ok=ok, workspace=ws[0])
+        fa.cache_copy(caches, src, dst)
+        fa.cache_compact(caches, t, r, where=where, live=live, workspace=ws[1])
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    saved = [x.clone() for x in (t, r)]
+    before = bits(caches)
+    with torch.cuda.stream(side):
+        src.fill_(-1)
+        keep.fill_(W * page)
+        parent.copy_(torch.arange(B, device="cuda"))
+        step()
+        with torch.cuda.graph(graph, stream=side):
+            step()
+        for x, y in zip((t, r), saved):
+            x.copy_(y)
+        for x, y in zip([x for c in caches for x in (c.k, c.v, c.k_scale, c.v_scale)], before):
+            (x.view(torch.uint8) if x.dtype != torch.float32 else x).copy_(y)
+        for _ in range(12):
+            values = [rng.integers(-1, B, B), rng.integers(0, W * page, B), rng.integers(0, W * page, B), rng.integers(0, 40, B),
+                      rng.choice(P, 2, replace=False), np.array([-1, P - 1])]
+            values[4][1] = rng.choice(np.setdiff1d(np.arange(P - 1), values[4][:1]))
+            for x, v in zip((parent, keep, start, count, src, dst), values):
+                x.copy_(i32(v))
+            graph.replay()
+            op.fork(table, refs, page, values[0], values[1])
+            want, moves, _ = op.reserve(table, refs, page, values[2], values[3])
+            moved(before, moves)
+            moved(before, [(int(values[4][1]), P - 1)])
+            places, L, moves, _ = op.compact(table, refs)
+            moved(before, moves)
+            assert np.array_equal(ok.cpu().numpy(), want) and np.array_equal(where.cpu().numpy(), places) and live.item() == L
+            assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(r.cpu().numpy(), refs) and same(caches, before)
+    torch.cuda.current_stream().wait_stream(side)
+    assert fa.device_status() == fa.FA_OK
+
+
+def test_two_tables_on_two_streams(fa):
+    """Calls on streams that are not the current one, two pools at a time."""
+    B, W, P, page = 20, 30, 900, 32
+    rng = np.random.default_rng(4)
+    streams, state = [torch.cuda.Stream() for _ in range(2)], []
+    for k in range(2):
+        table, refs, length = random_table(rng, B, W, P - 300, page, shared=0.7)
+        refs = np.concatenate([refs, np.zeros(300, np.int32)])
+        caches = pools(fa, 2, P, 1, page, 64, seed=k)
+        ws = torch.empty(fa.cache_reserve_workspace_bytes(caches[0], B, W), dtype=torch.uint8, device="cuda")
+        state.append([table, refs, length, caches, bits(caches), i32(table), i32(refs), ws, torch.empty(B, dtype=torch.int32, device="cuda")])
+    args = [[(i32(rng.integers(0, B, B)), i32(rng.integers(0, W * page - 9, B))) for _ in range(6)] for _ in range(2)]
+    torch.cuda.synchronize()
+    for i in range(6):
+        for s, x, a in zip(streams, state, args):
+            fa.cache_fork(x[5], x[6], page, parent=a[i][0], stream=s)
+            fa.cache_reserve(x[3], x[5], x[6], a[i][1], 8, ok=x[8], workspace=x[7], stream=s)
+    torch.cuda.synchronize()
+    for (table, refs, _, caches, before, t, r, _, ok), a in zip(state, args):
+        for p, n in a:
+            op.fork(table, refs, page, p.cpu().numpy())
+            want, moves, _ = op.reserve(table, refs, page, n.cpu().numpy(), [8] * B)
+            moved(before, moves)
+        assert np.array_equal(t.cpu().numpy(), table) and np.array_equal(r.cpu().numpy(), refs)
+        assert np.array_equal(ok.cpu().numpy(), want) and same(caches, before)
+    assert fa.device_status() == fa.FA_OK
