@@ -63,9 +63,13 @@ SIGNATURES["fa_cache_attention_shared_workspace_bytes"] = (_SZ, [ctypes.POINTER(
 SIGNATURES["fa_cache_attention_shared"] = (_I, [_P, _P, _P, _P, _I, _I, _I, _P, _P, _P, _I, _P, _SZ, _P])  # structs as bytes
 
 # These calls are made once per layer and token: the checks below read each attribute once,
-# and the stream comes from the binding that torch.cuda.current_stream wraps (0.1 us against 2).
+# and the stream comes from the binding that torch.cuda.current_stream wraps (0.1 us against 2), as does
+# the device (whose tensors the caller has, so that CUDA is up).
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
+_raw_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_INT32, _FLOAT32 = torch.int32, torch.float32
+_Tensor = torch.Tensor
 
 
 def _on(call, device, stream, *args):
@@ -75,7 +79,7 @@ def _on(call, device, stream, *args):
             raise ValueError("the stream belongs to another device than the tensors")
         with torch.cuda.stream(stream):
             return call(*args)
-    if device.index == torch.cuda.current_device():
+    if device.index == _raw_device():
         return call(*args)
     with torch.cuda.device(device):
         return call(*args)
@@ -110,11 +114,21 @@ assert _OPTIONS.size == ctypes.sizeof(CacheAttentionOptions)
 
 def _ints(t, what, index, n):
     """The address of a contiguous int32 vector of n values (None: any) on device `index`."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index or t.dim() != 1:
+    if not isinstance(t, _Tensor) or t.dtype is not _INT32 or t.get_device() != index or t.dim() != 1:
         raise ValueError(f"{what} must be an int32 vector on the tensors' device")
-    if (n is not None and t.shape[0] != n) or not t.is_contiguous():
+    if not t.is_contiguous() or (n is not None and t.numel() != n):
         raise ValueError(f"{what} must be contiguous and have {n} values")
     return t.data_ptr()
+
+
+def _matrix(t, what, index):
+    """The address of an int32 [rows, columns] tensor with a contiguous last axis, its row stride (0: one row), rows and columns."""
+    if not isinstance(t, _Tensor) or t.dtype is not _INT32 or t.get_device() != index or t.dim() != 2:
+        raise ValueError(f"{what} must be an int32 tensor of 2 dimensions on the tensors' device")
+    (rows, width), (stride, one) = t.shape, t.stride()
+    if rows < 1 or width < 1 or (width > 1 and one != 1):
+        raise ValueError(f"{what} must be [rows, pages per row] with a contiguous last axis")
+    return t.data_ptr(), stride if rows > 1 else 0, rows, width
 
 
 def _check_lengths(t, what, device, B):
@@ -436,14 +450,16 @@ def _cache_attention_shared(q, cache, page_table, kv_len, prefix_of, prefix_len,
     B, H, N, d = n
     if d != cache.head_dim or H % cache.heads:
         raise ValueError("q must have the cache's d and a multiple of its heads")
-    table, table_stride, pages = _check_table(page_table, dev, B)
+    table, table_stride, rows, pages = _matrix(page_table, "page_table", index)
+    if rows != B:
+        raise ValueError("page_table must be [B, pages per sequence]")
     kl, of = _ints(kv_len, "kv_len", index, B), _ints(prefix_of, "prefix_of", index, B)
     ql = None if q_len is None else _ints(q_len, "q_len", index, B)
-    pl, groups = _ints(prefix_len, "prefix_len", index, None), prefix_len.shape[0]
+    pl, groups = _ints(prefix_len, "prefix_len", index, None), prefix_len.numel()
     o, os = _out(out, q, n, "out", dev)
     if lse is None:
-        lse = torch.empty((B, H, N), dtype=torch.float32, device=dev)
-    elif lse.dtype != torch.float32 or lse.device != dev or tuple(lse.shape) != (B, H, N) or not lse.is_contiguous():
+        lse = torch.empty((B, H, N), dtype=_FLOAT32, device=dev)
+    elif not isinstance(lse, _Tensor) or lse.dtype is not _FLOAT32 or lse.get_device() != index or lse.shape != (B, H, N) or not lse.is_contiguous():
         raise ValueError("lse must be contiguous float32 [B, H, N] on the tensors' device")
     L = lib()
     if workspace is None:

@@ -12,7 +12,7 @@ import struct
 
 import torch
 
-from ._cache import _I32, _I64, _SZ, KVCache, _done, _ints, _on, _raw_stream
+from ._cache import _I32, _I64, _SZ, KVCache, _done, _ints, _matrix, _on, _raw_stream
 from ._lib import _I, _P, SIGNATURES, lib
 
 
@@ -54,13 +54,10 @@ def _layers(caches):
 
 def _table(t, refs, page_size, index):
     """The fa_page_table of a table and its counts, the table's rows and columns, and the pages."""
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or t.get_device() != index or t.dim() != 2:
-        raise ValueError("page_table must be an int32 tensor of 2 dimensions on the tensors' device")
+    entries, stride, rows, width = _matrix(t, "page_table", index)
     counts = _ints(refs, "refs", index, None)
-    (rows, width), (stride, one), pages = t.shape, t.stride(), refs.shape[0]
-    if rows < 1 or width < 1 or (width > 1 and one != 1):
-        raise ValueError("page_table must be [rows, pages per row] with a contiguous last axis")
-    return _PACK.pack(t.data_ptr(), stride if rows > 1 else 0, rows, width, counts, pages, page_size), rows, width, pages
+    pages = refs.numel()
+    return _PACK.pack(entries, stride, rows, width, counts, pages, page_size), rows, width, pages
 
 
 def _maybe(t, what, index, n):
@@ -71,7 +68,7 @@ def _workspace(workspace, need, dev):
     """The caller's workspace, or a new one, and its bytes."""
     if workspace is None:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev.index or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous CUDA tensor on the tensors' device")
     return workspace, workspace.numel() * workspace.element_size()
 
@@ -93,7 +90,7 @@ def cache_copy(caches, src, dst, stream=None) -> None:
 
 def _copy(s, layers, index, src, dst):
     a = _ints(src, "src", index, None)
-    n = src.shape[0]
+    n = src.numel()
     _done(lib().fa_cache_copy(s, layers, a, _ints(dst, "dst", index, n), n, _raw_stream(index)), "fa_cache_copy")
 
 
