@@ -41,7 +41,7 @@ struct AttnGrid {
   const int* entries;  // how many, and the CTAs that work on them
   const int* member;
   int2* unit_parts;
-  int late;  // the kernel runs beside the one before it, and waits for it at its end (shared_wait)
+  int late;  // the kernel runs beside the one before it, and waits for it at its end (attn_wait)
 };
 
 // One (sequence, row tile).
