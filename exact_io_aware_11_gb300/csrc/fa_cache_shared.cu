@@ -244,6 +244,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
   }
 }
 
+// Rows from which on a warp of the join takes four: 256 sequences of 32 heads behind four prefixes 84.7 us, with one row a
+// warp 87.7; 64 sequences (2048 rows) 50.9 and 50.5.
+constexpr long long kJoinMany = 4096;
+
 // One list's parts, as the kernels leave them.
 struct JoinList {
   const int2* unit_parts;
@@ -258,14 +262,16 @@ struct JoinLaunch {
   int rows_b, tiles_b, HK;
 };
 
-// The parts of every row of O whose units have not written it: a warp a row. Lane q looks up the
-// q-th part and its weight, then each lane sums 4 channels, eight parts in flight (four, with more blocks an SM: groups 54.4 us, with eight 53.2). Bound: latency
-// and the L2 cache (a part is 4 D + 8 bytes a row).
-template <int D>
+// The parts of every row of O whose units have not written it: R rows a warp, 32 / R lanes a row. A row's lanes look up
+// a part and its weight each, then sum D R / 32 channels each, up to eight parts in flight. Bound: latency and the L2
+// cache (a part is 4 D + 8 bytes a row). One row a warp for few rows, four for many (kJoinMany).
+template <int D, int R>
 __global__ void __launch_bounds__(256, 3) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
-  constexpr int kBatch = 8;
-  const int lane = threadIdx.x & 31;
-  const long long row = blockIdx.x * 8LL + (threadIdx.x >> 5);
+  constexpr int kLanes = 32 / R, kQuads = D / 4 < kLanes ? 1 : D / 4 / kLanes;  // of a row; 4 channels each, of a lane
+  constexpr int kBatch = 8 / kQuads;
+  const int lane = threadIdx.x & (kLanes - 1);
+  const bool active = lane < D / 4;
+  const long long row = blockIdx.x * (8LL * R) + threadIdx.x / kLanes;
   const int bh = static_cast<int>(row / a.N), i = static_cast<int>(row - static_cast<long long>(bh) * a.N);
   const int b = bh / a.Hq, head = bh - b * a.Hq, hk = head / a.G, r = i * a.G + head - hk * a.G;
   const int tile = r / j.rows_b, own = (b * j.tiles_b + tile) * j.HK + hk;
@@ -281,21 +287,25 @@ __global__ void __launch_bounds__(256, 3) shared_join_kernel(const __grid_consta
   }
   grid_dep_wait();
   grid_dep_launch();
-  if (!row_ok) return;
-  const int2 parts = j.list[1].unit_parts[own], p = s.x != 0 ? pl.unit_parts[unit] : make_int2(0, 0);
-  if (s.x == 0 && parts.x < 0) return;  // straight from its unit
+  if (R == 1 && !row_ok) return;
+  const int2 none2 = make_int2(0, -1);
+  const int2 parts = row_ok ? j.list[1].unit_parts[own] : none2, p = s.x != 0 ? pl.unit_parts[unit] : none2;
+  const bool write = row_ok && !(s.x == 0 && parts.x < 0);  // otherwise straight from its unit
+  if (R == 1 && !write) return;
   // the prefix's parts, then the row's own; each list's first CTA, and how many
-  int first = 0, n = 0;
-  bool whole = false;
-  if (s.x != 0) {
-    whole = p.x < 0;
-    first = whole ? 0 : p.x;
-    n = whole ? 1 : p.y - p.x + 1;
+  const bool whole = p.x < 0;
+  const int first = whole ? 0 : p.x, n = whole ? 1 : p.y - p.x + 1;
+  const int all = !write ? 0 : n + (parts.x < 0 ? 1 : parts.y - parts.x + 1);
+  int most = all;  // of the warp's rows
+  if constexpr (R > 1) {
+    most = __reduce_max_sync(0xffffffffu, all);
+    if (most == 0) return;
   }
-  const int all = n + (parts.x < 0 ? 1 : parts.y - parts.x + 1);
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  float4 acc[kQuads];
+#pragma unroll
+  for (int c = 0; c < kQuads; ++c) acc[c] = make_float4(0.f, 0.f, 0.f, 0.f);
   float sum = 0.f, M = -INFINITY;
-  for (int q0 = 0; q0 < all; q0 += 32) {
+  for (int q0 = 0; q0 < most; q0 += kLanes) {
     // this lane's part
     const int q = q0 + lane;
     const float* o = nullptr;
@@ -311,48 +321,60 @@ __global__ void __launch_bounds__(256, 3) shared_join_kernel(const __grid_consta
       l = x.l[pr];
       o = x.o + pr * D;
     }
-    const int count = min(32, all - q0);
+    const int count = min(kLanes, most - q0);
     // the first parts' values are on their way while their weights are formed
-    float4 v[kBatch];
+    float4 v[kBatch][kQuads];
     auto load = [&](int k0) {
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float4* const p = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + k) & 31));
-        v[k] = k0 + k < count && lane < D / 4 ? p[lane] : make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* const from = reinterpret_cast<const float4*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), (k0 + k) & (kLanes - 1), kLanes));
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c)
+          v[k][c] = k0 + k < count && active && (R == 1 || from != nullptr) ? from[c * kLanes + lane] : make_float4(0.f, 0.f, 0.f, 0.f);
       }
     };
     load(0);
     float Mn = fmaxf(M, m);
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, w));
+    for (int w = kLanes / 2; w > 0; w >>= 1) Mn = fmaxf(Mn, __shfl_xor_sync(0xffffffffu, Mn, w));
     const float zero = Mn == -INFINITY ? 0.f : Mn, e = ex2(M - zero), f = ex2(m - zero);
     M = Mn;
     float part = l * f;
 #pragma unroll
-    for (int w = 16; w > 0; w >>= 1) part += __shfl_xor_sync(0xffffffffu, part, w);
+    for (int w = kLanes / 2; w > 0; w >>= 1) part += __shfl_xor_sync(0xffffffffu, part, w);
     sum = sum * e + part;
-    acc.x *= e;
-    acc.y *= e;
-    acc.z *= e;
-    acc.w *= e;
+#pragma unroll
+    for (int c = 0; c < kQuads; ++c) {
+      acc[c].x *= e;
+      acc[c].y *= e;
+      acc[c].z *= e;
+      acc[c].w *= e;
+    }
     for (int k0 = 0; k0 < count; k0 += kBatch) {
       if (k0 > 0) load(k0);
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & 31);
-        acc.x = fmaf(v[k].x, w, acc.x);
-        acc.y = fmaf(v[k].y, w, acc.y);
-        acc.z = fmaf(v[k].z, w, acc.z);
-        acc.w = fmaf(v[k].w, w, acc.w);
+        const float w = __shfl_sync(0xffffffffu, f, (k0 + k) & (kLanes - 1), kLanes);
+#pragma unroll
+        for (int c = 0; c < kQuads; ++c) {
+          acc[c].x = fmaf(v[k][c].x, w, acc[c].x);
+          acc[c].y = fmaf(v[k][c].y, w, acc[c].y);
+          acc[c].z = fmaf(v[k][c].z, w, acc[c].z);
+          acc[c].w = fmaf(v[k][c].w, w, acc[c].w);
+        }
       }
     }
   }
+  if (!write) return;
   const bool none = sum == 0.f;  // a row that sees no key; NaN stays NaN
   const float inv = none ? 0.f : 1.f / sum;
-  if (lane < D / 4) {
-    uint2 w = make_uint2(0u, 0u);
-    if (!none) w = make_uint2(pack16(acc.x * inv, acc.y * inv, a.fp16), pack16(acc.z * inv, acc.w * inv, a.fp16));
-    *reinterpret_cast<uint2*>(a.o + b * a.so.b + head * a.so.h + i * a.so.n + lane * 4) = w;
+  if (active) {
+#pragma unroll
+    for (int c = 0; c < kQuads; ++c) {
+      uint2 w = make_uint2(0u, 0u);
+      if (!none) w = make_uint2(pack16(acc[c].x * inv, acc[c].y * inv, a.fp16), pack16(acc[c].z * inv, acc[c].w * inv, a.fp16));
+      *reinterpret_cast<uint2*>(a.o + b * a.so.b + head * a.so.h + i * a.so.n + (c * kLanes + lane) * 4) = w;
+    }
   }
   if (lane == 0) a.lse[row] = none ? -INFINITY : (M - kBias + log2f(sum)) * kLn2Cache;
 }
@@ -402,7 +424,7 @@ SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_w
   // (20 rows of 64 sequences with 50 to 1000 tokens, 109.1 us in tiles, 93.9; 32 rows 149.2, 123.7; 32 rows of 32 sequences with 3000 to 6000 139.9, 134.3).
   const bool few = NG <= 32;
   p.rows_b = NG <= 8 ? 8 : few ? 16 : NG <= 64 ? 64 : 128;
-  p.lead_b = !few ? own.lead : d == 64 && p.rows_b <= 8 ? 2 : 3;
+  p.lead_b = !few ? (p.rows_b == 64 ? 6 : 4) : d == 64 && p.rows_b <= 8 ? 2 : 3;
   p.lead_a = p.rows_a == 256 ? 6 : 3;
   p.only_b = few && B * NG <= 16;
   p.tiles_b = static_cast<int>((NG + p.rows_b - 1) / p.rows_b);
@@ -451,7 +473,8 @@ cudaError_t launch_shared(const CacheAttnLaunch& a, const AttnGrid& ga, const At
                      : launch_rows<D, 1, INT8, true>(a, gb, p.ctas_b, stream);
   if (e != cudaSuccess) return e;
   const long long rows = static_cast<long long>(a.B) * a.Hq * a.N;
-  return launch_pdl(shared_join_kernel<D>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, a, j);
+  if (rows < kJoinMany) return launch_pdl(shared_join_kernel<D, 1>, dim3(static_cast<unsigned>((rows + 7) / 8)), dim3(256), 0, stream, a, j);
+  return launch_pdl(shared_join_kernel<D, 4>, dim3(static_cast<unsigned>((rows + 31) / 32)), dim3(256), 0, stream, a, j);
 }
 
 }  // namespace
@@ -481,7 +504,8 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   pl.sms = sm_count();
   pl.ctas_a = p.ctas_a;
   pl.per_sm_b = pl.few ? few_row_ctas(a.c.d, p.rows_b) : 1;
-  const ListCost ca = tile_cost(a.c.d, p.rows_a), cb = pl.few ? few_cost(a.c.d, p.rows_b) : tile_cost(a.c.d, p.rows_b);
+  ListCost ca = tile_cost(a.c.d, p.rows_a), cb = pl.few ? few_cost(a.c.d, p.rows_b) : tile_cost(a.c.d, p.rows_b);
+  if (!pl.few) cb.start = 7500;  // units of few steps, one after another (64 sequences, 64 rows to a head, 16 to 64 own tokens: 216 us with 4000, 166)
   pl.step_a = ca.step;
   pl.start_a = ca.start;
   pl.step_b = cb.step;
