@@ -17,9 +17,10 @@ namespace {
 // consecutive channels and loads five parts at a time, statistics and all. A unit
 // of few parts gives each of the block's 8 warps a row; one of more parts gives a row
 // four or all of them, which take every fourth or eighth part and then join theirs (a
-// row of 76 parts with one warp, four at a time: 36 us by itself, with four warps 8 us).
+// row of 76 parts with one warp, four at a time: 36 us by itself, with four warps 8 us). g is read where it
+// lies: copied to registers, single tokens of 64 sequences of 2458 to 4096, 32 heads on 8, d = 64, 56.5 -> 57 to 63 us.
 template <int D>
-__global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
+__global__ void __launch_bounds__(256) cache_attn_merge_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ AttnGrid g) {
   constexpr int kV = D / 32, kBatch = 5, kRowWarps = 8;
   __shared__ float sm_m[kRowWarps], sm_l[kRowWarps], sm_o[kRowWarps][D];
   grid_dep_wait();

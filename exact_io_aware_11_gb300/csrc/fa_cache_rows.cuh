@@ -164,13 +164,13 @@ __device__ __noinline__ void put_nan(const CacheAttnLaunch& a, int b, int row0, 
   }
 }
 
-// The same for an entry of a list (AttnGrid::entry).
+// The same for an entry of a list (SharedGrid::entry).
 template <int D, int NT>
 __device__ __noinline__ void put_nan_shared(const CacheAttnLaunch& a, const int* member, SharedEntry x, int h, int first,
                                             float* o_part, int warp, int lane) {
   constexpr int kPer = D / 32;
   const int d0 = lane * kPer;
-  AttnGrid g{};
+  SharedGrid g{};
   g.N = a.N;
   g.G = a.G;
   g.causal = a.causal;
@@ -196,7 +196,7 @@ __device__ __noinline__ void put_nan_shared(const CacheAttnLaunch& a, const int*
 // the page's scales two steps ahead (one step is less than their way from memory),
 // and the first lane of each page copies its rows (the pages' K and V lie in rows of d bytes of one tensor map each).
 template <int D, int NT, bool SH>
-__device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor<SH> ld, uint8_t* smem,
+__device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, AttnCursor<SH> ld, uint8_t* smem,
                                         uint64_t* full, uint64_t* empty, const Watchdog& wd, int lane) {
   using L = Layout<D, NT>;
   constexpr int kStages = L::kStages;
@@ -268,10 +268,10 @@ __device__ __forceinline__ void produce(const CacheAttnLaunch& a, const AttnGrid
 }
 
 // NT groups of 8 query rows per unit. SH: the units are a list's, and their rows' parts are joined
-// afterwards, but where a sequence shares nothing (AttnGrid::entry).
+// afterwards, but where a sequence shares nothing (SharedGrid::entry).
 template <int D, int NT, bool INT8, bool SH>
 __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
-    cache_attn_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
+    cache_attn_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGridOf<SH> g) {
   using L = Layout<D, NT>;
   constexpr int kStages = L::kStages;
   constexpr int kM = D / 16;  // 16-channel tiles of O
@@ -683,7 +683,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
 }
 
 template <int D, int NT, bool INT8, bool SH = false>
-cudaError_t launch_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+cudaError_t launch_rows(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, int ctas, cudaStream_t stream) {
   auto kern = cache_attn_kernel<D, NT, INT8, SH>;
   static std::atomic<unsigned long long> smem_set{0};
   const cudaError_t e = set_smem_once(smem_set, reinterpret_cast<const void*>(kern), Layout<D, NT>::kSmem);

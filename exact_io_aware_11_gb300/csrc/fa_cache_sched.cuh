@@ -13,6 +13,8 @@
 // writes the unit's merge record.
 #pragma once
 
+#include <type_traits>
+
 #include "fa_cache_internal.h"
 #include "fa_ptx.cuh"
 
@@ -35,14 +37,22 @@ struct AttnGrid {
   float* m_part;  // [2 C][rows]
   float* l_part;
   float* o_part;  // [2 C][rows][D]; tiles (but not a list's): [2 C][rows / 32][D / 4][32 rows][4]
-  // shared prefixes (fa_cache_shared.cu): the entries, made on the device before, the sequences of
-  // the groups, and per unit the CTAs that its parts come from: {-1, 0} where a slot 2 C + unit has it whole
+};
+// Shared prefixes (fa_cache_shared.cu): the entries, made on the device before, the sequences of
+// the groups, and per unit the CTAs that its parts come from: {-1, 0} where a slot 2 C + unit has it whole.
+// A struct of its own: with these in AttnGrid as well, that is past the size up to which a kernel's argument is
+// held in registers, which cost the tile kernels without lists 1 to 3 % (128 rows of 16 sequences, 32 heads on 8,
+// e4m3, pages of 16: 84.6 -> 86.0 us; d = 64 75.4 -> 77.5).
+struct SharedGrid : AttnGrid {
   const SharedEntry* entry;
   const int* entries;  // how many, and the CTAs that work on them
   const int* member;
   int2* unit_parts;
   int late;  // the kernel runs beside the one before it, and waits for it at its end (attn_wait)
 };
+
+template <bool SH>
+using AttnGridOf = std::conditional_t<SH, SharedGrid, AttnGrid>;
 
 // One (sequence, row tile).
 struct AttnEntry {
@@ -68,7 +78,7 @@ struct AttnEntryOf<true> {
   using type = SharedEntry;
 };
 template <bool SH>
-__device__ __forceinline__ typename AttnEntryOf<SH>::type attn_entry(const AttnGrid& g, int e) {
+__device__ __forceinline__ typename AttnEntryOf<SH>::type attn_entry(const AttnGridOf<SH>& g, int e) {
   typename AttnEntryOf<SH>::type x;
   if constexpr (SH) {
     const int4* const p = reinterpret_cast<const int4*>(g.entry + e);
@@ -108,7 +118,7 @@ struct AttnRow {
   bool exists, real;
 };
 template <typename X>
-__device__ __forceinline__ AttnRow shared_row(const AttnGrid& g, const X& x, int r) {
+__device__ __forceinline__ AttnRow shared_row(const SharedGrid& g, const X& x, int r) {
   AttnRow y;
   int row = x.row0 + r, ql = x.ql;
   y.b = x.b;
@@ -131,8 +141,9 @@ __device__ __forceinline__ AttnRow shared_row(const AttnGrid& g, const X& x, int
 }
 
 template <bool SH>
-__device__ __forceinline__ int attn_entries(const AttnGrid& g) {
-  return SH ? __ldcg(g.entries) : g.B * g.row_tiles;
+__device__ __forceinline__ int attn_entries(const AttnGridOf<SH>& g) {
+  if constexpr (SH) return __ldcg(g.entries);
+  return g.B * g.row_tiles;
 }
 
 // A CTA's place in the list: unit (e, h) at `step`, which is `pos` places from the
@@ -142,25 +153,25 @@ struct AttnCursor {
   typename AttnEntryOf<SH>::type x;
   int e, h, step;
   long long pos, end;
-  __device__ __forceinline__ bool done(const AttnGrid& g) const {
+  __device__ __forceinline__ bool done(const AttnGridOf<SH>& g) const {
     // without a workspace a CTA finishes the units that start in its run
     return pos >= end && (g.split || step == 0);
   }
-  __device__ __forceinline__ void next(const AttnGrid& g) {
+  __device__ __forceinline__ void next(const AttnGridOf<SH>& g) {
     ++pos;
     if (++step == x.steps) next_unit(g);
   }
   // Steps of this unit that are the CTA's.
-  __device__ __forceinline__ int run(const AttnGrid& g) const {
+  __device__ __forceinline__ int run(const AttnGridOf<SH>& g) const {
     const int left = x.steps - step;
     return g.split && end - pos < left ? static_cast<int>(end - pos) : left;
   }
-  __device__ __forceinline__ void skip(const AttnGrid& g, int n) {
+  __device__ __forceinline__ void skip(const AttnGridOf<SH>& g, int n) {
     pos += n;
     step += n;
     if (step == x.steps) next_unit(g);
   }
-  __device__ __forceinline__ void next_unit(const AttnGrid& g) {
+  __device__ __forceinline__ void next_unit(const AttnGridOf<SH>& g) {
     step = 0;
     pos += g.lead;
     if (++h == g.HK) {
@@ -201,7 +212,7 @@ __device__ __forceinline__ long long attn_start(const AttnShareOf<true>& s, int 
 // This CTA's cursor. Called by the whole CTA of kThreads threads; `sh` and
 // `part` (kThreads / 32 words) are shared memory.
 template <int kThreads, bool SH>
-__device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGrid& g, AttnShareOf<SH>* sh, long long* part) {
+__device__ __forceinline__ AttnCursor<SH> attn_share(const AttnGridOf<SH>& g, AttnShareOf<SH>* sh, long long* part) {
   const int E = attn_entries<SH>(g), per = (E + kThreads - 1) / kThreads;
   const int e0 = min(E, static_cast<int>(threadIdx.x) * per), e1 = min(E, e0 + per);
   typename AttnEntryOf<SH>::type own{};  // the thread's only entry, where it has just one
@@ -306,7 +317,7 @@ __device__ __forceinline__ T attn_load(const T* p) {
 }
 // At the start (end false) and at the end of a kernel: the wait for the kernels before it.
 template <bool SH>
-__device__ __forceinline__ void attn_wait(const AttnGrid& g, bool end) {
+__device__ __forceinline__ void attn_wait(const AttnGridOf<SH>& g, bool end) {
   if constexpr (SH) {
     if ((g.late != 0) != end) return;
   } else if (end) {
@@ -329,8 +340,8 @@ cudaError_t launch_cache_attention_tiles_e4m3(const CacheAttnLaunch& a, const At
                                               cudaStream_t stream);
 cudaError_t launch_cache_attention_tiles_int8(const CacheAttnLaunch& a, const AttnGrid& g, int ctas,
                                               cudaStream_t stream);
-// The same over a list of entries (AttnGrid::entry).
-cudaError_t launch_shared_tiles_e4m3(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream);
-cudaError_t launch_shared_tiles_int8(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream);
+// The same over a list of entries (SharedGrid::entry).
+cudaError_t launch_shared_tiles_e4m3(const CacheAttnLaunch& a, const SharedGrid& g, int ctas, cudaStream_t stream);
+cudaError_t launch_shared_tiles_int8(const CacheAttnLaunch& a, const SharedGrid& g, int ctas, cudaStream_t stream);
 
 }  // namespace fa

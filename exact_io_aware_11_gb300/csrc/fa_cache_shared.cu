@@ -461,9 +461,9 @@ SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_w
 }
 
 template <int D, bool INT8>
-cudaError_t launch_shared(const CacheAttnLaunch& a, const AttnGrid& ga, const AttnGrid& gb, const SharedPlan& p, const JoinLaunch& j,
+cudaError_t launch_shared(const CacheAttnLaunch& a, const SharedGrid& ga, const SharedGrid& gb, const SharedPlan& p, const JoinLaunch& j,
                           cudaStream_t stream) {
-  auto tiles = [&](const AttnGrid& g, int ctas) {
+  auto tiles = [&](const SharedGrid& g, int ctas) {
     return INT8 ? launch_shared_tiles_int8(a, g, ctas, stream) : launch_shared_tiles_e4m3(a, g, ctas, stream);
   };
   cudaError_t e = p.only_b ? cudaSuccess : tiles(ga, p.ctas_a);
@@ -522,7 +522,7 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   const int most = a.B > groups ? a.B : groups, threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
   cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(threads), 0, stream, pl);
   if (e != cudaSuccess) return e;
-  AttnGrid g{};
+  SharedGrid g{};
   g.B = a.B;
   g.HK = a.c.H;
   g.N = a.N;
@@ -534,7 +534,7 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   g.kv_len = a.kv_len;
   g.q_len = a.q_len;
   g.member = pl.member;
-  AttnGrid ga = g, gb = g;
+  SharedGrid ga = g, gb = g;
   ga.rows = p.rows_a;
   ga.lead = p.lead_a;
   ga.entry = pl.entry_a;

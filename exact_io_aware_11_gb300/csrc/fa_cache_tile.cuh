@@ -75,7 +75,7 @@ struct __align__(16) TileUnit {
   int b, row0, h, first;  // sequence, first row, cache head, first step
   int steps, kv, ql, seen_last;  // seen: tokens the last row sees; top bit: the unit ends here
 };
-// A list's (AttnGrid::entry): rows, first column and number as AttnEntry has them.
+// A list's (SharedGrid::entry): rows, first column and number as AttnEntry has them.
 struct __align__(16) TileUnitShared : TileUnit {
   int list, count, col, unit;
 };
@@ -110,7 +110,7 @@ struct TileBars {
 // warp some 75 cycles each to issue. K's also describes the units to the other warps (TileLayout::kUnits), and
 // writes the record of a cut unit that the CTA ends, well before that end.
 template <int D, int NQ, bool SH>
-__device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGrid& g, AttnCursor<SH> ld,
+__device__ __forceinline__ void tile_produce(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, AttnCursor<SH> ld,
                                              const AttnShareOf<SH>& share, uint8_t* smem, const TileBars& b,
                                              const Watchdog& wd, int loader, int lane) {
   using L = TileLayout<D, NQ, SH>;
@@ -268,7 +268,7 @@ __device__ __noinline__ void convert_checked(uint32_t src, uint32_t dst, const f
 // apart) and in bit 0 (so do the results, at 2 c ^ (r & 7)), and every bank is met
 // once in both directions.
 template <int D, int NQ, bool INT8, bool SH>
-__device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGrid& g, uint8_t* smem,
+__device__ __forceinline__ void tile_convert(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, uint8_t* smem,
                                              const TileBars& b, const Watchdog& wd, int cw, int lane) {
   using L = TileLayout<D, NQ, SH>;
   using Unit = typename TileUnitOf<SH>::type;
@@ -442,10 +442,10 @@ __device__ __forceinline__ float weigh16(const uint32_t (&v)[32], int c0, float 
 // copy's warps take half of a step's keys, with weights of zero for the others; a unit ends
 // with the copies joined. All four softmax warps then work, each on half the columns.
 // SH: the units are a list's, and their rows' parts are joined afterwards, but where a sequence
-// shares nothing (AttnGrid::entry).
+// shares nothing (SharedGrid::entry).
 template <int D, int NQ, int REP, bool INT8, bool P16, bool SH>
 __global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
-    cache_attn_tile_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGrid g) {
+    cache_attn_tile_kernel(const __grid_constant__ CacheAttnLaunch a, const AttnGridOf<SH> g) {
   using L = TileLayout<D, NQ, SH>;
   using Unit = typename TileUnitOf<SH>::type;
   // The weights are handed over in halves of 64 keys, so that P V begins under the second
@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(TileLayout<D, NQ, SH>::kThreads, 1)
 }
 
 template <int D, int NQ, int REP, bool INT8, bool P16, bool SH>
-cudaError_t launch_tile_variant(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+cudaError_t launch_tile_variant(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, int ctas, cudaStream_t stream) {
   using L = TileLayout<D, NQ, SH>;
   auto kern = cache_attn_tile_kernel<D, NQ, REP, INT8, P16, SH>;
   static std::atomic<unsigned long long> smem_set{0};
@@ -932,14 +932,14 @@ cudaError_t launch_tile_variant(const CacheAttnLaunch& a, const AttnGrid& g, int
 }
 
 template <int D, bool INT8, bool P16, bool SH>
-cudaError_t launch_tile_rows(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+cudaError_t launch_tile_rows(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, int ctas, cudaStream_t stream) {
   if (g.rows == 64) return launch_tile_variant<D, 1, 2, INT8, P16, SH>(a, g, ctas, stream);
   return g.rows == 128 ? launch_tile_variant<D, 1, 1, INT8, P16, SH>(a, g, ctas, stream)
                        : launch_tile_variant<D, 2, 1, INT8, P16, SH>(a, g, ctas, stream);
 }
 
 template <int D, bool INT8, bool SH = false>
-cudaError_t launch_tiles(const CacheAttnLaunch& a, const AttnGrid& g, int ctas, cudaStream_t stream) {
+cudaError_t launch_tiles(const CacheAttnLaunch& a, const AttnGridOf<SH>& g, int ctas, cudaStream_t stream) {
   return a.c.page == 16 ? launch_tile_rows<D, INT8, true, SH>(a, g, ctas, stream)
                         : launch_tile_rows<D, INT8, false, SH>(a, g, ctas, stream);
 }
