@@ -425,7 +425,10 @@ SharedPlan shared_plan(int B, int HK, int G, int N, int d, int page, int table_w
   const bool few = NG <= 32;
   p.rows_b = NG <= 8 ? 8 : few ? 16 : NG <= 64 ? 64 : 128;
   p.lead_b = !few ? (p.rows_b == 64 ? 6 : 4) : d == 64 && p.rows_b <= 8 ? 2 : 3;
-  p.lead_a = p.rows_a == 256 ? 6 : 3;
+  // One gap for tiles of every size, although pairs of them take some 5 steps to begin: with 3, 6 and 8 of them 128 sequences behind two
+  // prefixes of 2000 and 16000 tokens 65.4, 65.5, 68.2 us (GPU time), 192 behind three of 1000 to 9000 (int8) 66.6, 68.7, 69.9, 512 behind
+  // eight of 1000 to 6000 128.6, 131.7, 134.2; 64 behind one of 8192 49.4, 50.2, 50.1, 256 behind 32768 209.0, 208.7, 208.7.
+  p.lead_a = 3;
   p.only_b = few && B * NG <= 16;
   p.tiles_b = static_cast<int>((NG + p.rows_b - 1) / p.rows_b);
   // (with the other SMs at work on list B, few steps a CTA are no reason for smaller tiles)
