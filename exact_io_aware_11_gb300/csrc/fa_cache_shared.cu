@@ -17,7 +17,7 @@
 // other CTAs of list A's kernel leave at once, and list B's kernel, let go by them, begins there without
 // waiting (its own wait, for list A's kernel, comes at its end, so that the join's covers both).
 // It may: list A's CTAs let it go after their wait for the plan, whose writes, and all
-// before them, are in the L2 cache then, where it reads (attn_load). It cannot keep a CTA of list A from running,
+// before them, it has by the plan's mark (attn_wait). It cannot keep a CTA of list A from running,
 // as they have all begun.
 //
 // What bounds it, and what it measured (GPU time; fa_cache_attention on the same sequences in brackets): 64 sequences behind
@@ -25,6 +25,8 @@
 // results, join and launches are some 25; 256 behind 32768 with 256 to 2048: 203 to 217 us (1548), bound by the SMs: 1.72 us
 // a step of 256 rows and 128 keys (1480 TFLOP/s on all SMs), 0.42 us of an SM a step of own tokens (32 KB: 78 GB/s, which
 // is what an SM takes in).
+#include <chrono>
+
 #include "fa_cache_rows.cuh"
 
 namespace fa {
@@ -48,6 +50,7 @@ struct PlanLaunch {
   int* member;       // [B]
   int4* seq;         // [B] where the sequence's part over the prefix is: list (0 none, 1 A, 2 B), its
                      // first row in the group, the group's first entry
+  PlanMark mark;
 };
 
 __device__ __forceinline__ SharedEntry make_entry(int b, int row0, int kv, int ql, int seen, int list, int count, int col) {
@@ -241,6 +244,8 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const __grid_
     a.entries[1] = n;
     a.entries[2] = at_b;
     a.entries[3] = (a.sms - n) * a.per_sm_b;
+    // after a barrier of the CTA, so for all of its writes
+    asm volatile("st.release.gpu.u64 [%0], %1;" ::"l"(__cvta_generic_to_global(a.mark.word)), "l"(a.mark.call) : "memory");
   }
 }
 
@@ -260,15 +265,18 @@ struct JoinLaunch {
   JoinList list[2];  // A, B
   const int4* seq;
   int rows_b, tiles_b, HK;
+  PlanMark mark;
 };
 
 // The parts of every row of O whose units have not written it: R rows a warp, 32 / R lanes a row. A row's lanes look up
 // a part and its weight each, then sum D R / 32 channels each, up to eight parts in flight. Bound: latency and the L2
-// cache (a part is 4 D + 8 bytes a row). One row a warp for few rows, four for many (kJoinMany).
+// cache (a part is 4 D + 8 bytes a row). One row a warp for few rows, four for many (kJoinMany); the former would spill
+// with the registers of three blocks an SM.
 template <int D, int R>
-__global__ void __launch_bounds__(256, 3) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
+__global__ void __launch_bounds__(256, R == 1 ? 2 : 3) shared_join_kernel(const __grid_constant__ CacheAttnLaunch a, const __grid_constant__ JoinLaunch j) {
   constexpr int kLanes = 32 / R, kQuads = D / 4 < kLanes ? 1 : D / 4 / kLanes;  // of a row; 4 channels each, of a lane
   constexpr int kBatch = 8 / kQuads;
+  plan_wait(j.mark);  // rows are looked up while the lists' kernels end
   const int lane = threadIdx.x & (kLanes - 1);
   const bool active = lane < D / 4;
   const long long row = blockIdx.x * (8LL * R) + threadIdx.x / kLanes;
@@ -276,7 +284,6 @@ __global__ void __launch_bounds__(256, 3) shared_join_kernel(const __grid_consta
   const int b = bh / a.Hq, head = bh - b * a.Hq, hk = head / a.G, r = i * a.G + head - hk * a.G;
   const int tile = r / j.rows_b, own = (b * j.tiles_b + tile) * j.HK + hk;
   const bool row_ok = row < static_cast<long long>(a.B) * a.Hq * a.N;
-  // (the plan's writes are in the L2 cache long since: this kernel was let go by list B's, that by list A's)
   const int4 s = row_ok ? __ldcg(j.seq + b) : make_int4(0, 0, 0, 0);
   const JoinList& pl = j.list[s.x == 2 ? 1 : 0];  // where the prefix's parts are
   int unit = 0, at = 0;
@@ -287,6 +294,7 @@ __global__ void __launch_bounds__(256, 3) shared_join_kernel(const __grid_consta
   }
   grid_dep_wait();
   grid_dep_launch();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *j.mark.word = 0ull;  // a graph may run this call again
   if (R == 1 && !row_ok) return;
   const int2 none2 = make_int2(0, -1);
   const int2 parts = row_ok ? j.list[1].unit_parts[own] : none2, p = s.x != 0 ? pl.unit_parts[unit] : none2;
@@ -522,6 +530,8 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   pl.entry_b = reinterpret_cast<SharedEntry*>(a.ws + p.entry_b);
   pl.member = reinterpret_cast<int*>(a.ws + p.member);
   pl.seq = reinterpret_cast<int4*>(a.ws + p.seq);
+  static std::atomic<unsigned long long> calls{static_cast<unsigned long long>(std::chrono::steady_clock::now().time_since_epoch().count()) << 16 | 1};
+  pl.mark = PlanMark{reinterpret_cast<unsigned long long*>(a.ws + 128), calls.fetch_add(2, std::memory_order_relaxed)};  // never 0
   const int most = a.B > groups ? a.B : groups, threads = most >= kPlanThreads ? kPlanThreads : (most + 31) / 32 * 32;
   cudaError_t e = launch_pdl(shared_plan_kernel, dim3(1), dim3(threads), 0, stream, pl);
   if (e != cudaSuccess) return e;
@@ -550,7 +560,7 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   gb.lead = p.lead_b;
   gb.entry = pl.entry_b;
   gb.entries = pl.entries + 2;
-  gb.late = p.only_b ? 0 : 1;
+  if (!p.only_b) gb.mark = pl.mark;
   gb.unit_parts = reinterpret_cast<int2*>(a.ws + p.unit_b);
   gb.m_part = reinterpret_cast<float*>(a.ws + p.m_b);
   gb.l_part = reinterpret_cast<float*>(a.ws + p.l_b);
@@ -562,6 +572,7 @@ cudaError_t launch_shared_attention(const CacheAttnLaunch& a, const int32_t* pre
   j.rows_b = p.rows_b;
   j.tiles_b = p.tiles_b;
   j.HK = a.c.H;
+  j.mark = pl.mark;
   if (a.c.d == 128)
     return a.c.int8 ? launch_shared<128, true>(a, ga, gb, p, j, stream) : launch_shared<128, false>(a, ga, gb, p, j, stream);
   return a.c.int8 ? launch_shared<64, true>(a, ga, gb, p, j, stream) : launch_shared<64, false>(a, ga, gb, p, j, stream);

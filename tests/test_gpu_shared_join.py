@@ -133,3 +133,29 @@ def test_more_sequences_than_the_plan_has_threads(fa, d, fmt, dt):
     pick = list(range(0, B, 61))
     check_attention(fa, m, q[pick], [lens[b] for b in pick], o=o[pick], lse=lse[pick], dt=dt, table=m.table[pick])
     assert fa.device_status() == fa.FA_OK
+
+
+def test_a_call_leaves_no_mark_of_its_plan(fa):
+    """Kernels that run beside each other know by a mark in the workspace that the call's plan is made. A graph runs the same call
+    again, so the mark is gone when the call ends, and what the workspace holds before a replay does not matter."""
+    m, of, prefix, lens, qlens = mixed(fa, 40, 2, 2, 32, 64, "e4m3", seed=3)
+    q, table, args = queries(40, 8, 2, 64, "bf16", 25), m.table.cuda(), (i32(lens), i32(of), i32(prefix))
+    need = fa.cache_attention_shared_workspace_bytes(m.cache, 40, 8, 2, table.shape[1], len(prefix))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device="cuda")
+    out, lse = torch.empty_like(q), torch.empty((40, 8, 2), device="cuda")
+    want = fa.cache_attention_shared(q, m.cache, table, *args, workspace=ws)
+    torch.cuda.synchronize()
+    assert not ws[128:136].any()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            fa.cache_attention_shared(q, m.cache, table, *args, out=out, lse=lse, workspace=ws)
+    left = None
+    for i in range(6):
+        ws.fill_(0xff) if left is None or i % 2 else ws.copy_(left)
+        out.fill_(7)
+        graph.replay()
+        torch.cuda.synchronize()
+        left = ws.clone()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1]) and not ws[128:136].any()
+    assert fa.device_status() == fa.FA_OK
