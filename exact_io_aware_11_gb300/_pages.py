@@ -57,6 +57,8 @@ def _table(t, refs, page_size, index):
     entries, stride, rows, width = _matrix(t, "page_table", index)
     counts = _ints(refs, "refs", index, None)
     pages = refs.numel()
+    if not -2 ** 31 <= page_size < 2 ** 31 or pages >= 2 ** 31:  # others the library refuses
+        raise ValueError("page_size and the values of refs must be numbers of 32 bits")
     return _PACK.pack(entries, stride, rows, width, counts, pages, page_size), rows, width, pages
 
 
