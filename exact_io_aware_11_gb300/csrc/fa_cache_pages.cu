@@ -324,7 +324,7 @@ __global__ void __launch_bounds__(count_threads(C), 1)
   extern __shared__ int2 cache[];  // row and state, entry
   constexpr int kThreads = count_threads(C);
   __shared__ int part[kThreads / 32];
-  __shared__ int slots[5][C];  // of the exchanges
+  __shared__ int slots[4][C];  // items that take a page (and whether any is shared), these after the election, free pages, the first row that fails
   __shared__ int fail_row, any_shared;
   const PageTable& t = a.t;
   const int rank = C == 1 ? 0 : blockIdx.x;  // the grid is one cluster

@@ -660,8 +660,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NT>::kCtas)
       int first = sm_nan[turn][0];
 #pragma unroll
       for (int w = 1; w < kWarps; ++w) first = min(first, sm_nan[turn][w]);
-      if (first != 0x7fffffff)
-        {
+      if (first != 0x7fffffff) {
         float* const at = direct ? nullptr : g.o_part + static_cast<long long>(slot) * g.rows * D;
         if constexpr (SH)
           put_nan_shared<D, NT>(a, g.member, x, h, first, at, warp, lane);
