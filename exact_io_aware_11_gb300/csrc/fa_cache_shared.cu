@@ -22,9 +22,9 @@
 //
 // What bounds it, and what it measured (GPU time; fa_cache_attention on the same sequences in brackets): 64 sequences behind
 // 8192 tokens with 50 to 2000 of their own, 32 heads on 8, d = 128, e4m3: 50 us (118), of which plan, first scores, last
-// results, join and launches are some 25; 256 behind 32768 with 256 to 2048: 203 to 217 us (1548), bound by the SMs: 1.72 us
-// a step of 256 rows and 128 keys (1480 TFLOP/s on all SMs), 0.42 us of an SM a step of own tokens (32 KB: 78 GB/s, which
-// is what an SM takes in).
+// results, join and launches are some 27; 256 behind 32768 with 256 to 2048: 207 to 213 us (1548), bound by the SMs: 1.72 us
+// a step of 256 rows and 128 keys (1480 TFLOP/s on all SMs), 0.42 us of an SM a step of own tokens (32 KB: 78 GB/s). Short
+// prefixes are sooner served without sharing: 64 sequences with 500 to 2000 tokens behind 128 52 us (37).
 #include <chrono>
 
 #include "fa_cache_rows.cuh"

@@ -489,7 +489,8 @@ size_t fa_cache_attention_shared_workspace_bytes(const fa_cache* cache, int B, i
  * The lengths of prefixes and sequences may be any: a sequence whose rows do not all see the whole
  * prefix, and one that is alone in its group, goes by itself. Calls of more than 128 query rows to a cache
  * head and sequence (N * Hq / H) share nothing, because their products bound them; nor do calls whose table has
- * room for few tokens in all, which fa_cache_attention serves sooner.
+ * room for few tokens in all, which fa_cache_attention serves sooner. Prefixes that are short beside
+ * the sequences' own tokens are shared all the same, though fa_cache_attention would be sooner done: name long ones.
  *   workspace : DEVICE, 16-byte aligned, fa_cache_attention_shared_workspace_bytes at least, contents
  *               ignored. Calls that share it must be ordered on the GPU. */
 int fa_cache_attention_shared(const void* q, void* o, float* lse, const fa_cache* cache, int B, int Hq, int N,
